@@ -257,4 +257,7 @@ int mla_verify_abi_version(void);
 }
 #endif
 
+/* the 4-bit latent cache, whose calls use the types above */
+#include "mla_kvq.h"
+
 #endif /* MLA_VERIFY_H */

@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in include/mla_verify.h and include/mla_ddtree.h.
+"""ctypes binding of the C ABI in include/mla_verify.h, include/mla_ddtree.h and
+include/mla_kvq.h.
 
 Argument marshalling only: torch tensors give device pointers, sizes and
 strides; every step of the computation runs in the CUDA library.  The library
@@ -23,16 +24,20 @@ ALGO = {"auto": 0, "simt": 1, "tc": 2}
 
 DEVERR = {
     0x1: "PREFIX", 0x2: "INDPTR", 0x4: "SLOT", 0x8: "PARENT", 0x10: "PAGES",
-    0x20: "CAPACITY", 0x40: "TIMEOUT", 0x80: "LAYOUT", 0x100: "DRAFT",
+    0x20: "CAPACITY", 0x40: "TIMEOUT", 0x80: "LAYOUT", 0x100: "DRAFT", 0x200: "NONFINITE",
 }
 
 # every symbol include/*.h declares
 EXPORTS = ("mla_verify_workspace_size", "mla_verify_attn", "mla_verify_attn_noalloc", "mla_verify_noalloc_check",
            "mla_verify_build_meta", "mla_verify_check", "mla_verify_splits_used", "mla_status_str",
            "mla_verify_abi_version",
-           "mla_verify_selftest_timeout", "mla_kv_compact", "mla_ddtree_build", "mla_ddtree_accept")
+           "mla_verify_selftest_timeout", "mla_kv_compact", "mla_ddtree_build", "mla_ddtree_accept",
+           "mla_kvq_write", "mla_kvq_read", "mla_kvq_attn", "mla_kvq_attn_workspace_size", "mla_kvq_check")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 DDTREE_WORKSPACE_BYTES = 256
+KVQ_ROW_BYTES = 416
+KVQ_MAX_EXPONENT = 32
+KVQ_WORKSPACE_BYTES = 16384
 
 
 class MlaVerifyArgs(ctypes.Structure):
@@ -70,6 +75,35 @@ class MlaDdtreeAcceptArgs(ctypes.Structure):
         ("node_slot", ctypes.c_void_p),
         ("accept_len", ctypes.c_void_p), ("accept_nodes", ctypes.c_void_p), ("accept_slots", ctypes.c_void_p),
         ("next_token", ctypes.c_void_p),
+    ]
+
+
+class MlaKvqCache(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("slots", ctypes.c_int64),
+                ("exponent", ctypes.c_int)]
+
+
+class MlaKvqRows(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64), ("dtype", ctypes.c_int),
+        ("kv_c", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
+        ("kv_c_stride", ctypes.c_int64), ("k_pe_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p),
+    ]
+
+
+class MlaKvqAttnArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("Q", ctypes.c_int), ("H", ctypes.c_int),
+        ("cache", MlaKvqCache),
+        ("q_lat", ctypes.c_void_p), ("q_pe", ctypes.c_void_p),
+        ("page_size", ctypes.c_int),
+        ("kv_indptr", ctypes.c_void_p), ("kv_indices", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int),
+        ("prefix_lens", ctypes.c_void_p), ("tree_parent", ctypes.c_void_p),
+        ("window", ctypes.c_int), ("sinks", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
     ]
 
 
@@ -119,6 +153,16 @@ def load(path: Optional[str] = None):
     lib.mla_ddtree_accept.restype = ctypes.c_int
     lib.mla_ddtree_accept.argtypes = [ctypes.POINTER(MlaDdtreeAcceptArgs), ctypes.c_void_p, ctypes.c_size_t,
                                       ctypes.c_void_p]
+    for f in (lib.mla_kvq_write, lib.mla_kvq_read):
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.POINTER(MlaKvqCache), ctypes.POINTER(MlaKvqRows), ctypes.c_void_p, ctypes.c_size_t,
+                      ctypes.c_void_p]
+    lib.mla_kvq_attn.restype = ctypes.c_int
+    lib.mla_kvq_attn.argtypes = [ctypes.POINTER(MlaKvqAttnArgs), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.mla_kvq_attn_workspace_size.restype = ctypes.c_size_t
+    lib.mla_kvq_attn_workspace_size.argtypes = [ctypes.POINTER(MlaKvqAttnArgs)]
+    lib.mla_kvq_check.restype = ctypes.c_int
+    lib.mla_kvq_check.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]
     lib.mla_verify_check.restype = ctypes.c_int
     lib.mla_verify_check.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]
     lib.mla_status_str.restype = ctypes.c_char_p
@@ -561,3 +605,205 @@ def ddtree_accept(tree_parent, tree_token, target_token, node_slot=None, workspa
     slots = None if node_slot is None else torch.full((B, Q), -7, dtype=torch.int32, device=dev)
     ddtree_accept_into(tree_parent, tree_token, target_token, n_len, nodes, nxt, workspace, node_slot, slots, stream)
     return n_len, nodes, nxt, slots, workspace
+
+
+# ----------------------------------------------------------------------------
+# 4-bit latent cache (include/mla_kvq.h)
+# ----------------------------------------------------------------------------
+@dataclass
+class QuantCache:
+    """A pool of packed cache rows: ``rows`` is a uint8 [slots][416] tensor or
+    view (row stride a multiple of 32 bytes), ``exponent`` the power of two its
+    latents are scaled by."""
+    rows: object
+    exponent: int = 0
+
+    def check(self):
+        import torch
+        r = self.rows
+        if r is None or r.dtype != torch.uint8 or r.dim() != 2 or r.shape[1] != KVQ_ROW_BYTES or r.stride(1) != 1:
+            raise ValueError(f"cache rows must be a [slots][{KVQ_ROW_BYTES}] uint8 view with unit column stride")
+        if not -KVQ_MAX_EXPONENT <= self.exponent <= KVQ_MAX_EXPONENT:
+            raise ValueError(f"cache exponent {self.exponent} outside +-{KVQ_MAX_EXPONENT}")
+
+    def c_struct(self) -> MlaKvqCache:
+        r = self.rows
+        # the row stride of a one-row tensor is whatever its maker left there
+        stride = r.stride(0) if r.shape[0] > 1 else KVQ_ROW_BYTES
+        return MlaKvqCache(r.data_ptr(), stride, r.shape[0], self.exponent)
+
+
+def kvq_alloc(slots: int, exponent: int = 0, device="cuda") -> QuantCache:
+    """A cache of ``slots`` rows that all stand for zeros."""
+    import torch
+    rows = torch.zeros((slots, KVQ_ROW_BYTES), dtype=torch.uint8, device=device)
+    return QuantCache(rows, exponent)
+
+
+def _one_device(**tensors):
+    """Every tensor on the same CUDA device; returns it."""
+    _on_cuda(**tensors)
+    devs = {t.device for t in tensors.values() if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    return devs.pop()
+
+
+def _kvq_launch(what: str, f, dev, stream, *args):
+    """Calls f(*args, stream) with the tensors' device current."""
+    import torch
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{what}: stream on {stream.device}, tensors on {dev}")
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(stream))
+    if st != MLA_OK:
+        raise MlaError(st, what)
+
+
+def _kvq_rows(what: str, f, cache: QuantCache, kv_c, k_pe, slots, workspace, stream, check: bool):
+    import torch
+    if check:
+        cache.check()
+        if kv_c is None or kv_c.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("kv_c must be a bfloat16 or float32 tensor")
+        for t, name, w in ((kv_c, "kv_c", 512), (k_pe, "k_pe", 64)):
+            if t is None or t.dtype != kv_c.dtype or t.dim() != 2 or t.shape[1] != w or t.stride(1) != 1:
+                raise ValueError(f"{name} must be a [n][{w}] {kv_c.dtype} view with unit column stride")
+            if t.shape[0] > 1 and t.stride(0) < w:
+                raise ValueError(f"{name}: rows overlap")
+        if k_pe.shape[0] != kv_c.shape[0]:
+            raise ValueError("kv_c and k_pe must have the same number of rows")
+        _need(slots, "slots", torch.int32, (kv_c.shape[0],))
+        _one_device(rows=cache.rows, kv_c=kv_c, k_pe=k_pe, slots=slots, workspace=workspace)
+    dev = cache.rows.device
+    if workspace is None:
+        workspace = alloc_workspace(KVQ_WORKSPACE_BYTES, dev)
+    n = kv_c.shape[0]
+    r = MlaKvqRows(n, MLA_BF16 if kv_c.dtype == torch.bfloat16 else MLA_FP32, kv_c.data_ptr(), k_pe.data_ptr(),
+                   kv_c.stride(0) if n > 1 else 512, k_pe.stride(0) if n > 1 else 64, slots.data_ptr())
+    _kvq_launch(what, f, dev, stream, ctypes.byref(cache.c_struct()), ctypes.byref(r), workspace.data_ptr(),
+                _ws_bytes(workspace))
+    return workspace
+
+
+def kvq_write(cache: QuantCache, kv_c, k_pe, slots, workspace=None, stream=None, check: bool = True):
+    """Run mla_kvq_write: quantise row i of kv_c [n][512] and k_pe [n][64]
+    (bf16 or fp32, any row stride) into pool slot slots[i] (int32; -1 skips).
+    Returns the workspace (kvq_check reads its error bits).  check=False skips
+    the tensor checks, for a loop that already passed them."""
+    return _kvq_rows("mla_kvq_write", load().mla_kvq_write, cache, kv_c, k_pe, slots, workspace, stream, check)
+
+
+def kvq_read(cache: QuantCache, slots, dtype: str = "bf16", kv_c=None, k_pe=None, workspace=None, stream=None,
+             check: bool = True):
+    """Run mla_kvq_read: the rows that pool slots ``slots`` stand for, exactly,
+    as ``dtype`` ("bf16" or "fp32"; that of kv_c when given).  Rows with slot
+    -1 keep what the given arrays hold (zeros in arrays made here).  Returns
+    (kv_c [n][512], k_pe [n][64], workspace)."""
+    import torch
+    dt = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype] if kv_c is None else kv_c.dtype
+    if kv_c is None:
+        kv_c = torch.zeros((slots.shape[0], 512), dtype=dt, device=cache.rows.device)
+    if k_pe is None:
+        k_pe = torch.zeros((slots.shape[0], 64), dtype=dt, device=cache.rows.device)
+    ws = _kvq_rows("mla_kvq_read", load().mla_kvq_read, cache, kv_c, k_pe, slots, workspace, stream, check)
+    return kv_c, k_pe, ws
+
+
+@dataclass
+class KvqInputs:
+    """Device tensors of one attention call over a 4-bit cache.  tree_parent
+    None: each node's parent is the node before it (decoding, a linear draft).
+    prefix_lens[b] = -1 marks an unused sequence of a padded batch."""
+    B: int
+    Q: int
+    H: int
+    scale: float
+    q_lat: object           # [B, Q, H, 512] bf16
+    q_pe: object            # [B, Q, H, 64] bf16
+    cache: QuantCache
+    prefix_lens: object     # [B] int32
+    page_size: int
+    tree_parent: object = None   # [B, Q] int32
+    kv_indptr: object = None     # [B + 1] int32    (page_size 1)
+    kv_indices: object = None    # int32            (page_size 1)
+    block_table: object = None   # [B, max_pages] int32  (page_size > 1)
+    window: int = 0
+    sinks: int = 0
+
+    def tensors(self):
+        return dict(q_lat=self.q_lat, q_pe=self.q_pe, rows=self.cache.rows, prefix_lens=self.prefix_lens,
+                    tree_parent=self.tree_parent, kv_indptr=self.kv_indptr, kv_indices=self.kv_indices,
+                    block_table=self.block_table)
+
+    def check_layout(self):
+        """What the C ABI cannot see from pointers.  Raises ValueError."""
+        import torch
+        B, Q, H = self.B, self.Q, self.H
+        self.cache.check()
+        _need(self.q_lat, "q_lat", torch.bfloat16, (B, Q, H, 512))
+        _need(self.q_pe, "q_pe", torch.bfloat16, (B, Q, H, 64))
+        _need(self.prefix_lens, "prefix_lens", torch.int32, (B,))
+        if self.tree_parent is not None:
+            _need(self.tree_parent, "tree_parent", torch.int32, (B, Q))
+        if self.page_size == 1:
+            _need(self.kv_indptr, "kv_indptr", torch.int32, (B + 1,))
+            if self.kv_indices is None or self.kv_indices.dtype != torch.int32 or self.kv_indices.dim() != 1 \
+                    or not self.kv_indices.is_contiguous():
+                raise ValueError("kv_indices must be a contiguous 1-D int32 tensor")
+        elif self.block_table is None or self.block_table.dtype != torch.int32 or self.block_table.dim() != 2 \
+                or self.block_table.shape[0] != B or not self.block_table.is_contiguous():
+            raise ValueError("block_table must be a contiguous [B][max_pages] int32 tensor")
+
+    def c_args(self, out=None, lse=None) -> MlaKvqAttnArgs:
+        return MlaKvqAttnArgs(
+            self.B, self.Q, self.H, self.cache.c_struct(), _ptr(self.q_lat), _ptr(self.q_pe), self.page_size,
+            _ptr(self.kv_indptr), _ptr(self.kv_indices), _ptr(self.block_table),
+            0 if self.block_table is None else self.block_table.shape[1], _ptr(self.prefix_lens),
+            _ptr(self.tree_parent), self.window, self.sinks, self.scale, _ptr(out), _ptr(lse))
+
+
+def kvq_workspace_size(ki: KvqInputs) -> int:
+    import torch
+    a = ki.c_args()
+    with torch.cuda.device(ki.q_lat.device):
+        n = load().mla_kvq_attn_workspace_size(ctypes.byref(a))
+    if n == 0:
+        raise MlaError(MLA_ERR_INVALID_ARG, "mla_kvq_attn_workspace_size")
+    return int(n)
+
+
+def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, check: bool = True):
+    """Run mla_kvq_attn; returns (out [B,Q,H,512] bf16, lse [B,Q,H] fp32).
+    Rows of unused sequences keep what the given arrays hold (zeros in arrays
+    made here).  check=False skips the tensor checks (a loop that already
+    passed them)."""
+    import torch
+    dev = ki.q_lat.device
+    if out is None:
+        out = torch.zeros((ki.B, ki.Q, ki.H, 512), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.zeros((ki.B, ki.Q, ki.H), dtype=torch.float32, device=dev)
+    if check:
+        ki.check_layout()
+        _need(out, "out", torch.bfloat16, (ki.B, ki.Q, ki.H, 512))
+        _need(lse, "lse", torch.float32, (ki.B, ki.Q, ki.H))
+        _one_device(out=out, lse=lse, workspace=workspace, **ki.tensors())
+    if workspace is None:
+        workspace = alloc_workspace(kvq_workspace_size(ki), dev)
+    _kvq_launch("mla_kvq_attn", load().mla_kvq_attn, dev, stream, ctypes.byref(ki.c_args(out, lse)),
+                workspace.data_ptr(), _ws_bytes(workspace))
+    return out, lse
+
+
+def kvq_check(workspace, stream=None) -> int:
+    """Synchronise and return the device error bits that the last kvq call on
+    this workspace left."""
+    bits = ctypes.c_uint32(0)
+    st = load().mla_kvq_check(ctypes.c_void_p(_ptr(workspace)), _stream(stream), ctypes.byref(bits))
+    if st not in (MLA_OK, MLA_ERR_DEVICE_CHECK):
+        raise MlaError(st, "mla_kvq_check")
+    return int(bits.value)

@@ -1,0 +1,202 @@
+// Shared definitions of the 4-bit latent cache: the packed row, the codes'
+// conversion to the two operand types, the launch parameter block of the
+// attention, and the per-call error words.
+//
+// A row (include/mla_kvq.h) stands for latents (code - 8) * scale * 2^exponent.
+// code - 8 has at most 4 significant bits and an e4m3 scale 4, so the product
+// fits the 8 bits of bf16 and the 11 of f16 (magnitudes 2^-9 .. 3840): both
+// conversions are exact, and the exponent is applied outside the products.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mla_kvq.h"
+#include "common.cuh"
+
+namespace mlav {
+namespace kvq {
+
+constexpr int kCodeBytes = 256;                // 512 codes
+constexpr int kScaleOff = kCodeBytes;          // 32 scales
+constexpr int kRopeOff = kCodeBytes + 32;      // 64 bf16
+static_assert(kRopeOff + 2 * kDr == MLA_KVQ_ROW_BYTES, "row layout");
+
+// ---------------------------------------------------------------------------
+// Error words.  Word 0 of a workspace holds the number of words that the call
+// uses from kErrFirst on; every block (or cluster) stores its own, so nothing
+// needs clearing before a call and no atomics are involved.
+// ---------------------------------------------------------------------------
+constexpr int kErrFirst = 16;  // first error word
+constexpr int kErrMax = (int)(MLA_KVQ_WORKSPACE_BYTES / 4) - kErrFirst;
+
+// ---------------------------------------------------------------------------
+// Codes to values.  Nibble pair t of a code word (bits 4t.. of both halves) is
+// moved into the mantissa of a number whose exponent is fixed, so that each
+// half reads base + code exactly; one fused multiply-add then gives
+// (base + code) * s - (base + 8) * s = (code - 8) * s, exact because the
+// product is formed without rounding and the constant (base + 8) * s is exact
+// too (base 16: 24 s, 5 bits of 8; base 64: 72 s, 8 bits of 11).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(m), "r"(o));  // (a & m) | o
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2_bf16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2_f16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2_f16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// bf16 operand values.
+struct ToBf16 {
+  // two scale bytes (bits 0-7 and 16-23 of b) as bf16 pair: the e4m3 field
+  // shifted to the bottom of the bf16 exponent is the magnitude times 2^-120
+  __device__ __forceinline__ static uint32_t scales(uint32_t b) {
+    return hmul2_bf16((b << 4) & 0x07F007F0u, 0x7B807B80u);  // * 2^120
+  }
+  __device__ __forceinline__ static uint32_t offsets(uint32_t s) { return hmul2_bf16(s, 0xC1C0C1C0u); }  // -24 s
+  // the eight values of a code word, in element order
+  __device__ __forceinline__ static void word(uint32_t w, uint32_t s, uint32_t o, uint32_t (&v)[4]) {
+    v[0] = hfma2_bf16(and_or(w << 3, 0x00780078u, 0x41804180u), s, o);
+    v[1] = hfma2_bf16(and_or(w >> 1, 0x00780078u, 0x41804180u), s, o);
+    v[2] = hfma2_bf16(and_or(w >> 5, 0x00780078u, 0x41804180u), s, o);
+    v[3] = hfma2_bf16(and_or(w >> 9, 0x00780078u, 0x41804180u), s, o);
+  }
+};
+
+// f16 operand values.
+struct ToF16 {
+  // the e4m3 field in the f16 exponent and mantissa is the magnitude times 2^-8
+  __device__ __forceinline__ static uint32_t scales(uint32_t b) {
+    return hmul2_f16((b << 7) & 0x3F803F80u, 0x5C005C00u);  // * 256
+  }
+  __device__ __forceinline__ static uint32_t offsets(uint32_t s) { return hmul2_f16(s, 0xD480D480u); }  // -72 s
+  __device__ __forceinline__ static void word(uint32_t w, uint32_t s, uint32_t o, uint32_t (&v)[4]) {
+    v[0] = hfma2_f16(and_or(w << 4, 0x00F000F0u, 0x54005400u), s, o);
+    v[1] = hfma2_f16(and_or(w, 0x00F000F0u, 0x54005400u), s, o);
+    v[2] = hfma2_f16(and_or(w >> 4, 0x00F000F0u, 0x54005400u), s, o);
+    v[3] = hfma2_f16(and_or(w >> 8, 0x00F000F0u, 0x54005400u), s, o);
+  }
+};
+
+// One half of a pair in both halves.
+__device__ __forceinline__ uint32_t lo2(uint32_t x) { return __byte_perm(x, x, 0x1010); }
+__device__ __forceinline__ uint32_t hi2(uint32_t x) { return __byte_perm(x, x, 0x3232); }
+
+// ---------------------------------------------------------------------------
+// The attention's launch parameters
+// ---------------------------------------------------------------------------
+struct Params {
+  int B, Q, H;
+  int rows;  // H * Q rows per sequence; row r = node (r / H), head (r % H)
+  const uint8_t* cache;
+  int64_t row_stride, slots;
+  const void* q_lat;
+  const void* q_pe;
+  int page_size;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* prefix_lens;
+  const int32_t* tree_parent;  // NULL: chain
+  int window, sinks;           // window 0: none
+  float qpe_mul;               // 2^-exponent, on the rope queries
+  float scale_log2;            // scale * 2^exponent * log2(e): scores in base-2 units
+  float out_mul;               // 2^exponent
+  void* out;
+  float* lse;
+  uint32_t* err;               // workspace
+};
+
+// MLA_DEVERR_* bits of sequence b's tables, read before anything of the call
+// is.  With kv_indptr[0] == 0 and every span equal to its sequence's length,
+// all reads stay in kv_indices[0 .. kv_indptr[B]).
+__device__ __forceinline__ uint32_t check_sequence(const Params& p, int b) {
+  const int64_t P = p.prefix_lens[b];
+  uint32_t e = P < -1 ? MLA_DEVERR_PREFIX : 0u;
+  const int64_t N = P < 0 ? 0 : P + p.Q;
+  if (p.page_size == 1) {
+    const int64_t lo = p.kv_indptr[b], hi = p.kv_indptr[b + 1];
+    if ((b == 0 && lo != 0) || lo < 0 || hi - lo != N) e |= MLA_DEVERR_INDPTR;
+  } else if (N > (int64_t)p.max_pages * p.page_size) {
+    e |= MLA_DEVERR_PAGES;
+  }
+  return e;
+}
+
+// Pool slot of logical position pos of sequence b, or -1 when the table names
+// none in the pool.
+__device__ __forceinline__ int64_t slot_at(const Params& p, int b, int64_t idx0, int64_t pos) {
+  int64_t s;
+  if (p.page_size == 1) {
+    s = p.kv_indices[idx0 + pos];
+  } else {
+    const uint32_t pg = (uint32_t)pos / (uint32_t)p.page_size;
+    const int64_t page = p.block_table[(int64_t)b * p.max_pages + pg];
+    s = page < 0 ? -1 : page * p.page_size + (uint32_t)((uint32_t)pos - pg * (uint32_t)p.page_size);
+  }
+  return (s < 0 || s >= p.slots) ? -1 : s;
+}
+
+// What one node sees of the tree: the mask of its visible nodes and its depth.
+struct NodeView {
+  uint64_t mask;  // bit t: node t is the node itself or a visible ancestor
+  int depth;      // 0 for a node without parent
+};
+
+// parent(t) gives node t's parent; a link outside [-1, t-1] sets *bad and ends
+// the walk.  Ancestors at least `window` places back are dropped unless their
+// place P + depth is among the first `sinks` ones: the walk meets ancestors
+// deepest first, so they are noted by distance and the depths follow from the
+// total.
+template <class F>
+__device__ __forceinline__ NodeView node_view(int i, int64_t P, int window, int sinks, bool* bad, F&& parent) {
+  NodeView v;
+  uint64_t all = 1ull << i;
+  int cur = i, n = 0;
+  while (true) {
+    const int up = parent(cur);
+    if (up < -1 || up >= cur) *bad = true;
+    if (up < 0 || up >= cur) break;
+    all |= 1ull << up;
+    cur = up;
+    ++n;
+  }
+  v.depth = n;
+  v.mask = all;
+  if (window > 0 && n >= window) {
+    // ancestors have smaller indices than their descendants, so the k-th
+    // highest set bit is the ancestor k places back, at depth n - k
+    uint64_t left = all, keep = 0;
+    for (int k = 0; left; ++k) {
+      const int t = 63 - __clzll((long long)left);
+      left &= ~(1ull << t);
+      if (k < window || P + (n - k) < sinks) keep |= 1ull << t;
+    }
+    v.mask = keep;
+  }
+  return v;
+}
+
+}  // namespace kvq
+}  // namespace mlav
