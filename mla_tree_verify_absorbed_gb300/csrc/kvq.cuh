@@ -125,7 +125,13 @@ struct Params {
   float out_mul;               // 2^exponent
   void* out;
   float* lse;
-  uint32_t* err;               // workspace
+  int groups;                  // row groups per sequence
+  int clusters;                // clusters launched
+  // workspace
+  uint32_t* err;               // word 0, and the error words from kErrFirst on
+  int32_t* starts;             // [clusters + 1][4]: see Start
+  float* part_lse;             // [2 clusters][rows of a group], natural log
+  float* part_o;               // [2 clusters][rows of a group][512], normalised
 };
 
 // MLA_DEVERR_* bits of sequence b's tables, read before anything of the call
@@ -164,34 +170,45 @@ struct NodeView {
   int depth;      // 0 for a node without parent
 };
 
-// parent(t) gives node t's parent; a link outside [-1, t-1] sets *bad and ends
-// the walk.  Ancestors at least `window` places back are dropped unless their
-// place P + depth is among the first `sinks` ones: the walk meets ancestors
-// deepest first, so they are noted by distance and the depths follow from the
-// total.
-template <class F>
-__device__ __forceinline__ NodeView node_view(int i, int64_t P, int window, int sinks, bool* bad, F&& parent) {
+// Node i of sequence b, for every lane of a warp at once (lanes may name
+// different nodes, or the same).  The warp holds the sequence's parents two to
+// a lane, so a step up is a shuffle rather than a load that waits for the one
+// before.  A link outside [-1, t-1] sets *bad and ends the walk.
+// A window drops ancestors at least `window` places back unless their place
+// P + depth is among the first `sinks`: ancestors have smaller indices than
+// their descendants, so the k-th highest bit is the ancestor k places back, at
+// depth n - k.
+__device__ __forceinline__ NodeView node_view_warp(const Params& p, int b, int i, int64_t P, bool* bad) {
   NodeView v;
-  uint64_t all = 1ull << i;
-  int cur = i, n = 0;
-  while (true) {
-    const int up = parent(cur);
-    if (up < -1 || up >= cur) *bad = true;
-    if (up < 0 || up >= cur) break;
-    all |= 1ull << up;
-    cur = up;
-    ++n;
+  if (!p.tree_parent) {
+    v.mask = ~0ull >> (63 - i);
+    v.depth = i;
+  } else {
+    const int lane = threadIdx.x & 31;
+    const int32_t* par = p.tree_parent + (int64_t)b * p.Q;
+    const int lo = lane < p.Q ? par[lane] : -1, hi = lane + 32 < p.Q ? par[lane + 32] : -1;
+    v.mask = 1ull << i;
+    v.depth = 0;
+    int cur = i;
+    bool more = true;
+    while (__any_sync(0xffffffffu, more)) {
+      const int a = __shfl_sync(0xffffffffu, lo, cur & 31), c = __shfl_sync(0xffffffffu, hi, cur & 31);
+      const int up = cur < 32 ? a : c;
+      if (more && (up < -1 || up >= cur)) *bad = true;
+      more = more && up >= 0 && up < cur;
+      if (more) {
+        v.mask |= 1ull << up;
+        cur = up;
+        ++v.depth;
+      }
+    }
   }
-  v.depth = n;
-  v.mask = all;
-  if (window > 0 && n >= window) {
-    // ancestors have smaller indices than their descendants, so the k-th
-    // highest set bit is the ancestor k places back, at depth n - k
-    uint64_t left = all, keep = 0;
+  if (p.window > 0 && v.depth >= p.window) {
+    uint64_t left = v.mask, keep = 0;
     for (int k = 0; left; ++k) {
       const int t = 63 - __clzll((long long)left);
       left &= ~(1ull << t);
-      if (k < window || P + (n - k) < sinks) keep |= 1ull << t;
+      if (k < p.window || P + (v.depth - k) < p.sinks) keep |= 1ull << t;
     }
     v.mask = keep;
   }

@@ -1,103 +1,922 @@
-// Verify attention over the 4-bit latent cache (mla_kvq_attn): one warp per
-// query row, online softmax in registers.  Lane l holds elements 16 l .. + 15
-// of the query and of the output, and rope elements 2 l, 2 l + 1.
+// Verify attention and decoding over the 4-bit latent cache (mla_kvq_attn) on
+// tcgen05 tensor cores.
+//
+// The work.  128 query rows ((node, head) pairs) against tiles of 64 tokens:
+// S = Q [128 x 576] . K^T, online softmax, O += P [128 x 64] . V [64 x 512],
+// V the latent part of K.  The latents arrive as 4-bit codes and are converted
+// to operands on the way into shared memory: to bf16 for S (whose other operand
+// is the caller's bf16 queries), to f16 for O, where the weights then keep 11
+// bits instead of 8; both conversions are exact (kvq.cuh).
+//
+// Two CTAs per work item.  An fp32 accumulator for 128 x 512 fills one SM's
+// Tensor Memory, so S and O live in different SMs of a cluster:
+//   rank 0, scores: queries in Tensor Memory (288 columns, the A operand), two
+//           S tiles (128 columns); converts the whole tile (64 tokens x 576) to
+//           bf16; softmax in registers, two threads per row;
+//   rank 1, values: O (512 columns); converts the same tile's latents to f16.
+// The weights and the rows' rescale factors go from rank 0 to rank 1 by a bulk
+// shared -> shared::cluster copy.  Both CTAs read the packed rows themselves:
+// 416 + 288 bytes per token and cluster, where a bf16 pair would exchange
+// operand halves of 1152.  What bounds a tile is shared memory: rank 0 writes
+// 72 KB of operand, the MMAs read it, and 16 KB of weights are written and
+// read (about 1,400 cycles at 128 B/clk, against 1,152 of MMA); rank 1 the same
+// with 64 KB of V, the weights read twice.
+//
+// Conversion.  8 producer warps per CTA, a lane per (token, 64-element chunk):
+// one 32-byte sector of codes and 4 scales make the 128 bytes of one operand
+// row in one chunk.  The 8 lanes of a quarter warp hold 8 different tokens, so
+// their 16-byte stores fall into 8 different bank groups of the 128-byte
+// swizzle.  The next tile's rows are in flight while a tile is converted, the
+// slots of the one after that too.
+//
+// Work split.  Row group g of sequence b costs T_b + kFixed units (T_b tiles).
+// The units of all row groups, in order, are cut into equal intervals, one per
+// cluster; a row group that falls into several clusters is merged from their
+// partial results by a second kernel.  Every CTA computes the cut itself from
+// prefix_lens, so there is no planning kernel, and equal arguments give equal
+// cuts.
+//
+// Masks.  Tiles that hold no visible position are never visited (a window
+// leaves the tiles of the first `sinks` tokens and those from the oldest
+// visible position on); inside a tile the mask is applied to the scores of
+// tiles that need one.  Masked scores are -inf by selection, and any bytes in
+// the cache stand for finite latents, so 0 * V is 0 whatever V holds.
+//
+// Every wait is bounded (2 s); on timeout both CTAs stop issuing, drain what
+// they issued, free their Tensor Memory and report MLA_DEVERR_TIMEOUT.
 #include <cmath>
+#include <mutex>
 
 #include "kvq.cuh"
+#include "sm100.cuh"
 
 namespace mlav {
 namespace kvq {
+using namespace sm100;
 
 mla_status validate_cache(const mla_kvq_cache* c);
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kRG = 128;       // query rows per work item
+constexpr int kTK = 64;        // tokens per tile
+constexpr int kThreads = 576;  // 18 warps
+constexpr uint32_t kTmemCols = 512;
+constexpr int kProducerWarps = 8;
+constexpr int kWarpRows = 8, kRowWarps = 8;  // warps 8-15: two per TMEM lane quadrant, column halves
+constexpr int kWarpMma = 16;
+constexpr int kWarpAux = 17;  // TMEM allocation; lane 0 of rank 0: weight copies
 
-__global__ void __launch_bounds__(kThreads) kvq_attn_kernel(const Params p) {
-  const int lane = threadIdx.x & 31;
-  uint32_t e = 0;
-  for (int b = threadIdx.x; b < p.B; b += kThreads) e |= check_sequence(p, b);
-  const int stop = __syncthreads_or((int)e);
-  const int64_t total = (int64_t)p.B * p.rows;
-  for (int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); !stop && w < total;
-       w += (int64_t)gridDim.x * kWarps) {
-    const int b = (int)(w / p.rows), i = (int)(w % p.rows) / p.H;
-    const int64_t P = p.prefix_lens[b];
-    if (P < 0) continue;
-    bool bad = false;
-    const NodeView nv = node_view(i, P, p.window, p.sinks, &bad, [&](int t) {
-      return p.tree_parent ? p.tree_parent[(int64_t)b * p.Q + t] : t - 1;
-    });
-    if (bad) e |= MLA_DEVERR_PARENT;
-    float q[16], o[16];
-    const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(p.q_lat) + w * kDl + 16 * lane;
-    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q_pe) + w * kDr + 2 * lane;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      q[k] = __bfloat162float(ql[k]);
-      o[k] = 0.f;
-    }
-    const float q0 = __bfloat162float(qp[0]) * p.qpe_mul, q1 = __bfloat162float(qp[1]) * p.qpe_mul;
-    const int64_t idx0 = p.page_size == 1 ? p.kv_indptr[b] : 0;
-    float m = -INFINITY, l = 0.f;
-    for (int64_t pos = 0; pos < P + p.Q; ++pos) {
-      if (pos < P) {
-        if (p.window && pos >= p.sinks && P + nv.depth - pos >= p.window) {
-          pos = P + nv.depth - p.window;  // the first position inside the window is next
-          if (pos >= P) pos = P - 1;
-          continue;
-        }
-      } else if (!((nv.mask >> (pos - P)) & 1ull)) {
-        continue;
-      }
-      int64_t s = slot_at(p, b, idx0, pos);
-      if (s < 0) {
-        e |= MLA_DEVERR_SLOT;
-        s = 0;
-      }
-      const uint8_t* row = p.cache + s * p.row_stride;
-      const uint2 cw = reinterpret_cast<const uint2*>(row)[lane];
-      const uint32_t sc = ToBf16::scales((uint32_t)row[kScaleOff + lane] * 0x10001u);
-      const uint32_t of = ToBf16::offsets(sc);
-      const uint32_t kr = reinterpret_cast<const uint32_t*>(row + kRopeOff)[lane];
-      uint32_t a[4], c[4];
-      ToBf16::word(cw.x, sc, of, a);
-      ToBf16::word(cw.y, sc, of, c);
-      float v[16];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(a[k] << 16);
-        v[2 * k + 1] = __uint_as_float(a[k] & 0xffff0000u);
-        v[8 + 2 * k] = __uint_as_float(c[k] << 16);
-        v[8 + 2 * k + 1] = __uint_as_float(c[k] & 0xffff0000u);
-      }
-      float d = q0 * __uint_as_float(kr << 16) + q1 * __uint_as_float(kr & 0xffff0000u);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) d = fmaf(q[k], v[k], d);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-      d *= p.scale_log2;
-      const float mn = fmaxf(m, d), alpha = exp2f(m - mn), pw = exp2f(d - mn);
-      m = mn;
-      l = l * alpha + pw;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) o[k] = fmaf(pw, v[k], o[k] * alpha);
-    }
-    const float inv = p.out_mul / l;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + w * kDl + 16 * lane;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) out[k] = __float2bfloat16_rn(o[k] * inv);
-    if (lane == 0 && p.lse) p.lse[w] = (m + log2f(l)) * 0.69314718055994530942f;
+// A tile is staged as two halves, each with its own full / empty barriers:
+// half h holds latent columns [256 h, 256 h + 256) as 4 chunks of 64 columns
+// (64 token rows of 128 bytes each); in the score CTA half 1 ends with the
+// rope chunk.
+constexpr int kChunk = kTK * 128;             // 8 KB
+constexpr int kStageS = 9 * kChunk;           // score CTA: 72 KB per tile
+constexpr int kStagesS = 2;
+constexpr int kUnitV = 4 * kChunk;            // value CTA: 32 KB per half tile
+constexpr int kUnitsV = 5;
+constexpr int kUnitsMax = 5;
+static_assert(2 * kStagesS <= kUnitsMax && kUnitsV <= kUnitsMax, "barrier arrays");
+constexpr int kPBytes = kRG * 128;            // weights of a tile, f16
+constexpr int kPBufs = 3;
+constexpr int kOffP = kUnitsV * kUnitV;       // weights: staged at this offset in rank 0, copied to it in rank 1
+static_assert(kStagesS * kStageS <= kOffP, "score stages reach into the weights");
+constexpr int kOffRed = kOffP + kPBufs * kPBytes;        // [2 tiles][2 halves][128] partial row maxima, [128] sums
+constexpr int kOffCtl = kOffRed + (2 * 2 * kRG + kRG) * 4;
+constexpr uint32_t kPTxBytes = kPBytes + kRG * 4;        // weights + rescale factors
+
+constexpr uint32_t kIdescS = idesc_bf16_f32(kRG, kTK, 0, 0);   // queries (TMEM), keys K-major
+constexpr uint32_t kIdescPV = idesc_f16_f32(kRG, 256, 0, 1);   // weights K-major, values MN-major
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 20000000ull;
+
+// Weights are 2^(score - max + kWeightShift) in f16: a lazy maximum lets them
+// reach 2^8 above 1, which the shift puts at 2^15, below f16's 65504, so that
+// weights down to 2^-21 of the maximum keep 11 bits and down to 2^-31 some.
+constexpr float kLazy = 8.f;
+constexpr float kWeightShift = 7.f;
+
+// Cost of starting a row group or a piece of one, in tiles, and the fewest
+// tiles worth a cluster of its own.
+constexpr int kFixed = 8;
+constexpr int kMinTiles = 6;
+
+struct alignas(16) Ctl {
+  uint64_t full[kUnitsMax];    // half tile converted (8 producer warps)
+  uint64_t empty[kUnitsMax];   // the MMAs reading it are complete
+  uint64_t s_full[2];          // score: S tile in TMEM
+  uint64_t s_free[2];          // score: softmax has loaded S (8 row warps)
+  uint64_t q_ready;            // score: queries in TMEM (8 row warps)
+  uint64_t p_free[kPBufs];     // score: the PV MMAs that read this buffer are complete (rank 1's commit)
+  uint64_t fin_free;           // score: rank 1 consumed lfin / mfin (256 arrivals)
+  uint64_t xch[2];             // score: both halves' partial row maxima written (8 row warps)
+  uint64_t xfin;               // score: half 1's row sums written (4 row warps)
+  uint64_t p_staged[kPBufs];   // score: weights and factors staged (8 row warps)
+  uint64_t p_full[kPBufs];     // value: weights and factors landed (copy bytes)
+  uint64_t pv_done[2];         // value: PV MMAs of a tile complete
+  uint64_t o_ready[2];         // value: O rescaled, weights in (8 row warps)
+  uint64_t fin_full;           // value: lfin / mfin written (128 remote arrivals)
+  uint64_t drain;
+  alignas(16) float alpha[kPBufs][kRG];  // staged in rank 0, copied to rank 1
+  float lfin[kRG];             // value: row sums of the shifted weights
+  float mfin[kRG];             // value: row maxima, base-2 units
+  int64_t scan[kThreads / 32];
+  int64_t total;               // units of the whole call
+  int64_t start_x;             // this cluster's first unit within sequence start_b
+  int start_b;
+  uint32_t tmem_base;
+  int abort;
+  int abort_site;
+  uint32_t err;
+};
+constexpr int kSmemBytes = kOffCtl + (int)sizeof(Ctl);
+constexpr int kSmemAlloc = 232448;  // the per-CTA maximum
+static_assert(kSmemBytes <= kSmemAlloc, "shared memory budget");
+static_assert(offsetof(Ctl, alpha) % 16 == 0 && kOffCtl % 16 == 0, "bulk-copy alignment");
+static_assert(kOffP % 1024 == 0 && kStageS % 1024 == 0, "swizzle atoms");
+
+enum {
+  kSiteEmpty = 1, kSiteQReady, kSiteFullS, kSiteSFree, kSiteSFull, kSitePFree, kSiteFinFree, kSiteFullV,
+  kSiteOReady, kSitePFull, kSitePvPrev, kSitePvLast, kSiteFinFull, kSiteXch, kSitePStaged
+};
+
+__device__ __noinline__ void raise_abort(Ctl* c, int site) {
+  if (*reinterpret_cast<volatile int*>(&c->abort) == 0) atomicCAS(&c->abort_site, 0, site);
+  for (uint32_t rk = 0; rk < 2; ++rk) st_cluster_u32(mapa_shared(smem_u32(&c->abort), rk), 1u);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* c, int site) {
+  if (mbar_wait(bar, parity, &c->abort, kWaitLimitNs, true)) return true;
+  raise_abort(c, site);
+  return false;
+}
+// Every lane waits; the result is warp-uniform and the warp converged.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c, int site) {
+  return __all_sync(0xffffffffu, wait(bar, parity, c, site));
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void ld_global_v8(const void* ptr, uint32_t (&v)[8]) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "l"(ptr));
+}
+
+// ---------------------------------------------------------------------------
+// work split
+// ---------------------------------------------------------------------------
+// The tiles of a sequence that any of its nodes sees: [0, ns) and [tw, te).
+struct Tiles {
+  int ns, tw;
+  int T;  // ns + te - tw; 0 for an unused sequence
+  int64_t lo;  // positions in [sinks, lo) are seen by no node
+  __device__ __forceinline__ int at(int v) const { return v < ns ? v : v - ns + tw; }
+};
+__device__ __forceinline__ Tiles tiles_of(const Params& p, int b) {
+  Tiles t;
+  const int64_t P = p.prefix_lens[b];
+  t.lo = 0;
+  t.ns = t.tw = t.T = 0;
+  if (P < 0) return t;
+  if (p.window > 0 && P - p.window + 1 > 0) {
+    t.lo = P - p.window + 1;
+    t.tw = (int)(t.lo / kTK);
+    const int64_t ns = ((int64_t)p.sinks + kTK - 1) / kTK;
+    t.ns = (int)(ns < t.tw ? ns : t.tw);
   }
-  const int any = __syncthreads_or((int)e);
-  // the words of all threads of a block, bit by bit
-  uint32_t bits = 0;
+  t.T = t.ns + (int)((P + p.Q + kTK - 1) / kTK) - t.tw;
+  return t;
+}
+
+// First tile of what a cut at unit z of a row group (kFixed + T units) leaves
+// to the right: the fixed cost comes first, and a cut that would leave fewer
+// than kSnap tiles on a side moves to that side's end.
+constexpr int kSnap = 3;
+__device__ __forceinline__ int cut_tile(int64_t z, int T) {
+  if (z >= kFixed + T) return T;
+  if (z < kFixed + kSnap) return 0;
+  return z > kFixed + T - kSnap ? T : (int)(z - kFixed);
+}
+
+// Clusters that share `total` units.
+__device__ __forceinline__ int active_clusters(const Params& p, int64_t total) {
+  const int64_t n = total / (kFixed + kMinTiles);
+  return (int)(n < 1 ? 1 : n > p.clusters ? p.clusters : n);
+}
+__device__ __forceinline__ int64_t first_unit(int64_t total, int n, int k) { return total * k / n; }
+
+// Where a cluster's interval begins: sequence b and unit x of its
+// groups * (kFixed + T) units, for the merging kernel.
+struct Start {
+  int32_t b, x_lo, x_hi, n;  // n: clusters that share the call (0: nothing to merge)
+  __device__ __forceinline__ int64_t x() const { return (int64_t)(uint32_t)x_lo | (int64_t)x_hi << 32; }
+};
+
+// Calls f(slot, b, g, t0, t1, tiles) for this cluster's pieces in order; slot
+// is the piece's partial-result slot, or -1 for a whole row group.  A piece
+// that does not begin its row group is the cluster's first, one that does not
+// end it the last, so two slots are enough.
+template <class F>
+__device__ __forceinline__ void for_pieces(const Params& p, const Ctl* c, int cluster, F&& f) {
+  const int n = active_clusters(p, c->total);
+  int64_t left = first_unit(c->total, n, cluster + 1) - first_unit(c->total, n, cluster);
+  int64_t x = c->start_x;
+  for (int b = c->start_b; left > 0 && b < p.B; ++b, x = 0) {
+    const Tiles tl = tiles_of(p, b);
+    if (tl.T == 0) continue;
+    const int L = kFixed + tl.T;
+    for (int g = (int)(x / L); g < p.groups && left > 0; ++g) {
+      const int64_t z = x - (int64_t)g * L;
+      const int64_t take = L - z < left ? L - z : left;
+      const int t0 = cut_tile(z, tl.T), t1 = cut_tile(z + take, tl.T);
+      x += take;
+      left -= take;
+      if (t1 <= t0) continue;
+      const int slot = t0 == 0 && t1 == tl.T ? -1 : 2 * cluster + (t0 == 0);
+      if (!f(slot, b, g, t0, t1, tl)) return;
+    }
+  }
+}
+
+// Block-wide: validates every sequence, sums the units and finds where this
+// cluster's interval begins.  Returns the clusters that share the call, 0 when
+// a table is bad.  Threads take consecutive sequences.
+__device__ int make_split(const Params& p, Ctl* c, int cluster) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = tid * per, b1 = min(b0 + per, p.B);
+  uint32_t e = 0;
+  int64_t sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const uint32_t eb = check_sequence(p, b);
+    e |= eb;
+    const int T = eb ? 0 : tiles_of(p, b).T;
+    sum += T ? (int64_t)p.groups * (kFixed + T) : 0;
+  }
+  int64_t inc = sum;
 #pragma unroll
-  for (int k = 0; k < 10; ++k) bits |= __syncthreads_or((int)((e >> k) & 1u)) ? 1u << k : 0u;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) c->scan[warp] = inc;
+  if (e) atomicOr(&c->err, e);
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += c->scan[w];
+    total += c->scan[w];
+  }
+  if (c->err) return 0;  // the same in every CTA: each has read every sequence
+  const int n = active_clusters(p, total);
+  if (cluster < n && total > 0) {
+    const int64_t w0 = first_unit(total, n, cluster);
+    int64_t at = before + inc - sum;
+    if (w0 >= at && w0 < at + sum) {
+      for (int b = b0; b < b1; ++b) {
+        const int T = tiles_of(p, b).T;
+        const int64_t u = T ? (int64_t)p.groups * (kFixed + T) : 0;
+        if (w0 < at + u) {
+          c->start_b = b;
+          c->start_x = w0 - at;
+          break;
+        }
+        at += u;
+      }
+    }
+  }
+  if (tid == 0) c->total = total;
+  __syncthreads();
+  return total > 0 ? n : -1;  // -1: every sequence is unused
+}
+
+// ---------------------------------------------------------------------------
+// producers
+// ---------------------------------------------------------------------------
+// What one lane holds of a tile: token (lane & 7) of its warp's 8, chunks
+// lane >> 3 and 4 + (lane >> 3), and two 16-byte pieces of the rope key.
+template <bool kScore>
+struct Packed {
+  uint32_t code[2][8];
+  uint32_t scale[2];
+  uint4 rope[kScore ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t* row, int ch) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      ld_global_v8(row + 32 * (4 * h + ch), code[h]);
+      scale[h] = __ldg(reinterpret_cast<const uint32_t*>(row + kScaleOff) + 4 * h + ch);
+    }
+    if (kScore) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) rope[q] = __ldg(reinterpret_cast<const uint4*>(row + kRopeOff) + 4 * q + ch);
+    }
+  }
+};
+
+// Converts one sector of codes with its 4 scales into the 8 pieces of an
+// operand row.
+template <class To>
+__device__ __forceinline__ void convert_chunk(const uint32_t (&code)[8], uint32_t scale, uint32_t dst, int r7) {
+#pragma unroll
+  for (int pr = 0; pr < 2; ++pr) {
+    const uint32_t s = To::scales(__byte_perm(scale, 0, pr ? 0x4342 : 0x4140));
+    const uint32_t o = To::offsets(s);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t sk = k ? hi2(s) : lo2(s), ok = k ? hi2(o) : lo2(o);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int q = 4 * pr + 2 * k + w;
+        uint32_t v[4];
+        To::word(code[q], sk, ok, v);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((q ^ r7) << 4)), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3])
+                     : "memory");
+      }
+    }
+  }
+}
+
+template <bool kScore>
+__device__ void producer(const Params& p, uint8_t* smem, Ctl* c, int pw, int cluster) {
+  using To = typename std::conditional<kScore, ToBf16, ToF16>::type;
+  const int lane = threadIdx.x & 31;
+  const int r7 = lane & 7, ch = lane >> 3;
+  const int r = 8 * pw + r7;  // token row within the tile
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t err = 0;
+  int j = 0;
+  for_pieces(p, c, cluster, [&](int, int b, int, int t0, int t1, const Tiles& tl) {
+    const int64_t N = (int64_t)p.prefix_lens[b] + p.Q;
+    const int64_t idx0 = p.page_size == 1 ? (int64_t)p.kv_indptr[b] : 0;
+    // address of the row of this lane's token in tile v; positions that no
+    // node sees read slot 0, whose weight is zero
+    auto row_of = [&](int v) -> const uint8_t* {
+      const int64_t pos = (int64_t)tl.at(v) * kTK + r;
+      int64_t s = 0;
+      if (pos < N && (pos >= tl.lo || pos < p.sinks)) {
+        s = slot_at(p, b, idx0, pos);
+        if (s < 0) {
+          err |= MLA_DEVERR_SLOT;
+          s = 0;
+        }
+      }
+      return p.cache + s * p.row_stride;
+    };
+    Packed<kScore> nxt;
+    nxt.load(row_of(t0), ch);
+    const uint8_t* row = t0 + 1 < t1 ? row_of(t0 + 1) : nullptr;
+    for (int t = t0; t < t1; ++t, ++j) {
+      const Packed<kScore> cur = nxt;
+      if (t + 1 < t1) nxt.load(row, ch);
+      if (t + 2 < t1) row = row_of(t + 2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // score: stage j % 2, its halves in turn; value: a ring of half tiles
+        const int u = 2 * j + h;
+        const int slot = kScore ? u % (2 * kStagesS) : u % kUnitsV;
+        const uint32_t turn = kScore ? (uint32_t)(u / (2 * kStagesS)) : (uint32_t)(u / kUnitsV);
+        if (!wait_warp(&c->empty[slot], (turn & 1u) ^ 1u, c, kSiteEmpty)) return false;
+        const uint32_t base = kScore ? sbase + (j % kStagesS) * kStageS + h * 4 * kChunk : sbase + slot * kUnitV;
+        convert_chunk<To>(cur.code[h], cur.scale[h], base + ch * kChunk + r * 128, r7);
+        if (kScore && h == 1) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<uint4*>(smem + (j % kStagesS) * kStageS + 8 * kChunk + r * 128 +
+                                      (((4 * q + ch) ^ r7) << 4)) = cur.rope[q];
+        }
+        fence_proxy_async_smem();  // generic stores, read by the MMA
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->full[slot]);
+      }
+    }
+    return true;
+  });
+  if (err) atomicOr(&c->err, err);
+}
+
+// ---------------------------------------------------------------------------
+// score CTA
+// ---------------------------------------------------------------------------
+__device__ void score_mma(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
+  const uint32_t tS = c->tmem_base;        // columns [0, 128): two S tiles
+  const uint32_t tQ = c->tmem_base + 128;  // columns [128, 416): queries, bf16 pairs
+  int j = 0, seg = 0;
+  for_pieces(p, c, cluster, [&](int, int, int, int t0, int t1, const Tiles&) {
+    if (!wait_warp(&c->q_ready, (uint32_t)seg & 1u, c, kSiteQReady)) return false;
+    for (int t = t0; t < t1; ++t, ++j) {
+      const int sb = j & 1;
+      if (j >= 2 && !wait_warp(&c->s_free[sb], (((uint32_t)j >> 1) & 1u) ^ 1u, c, kSiteSFree)) return false;
+      const uint64_t dk = smem_desc(smem_u32(smem + (j % kStagesS) * kStageS), 16, 1024, kLayoutSw128);
+      const uint32_t ts = tS + sb * kTK;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int u = 2 * j + h, slot = u % (2 * kStagesS);
+        if (!wait_warp(&c->full[slot], (uint32_t)(u / (2 * kStagesS)) & 1u, c, kSiteFullS)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kc = 4 * h; kc < (h ? 9 : 4); ++kc) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_cta_ts_warp(ts, tQ + kc * 32 + kk * 8, dk + (uint64_t)((kc * kChunk + kk * 32) >> 4), kIdescS,
+                            (kc | kk) != 0);
+        }
+        if (h) mma_cta_commit_warp(&c->s_full[sb]);
+        mma_cta_commit_warp(&c->empty[slot]);
+      }
+    }
+    ++seg;
+    return true;
+  });
+  if (__any_sync(0xffffffffu, c->abort != 0)) {
+    // outstanding MMAs must finish before TMEM is released
+    mma_cta_commit_warp(&c->drain);
+    if ((threadIdx.x & 31) == 0) mbar_wait_drain(&c->drain, 0, kDrainLimitNs);
+    __syncwarp();
+  }
+}
+
+// Stages query row `row` into Tensor Memory: half h of the row's two threads
+// takes columns [144 h, 144 h + 144) (column c holds elements 2c, 2c + 1 of
+// 512 latent and 64 rope ones), 48 columns of loads in flight at a time.
+__device__ __forceinline__ void stage_query_row(const Params& p, int b, int row, bool live, int h, uint32_t tQ) {
+  const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat) + ((int64_t)b * p.rows + row) * (kDl / 8);
+  const uint4* qp = reinterpret_cast<const uint4*>(p.q_pe) + ((int64_t)b * p.rows + row) * (kDr / 8);
+  const uint32_t mul = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(p.qpe_mul)) * 0x10001u;  // a power of two
+#pragma unroll 1
+  for (int c0 = 144 * h; c0 < 144 * h + 144; c0 += 48) {
+    uint4 x[12];
+#pragma unroll
+    for (int v = 0; v < 12; ++v) {
+      const int col = c0 + 4 * v;
+      x[v] = make_uint4(0, 0, 0, 0);
+      if (live) x[v] = col < 256 ? __ldg(ql + col / 4) : __ldg(qp + (col - 256) / 4);
+    }
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      uint32_t w[16];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        uint4 y = x[4 * s + v];
+        if (c0 + 16 * s + 4 * v >= 256) {
+          y.x = hmul2_bf16(y.x, mul);
+          y.y = hmul2_bf16(y.y, mul);
+          y.z = hmul2_bf16(y.z, mul);
+          y.w = hmul2_bf16(y.w, mul);
+        }
+        w[4 * v + 0] = y.x;
+        w[4 * v + 1] = y.y;
+        w[4 * v + 2] = y.z;
+        w[4 * v + 3] = y.w;
+      }
+      __syncwarp();
+      tmem_st_32x32b_x16(tQ + c0 + 16 * s, w);
+    }
+  }
+  tmem_wait_st();
+}
+
+// Online softmax, two threads per row with 32 of a tile's 64 columns each.
+__device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
+  const int lane = threadIdx.x & 31;
+  const int w = (threadIdx.x >> 5) - kWarpRows;
+  const int wq = w & 3, h = w >> 2;
+  const int r = wq * 32 + lane;
+  const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+  const uint32_t tS = c->tmem_base + lane_off + (uint32_t)(h * 32);
+  const uint32_t tQ = c->tmem_base + 128 + lane_off;
+  float* red_max = reinterpret_cast<float*>(smem + kOffRed);
+  float* red_l = red_max + 4 * kRG;
+  const float sl2 = p.scale_log2;
+  const int nq = p.Q;
+  int j = 0, seg = 0;
+  bool bad = false;
+  for_pieces(p, c, cluster, [&](int, int b, int g, int t0, int t1, const Tiles& tl) {
+    const int row = g * kRG + r;
+    const bool live = row < p.rows;
+    const int64_t P = p.prefix_lens[b];
+    stage_query_row(p, b, row, live, h, tQ);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c->q_ready);
+    // rows past the last take the last one's mask: their results are dropped
+    const NodeView nv = node_view_warp(p, b, (live ? row : p.rows - 1) / p.H, P, &bad);
+    // prefix positions up to this one are outside the window (unless sinks)
+    const int64_t past = p.window > 0 ? P + nv.depth - p.window : -1;
+    const int64_t past_any = p.window > 0 ? P + nq - 1 - p.window : -1;
+
+    // m: running maximum of the scaled scores (base-2 units), the same in both
+    // halves; l: this half's sum of the shifted weights before rounding
+    float m = -INFINITY, l = 0.f;
+    for (int t = t0; t < t1; ++t, ++j) {
+      const int sb = j & 1;
+      if (!wait_warp(&c->s_full[sb], (uint32_t)(j >> 1) & 1u, c, kSiteSFull)) return false;
+      tc_fence_after();
+      uint32_t u[32];
+      tmem_ld32_sync(tS + sb * kTK, u);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->s_free[sb]);
+
+      const int64_t pos0 = (int64_t)tl.at(t) * kTK + 32 * h;
+      if (pos0 + 32 > P || pos0 <= past_any) {
+        const int rel0 = (int)(pos0 - P);  // > -2^31: positions and lengths fit 32 bits
+        const int gone = (int)max(past - pos0, (int64_t)-1), first = (int)min((int64_t)p.sinks - pos0, (int64_t)32);
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+          const int rel = rel0 + q;
+          const bool vis = rel < 0 ? (q > gone || q < first) : (rel < nq && ((nv.mask >> (rel & 63)) & 1ull));
+          if (!vis) u[q] = 0xff800000u;  // -inf
+        }
+      }
+      float mx[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) mx[v] = __uint_as_float(u[v]);
+#pragma unroll
+      for (int q = 4; q < 32; ++q) mx[q & 3] = fmaxf(mx[q & 3], __uint_as_float(u[q]));
+      const float pmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      red_max[((j & 1) * 2 + h) * kRG + r] = pmax;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->xch[j & 1]);
+      if (!wait_warp(&c->xch[j & 1], (uint32_t)(j >> 1) & 1u, c, kSiteXch)) return false;
+      // the scale is positive: the scaled maximum is the maximum of the scaled scores
+      const float tmax = fmaxf(pmax, red_max[((j & 1) * 2 + (h ^ 1)) * kRG + r]) * sl2;
+      // the maximum moves only when this tile beats it by 2^kLazy
+      float alpha = 1.f;
+      if (tmax > m + kLazy) {
+        alpha = exp2f(m - tmax);  // 0 when m is -inf
+        l *= alpha;
+        m = tmax;
+      }
+      const float nmu = m == -INFINITY ? 0.f : kWeightShift - m;
+
+      const int pb = j % kPBufs;
+      if (!wait_warp(&c->p_free[pb], ((uint32_t)(j / kPBufs) & 1u) ^ 1u, c, kSitePFree)) return false;
+      uint8_t* pst = smem + kOffP + pb * kPBytes;
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q8 = 0; q8 < 4; ++q8) {
+        uint32_t wv[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float e0 = ex2_approx(fmaf(__uint_as_float(u[8 * q8 + 2 * v]), sl2, nmu));
+          const float e1 = ex2_approx(fmaf(__uint_as_float(u[8 * q8 + 2 * v + 1]), sl2, nmu));
+          ls[v] += e0 + e1;
+          wv[v] = pack_f16(e0, e1);
+        }
+        *reinterpret_cast<uint4*>(pst + sw128_offset(r, 32 * h + 8 * q8)) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+      }
+      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      if (h == 0) c->alpha[pb][r] = alpha;
+      fence_proxy_async_smem();  // read by the copy engine
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->p_staged[pb]);
+    }
+
+    if (h == 1) {
+      red_l[r] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->xfin);
+    } else {
+      if (!wait_warp(&c->xfin, (uint32_t)seg & 1u, c, kSiteXch)) return false;
+      l += red_l[r];
+      if (!wait_warp(&c->fin_free, ((uint32_t)seg & 1u) ^ 1u, c, kSiteFinFree)) return false;
+      st_cluster_f32(mapa_shared(smem_u32(&c->lfin[r]), 1), l);
+      st_cluster_f32(mapa_shared(smem_u32(&c->mfin[r]), 1), m);
+      mbar_arrive_cluster(&c->fin_full, 1);
+    }
+    ++seg;
+    return true;
+  });
+  if (bad) atomicOr(&c->err, MLA_DEVERR_PARENT);
+}
+
+// One thread of the score CTA: ships each tile's weights and factors to the
+// value CTA, where their bytes complete p_full.
+__device__ void weight_copier(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
+  int j = 0;
+  for_pieces(p, c, cluster, [&](int, int, int, int t0, int t1, const Tiles&) {
+    for (int t = t0; t < t1; ++t, ++j) {
+      const int pb = j % kPBufs;
+      if (!wait(&c->p_staged[pb], (uint32_t)(j / kPBufs) & 1u, c, kSitePStaged)) return false;
+      const uint32_t bar = mapa_shared(smem_u32(&c->p_full[pb]), 1);
+      bulk_copy_s2c(mapa_shared(smem_u32(smem + kOffP + pb * kPBytes), 1), smem + kOffP + pb * kPBytes, kPBytes, bar);
+      bulk_copy_s2c(mapa_shared(smem_u32(&c->alpha[pb][0]), 1), &c->alpha[pb][0], kRG * 4, bar);
+      bulk_commit_group();
+    }
+    return true;
+  });
+  bulk_wait_group<0>();
+}
+
+// ---------------------------------------------------------------------------
+// value CTA
+// ---------------------------------------------------------------------------
+__device__ void value_mma(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
+  const uint32_t tO = c->tmem_base;
+  int j = 0;
+  for_pieces(p, c, cluster, [&](int, int, int, int t0, int t1, const Tiles&) {
+    for (int t = t0; t < t1; ++t, ++j) {
+      const int pb = j % kPBufs;
+      if (!wait_warp(&c->o_ready[j & 1], (uint32_t)(j >> 1) & 1u, c, kSiteOReady)) return false;
+      const uint64_t da = smem_desc(smem_u32(smem + kOffP + pb * kPBytes), 16, 1024, kLayoutSw128);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int u = 2 * j + h, slot = u % kUnitsV;
+        if (!wait_warp(&c->full[slot], (uint32_t)(u / kUnitsV) & 1u, c, kSiteFullV)) return false;
+        tc_fence_after();
+        // 64-column chunks 8 KB apart along N, 8-token groups 1 KB apart along K
+        const uint64_t dv = smem_desc(smem_u32(smem + slot * kUnitV), kChunk, 1024, kLayoutSw128);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_cta_ss_warp(tO + h * 256, da + (uint64_t)((kk * 32) >> 4), dv + (uint64_t)((kk * 16 * 128) >> 4),
+                          kIdescPV, !(t == t0 && kk == 0));
+        mma_cta_commit_warp(&c->empty[slot]);
+      }
+      mma_cta_commit_warp(&c->p_free[pb], 0x1);
+      mma_cta_commit_warp(&c->pv_done[j & 1]);
+    }
+    return true;
+  });
+  if (__any_sync(0xffffffffu, c->abort != 0)) {
+    mma_cta_commit_warp(&c->drain);
+    if ((threadIdx.x & 31) == 0) mbar_wait_drain(&c->drain, 0, kDrainLimitNs);
+    __syncwarp();
+  }
+}
+
+// Row warps of the value CTA (warpgroup h: columns [256 h, 256 h + 256)):
+// rescale O where a factor is not 1, and per piece normalise and store it.
+__device__ void value_rows(const Params& p, Ctl* c, int cluster) {
+  const int lane = threadIdx.x & 31;
+  const int w = (threadIdx.x >> 5) - kWarpRows;
+  const int wq = w & 3, h = w >> 2;
+  const int r = wq * 32 + lane;
+  const int col0 = 256 * h;
+  const uint32_t tO = c->tmem_base + ((uint32_t)(wq * 32) << 16) + (uint32_t)col0;
+  int j = 0, seg = 0;
+  for_pieces(p, c, cluster, [&](int slot, int b, int g, int t0, int t1, const Tiles&) {
+    for (int t = t0; t < t1; ++t, ++j) {
+      const int pb = j % kPBufs;
+      if (w == 0 && lane == 0) mbar_arrive_expect_tx(&c->p_full[pb], kPTxBytes);
+      if (!wait_warp(&c->p_full[pb], (uint32_t)(j / kPBufs) & 1u, c, kSitePFull)) return false;
+      if (t != t0) {
+        const float a = c->alpha[pb][r];
+        if (__any_sync(0xffffffffu, a != 1.f)) {
+          if (!wait_warp(&c->pv_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, c, kSitePvPrev)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < 256; c0 += 32) {
+            uint32_t u[32];
+            tmem_ld32_sync(tO + c0, u);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) * a);
+            tmem_st_32x32b_x32(tO + c0, u);
+          }
+          tmem_wait_st();
+        }
+      }
+      fence_proxy_async_smem();  // the weights feed the MMA
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->o_ready[j & 1]);
+    }
+
+    if (!wait_warp(&c->pv_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, c, kSitePvLast)) return false;
+    if (!wait_warp(&c->fin_full, (uint32_t)seg & 1u, c, kSiteFinFull)) return false;
+    tc_fence_after();
+    const float l = c->lfin[r], m = c->mfin[r];
+    mbar_arrive_cluster_relaxed(&c->fin_free, 0);
+    ++seg;
+    const int row = g * kRG + r;
+    const bool live = row < p.rows;
+    // a row that sees nothing of this piece has l = 0 and O = 0
+    const float inv = l > 0.f ? p.out_mul / l : l;
+    const float lse = l > 0.f ? (m + log2f(l) - kWeightShift) * 0.69314718055994530942f : l == 0.f ? -INFINITY : l;
+    const int64_t orow = (int64_t)b * p.rows + row;
+    if (slot < 0) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + col0);
+      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < 256; c0 += 32) {
+        uint32_t u[32];
+        __syncwarp();
+        tmem_ld32_sync(tO + c0, u);
+        if (live) {
+          uint32_t o[16];
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            o[v] = pack_bf16(__uint_as_float(u[2 * v]) * inv, __uint_as_float(u[2 * v + 1]) * inv);
+          if (wide) {
+            st_global_v8(dst + c0 / 2, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+            st_global_v8(dst + c0 / 2 + 8, o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              reinterpret_cast<uint4*>(dst + c0 / 2)[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          }
+        }
+      }
+      if (live && p.lse && h == 0) p.lse[orow] = lse;
+    } else {
+      const int64_t prow = (int64_t)slot * kRG + r;
+      float* dst = p.part_o + prow * kDl + col0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < 256; c0 += 32) {
+        uint32_t u[32];
+        __syncwarp();
+        tmem_ld32_sync(tO + c0, u);
+        if (live) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            st_global_v8(dst + c0 + 8 * v, __uint_as_float(u[8 * v + 0]) * inv, __uint_as_float(u[8 * v + 1]) * inv,
+                         __uint_as_float(u[8 * v + 2]) * inv, __uint_as_float(u[8 * v + 3]) * inv,
+                         __uint_as_float(u[8 * v + 4]) * inv, __uint_as_float(u[8 * v + 5]) * inv,
+                         __uint_as_float(u[8 * v + 6]) * inv, __uint_as_float(u[8 * v + 7]) * inv);
+        }
+      }
+      if (live && h == 0) p.part_lse[prow] = lse;
+    }
+    tc_fence_before();
+    return true;
+  });
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_attn_kernel(const Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t rank = cluster_ctarank();
+  const int warp = threadIdx.x >> 5;
+  const int cluster = blockIdx.x / 2;
+  Ctl* c = reinterpret_cast<Ctl*>(smem + kOffCtl);
   if (threadIdx.x == 0) {
-    p.err[kErrFirst + blockIdx.x] = any ? bits : 0u;
+    for (int s = 0; s < kUnitsMax; ++s) {
+      mbar_init(&c->full[s], kProducerWarps);
+      mbar_init(&c->empty[s], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&c->s_full[q], 1);
+      mbar_init(&c->s_free[q], kRowWarps);
+      mbar_init(&c->xch[q], kRowWarps);
+      mbar_init(&c->pv_done[q], 1);
+      mbar_init(&c->o_ready[q], kRowWarps);
+    }
+    for (int q = 0; q < kPBufs; ++q) {
+      mbar_init(&c->p_staged[q], kRowWarps);
+      mbar_init(&c->p_free[q], 1);
+      mbar_init(&c->p_full[q], 1);
+    }
+    mbar_init(&c->q_ready, kRowWarps);
+    mbar_init(&c->fin_free, 32 * kRowWarps);
+    mbar_init(&c->xfin, kRowWarps / 2);
+    mbar_init(&c->fin_full, kRG);
+    mbar_init(&c->drain, 1);
+    c->abort = 0;
+    c->abort_site = 0;
+    c->start_b = p.B;
+    c->start_x = 0;
+    c->err = (smem_u32(smem) & 1023u) ? MLA_DEVERR_LAYOUT : 0u;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int n = make_split(p, c, cluster);  // the same n in every CTA
+  const bool work = cluster < n;
+  if (threadIdx.x == 0) {
+    if (rank == 0) {
+      Start* st = reinterpret_cast<Start*>(p.starts) + cluster;
+      *st = Start{c->start_b, (int32_t)c->start_x, (int32_t)(c->start_x >> 32), n > 0 ? n : 0};
+    }
     if (blockIdx.x == 0) p.err[0] = gridDim.x;
   }
+  if (!work) {
+    // both CTAs of the cluster leave here
+    grid_dep_launch();
+    if (threadIdx.x == 0) p.err[kErrFirst + blockIdx.x] = c->err;
+    return;
+  }
+  if (warp == kWarpAux) {
+    tmem_alloc_cta(&c->tmem_base, kTmemCols);
+    tmem_relinquish_cta();
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs initialised before any remote use
+  tc_fence_after();
+
+  if (warp < kProducerWarps) {
+    if (rank == 0) producer<true>(p, smem, c, warp, cluster);
+    else producer<false>(p, smem, c, warp, cluster);
+  } else if (warp == kWarpMma) {
+    if (rank == 0) score_mma(p, smem, c, cluster);
+    else value_mma(p, smem, c, cluster);
+  } else if (warp == kWarpAux) {
+    if (rank == 0 && (threadIdx.x & 31) == 0) weight_copier(p, smem, c, cluster);
+  } else {
+    if (rank == 0) score_softmax(p, smem, c, cluster);
+    else value_rows(p, c, cluster);
+  }
+
+  __syncwarp();
+  grid_dep_launch();  // the merging kernel may start launching; it waits for this grid
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) p.err[kErrFirst + blockIdx.x] = c->err | (c->abort ? MLA_DEVERR_TIMEOUT : 0u);
+  tc_fence_after();
+  cluster_sync();  // no CTA leaves while its peer may still touch its shared memory
+  if (warp == kWarpAux) tmem_dealloc_cta(c->tmem_base, kTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// merge
+// ---------------------------------------------------------------------------
+// The pieces of a row group that several clusters shared:
+//   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k.
+// Row k of the grid looks at the boundary between clusters k - 1 and k; the
+// first boundary inside a row group merges it.  One warp per (row, quarter of
+// the columns), four pieces in flight.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const Params p) {
+  grid_dep_wait();
+  const Start* st = reinterpret_cast<const Start*>(p.starts);
+  const int k = (int)blockIdx.y + 1;
+  const Start s0 = st[k - 1], s = st[k];
+  if (k >= s.n) return;
+  const Tiles tl = tiles_of(p, s.b);
+  const int L = kFixed + tl.T;
+  const int64_t g = s.x() / L;
+  const int64_t base = g * L;
+  if (s.x() == base) return;                      // the boundary lies between two row groups
+  if (s0.b == s.b && s0.x() > base) return;       // not the first inside this one
+  const int lane = threadIdx.x & 31;
+  const int wi = (int)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const int r = wi >> 2, col = (wi & 3) * 128 + 4 * lane;
+  const int64_t row = g * kRG + r;
+  if (r >= kRG || row >= p.rows) return;
+  // pieces: cluster k - 1 holds units [0, x_k), cluster i >= k units [x_i, x_{i+1})
+  auto unit = [&](int i) -> int64_t {
+    if (i < k) return 0;
+    if (i >= s.n) return L;
+    const Start q = st[i];
+    return q.b != s.b || q.x() - base > L ? L : q.x() - base;
+  };
+  float M = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  int64_t z0 = 0;
+  for (int i = k - 1; z0 < L;) {
+    // up to four pieces at once
+    float4 v[4];
+    float ls[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      ls[q] = -INFINITY;
+      if (z0 >= L) continue;
+      const int64_t z1 = unit(i + 1);
+      const int t0 = cut_tile(z0, tl.T), t1 = cut_tile(z1, tl.T);
+      if (t0 == 0 && t1 == tl.T) return;  // one cluster has it all: it stored the results
+      if (t1 > t0) {
+        const int64_t prow = (int64_t)(2 * i + (t0 == 0)) * kRG + r;
+        ls[q] = p.part_lse[prow];
+        v[q] = *reinterpret_cast<const float4*>(p.part_o + prow * kDl + col);
+      }
+      z0 = z1;
+      ++i;
+    }
+    float mb = fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3]));
+    mb = fmaxf(mb, M);
+    if (mb != -INFINITY) {
+      const float a = __expf(M - mb);  // 0 for the first pieces
+      sum *= a;
+      acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
+      M = mb;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (ls[q] == -INFINITY) continue;
+      const float wt = __expf(ls[q] - M);
+      sum += wt;
+      acc.x = fmaf(wt, v[q].x, acc.x);
+      acc.y = fmaf(wt, v[q].y, acc.y);
+      acc.z = fmaf(wt, v[q].z, acc.z);
+      acc.w = fmaf(wt, v[q].w, acc.w);
+    }
+  }
+  const float inv = 1.f / sum;
+  const int64_t orow = (int64_t)s.b * p.rows + row;
+  uint2 o;
+  o.x = pack_bf16(acc.x * inv, acc.y * inv);
+  o.y = pack_bf16(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + col) = o;
+  if (p.lse && (wi & 3) == 0 && lane == 0) p.lse[orow] = M + logf(sum);
 }
 
 namespace {
@@ -132,7 +951,52 @@ mla_status validate_call(const mla_kvq_attn_args* a) {
   return MLA_OK;
 }
 
-Params make_params(const mla_kvq_attn_args* a, void* ws) {
+// Two-CTA clusters that can be resident at once on the current device, looked
+// up once per device under a lock; 0 when it cannot be had.
+int clusters_per_gpu() {
+  constexpr int kMaxDevices = 64;
+  static std::mutex mu;
+  static int cached[kMaxDevices] = {};
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return 0;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (cached[dev] > 0) return cached[dev];
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaFuncSetAttribute(kvq_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemAlloc;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kvq_attn_kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = sms / 2;
+  }
+  if (2 * n > kErrMax) n = kErrMax / 2;
+  cached[dev] = n;
+  return n;
+}
+
+struct Layout {
+  size_t starts, part_lse, part_o, total;
+};
+Layout layout(int clusters) {
+  Layout l;
+  size_t o = MLA_KVQ_WORKSPACE_BYTES;
+  l.starts = o;    o = align256(o + 16 * ((size_t)clusters + 1));
+  l.part_lse = o;  o = align256(o + sizeof(float) * 2 * (size_t)clusters * kRG);
+  l.part_o = o;    o = align256(o + sizeof(float) * 2 * (size_t)clusters * kRG * kDl);
+  l.total = o;
+  return l;
+}
+
+Params make_params(const mla_kvq_attn_args* a, void* ws, int clusters) {
   Params p = {};
   p.B = a->B;
   p.Q = a->Q;
@@ -158,7 +1022,14 @@ Params make_params(const mla_kvq_attn_args* a, void* ws) {
   p.out_mul = (float)std::ldexp(1.0, e);
   p.out = a->out;
   p.lse = a->lse;
-  p.err = static_cast<uint32_t*>(ws);
+  p.groups = (p.rows + kRG - 1) / kRG;
+  p.clusters = clusters;
+  const Layout l = layout(clusters);
+  char* base = static_cast<char*>(ws);
+  p.err = reinterpret_cast<uint32_t*>(base);
+  p.starts = reinterpret_cast<int32_t*>(base + l.starts);
+  p.part_lse = reinterpret_cast<float*>(base + l.part_lse);
+  p.part_o = reinterpret_cast<float*>(base + l.part_o);
   return p;
 }
 
@@ -166,11 +1037,13 @@ Params make_params(const mla_kvq_attn_args* a, void* ws) {
 }  // namespace kvq
 }  // namespace mlav
 
+using namespace mlav;
 using namespace mlav::kvq;
 
 extern "C" size_t mla_kvq_attn_workspace_size(const mla_kvq_attn_args* a) {
   if (validate_shape(a) != MLA_OK) return 0;
-  return MLA_KVQ_WORKSPACE_BYTES;
+  const int n = clusters_per_gpu();
+  return n > 0 ? layout(n).total : 0;
 }
 
 extern "C" mla_status mla_kvq_attn(const mla_kvq_attn_args* a, void* workspace, size_t ws_bytes, mla_stream_t stream) {
@@ -180,9 +1053,18 @@ extern "C" mla_status mla_kvq_attn(const mla_kvq_attn_args* a, void* workspace, 
   st = validate_call(a);
   if (st != MLA_OK) return st;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < MLA_KVQ_WORKSPACE_BYTES) return MLA_ERR_WORKSPACE;
-  const Params p = make_params(a, workspace);
-  int64_t grid = ((int64_t)p.B * p.rows + kWarps - 1) / kWarps;
-  if (grid > kErrMax) grid = kErrMax;
-  kvq_attn_kernel<<<(int)grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  const int n = clusters_per_gpu();
+  if (n < 1) return MLA_ERR_CUDA;
+  if (ws_bytes < layout(n).total) return MLA_ERR_WORKSPACE;
+  const kvq::Params p = make_params(a, workspace, n);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // per call: the attribute belongs to the context, which may be a new one
+  if (cudaFuncSetAttribute(kvq_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  if (launch_kernel(kvq_attn_kernel, dim3(2 * n), dim3(kThreads), kSmemAlloc, s, false, p) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  if (n > 1 && launch_kernel(kvq_merge_kernel, dim3(4 * kRG / (kMergeThreads / 32), n - 1), dim3(kMergeThreads), 0, s,
+                             true, p) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return MLA_OK;
 }
