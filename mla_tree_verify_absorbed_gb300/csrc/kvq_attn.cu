@@ -113,8 +113,11 @@ struct alignas(16) Ctl {
   uint64_t xfin;               // score: half 1's row sums written (4 row warps)
   uint64_t p_staged[kPBufs];   // score: weights and factors staged (8 row warps)
   uint64_t p_full[kPBufs];     // value: weights and factors landed (copy bytes)
-  uint64_t pv_done[2];         // value: PV MMAs of a tile complete
-  uint64_t o_ready[2];         // value: O rescaled, weights in (8 row warps)
+  uint64_t pv_done[kPBufs];    // value: PV MMAs of a tile complete; when a tile's weights have landed, the PV
+                               // kPBufs tiles back is done but maybe no later one, so a barrier fewer would let a
+                               // wait for the piece's last PV pass on the parity of the one before
+  uint64_t o_ready[kPBufs];    // value: O rescaled, weights in (8 row warps); one per buffer, or a warp that
+                               // runs ahead could arrive twice where another has not arrived yet
   uint64_t fin_full;           // value: lfin / mfin written (128 remote arrivals)
   uint64_t drain;
   alignas(16) float alpha[kPBufs][kRG];  // staged in rank 0, copied to rank 1
@@ -630,7 +633,7 @@ __device__ void value_mma(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
   for_pieces(p, c, cluster, [&](int, int, int, int t0, int t1, const Tiles&) {
     for (int t = t0; t < t1; ++t, ++j) {
       const int pb = j % kPBufs;
-      if (!wait_warp(&c->o_ready[j & 1], (uint32_t)(j >> 1) & 1u, c, kSiteOReady)) return false;
+      if (!wait_warp(&c->o_ready[pb], (uint32_t)(j / kPBufs) & 1u, c, kSiteOReady)) return false;
       const uint64_t da = smem_desc(smem_u32(smem + kOffP + pb * kPBytes), 16, 1024, kLayoutSw128);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -646,7 +649,7 @@ __device__ void value_mma(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
         mma_cta_commit_warp(&c->empty[slot]);
       }
       mma_cta_commit_warp(&c->p_free[pb], 0x1);
-      mma_cta_commit_warp(&c->pv_done[j & 1]);
+      mma_cta_commit_warp(&c->pv_done[pb]);
     }
     return true;
   });
@@ -675,7 +678,7 @@ __device__ void value_rows(const Params& p, Ctl* c, int cluster) {
       if (t != t0) {
         const float a = c->alpha[pb][r];
         if (__any_sync(0xffffffffu, a != 1.f)) {
-          if (!wait_warp(&c->pv_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, c, kSitePvPrev)) return false;
+          if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c, kSitePvPrev)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < 256; c0 += 32) {
@@ -691,10 +694,10 @@ __device__ void value_rows(const Params& p, Ctl* c, int cluster) {
       fence_proxy_async_smem();  // the weights feed the MMA
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c->o_ready[j & 1]);
+      if (lane == 0) mbar_arrive(&c->o_ready[pb]);
     }
 
-    if (!wait_warp(&c->pv_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, c, kSitePvLast)) return false;
+    if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c, kSitePvLast)) return false;
     if (!wait_warp(&c->fin_full, (uint32_t)seg & 1u, c, kSiteFinFull)) return false;
     tc_fence_after();
     const float l = c->lfin[r], m = c->mfin[r];
@@ -769,11 +772,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
       mbar_init(&c->s_full[q], 1);
       mbar_init(&c->s_free[q], kRowWarps);
       mbar_init(&c->xch[q], kRowWarps);
-      mbar_init(&c->pv_done[q], 1);
-      mbar_init(&c->o_ready[q], kRowWarps);
     }
     for (int q = 0; q < kPBufs; ++q) {
       mbar_init(&c->p_staged[q], kRowWarps);
+      mbar_init(&c->o_ready[q], kRowWarps);
+      mbar_init(&c->pv_done[q], 1);
       mbar_init(&c->p_free[q], 1);
       mbar_init(&c->p_full[q], 1);
     }

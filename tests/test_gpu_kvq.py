@@ -407,6 +407,43 @@ def test_window_and_sinks_match_oracle(kw, freed):
     check_attn(problem(seed=31, freed=freed, **kw))
 
 
+@pytest.mark.parametrize("seed", range(8))
+def test_maximum_moves_after_a_few_first_tokens(seed):
+    # the first tile of the row group shows 4 tokens, so the next ones move the maxima of most rows, at tiles
+    # that differ from warp to warp, in pieces of a few tiles: the oracle's values, and the same bytes every time
+    B = 1 + seed % 2
+    p = problem(B=B, Q=1, H=64, lens=[60000 + 1000 * seed, 9000][:B], seed=40 + seed, window=4096 - 60 * seed,
+                sinks=4, page=64, tree="null", freed=True)
+    n = len(p.rows)
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(n, 576, generator=g)
+    x[:, :512] *= torch.exp(0.4 * torch.randn(512, generator=g))
+    x = x.to(torch.bfloat16).cuda()
+    api.kvq_write(p.ki.cache, x[:, :512], x[:, 512:], torch.arange(n, dtype=torch.int32).cuda())
+    p = dataclasses.replace(p, rows=p.ki.cache.rows.cpu().numpy())
+    out, lse = check_attn(p)
+    for _ in range(10):
+        o, l = run(p.ki)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("tiles", range(2, 13))
+def test_some_rows_maxima_move_at_every_tile_and_others_never(tiles):
+    # heads 32-63 meet their keys in rising order, far apart; heads 0-31 see flat scores
+    p = problem(B=1, Q=1, H=64, lens=[64 * tiles - 1], seed=60, tree="null")
+    p.ki.q_lat[0, 0, 32:] = p.ki.q_lat[0, 0, 32].clone() * 16
+    p.ki.q_pe[0, 0, 32:] = p.ki.q_pe[0, 0, 32].clone() * 16
+    p.ki.q_lat[0, 0, :32] *= 2.0 ** -6
+    p.ki.q_pe[0, 0, :32] *= 2.0 ** -6
+    lat, rope = O.unpack_rows(p.rows)
+    s = lat[p.slots[0]] @ p.ki.q_lat[0, 0, 32].double().cpu().numpy() \
+        + rope[p.slots[0]] @ p.ki.q_pe[0, 0, 32].double().cpu().numpy()
+    p.slots[0] = p.slots[0][np.argsort(s)]
+    p.ki.kv_indices.copy_(torch.from_numpy(p.slots[0].astype(np.int32)))
+    for _ in range(3):
+        check_attn(p)
+
+
 def test_window_that_covers_everything_changes_nothing():
     p = problem(B=2, Q=6, H=8, lens=[333, 70], seed=32)
     out, lse = run(p.ki)
