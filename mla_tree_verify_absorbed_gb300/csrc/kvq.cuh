@@ -150,20 +150,6 @@ __device__ __forceinline__ uint32_t check_sequence(const Params& p, int b) {
   return e;
 }
 
-// Pool slot of logical position pos of sequence b, or -1 when the table names
-// none in the pool.
-__device__ __forceinline__ int64_t slot_at(const Params& p, int b, int64_t idx0, int64_t pos) {
-  int64_t s;
-  if (p.page_size == 1) {
-    s = p.kv_indices[idx0 + pos];
-  } else {
-    const uint32_t pg = (uint32_t)pos / (uint32_t)p.page_size;
-    const int64_t page = p.block_table[(int64_t)b * p.max_pages + pg];
-    s = page < 0 ? -1 : page * p.page_size + (uint32_t)((uint32_t)pos - pg * (uint32_t)p.page_size);
-  }
-  return (s < 0 || s >= p.slots) ? -1 : s;
-}
-
 // What one node sees of the tree: the mask of its visible nodes and its depth.
 struct NodeView {
   uint64_t mask;  // bit t: node t is the node itself or a visible ancestor

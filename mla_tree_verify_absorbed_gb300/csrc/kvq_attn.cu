@@ -58,31 +58,51 @@ mla_status validate_cache(const mla_kvq_cache* c);
 
 constexpr int kRG = 128;       // query rows per work item
 constexpr int kTK = 64;        // tokens per tile
-constexpr int kThreads = 576;  // 18 warps
+constexpr int kThreads = 640;  // 20 warps: 96 registers a thread
 constexpr uint32_t kTmemCols = 512;
-constexpr int kProducerWarps = 8;
-constexpr int kWarpRows = 8, kRowWarps = 8;  // warps 8-15: two per TMEM lane quadrant, column halves
+// Warps 0-7 convert, warps 8-15 hold rows; each in two groups that take the
+// tiles of one parity, so a group has two tile periods for its chain of loads,
+// conversion and barriers.  The roles' loops are kept short: together they have
+// to stay in the SM's instruction cache (unrolled twice as far they ran at half
+// the speed).
+constexpr int kProducerWarps = 8, kGroupWarps = 4;
+constexpr int kWarpRows = 8, kRowWarps = 8;
 constexpr int kWarpMma = 16;
-constexpr int kWarpAux = 17;  // TMEM allocation; lane 0 of rank 0: weight copies
+constexpr int kWarpAux = 17;    // TMEM allocation; rank 0: weight copies
+constexpr int kWarpSched = 18;  // the pieces of work
 
 // A tile is staged as two halves, each with its own full / empty barriers:
 // half h holds latent columns [256 h, 256 h + 256) as 4 chunks of 64 columns
 // (64 token rows of 128 bytes each); in the score CTA half 1 ends with the
-// rope chunk.
+// rope chunk.  Tile j uses stage j % 2.
 constexpr int kChunk = kTK * 128;             // 8 KB
 constexpr int kStageS = 9 * kChunk;           // score CTA: 72 KB per tile
-constexpr int kStagesS = 2;
-constexpr int kUnitV = 4 * kChunk;            // value CTA: 32 KB per half tile
-constexpr int kUnitsV = 5;
-constexpr int kUnitsMax = 5;
-static_assert(2 * kStagesS <= kUnitsMax && kUnitsV <= kUnitsMax, "barrier arrays");
+constexpr int kStageV = 8 * kChunk;           // value CTA: 64 KB
+constexpr int kHalf = 4 * kChunk;
 constexpr int kPBytes = kRG * 128;            // weights of a tile, f16
-constexpr int kPBufs = 3;
-constexpr int kOffP = kUnitsV * kUnitV;       // weights: staged at this offset in rank 0, copied to it in rank 1
-static_assert(kStagesS * kStageS <= kOffP, "score stages reach into the weights");
-constexpr int kOffRed = kOffP + kPBufs * kPBytes;        // [2 tiles][2 halves][128] partial row maxima, [128] sums
-constexpr int kOffCtl = kOffRed + (2 * 2 * kRG + kRG) * 4;
+constexpr int kPBufs = 4;
+constexpr int kOffP = 2 * kStageS;            // weights: staged at this offset in rank 0, copied to it in rank 1
+constexpr int kOffCtl = kOffP + kPBufs * kPBytes;
 constexpr uint32_t kPTxBytes = kPBytes + kRG * 4;        // weights + rescale factors
+
+// Tensor Memory columns: score CTA, two S tiles and the queries (bf16 pairs);
+// value CTA, O from column 0
+constexpr uint32_t kColS = 0, kColQ = 2 * kTK;
+// upper halves of the operand descriptors (smem_desc): only the start address,
+// in the lower half, differs from MMA to MMA
+constexpr uint32_t kDescHiK = (1024u >> 4) | (1u << 14) | (kLayoutSw128 << 29);
+constexpr uint32_t kDescLoK = (16u >> 4) << 16;        // K-major: queries' and weights' operands
+constexpr uint32_t kDescLoV = ((uint32_t)kChunk >> 4) << 16;  // MN-major: 64-column chunks 8 KB apart
+// start-address field of offset `off` (the window's address of a cluster CTA
+// has bits above the field)
+__device__ __forceinline__ uint32_t desc_addr(const uint8_t* smem, uint32_t off) {
+  return ((smem_u32(smem) & 0x3FFFFu) + off) >> 4;
+}
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
 
 constexpr uint32_t kIdescS = idesc_bf16_f32(kRG, kTK, 0, 0);   // queries (TMEM), keys K-major
 constexpr uint32_t kIdescPV = idesc_f16_f32(kRG, 256, 0, 1);   // weights K-major, values MN-major
@@ -101,27 +121,41 @@ constexpr float kWeightShift = 7.f;
 constexpr int kFixed = 8;
 constexpr int kMinTiles = 6;
 
+// One cluster's share of a row group, as the roles need it.
+struct alignas(16) Piece {
+  int32_t b, g, slot, t0;      // slot: partial-result slot, -1 for a whole row group
+  int32_t t1, ns, tw, N;       // tiles [t0, t1), numbered over [0, ns) and from tw on; b < 0: no more pieces
+  int32_t lo, P, pad0, pad1;
+  int64_t entry;               // first table entry of the sequence
+  int64_t pad2;
+  __device__ __forceinline__ int tile(int v) const { return v < ns ? v : v - ns + tw; }
+};
+constexpr int kPieces = 4;
+
+// Barriers that two groups of warps pass at different tiles have one instance
+// per buffer they guard: a wait must never be able to pass on the parity of an
+// older phase.
 struct alignas(16) Ctl {
-  uint64_t full[kUnitsMax];    // half tile converted (8 producer warps)
-  uint64_t empty[kUnitsMax];   // the MMAs reading it are complete
+  uint64_t full[4];            // half tile converted (8 producer warps); index 2 (j % 2) + half
+  uint64_t empty[4];           // the MMAs reading it are complete
   uint64_t s_full[2];          // score: S tile in TMEM
-  uint64_t s_free[2];          // score: softmax has loaded S (8 row warps)
+  uint64_t s_free[2];          // score: softmax has loaded S (4 row warps)
   uint64_t q_ready;            // score: queries in TMEM (8 row warps)
+  uint64_t m_ready[2][4];      // score: running maxima after a tile written (per lane quadrant, 1 warp)
   uint64_t p_free[kPBufs];     // score: the PV MMAs that read this buffer are complete (rank 1's commit)
   uint64_t fin_free;           // score: rank 1 consumed lfin / mfin (256 arrivals)
-  uint64_t xch[2];             // score: both halves' partial row maxima written (8 row warps)
-  uint64_t xfin;               // score: half 1's row sums written (4 row warps)
-  uint64_t p_staged[kPBufs];   // score: weights and factors staged (8 row warps)
+  uint64_t p_staged[kPBufs];   // score: weights and factors staged (4 row warps)
   uint64_t p_full[kPBufs];     // value: weights and factors landed (copy bytes)
-  uint64_t pv_done[kPBufs];    // value: PV MMAs of a tile complete; when a tile's weights have landed, the PV
-                               // kPBufs tiles back is done but maybe no later one, so a barrier fewer would let a
-                               // wait for the piece's last PV pass on the parity of the one before
-  uint64_t o_ready[kPBufs];    // value: O rescaled, weights in (8 row warps); one per buffer, or a warp that
-                               // runs ahead could arrive twice where another has not arrived yet
-  uint64_t fin_full;           // value: lfin / mfin written (128 remote arrivals)
+  uint64_t pv_done[kPBufs];    // value: PV MMAs of a tile complete
+  uint64_t o_ready[kPBufs];    // value: O rescaled, weights in (8 row warps)
+  uint64_t fin_full;           // value: lfin / mfin written (256 remote arrivals)
   uint64_t drain;
+  uint64_t piece_full[kPieces];   // piece written (scheduler warp)
+  uint64_t piece_empty[kPieces];  // read by every warp of this CTA that follows the pieces
+  Piece piece[kPieces];
   alignas(16) float alpha[kPBufs][kRG];  // staged in rank 0, copied to rank 1
-  float lfin[kRG];             // value: row sums of the shifted weights
+  float m_run[2][kRG];         // score: running maxima after the last tile of each parity
+  float lfin[2][kRG];          // value: each group's row sums of the shifted weights
   float mfin[kRG];             // value: row maxima, base-2 units
   int64_t scan[kThreads / 32];
   int64_t total;               // units of the whole call
@@ -137,20 +171,27 @@ constexpr int kSmemAlloc = 232448;  // the per-CTA maximum
 static_assert(kSmemBytes <= kSmemAlloc, "shared memory budget");
 static_assert(offsetof(Ctl, alpha) % 16 == 0 && kOffCtl % 16 == 0, "bulk-copy alignment");
 static_assert(kOffP % 1024 == 0 && kStageS % 1024 == 0, "swizzle atoms");
+static_assert(kStageV <= kStageS, "value stages reach into the weights");
 
 enum {
   kSiteEmpty = 1, kSiteQReady, kSiteFullS, kSiteSFree, kSiteSFull, kSitePFree, kSiteFinFree, kSiteFullV,
-  kSiteOReady, kSitePFull, kSitePvPrev, kSitePvLast, kSiteFinFull, kSiteXch, kSitePStaged
+  kSiteOReady, kSitePFull, kSitePvPrev, kSitePvLast, kSiteFinFull, kSiteMReady, kSitePStaged, kSitePiece,
+  kSitePieceFree
 };
 
 __device__ __noinline__ void raise_abort(Ctl* c, int site) {
   if (*reinterpret_cast<volatile int*>(&c->abort) == 0) atomicCAS(&c->abort_site, 0, site);
   for (uint32_t rk = 0; rk < 2; ++rk) st_cluster_u32(mapa_shared(smem_u32(&c->abort), rk), 1u);
 }
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* c, int site) {
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* c, int site) {
   if (mbar_wait(bar, parity, &c->abort, kWaitLimitNs, true)) return true;
   raise_abort(c, site);
   return false;
+}
+// The first try is inline, everything after it one shared copy: the roles'
+// loops have to fit the instruction cache together.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* c, int site) {
+  return mbar_try_wait_cluster(bar, parity) || wait_slow(bar, parity, c, site);
 }
 // Every lane waits; the result is warp-uniform and the warp converged.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c, int site) {
@@ -226,31 +267,74 @@ struct Start {
   __device__ __forceinline__ int64_t x() const { return (int64_t)(uint32_t)x_lo | (int64_t)x_hi << 32; }
 };
 
-// Calls f(slot, b, g, t0, t1, tiles) for this cluster's pieces in order; slot
-// is the piece's partial-result slot, or -1 for a whole row group.  A piece
-// that does not begin its row group is the cluster's first, one that does not
-// end it the last, so two slots are enough.
-template <class F>
-__device__ __forceinline__ void for_pieces(const Params& p, const Ctl* c, int cluster, F&& f) {
+// Scheduler warp of each CTA: writes this cluster's pieces in order, then an
+// end mark, into the ring that the other roles follow.  A piece that does not
+// begin its row group is the cluster's first, one that does not end it the
+// last, so two partial slots are enough.
+__device__ void schedule(const Params& p, Ctl* c, int cluster) {
+  const int lane = threadIdx.x & 31;
   const int n = active_clusters(p, c->total);
   int64_t left = first_unit(c->total, n, cluster + 1) - first_unit(c->total, n, cluster);
   int64_t x = c->start_x;
+  uint32_t seg = 0;
+  auto put = [&](const Piece& pc) {
+    const uint32_t q = seg % kPieces;
+    if (!wait_warp(&c->piece_empty[q], ((seg / kPieces) & 1u) ^ 1u, c, kSitePieceFree)) return false;
+    if (lane == 0) {
+      c->piece[q] = pc;
+      mbar_arrive(&c->piece_full[q]);
+    }
+    __syncwarp();
+    ++seg;
+    return true;
+  };
   for (int b = c->start_b; left > 0 && b < p.B; ++b, x = 0) {
     const Tiles tl = tiles_of(p, b);
     if (tl.T == 0) continue;
     const int L = kFixed + tl.T;
+    Piece pc;
+    pc.b = b;
+    pc.ns = tl.ns;
+    pc.tw = tl.tw;
+    pc.lo = (int32_t)tl.lo;
+    pc.P = p.prefix_lens[b];
+    pc.N = (int32_t)((int64_t)pc.P + p.Q);
+    pc.entry = p.page_size == 1 ? (int64_t)p.kv_indptr[b] : (int64_t)b * p.max_pages;
     for (int g = (int)(x / L); g < p.groups && left > 0; ++g) {
       const int64_t z = x - (int64_t)g * L;
       const int64_t take = L - z < left ? L - z : left;
-      const int t0 = cut_tile(z, tl.T), t1 = cut_tile(z + take, tl.T);
+      pc.g = g;
+      pc.t0 = cut_tile(z, tl.T);
+      pc.t1 = cut_tile(z + take, tl.T);
+      pc.slot = pc.t0 == 0 && pc.t1 == tl.T ? -1 : 2 * cluster + (pc.t0 == 0);
       x += take;
       left -= take;
-      if (t1 <= t0) continue;
-      const int slot = t0 == 0 && t1 == tl.T ? -1 : 2 * cluster + (t0 == 0);
-      if (!f(slot, b, g, t0, t1, tl)) return;
+      if (pc.t1 > pc.t0 && !put(pc)) return;
     }
   }
+  Piece end = {};
+  end.b = -1;
+  put(end);
 }
+
+// Calls f(piece) for the pieces of the ring in order; f's piece stays valid
+// only as far as f copied it.  Every lane of the warp takes part.
+template <class F>
+__device__ __forceinline__ void for_pieces(Ctl* c, F&& f) {
+#pragma unroll 1
+  for (uint32_t seg = 0;; ++seg) {
+    const uint32_t q = seg % kPieces;
+    if (!wait_warp(&c->piece_full[q], (seg / kPieces) & 1u, c, kSitePiece)) return;
+    const Piece pc = c->piece[q];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&c->piece_empty[q]);
+    if (pc.b < 0) return;
+    if (!f(pc)) return;
+  }
+}
+// Warps that follow the pieces: producers, row warps, the MMA warp and, in the
+// score CTA, the copier.
+constexpr int kFollowers = kProducerWarps + kRowWarps + 1;
 
 // Block-wide: validates every sequence, sums the units and finds where this
 // cluster's interval begins.  Returns the clusters that share the call, 0 when
@@ -308,26 +392,6 @@ __device__ int make_split(const Params& p, Ctl* c, int cluster) {
 // ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
-// What one lane holds of a tile: token (lane & 7) of its warp's 8, chunks
-// lane >> 3 and 4 + (lane >> 3), and two 16-byte pieces of the rope key.
-template <bool kScore>
-struct Packed {
-  uint32_t code[2][8];
-  uint32_t scale[2];
-  uint4 rope[kScore ? 2 : 1];
-  __device__ __forceinline__ void load(const uint8_t* row, int ch) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      ld_global_v8(row + 32 * (4 * h + ch), code[h]);
-      scale[h] = __ldg(reinterpret_cast<const uint32_t*>(row + kScaleOff) + 4 * h + ch);
-    }
-    if (kScore) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) rope[q] = __ldg(reinterpret_cast<const uint4*>(row + kRopeOff) + 4 * q + ch);
-    }
-  }
-};
-
 // Converts one sector of codes with its 4 scales into the 8 pieces of an
 // operand row.
 template <class To>
@@ -352,103 +416,160 @@ __device__ __forceinline__ void convert_chunk(const uint32_t (&code)[8], uint32_
   }
 }
 
+// One warp of producer group `grp`: tokens 16 pw .. + 15 of the tiles of that
+// parity, as two sets of 8; lane l holds token l & 7 of a set, chunk l >> 3 of
+// a half tile and, with the second half, two 16-byte pieces of the rope key.
+// When a set's registers have been converted, the sector that the set needs
+// next is loaded into them: it is in flight while the other set is converted.
+// The table entries of the tile after that (a lane per token) are in flight
+// for a whole tile.
 template <bool kScore>
-__device__ void producer(const Params& p, uint8_t* smem, Ctl* c, int pw, int cluster) {
-  using To = typename std::conditional<kScore, ToBf16, ToF16>::type;
+struct Sector {
+  uint32_t code[8];
+  uint32_t scale;
+  uint4 rope[kScore ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t* row, int h, int ch) {
+    ld_global_v8(row + 128 * h + 32 * ch, code);
+    scale = __ldg(reinterpret_cast<const uint32_t*>(row + kScaleOff) + 4 * h + ch);
+    if (kScore && h) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) rope[q] = __ldg(reinterpret_cast<const uint4*>(row + kRopeOff) + 4 * q + ch);
+    }
+  }
+  // dst: shared address of the token's row in the half's chunk ch; rope_dst:
+  // of its row in the rope chunk
+  __device__ __forceinline__ void store(uint32_t dst, uint32_t rope_dst, int h, int ch, int r7) const {
+    convert_chunk<typename std::conditional<kScore, ToBf16, ToF16>::type>(code, scale, dst, r7);
+    if (kScore && h) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rope_dst + (((4 * q + ch) ^ r7) << 4)),
+                     "r"(rope[q].x), "r"(rope[q].y), "r"(rope[q].z), "r"(rope[q].w)
+                     : "memory");
+    }
+  }
+};
+
+template <bool kScore>
+__device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c, int warp) {
   const int lane = threadIdx.x & 31;
+  const int grp = warp / kGroupWarps, pw = warp % kGroupWarps;
   const int r7 = lane & 7, ch = lane >> 3;
-  const int r = 8 * pw + r7;  // token row within the tile
-  const uint32_t sbase = smem_u32(smem);
+  const int r = 16 * pw + r7;  // token row of set 0 within the tile
+  const uint32_t stage = smem_u32(smem) + grp * (kScore ? kStageS : kStageV) + r * 128;
   uint32_t err = 0;
-  int j = 0;
-  for_pieces(p, c, cluster, [&](int, int b, int, int t0, int t1, const Tiles& tl) {
-    const int64_t N = (int64_t)p.prefix_lens[b] + p.Q;
-    const int64_t idx0 = p.page_size == 1 ? (int64_t)p.kv_indptr[b] : 0;
-    // address of the row of this lane's token in tile v; positions that no
-    // node sees read slot 0, whose weight is zero
-    auto row_of = [&](int v) -> const uint8_t* {
-      const int64_t pos = (int64_t)tl.at(v) * kTK + r;
-      int64_t s = 0;
-      if (pos < N && (pos >= tl.lo || pos < p.sinks)) {
-        s = slot_at(p, b, idx0, pos);
-        if (s < 0) {
-          err |= MLA_DEVERR_SLOT;
-          s = 0;
-        }
-      }
-      return p.cache + s * p.row_stride;
+  uint32_t j = 0;
+  for_pieces(c, [&](const Piece& pc) {
+    int t = pc.t0 + (int)((grp ^ j) & 1u);
+    j += (uint32_t)(pc.t1 - pc.t0);
+    if (t >= pc.t1) return true;
+    uint32_t turn = (j - (uint32_t)(pc.t1 - t)) >> 1;  // tiles this group has taken before
+    const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
+    // Pool row of token 16 pw + (lane & 15) of tile v, in two steps: the table
+    // entry (a slot, or a page; -2 where no node sees the position), and, a
+    // tile later, the row.  Positions that no node sees read slot 0, under a
+    // weight of zero.
+    auto entry_of = [&](int v) -> int32_t {
+      const int pos = pc.tile(v) * kTK + 16 * pw + (lane & 15);
+      if (v >= pc.t1 || pos >= pc.N || (pos < pc.lo && pos >= p.sinks)) return -2;
+      return __ldg(idx + (p.page_size == 1 ? (uint32_t)pos : (uint32_t)pos / (uint32_t)p.page_size));
     };
-    Packed<kScore> nxt;
-    nxt.load(row_of(t0), ch);
-    const uint8_t* row = t0 + 1 < t1 ? row_of(t0 + 1) : nullptr;
-    for (int t = t0; t < t1; ++t, ++j) {
-      const Packed<kScore> cur = nxt;
-      if (t + 1 < t1) nxt.load(row, ch);
-      if (t + 2 < t1) row = row_of(t + 2);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // score: stage j % 2, its halves in turn; value: a ring of half tiles
-        const int u = 2 * j + h;
-        const int slot = kScore ? u % (2 * kStagesS) : u % kUnitsV;
-        const uint32_t turn = kScore ? (uint32_t)(u / (2 * kStagesS)) : (uint32_t)(u / kUnitsV);
-        if (!wait_warp(&c->empty[slot], (turn & 1u) ^ 1u, c, kSiteEmpty)) return false;
-        const uint32_t base = kScore ? sbase + (j % kStagesS) * kStageS + h * 4 * kChunk : sbase + slot * kUnitV;
-        convert_chunk<To>(cur.code[h], cur.scale[h], base + ch * kChunk + r * 128, r7);
-        if (kScore && h == 1) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<uint4*>(smem + (j % kStagesS) * kStageS + 8 * kChunk + r * 128 +
-                                      (((4 * q + ch) ^ r7) << 4)) = cur.rope[q];
-        }
-        fence_proxy_async_smem();  // generic stores, read by the MMA
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->full[slot]);
+    auto slot_of = [&](int32_t e, int v) -> uint32_t {
+      int64_t s = e;
+      if (p.page_size > 1) {
+        const uint32_t pos = (uint32_t)(pc.tile(v) * kTK + 16 * pw + (lane & 15));
+        s = s * p.page_size + pos % (uint32_t)p.page_size;
       }
+      if (e < 0 || s >= p.slots) {
+        if (e != -2 && v < pc.t1) err |= MLA_DEVERR_SLOT;
+        s = 0;
+      }
+      return (uint32_t)s;
+    };
+    auto row_of = [&](uint32_t slot, int set) {
+      return p.cache + (uint64_t)__shfl_sync(0xffffffffu, slot, 8 * set + r7) * (uint32_t)p.row_stride;
+    };
+    uint32_t slot = slot_of(entry_of(t), t);
+    Sector<kScore> a, b;
+    a.load(row_of(slot, 0), 0, ch);
+    b.load(row_of(slot, 1), 0, ch);
+    int32_t ent = entry_of(t + 2);
+#pragma unroll 1
+    for (int h = 0; t < pc.t1; h ^= 1) {
+      const uint32_t full = 2 * grp + h;
+      if (!wait_warp(&c->empty[full], (turn & 1u) ^ 1u, c, kSiteEmpty)) return false;
+      const uint32_t dst = stage + h * kHalf + ch * kChunk, rope_dst = stage + 8 * kChunk;
+      if (h) {  // what follows this half is the next tile's first
+        t += 2;
+        ++turn;
+        slot = slot_of(ent, t);
+        ent = entry_of(t + 2);
+      }
+      a.store(dst, rope_dst, h, ch, r7);
+      a.load(row_of(slot, 0), h ^ 1, ch);
+      b.store(dst + 8 * 128, rope_dst + 8 * 128, h, ch, r7);
+      b.load(row_of(slot, 1), h ^ 1, ch);
+      fence_proxy_async_smem();  // generic stores, read by the MMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->full[full]);
     }
     return true;
   });
   if (err) atomicOr(&c->err, err);
 }
 
+// On abort, outstanding MMAs must finish before Tensor Memory is released.
+__device__ void drain_mmas(Ctl* c, bool leader) {
+  __syncwarp();
+  if (!__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&c->abort) != 0)) return;
+  if (leader) {
+    mma_cta_commit(&c->drain);
+    mbar_wait_drain(&c->drain, 0, kDrainLimitNs);
+  }
+  __syncwarp();
+}
+
 // ---------------------------------------------------------------------------
 // score CTA
 // ---------------------------------------------------------------------------
-__device__ void score_mma(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
-  const uint32_t tS = c->tmem_base;        // columns [0, 128): two S tiles
-  const uint32_t tQ = c->tmem_base + 128;  // columns [128, 416): queries, bf16 pairs
-  int j = 0, seg = 0;
-  for_pieces(p, c, cluster, [&](int, int, int, int t0, int t1, const Tiles&) {
-    if (!wait_warp(&c->q_ready, (uint32_t)seg & 1u, c, kSiteQReady)) return false;
-    for (int t = t0; t < t1; ++t, ++j) {
-      const int sb = j & 1;
-      if (j >= 2 && !wait_warp(&c->s_free[sb], (((uint32_t)j >> 1) & 1u) ^ 1u, c, kSiteSFree)) return false;
-      const uint64_t dk = smem_desc(smem_u32(smem + (j % kStagesS) * kStageS), 16, 1024, kLayoutSw128);
-      const uint32_t ts = tS + sb * kTK;
-#pragma unroll
+// Tensor Memory addresses are constants here (all 512 columns are allocated, so
+// the base is 0).  Three chunks' MMAs per iteration keep the loop short and the
+// tensor pipe fed (9 MMAs of 32 cycles are queued while the next are prepared).
+__device__ void score_mma(uint8_t* smem, Ctl* c) {
+  const bool leader = elect_one();
+  uint32_t j = 0, seg = 0;
+  for_pieces(c, [&](const Piece& pc) {
+    if (!wait_warp(&c->q_ready, seg & 1u, c, kSiteQReady)) return false;
+#pragma unroll 1
+    for (int t = pc.t0; t < pc.t1; ++t, ++j) {
+      const uint32_t par = j & 1u, turn = j >> 1;
+      if (turn >= 1 && !wait_warp(&c->s_free[par], (turn & 1u) ^ 1u, c, kSiteSFree)) return false;
+      uint32_t lo = desc_addr(smem, par * kStageS) | kDescLoK;
+      uint32_t tq = kColQ;
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        const int u = 2 * j + h, slot = u % (2 * kStagesS);
-        if (!wait_warp(&c->full[slot], (uint32_t)(u / (2 * kStagesS)) & 1u, c, kSiteFullS)) return false;
+        if (!wait_warp(&c->full[2 * par + h], turn & 1u, c, kSiteFullS)) return false;
         tc_fence_after();
+        if (leader) {
+#pragma unroll 1
+          for (int kc = 0; kc < 4 + h; ++kc) {
 #pragma unroll
-        for (int kc = 4 * h; kc < (h ? 9 : 4); ++kc) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_cta_ts_warp(ts, tQ + kc * 32 + kk * 8, dk + (uint64_t)((kc * kChunk + kk * 32) >> 4), kIdescS,
-                            (kc | kk) != 0);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_cta_ts(kColS + par * kTK, tq + kk * 8, desc_at(lo + ((kk * 32) >> 4), kDescHiK), kIdescS,
+                         (uint32_t)(h | kc | kk));
+            lo += kChunk >> 4;
+            tq += 32;
+          }
+          if (h) mma_cta_commit(&c->s_full[par]);
+          mma_cta_commit(&c->empty[2 * par + h]);
         }
-        if (h) mma_cta_commit_warp(&c->s_full[sb]);
-        mma_cta_commit_warp(&c->empty[slot]);
+        __syncwarp();
       }
     }
     ++seg;
     return true;
   });
-  if (__any_sync(0xffffffffu, c->abort != 0)) {
-    // outstanding MMAs must finish before TMEM is released
-    mma_cta_commit_warp(&c->drain);
-    if ((threadIdx.x & 31) == 0) mbar_wait_drain(&c->drain, 0, kDrainLimitNs);
-    __syncwarp();
-  }
+  drain_mmas(c, leader);
 }
 
 // Stages query row `row` into Tensor Memory: half h of the row's two threads
@@ -491,129 +612,188 @@ __device__ __forceinline__ void stage_query_row(const Params& p, int b, int row,
   tmem_wait_st();
 }
 
-// Online softmax, two threads per row with 32 of a tile's 64 columns each.
-__device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
+// Pairs of fp32 in a 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float lo_f32(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_f32(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// The low n bits, n clamped to [0, 64].
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : ~0ull >> (64 - n); }
+// Scores of the tokens whose bit is 0 become -inf, whatever they were.
+__device__ __forceinline__ void mask32(uint32_t (&u)[32], uint32_t vis) {
+#pragma unroll
+  for (int q = 0; q < 32; ++q)
+    if (!((vis >> q) & 1u)) u[q] = 0xff800000u;
+}
+
+// Online softmax: a thread per row and group of row warps; group `wg` takes
+// the tiles of its parity, all 64 columns of a row in one thread.  The running
+// maximum passes from group to group, warp to warp of the same rows, before
+// the exponentials; each group sums its own weights.
+__device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
   const int lane = threadIdx.x & 31;
-  const int w = (threadIdx.x >> 5) - kWarpRows;
-  const int wq = w & 3, h = w >> 2;
+  const int wq = warp & 3, wg = (warp - kWarpRows) >> 2;
   const int r = wq * 32 + lane;
   const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-  const uint32_t tS = c->tmem_base + lane_off + (uint32_t)(h * 32);
-  const uint32_t tQ = c->tmem_base + 128 + lane_off;
-  float* red_max = reinterpret_cast<float*>(smem + kOffRed);
-  float* red_l = red_max + 4 * kRG;
   const float sl2 = p.scale_log2;
+  const uint64_t sl2x2 = pair(sl2, sl2);
   const int nq = p.Q;
-  int j = 0, seg = 0;
+  uint32_t j = 0, seg = 0;
   bool bad = false;
-  for_pieces(p, c, cluster, [&](int, int b, int g, int t0, int t1, const Tiles& tl) {
-    const int row = g * kRG + r;
+  for_pieces(c, [&](const Piece& pc) {
+    const int t0 = pc.t0, t1 = pc.t1;
+    const int row = pc.g * kRG + r;
     const bool live = row < p.rows;
-    const int64_t P = p.prefix_lens[b];
-    stage_query_row(p, b, row, live, h, tQ);
+    const int P = pc.P;
+    stage_query_row(p, pc.b, row, live, wg, lane_off + kColQ);
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&c->q_ready);
     // rows past the last take the last one's mask: their results are dropped
-    const NodeView nv = node_view_warp(p, b, (live ? row : p.rows - 1) / p.H, P, &bad);
-    // prefix positions up to this one are outside the window (unless sinks)
-    const int64_t past = p.window > 0 ? P + nv.depth - p.window : -1;
-    const int64_t past_any = p.window > 0 ? P + nq - 1 - p.window : -1;
+    const NodeView nv = node_view_warp(p, pc.b, (live ? row : p.rows - 1) / p.H, P, &bad);
+    // prefix positions up to this one are outside the window (unless sinks);
+    // lengths fit 32 bits with the nodes counted, so these do too
+    const int past = p.window > 0 ? P - p.window + nv.depth : -1;
+    const int past_any = p.window > 0 ? P - p.window + nq - 1 : -1;
 
-    // m: running maximum of the scaled scores (base-2 units), the same in both
-    // halves; l: this half's sum of the shifted weights before rounding
+    // m: running maximum of the scaled scores (base-2 units) as of this
+    // group's last tile; l: its sum of the shifted weights before rounding
     float m = -INFINITY, l = 0.f;
-    for (int t = t0; t < t1; ++t, ++j) {
-      const int sb = j & 1;
-      if (!wait_warp(&c->s_full[sb], (uint32_t)(j >> 1) & 1u, c, kSiteSFull)) return false;
+    const uint32_t jl = j + (uint32_t)(t1 - t0) - 1;  // the piece's last tile
+    uint32_t i = j + ((wg ^ j) & 1u);
+#pragma unroll 1
+    for (int t = t0 + (int)(i - j); t < t1; t += 2, i += 2) {
+      if (!wait_warp(&c->s_full[wg], (i >> 1) & 1u, c, kSiteSFull)) return false;
       tc_fence_after();
-      uint32_t u[32];
-      tmem_ld32_sync(tS + sb * kTK, u);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->s_free[sb]);
-
-      const int64_t pos0 = (int64_t)tl.at(t) * kTK + 32 * h;
-      if (pos0 + 32 > P || pos0 <= past_any) {
-        const int rel0 = (int)(pos0 - P);  // > -2^31: positions and lengths fit 32 bits
-        const int gone = (int)max(past - pos0, (int64_t)-1), first = (int)min((int64_t)p.sinks - pos0, (int64_t)32);
-#pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          const int rel = rel0 + q;
-          const bool vis = rel < 0 ? (q > gone || q < first) : (rel < nq && ((nv.mask >> (rel & 63)) & 1ull));
-          if (!vis) u[q] = 0xff800000u;  // -inf
-        }
+      // which of the tile's 64 tokens the row sees, where not all of them
+      const int pos0 = pc.tile(t) * kTK;
+      const bool masked = pos0 > P - kTK || pos0 <= past_any;
+      uint64_t vis = ~0ull;
+      if (masked) {
+        const int rel0 = pos0 - P;
+        vis = low_bits(-rel0) & ~(low_bits(past - pos0 + 1) & ~low_bits(p.sinks - pos0));
+        if (rel0 < 64 && rel0 > -64) vis |= rel0 >= 0 ? nv.mask >> rel0 : nv.mask << -rel0;
       }
-      float mx[4];
+      // Two passes of 32 columns, for the maximum and for the weights: the
+      // scores stay in Tensor Memory in between, which halves the registers
+      // and the code.
+      const uint32_t tS = lane_off + kColS + wg * kTK;
+      float tmax = -INFINITY;
+#pragma unroll 1
+      for (int hc = 0; hc < 2; ++hc) {
+        uint32_t u[32];
+        tmem_ld32_sync(tS + 32 * hc, u);
+        if (masked) mask32(u, (uint32_t)(vis >> (32 * hc)));
+        float mx[2] = {tmax, __uint_as_float(u[31])};
 #pragma unroll
-      for (int v = 0; v < 4; ++v) mx[v] = __uint_as_float(u[v]);
-#pragma unroll
-      for (int q = 4; q < 32; ++q) mx[q & 3] = fmaxf(mx[q & 3], __uint_as_float(u[q]));
-      const float pmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      red_max[((j & 1) * 2 + h) * kRG + r] = pmax;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->xch[j & 1]);
-      if (!wait_warp(&c->xch[j & 1], (uint32_t)(j >> 1) & 1u, c, kSiteXch)) return false;
+        for (int q = 0; q < 30; q += 2)
+          mx[(q >> 1) & 1] = max3(mx[(q >> 1) & 1], __uint_as_float(u[q]), __uint_as_float(u[q + 1]));
+        tmax = max3(mx[0], mx[1], __uint_as_float(u[30]));
+      }
       // the scale is positive: the scaled maximum is the maximum of the scaled scores
-      const float tmax = fmaxf(pmax, red_max[((j & 1) * 2 + (h ^ 1)) * kRG + r]) * sl2;
-      // the maximum moves only when this tile beats it by 2^kLazy
-      float alpha = 1.f;
-      if (tmax > m + kLazy) {
-        alpha = exp2f(m - tmax);  // 0 when m is -inf
-        l *= alpha;
-        m = tmax;
+      tmax *= sl2;
+      // the maximum after the tile before, from the other group (in the first
+      // tile of a piece the wait only keeps the groups in step)
+      float mp = -INFINITY;
+      if (i > 0) {
+        if (!wait_warp(&c->m_ready[wg ^ 1][wq], ((i - 1) >> 1) & 1u, c, kSiteMReady)) return false;
+        if (t > t0) mp = c->m_run[wg ^ 1][r];
+      }
+      // it moves only when this tile beats it by 2^kLazy
+      const float mn = tmax > mp + kLazy ? tmax : mp;
+      c->m_run[wg][r] = mn;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->m_ready[wg][wq]);
+      const float alpha = mn == mp ? 1.f : exp2f(mp - mn);  // 0 when mp is -inf
+      if (mn != m) {
+        l *= exp2f(m - mn);
+        m = mn;
       }
       const float nmu = m == -INFINITY ? 0.f : kWeightShift - m;
 
-      const int pb = j % kPBufs;
-      if (!wait_warp(&c->p_free[pb], ((uint32_t)(j / kPBufs) & 1u) ^ 1u, c, kSitePFree)) return false;
-      uint8_t* pst = smem + kOffP + pb * kPBytes;
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int q8 = 0; q8 < 4; ++q8) {
-        uint32_t wv[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float e0 = ex2_approx(fmaf(__uint_as_float(u[8 * q8 + 2 * v]), sl2, nmu));
-          const float e1 = ex2_approx(fmaf(__uint_as_float(u[8 * q8 + 2 * v + 1]), sl2, nmu));
-          ls[v] += e0 + e1;
-          wv[v] = pack_f16(e0, e1);
+      const uint32_t pb = i % kPBufs;
+      if (!wait_warp(&c->p_free[pb], ((i / kPBufs) & 1u) ^ 1u, c, kSitePFree)) return false;
+      const uint32_t pst = smem_u32(smem) + kOffP + pb * kPBytes + r * 128;
+      uint64_t ls = 0;  // two fp32 sums
+#pragma unroll 1
+      for (int hc = 0; hc < 2; ++hc) {
+        uint32_t u[32];
+        tmem_ld32_sync(tS + 32 * hc, u);
+        if (hc) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c->s_free[wg]);
         }
-        *reinterpret_cast<uint4*>(pst + sw128_offset(r, 32 * h + 8 * q8)) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+        if (masked) mask32(u, (uint32_t)(vis >> (32 * hc)));
+#pragma unroll
+        for (int q8 = 0; q8 < 4; ++q8) {
+          uint32_t wv[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const uint64_t x = fma_f32x2(pair(u[8 * q8 + 2 * v], u[8 * q8 + 2 * v + 1]), sl2x2, pair(nmu, nmu));
+            const float e0 = ex2_approx(lo_f32(x)), e1 = ex2_approx(hi_f32(x));
+            ls = add_f32x2(ls, pair(e0, e1));
+            wv[v] = pack_f16(e0, e1);
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(pst + (((4 * hc + q8) ^ (r & 7)) << 4)),
+                       "r"(wv[0]), "r"(wv[1]), "r"(wv[2]), "r"(wv[3])
+                       : "memory");
+        }
       }
-      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      if (h == 0) c->alpha[pb][r] = alpha;
+      l += lo_f32(ls) + hi_f32(ls);
+      c->alpha[pb][r] = alpha;
       fence_proxy_async_smem();  // read by the copy engine
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->p_staged[pb]);
     }
 
-    if (h == 1) {
-      red_l[r] = l;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->xfin);
-    } else {
-      if (!wait_warp(&c->xfin, (uint32_t)seg & 1u, c, kSiteXch)) return false;
-      l += red_l[r];
-      if (!wait_warp(&c->fin_free, ((uint32_t)seg & 1u) ^ 1u, c, kSiteFinFree)) return false;
-      st_cluster_f32(mapa_shared(smem_u32(&c->lfin[r]), 1), l);
-      st_cluster_f32(mapa_shared(smem_u32(&c->mfin[r]), 1), m);
-      mbar_arrive_cluster(&c->fin_full, 1);
+    // both groups' sums go to the value CTA relative to the final maximum,
+    // which the group of the last tile has
+    if ((jl & 1u) != (uint32_t)wg) {
+      if (!wait_warp(&c->m_ready[wg ^ 1][wq], (jl >> 1) & 1u, c, kSiteMReady)) return false;
+      const float mn = c->m_run[wg ^ 1][r];
+      if (mn != m) l *= exp2f(m - mn);
     }
+    if (!wait_warp(&c->fin_free, (seg & 1u) ^ 1u, c, kSiteFinFree)) return false;
+    st_cluster_f32(mapa_shared(smem_u32(&c->lfin[wg][r]), 1), l);
+    if ((jl & 1u) == (uint32_t)wg) st_cluster_f32(mapa_shared(smem_u32(&c->mfin[r]), 1), m);
+    mbar_arrive_cluster(&c->fin_full, 1);
+    j = jl + 1;
     ++seg;
     return true;
   });
   if (bad) atomicOr(&c->err, MLA_DEVERR_PARENT);
 }
 
-// One thread of the score CTA: ships each tile's weights and factors to the
+// One warp of the score CTA, one thread of it copying: ships each tile's weights and factors to the
 // value CTA, where their bytes complete p_full.
-__device__ void weight_copier(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
-  int j = 0;
-  for_pieces(p, c, cluster, [&](int, int, int, int t0, int t1, const Tiles&) {
-    for (int t = t0; t < t1; ++t, ++j) {
-      const int pb = j % kPBufs;
-      if (!wait(&c->p_staged[pb], (uint32_t)(j / kPBufs) & 1u, c, kSitePStaged)) return false;
+__device__ void weight_copier(uint8_t* smem, Ctl* c) {
+  const bool leader = elect_one();
+  uint32_t j = 0;
+  for_pieces(c, [&](const Piece& pc) {
+    for (int t = pc.t0; t < pc.t1; ++t, ++j) {
+      const uint32_t pb = j % kPBufs;
+      if (!wait_warp(&c->p_staged[pb], (j / kPBufs) & 1u, c, kSitePStaged)) return false;
+      if (!leader) continue;
       const uint32_t bar = mapa_shared(smem_u32(&c->p_full[pb]), 1);
       bulk_copy_s2c(mapa_shared(smem_u32(smem + kOffP + pb * kPBytes), 1), smem + kOffP + pb * kPBytes, kPBytes, bar);
       bulk_copy_s2c(mapa_shared(smem_u32(&c->alpha[pb][0]), 1), &c->alpha[pb][0], kRG * 4, bar);
@@ -621,57 +801,61 @@ __device__ void weight_copier(const Params& p, uint8_t* smem, Ctl* c, int cluste
     }
     return true;
   });
-  bulk_wait_group<0>();
+  if (leader) bulk_wait_group<0>();
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
 // value CTA
 // ---------------------------------------------------------------------------
-__device__ void value_mma(const Params& p, uint8_t* smem, Ctl* c, int cluster) {
-  const uint32_t tO = c->tmem_base;
-  int j = 0;
-  for_pieces(p, c, cluster, [&](int, int, int, int t0, int t1, const Tiles&) {
-    for (int t = t0; t < t1; ++t, ++j) {
-      const int pb = j % kPBufs;
-      if (!wait_warp(&c->o_ready[pb], (uint32_t)(j / kPBufs) & 1u, c, kSiteOReady)) return false;
-      const uint64_t da = smem_desc(smem_u32(smem + kOffP + pb * kPBytes), 16, 1024, kLayoutSw128);
-#pragma unroll
+__device__ void value_mma(uint8_t* smem, Ctl* c) {
+  const bool leader = elect_one();
+  uint32_t j = 0;
+  for_pieces(c, [&](const Piece& pc) {
+#pragma unroll 1
+    for (int t = pc.t0; t < pc.t1; ++t, ++j) {
+      const uint32_t par = j & 1u, pb = j % kPBufs;
+      if (!wait_warp(&c->o_ready[pb], (j / kPBufs) & 1u, c, kSiteOReady)) return false;
+      const uint32_t da = desc_addr(smem, kOffP + pb * kPBytes) | kDescLoK;
+      const uint32_t dv = desc_addr(smem, par * kStageV) | kDescLoV;
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        const int u = 2 * j + h, slot = u % kUnitsV;
-        if (!wait_warp(&c->full[slot], (uint32_t)(u / kUnitsV) & 1u, c, kSiteFullV)) return false;
+        if (!wait_warp(&c->full[2 * par + h], (j >> 1) & 1u, c, kSiteFullV)) return false;
         tc_fence_after();
-        // 64-column chunks 8 KB apart along N, 8-token groups 1 KB apart along K
-        const uint64_t dv = smem_desc(smem_u32(smem + slot * kUnitV), kChunk, 1024, kLayoutSw128);
+        if (leader) {
+          // 8-token groups 1 KB apart along K
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_cta_ss_warp(tO + h * 256, da + (uint64_t)((kk * 32) >> 4), dv + (uint64_t)((kk * 16 * 128) >> 4),
-                          kIdescPV, !(t == t0 && kk == 0));
-        mma_cta_commit_warp(&c->empty[slot]);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_cta_ss(h * 256, desc_at(da + ((kk * 32) >> 4), kDescHiK),
+                       desc_at(dv + ((h * kHalf + kk * 16 * 128) >> 4), kDescHiK), kIdescPV,
+                       (uint32_t)(kk | (t - pc.t0)));
+          mma_cta_commit(&c->empty[2 * par + h]);
+          if (h) {
+            mma_cta_commit(&c->p_free[pb], 0x1);
+            mma_cta_commit(&c->pv_done[pb]);
+          }
+        }
+        __syncwarp();
       }
-      mma_cta_commit_warp(&c->p_free[pb], 0x1);
-      mma_cta_commit_warp(&c->pv_done[pb]);
     }
     return true;
   });
-  if (__any_sync(0xffffffffu, c->abort != 0)) {
-    mma_cta_commit_warp(&c->drain);
-    if ((threadIdx.x & 31) == 0) mbar_wait_drain(&c->drain, 0, kDrainLimitNs);
-    __syncwarp();
-  }
+  drain_mmas(c, leader);
 }
 
 // Row warps of the value CTA (warpgroup h: columns [256 h, 256 h + 256)):
 // rescale O where a factor is not 1, and per piece normalise and store it.
-__device__ void value_rows(const Params& p, Ctl* c, int cluster) {
+__device__ void value_rows(const Params& p, Ctl* c) {
   const int lane = threadIdx.x & 31;
   const int w = (threadIdx.x >> 5) - kWarpRows;
   const int wq = w & 3, h = w >> 2;
   const int r = wq * 32 + lane;
   const int col0 = 256 * h;
-  const uint32_t tO = c->tmem_base + ((uint32_t)(wq * 32) << 16) + (uint32_t)col0;
+  const uint32_t tO = ((uint32_t)(wq * 32) << 16) + (uint32_t)col0;
   int j = 0, seg = 0;
-  for_pieces(p, c, cluster, [&](int slot, int b, int g, int t0, int t1, const Tiles&) {
-    for (int t = t0; t < t1; ++t, ++j) {
+  for_pieces(c, [&](const Piece& pc) {
+    const int slot = pc.slot, b = pc.b, g = pc.g, t0 = pc.t0;
+    for (int t = t0; t < pc.t1; ++t, ++j) {
       const int pb = j % kPBufs;
       if (w == 0 && lane == 0) mbar_arrive_expect_tx(&c->p_full[pb], kPTxBytes);
       if (!wait_warp(&c->p_full[pb], (uint32_t)(j / kPBufs) & 1u, c, kSitePFull)) return false;
@@ -700,7 +884,7 @@ __device__ void value_rows(const Params& p, Ctl* c, int cluster) {
     if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c, kSitePvLast)) return false;
     if (!wait_warp(&c->fin_full, (uint32_t)seg & 1u, c, kSiteFinFull)) return false;
     tc_fence_after();
-    const float l = c->lfin[r], m = c->mfin[r];
+    const float l = c->lfin[0][r] + c->lfin[1][r], m = c->mfin[r];
     mbar_arrive_cluster_relaxed(&c->fin_free, 0);
     ++seg;
     const int row = g * kRG + r;
@@ -764,27 +948,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
   const int cluster = blockIdx.x / 2;
   Ctl* c = reinterpret_cast<Ctl*>(smem + kOffCtl);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kUnitsMax; ++s) {
-      mbar_init(&c->full[s], kProducerWarps);
-      mbar_init(&c->empty[s], 1);
+    for (int q = 0; q < 4; ++q) {
+      mbar_init(&c->full[q], kGroupWarps);
+      mbar_init(&c->empty[q], 1);
+      mbar_init(&c->m_ready[0][q], 1);
+      mbar_init(&c->m_ready[1][q], 1);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&c->s_full[q], 1);
-      mbar_init(&c->s_free[q], kRowWarps);
-      mbar_init(&c->xch[q], kRowWarps);
+      mbar_init(&c->s_free[q], kRowWarps / 2);
     }
     for (int q = 0; q < kPBufs; ++q) {
-      mbar_init(&c->p_staged[q], kRowWarps);
-      mbar_init(&c->o_ready[q], kRowWarps);
-      mbar_init(&c->pv_done[q], 1);
+      mbar_init(&c->p_staged[q], kRowWarps / 2);
       mbar_init(&c->p_free[q], 1);
       mbar_init(&c->p_full[q], 1);
+      mbar_init(&c->pv_done[q], 1);
+      mbar_init(&c->o_ready[q], kRowWarps);
     }
     mbar_init(&c->q_ready, kRowWarps);
     mbar_init(&c->fin_free, 32 * kRowWarps);
-    mbar_init(&c->xfin, kRowWarps / 2);
-    mbar_init(&c->fin_full, kRG);
+    mbar_init(&c->fin_full, 32 * kRowWarps);
     mbar_init(&c->drain, 1);
+    for (int q = 0; q < kPieces; ++q) {
+      mbar_init(&c->piece_full[q], 1);
+      mbar_init(&c->piece_empty[q], kFollowers + (rank == 0 ? 1 : 0));
+    }
     c->abort = 0;
     c->abort_site = 0;
     c->start_b = p.B;
@@ -816,17 +1004,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
   cluster_sync();  // barriers of both CTAs initialised before any remote use
   tc_fence_after();
 
+  const bool base0 = c->tmem_base == 0;  // all columns are allocated
+  if (!base0 && threadIdx.x == 0) c->err = MLA_DEVERR_LAYOUT;
   if (warp < kProducerWarps) {
-    if (rank == 0) producer<true>(p, smem, c, warp, cluster);
-    else producer<false>(p, smem, c, warp, cluster);
-  } else if (warp == kWarpMma) {
-    if (rank == 0) score_mma(p, smem, c, cluster);
-    else value_mma(p, smem, c, cluster);
-  } else if (warp == kWarpAux) {
-    if (rank == 0 && (threadIdx.x & 31) == 0) weight_copier(p, smem, c, cluster);
+    if (!base0) {
+    } else if (rank == 0) {
+      producer<true>(p, smem, c, warp);
+    } else {
+      producer<false>(p, smem, c, warp);
+    }
+  } else if (warp < kWarpRows + kRowWarps) {
+    if (!base0) {
+    } else if (rank == 0) {
+      score_softmax(p, smem, c, warp);
+    } else {
+      value_rows(p, c);
+    }
   } else {
-    if (rank == 0) score_softmax(p, smem, c, cluster);
-    else value_rows(p, c, cluster);
+    if (!base0) {
+    } else if (warp == kWarpMma) {
+      if (rank == 0) score_mma(smem, c);
+      else value_mma(smem, c);
+    } else if (warp == kWarpAux) {
+      if (rank == 0) weight_copier(smem, c);
+    } else if (warp == kWarpSched) {
+      schedule(p, c, cluster);
+    }
   }
 
   __syncwarp();
