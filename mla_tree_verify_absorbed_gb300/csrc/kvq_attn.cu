@@ -10,8 +10,8 @@
 //
 // Two CTAs per work item.  An fp32 accumulator for 128 x 512 fills one SM's
 // Tensor Memory, so S and O live in different SMs of a cluster:
-//   rank 0, scores: queries in Tensor Memory (288 columns, the A operand), two
-//           S tiles (128 columns); converts the whole tile (64 tokens x 576) to
+//   rank 0, scores: queries in Tensor Memory (288 columns, the A operand), three
+//           S tiles (192 columns); converts the whole tile (64 tokens x 576) to
 //           bf16; softmax in registers, two threads per row;
 //   rank 1, values: O (512 columns); converts the same tile's latents to f16.
 // The weights and the rows' rescale factors go from rank 0 to rank 1 by a bulk
@@ -22,12 +22,11 @@
 // read (about 1,400 cycles at 128 B/clk, against 1,152 of MMA); rank 1 the same
 // with 64 KB of V, the weights read twice.
 //
-// Conversion.  8 producer warps per CTA, a lane per (token, 64-element chunk):
-// one 32-byte sector of codes and 4 scales make the 128 bytes of one operand
-// row in one chunk.  The 8 lanes of a quarter warp hold 8 different tokens, so
+// Conversion.  8 producer warps per CTA, in each a lane per (token, 64-element
+// chunk): 32 bytes of codes and 4 scales make the 128 bytes of one operand row
+// in one chunk.  The 8 lanes of a quarter warp hold 8 different tokens, so
 // their 16-byte stores fall into 8 different bank groups of the 128-byte
-// swizzle.  The next tile's rows are in flight while a tile is converted, the
-// slots of the one after that too.
+// swizzle.
 //
 // Work split.  Row group g of sequence b costs T_b + kFixed units (T_b tiles).
 // The units of all row groups, in order, are cut into equal intervals, one per
@@ -80,14 +79,23 @@ constexpr int kStageS = 9 * kChunk;           // score CTA: 72 KB per tile
 constexpr int kStageV = 8 * kChunk;           // value CTA: 64 KB
 constexpr int kHalf = 4 * kChunk;
 constexpr int kPBytes = kRG * 128;            // weights of a tile, f16
-constexpr int kPBufs = 4;
-constexpr int kOffP = 2 * kStageS;            // weights: staged at this offset in rank 0, copied to it in rank 1
-constexpr int kOffCtl = kOffP + kPBufs * kPBytes;
+constexpr int kPBufs = 3;                     // value CTA: weights landed
+constexpr int kPStages = 2;                   // score CTA: weights staged
+constexpr int kRawRow = 336;                  // 256 bytes of codes, two buffers of 32 bytes of scales
+constexpr int kRawWarp = 16 * kRawRow;        // a producer warp's 16 tokens
+// Offsets: stages first in both CTAs, then the score CTA's staged weights or
+// the value CTA's landed ones, then the raw rows.
+constexpr int kOffPS = 2 * kStageS, kOffPV = 2 * kStageV;
+constexpr int kOffRaw = kOffPS + kPStages * kPBytes > kOffPV + kPBufs * kPBytes ? kOffPS + kPStages * kPBytes
+                                                                                : kOffPV + kPBufs * kPBytes;
+constexpr int kOffCtl = kOffRaw + kProducerWarps * kRawWarp;
 constexpr uint32_t kPTxBytes = kPBytes + kRG * 4;        // weights + rescale factors
 
-// Tensor Memory columns: score CTA, two S tiles and the queries (bf16 pairs);
+// Tensor Memory columns: score CTA, three S tiles and the queries (bf16 pairs);
 // value CTA, O from column 0
-constexpr uint32_t kColS = 0, kColQ = 2 * kTK;
+constexpr int kSBufs = 3;
+constexpr uint32_t kColS = 0, kColQ = kSBufs * kTK;
+static_assert(kColQ + kDk / 2 <= kTmemCols, "Tensor Memory columns");
 // upper halves of the operand descriptors (smem_desc): only the start address,
 // in the lower half, differs from MMA to MMA
 constexpr uint32_t kDescHiK = (1024u >> 4) | (1u << 14) | (kLayoutSw128 << 29);
@@ -138,13 +146,14 @@ constexpr int kPieces = 4;
 struct alignas(16) Ctl {
   uint64_t full[4];            // half tile converted (8 producer warps); index 2 (j % 2) + half
   uint64_t empty[4];           // the MMAs reading it are complete
-  uint64_t s_full[2];          // score: S tile in TMEM
-  uint64_t s_free[2];          // score: softmax has loaded S (4 row warps)
+  uint64_t s_full[kSBufs];     // score: S tile in TMEM
+  uint64_t s_free[kSBufs];         // score: softmax has loaded S (4 row warps)
   uint64_t q_ready;            // score: queries in TMEM (8 row warps)
   uint64_t m_ready[2][4];      // score: running maxima after a tile written (per lane quadrant, 1 warp)
-  uint64_t p_free[kPBufs];     // score: the PV MMAs that read this buffer are complete (rank 1's commit)
+  uint64_t p_free[kPBufs];     // score: the PV MMAs that read rank 1's buffer are complete (its commit)
+  uint64_t ps_free[kPStages];  // score: the staged weights have landed in rank 1 (its first row warp)
   uint64_t fin_free;           // score: rank 1 consumed lfin / mfin (256 arrivals)
-  uint64_t p_staged[kPBufs];   // score: weights and factors staged (4 row warps)
+  uint64_t p_staged[kPStages]; // score: weights and factors staged (4 row warps)
   uint64_t p_full[kPBufs];     // value: weights and factors landed (copy bytes)
   uint64_t pv_done[kPBufs];    // value: PV MMAs of a tile complete
   uint64_t o_ready[kPBufs];    // value: O rescaled, weights in (8 row warps)
@@ -153,7 +162,7 @@ struct alignas(16) Ctl {
   uint64_t piece_full[kPieces];   // piece written (scheduler warp)
   uint64_t piece_empty[kPieces];  // read by every warp of this CTA that follows the pieces
   Piece piece[kPieces];
-  alignas(16) float alpha[kPBufs][kRG];  // staged in rank 0, copied to rank 1
+  alignas(16) float alpha[kPBufs][kRG];  // rescale factors: staged in rank 0 ([kPStages]), landed in rank 1
   float m_run[2][kRG];         // score: running maxima after the last tile of each parity
   float lfin[2][kRG];          // value: each group's row sums of the shifted weights
   float mfin[kRG];             // value: row maxima, base-2 units
@@ -167,16 +176,15 @@ struct alignas(16) Ctl {
   uint32_t err;
 };
 constexpr int kSmemBytes = kOffCtl + (int)sizeof(Ctl);
-constexpr int kSmemAlloc = 232448;  // the per-CTA maximum
-static_assert(kSmemBytes <= kSmemAlloc, "shared memory budget");
+constexpr int kSmemAlloc = (kSmemBytes + 1023) & ~1023;
+static_assert(kSmemAlloc <= 232448, "shared memory budget");
 static_assert(offsetof(Ctl, alpha) % 16 == 0 && kOffCtl % 16 == 0, "bulk-copy alignment");
-static_assert(kOffP % 1024 == 0 && kStageS % 1024 == 0, "swizzle atoms");
-static_assert(kStageV <= kStageS, "value stages reach into the weights");
+static_assert(kOffPS % 1024 == 0 && kOffPV % 1024 == 0 && kStageS % 1024 == 0, "swizzle atoms");
 
 enum {
   kSiteEmpty = 1, kSiteQReady, kSiteFullS, kSiteSFree, kSiteSFull, kSitePFree, kSiteFinFree, kSiteFullV,
   kSiteOReady, kSitePFull, kSitePvPrev, kSitePvLast, kSiteFinFull, kSiteMReady, kSitePStaged, kSitePiece,
-  kSitePieceFree
+  kSitePieceFree, kSitePsFree
 };
 
 __device__ __noinline__ void raise_abort(Ctl* c, int site) {
@@ -211,12 +219,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void ld_global_v8(const void* ptr, uint32_t (&v)[8]) {
-  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-      : "l"(ptr));
-}
-
 // ---------------------------------------------------------------------------
 // work split
 // ---------------------------------------------------------------------------
@@ -392,8 +394,7 @@ __device__ int make_split(const Params& p, Ctl* c, int cluster) {
 // ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
-// Converts one sector of codes with its 4 scales into the 8 pieces of an
-// operand row.
+// Converts 64 codes with their 4 scales into the 8 pieces of an operand row.
 template <class To>
 __device__ __forceinline__ void convert_chunk(const uint32_t (&code)[8], uint32_t scale, uint32_t dst, int r7) {
 #pragma unroll
@@ -415,48 +416,33 @@ __device__ __forceinline__ void convert_chunk(const uint32_t (&code)[8], uint32_
     }
   }
 }
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 // One warp of producer group `grp`: tokens 16 pw .. + 15 of the tiles of that
-// parity, as two sets of 8; lane l holds token l & 7 of a set, chunk l >> 3 of
-// a half tile and, with the second half, two 16-byte pieces of the rope key.
-// When a set's registers have been converted, the sector that the set needs
-// next is loaded into them: it is in flight while the other set is converted.
-// The table entries of the tile after that (a lane per token) are in flight
-// for a whole tile.
-template <bool kScore>
-struct Sector {
-  uint32_t code[8];
-  uint32_t scale;
-  uint4 rope[kScore ? 2 : 1];
-  __device__ __forceinline__ void load(const uint8_t* row, int h, int ch) {
-    ld_global_v8(row + 128 * h + 32 * ch, code);
-    scale = __ldg(reinterpret_cast<const uint32_t*>(row + kScaleOff) + 4 * h + ch);
-    if (kScore && h) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) rope[q] = __ldg(reinterpret_cast<const uint4*>(row + kRopeOff) + 4 * q + ch);
-    }
-  }
-  // dst: shared address of the token's row in the half's chunk ch; rope_dst:
-  // of its row in the rope chunk
-  __device__ __forceinline__ void store(uint32_t dst, uint32_t rope_dst, int h, int ch, int r7) const {
-    convert_chunk<typename std::conditional<kScore, ToBf16, ToF16>::type>(code, scale, dst, r7);
-    if (kScore && h) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rope_dst + (((4 * q + ch) ^ r7) << 4)),
-                     "r"(rope[q].x), "r"(rope[q].y), "r"(rope[q].z), "r"(rope[q].w)
-                     : "memory");
-    }
-  }
-};
-
+// parity.  The packed rows (codes and scales, 288 bytes) come by cp.async into
+// 16 rows of shared memory that the warp has to itself; a half tile's codes are
+// fetched as soon as the tile before has been converted that far, so they have
+// about two tile periods to arrive.  (Loads into registers pass through the
+// small L1 that this much shared memory leaves, and its lines, not the latency,
+// then limited the bytes in flight.)  The rope keys need no conversion and go
+// straight to their place in the stage.  Rows 336 bytes apart put the 8 tokens
+// that a quarter warp reads at once into different banks.
 template <bool kScore>
 __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c, int warp) {
+  using To = typename std::conditional<kScore, ToBf16, ToF16>::type;
   const int lane = threadIdx.x & 31;
   const int grp = warp / kGroupWarps, pw = warp % kGroupWarps;
   const int r7 = lane & 7, ch = lane >> 3;
-  const int r = 16 * pw + r7;  // token row of set 0 within the tile
-  const uint32_t stage = smem_u32(smem) + grp * (kScore ? kStageS : kStageV) + r * 128;
+  const int r = 16 * pw + r7;  // token row of the first set of 8 within the tile
+  const uint32_t stage = smem_u32(smem) + grp * (kScore ? kStageS : kStageV);
+  const uint32_t raw = smem_u32(smem) + kOffRaw + warp * kRawWarp;
   uint32_t err = 0;
   uint32_t j = 0;
   for_pieces(c, [&](const Piece& pc) {
@@ -467,7 +453,7 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
     // Pool row of token 16 pw + (lane & 15) of tile v, in two steps: the table
     // entry (a slot, or a page; -2 where no node sees the position), and, a
-    // tile later, the row.  Positions that no node sees read slot 0, under a
+    // tile later, the slot.  Positions that no node sees read slot 0, under a
     // weight of zero.
     auto entry_of = [&](int v) -> int32_t {
       const int pos = pc.tile(v) * kTK + 16 * pw + (lane & 15);
@@ -486,35 +472,73 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
       }
       return (uint32_t)s;
     };
-    auto row_of = [&](uint32_t slot, int set) {
-      return p.cache + (uint64_t)__shfl_sync(0xffffffffu, slot, 8 * set + r7) * (uint32_t)p.row_stride;
+    auto row_of = [&](uint32_t slot, int token) {
+      return p.cache + (uint64_t)__shfl_sync(0xffffffffu, slot, token) * (uint32_t)p.row_stride;
     };
-    uint32_t slot = slot_of(entry_of(t), t);
-    Sector<kScore> a, b;
-    a.load(row_of(slot, 0), 0, ch);
-    b.load(row_of(slot, 1), 0, ch);
+    // 16-byte piece lane & 7 of tokens lane >> 3, + 4, + 8, + 12 of half h, and
+    // with the first half all scales, into the buffer of this turn's parity.
+    // Past the piece's last tile nothing is fetched: what the next piece
+    // fetches first must not race with it.
+    auto fetch = [&](uint32_t slot, int h, uint32_t turn, bool more) {
+#pragma unroll
+      for (int i = 0; more && i < 4; ++i) {
+        const int token = 4 * i + ch;
+        cp_async_16(raw + token * kRawRow + 128 * h + 16 * r7, row_of(slot, token) + 128 * h + 16 * r7);
+      }
+      const int token = lane >> 1;
+      const uint8_t* row = row_of(slot, token);
+      if (more && h == 0)
+        cp_async_16(raw + token * kRawRow + kScaleOff + 32 * (turn & 1u) + 16 * (lane & 1),
+                    row + kScaleOff + 16 * (lane & 1));
+      cp_async_commit();
+    };
+    uint32_t slot = slot_of(entry_of(t), t), slot_next = 0;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) fetch(slot, h, turn, true);
     int32_t ent = entry_of(t + 2);
 #pragma unroll 1
     for (int h = 0; t < pc.t1; h ^= 1) {
+      cp_async_wait_group<1>();  // this half's pieces, of this lane
+      __syncwarp();              // of every lane
       const uint32_t full = 2 * grp + h;
       if (!wait_warp(&c->empty[full], (turn & 1u) ^ 1u, c, kSiteEmpty)) return false;
-      const uint32_t dst = stage + h * kHalf + ch * kChunk, rope_dst = stage + 8 * kChunk;
-      if (h) {  // what follows this half is the next tile's first
-        t += 2;
-        ++turn;
-        slot = slot_of(ent, t);
-        ent = entry_of(t + 2);
+      if (kScore && h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int token = 4 * i + ch, row = 16 * pw + token;
+          cp_async_16(stage + 8 * kChunk + row * 128 + ((r7 ^ (row & 7)) << 4),
+                      row_of(slot, token) + kRopeOff + 16 * r7);
+        }
+        cp_async_mbar_arrive(&c->full[full]);  // when they have landed
       }
-      a.store(dst, rope_dst, h, ch, r7);
-      a.load(row_of(slot, 0), h ^ 1, ch);
-      b.store(dst + 8 * 128, rope_dst + 8 * 128, h, ch, r7);
-      b.load(row_of(slot, 1), h ^ 1, ch);
+      uint32_t src = raw + r7 * kRawRow, dst = stage + h * kHalf + ch * kChunk + r * 128;
+#pragma unroll 1
+      for (int s = 0; s < 2; ++s) {
+        uint32_t code[8];
+        ld_shared_v4(src + 128 * h + 32 * ch, code[0], code[1], code[2], code[3]);
+        ld_shared_v4(src + 128 * h + 32 * ch + 16, code[4], code[5], code[6], code[7]);
+        convert_chunk<To>(code, ld_shared(src + kScaleOff + 32 * (turn & 1u) + 16 * h + 4 * ch), dst, r7);
+        src += 8 * kRawRow;
+        dst += 8 * 128;
+      }
       fence_proxy_async_smem();  // generic stores, read by the MMA
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->full[full]);
+      // the next tile's half into the place of this one
+      if (h == 0) {
+        slot_next = slot_of(ent, t + 2);
+        ent = entry_of(t + 4);
+        fetch(slot_next, 0, turn + 1, t + 2 < pc.t1);
+      } else {
+        t += 2;
+        ++turn;
+        slot = slot_next;
+        fetch(slot, 1, turn, t < pc.t1);
+      }
     }
     return true;
   });
+  cp_async_wait_all();
   if (err) atomicOr(&c->err, err);
 }
 
@@ -533,8 +557,8 @@ __device__ void drain_mmas(Ctl* c, bool leader) {
 // score CTA
 // ---------------------------------------------------------------------------
 // Tensor Memory addresses are constants here (all 512 columns are allocated, so
-// the base is 0).  Three chunks' MMAs per iteration keep the loop short and the
-// tensor pipe fed (9 MMAs of 32 cycles are queued while the next are prepared).
+// the base is 0).  A tile's 36 MMAs of 32 cycles are issued straight: in a loop
+// of four per iteration the one issuing thread took 75 cycles for each.
 __device__ void score_mma(uint8_t* smem, Ctl* c) {
   const bool leader = elect_one();
   uint32_t j = 0, seg = 0;
@@ -542,25 +566,23 @@ __device__ void score_mma(uint8_t* smem, Ctl* c) {
     if (!wait_warp(&c->q_ready, seg & 1u, c, kSiteQReady)) return false;
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
-      const uint32_t par = j & 1u, turn = j >> 1;
-      if (turn >= 1 && !wait_warp(&c->s_free[par], (turn & 1u) ^ 1u, c, kSiteSFree)) return false;
-      uint32_t lo = desc_addr(smem, par * kStageS) | kDescLoK;
-      uint32_t tq = kColQ;
-#pragma unroll 1
+      const uint32_t par = j & 1u, turn = j >> 1, sb = j % kSBufs;
+      if (!wait_warp(&c->s_free[sb], ((j / kSBufs) & 1u) ^ 1u, c, kSiteSFree)) return false;
+      const uint32_t lo = desc_addr(smem, par * kStageS) | kDescLoK;
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!wait_warp(&c->full[2 * par + h], turn & 1u, c, kSiteFullS)) return false;
+        if (h) fence_proxy_async_smem();  // the rope keys came by cp.async, without a fence of their writers
         tc_fence_after();
         if (leader) {
-#pragma unroll 1
-          for (int kc = 0; kc < 4 + h; ++kc) {
+#pragma unroll 2
+          for (int kc = 4 * h; kc < (h ? 9 : 4); ++kc) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_cta_ts(kColS + par * kTK, tq + kk * 8, desc_at(lo + ((kk * 32) >> 4), kDescHiK), kIdescS,
-                         (uint32_t)(h | kc | kk));
-            lo += kChunk >> 4;
-            tq += 32;
+              mma_cta_ts(kColS + sb * kTK, kColQ + kc * 32 + kk * 8,
+                         desc_at(lo + ((kc * kChunk + kk * 32) >> 4), kDescHiK), kIdescS, (kc | kk) != 0);
           }
-          if (h) mma_cta_commit(&c->s_full[par]);
+          if (h) mma_cta_commit(&c->s_full[sb]);
           mma_cta_commit(&c->empty[2 * par + h]);
         }
         __syncwarp();
@@ -682,7 +704,8 @@ __device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) 
     uint32_t i = j + ((wg ^ j) & 1u);
 #pragma unroll 1
     for (int t = t0 + (int)(i - j); t < t1; t += 2, i += 2) {
-      if (!wait_warp(&c->s_full[wg], (i >> 1) & 1u, c, kSiteSFull)) return false;
+      const uint32_t sb = i % kSBufs;
+      if (!wait_warp(&c->s_full[sb], (i / kSBufs) & 1u, c, kSiteSFull)) return false;
       tc_fence_after();
       // which of the tile's 64 tokens the row sees, where not all of them
       const int pos0 = pc.tile(t) * kTK;
@@ -696,7 +719,7 @@ __device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) 
       // Two passes of 32 columns, for the maximum and for the weights: the
       // scores stay in Tensor Memory in between, which halves the registers
       // and the code.
-      const uint32_t tS = lane_off + kColS + wg * kTK;
+      const uint32_t tS = lane_off + kColS + sb * kTK;
       float tmax = -INFINITY;
 #pragma unroll 1
       for (int hc = 0; hc < 2; ++hc) {
@@ -730,9 +753,9 @@ __device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) 
       }
       const float nmu = m == -INFINITY ? 0.f : kWeightShift - m;
 
-      const uint32_t pb = i % kPBufs;
-      if (!wait_warp(&c->p_free[pb], ((i / kPBufs) & 1u) ^ 1u, c, kSitePFree)) return false;
-      const uint32_t pst = smem_u32(smem) + kOffP + pb * kPBytes + r * 128;
+      const uint32_t ps = i % kPStages;
+      if (!wait_warp(&c->ps_free[ps], ((i / kPStages) & 1u) ^ 1u, c, kSitePsFree)) return false;
+      const uint32_t pst = smem_u32(smem) + kOffPS + ps * kPBytes + r * 128;
       uint64_t ls = 0;  // two fp32 sums
 #pragma unroll 1
       for (int hc = 0; hc < 2; ++hc) {
@@ -741,7 +764,7 @@ __device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) 
         if (hc) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&c->s_free[wg]);
+          if (lane == 0) mbar_arrive(&c->s_free[sb]);
         }
         if (masked) mask32(u, (uint32_t)(vis >> (32 * hc)));
 #pragma unroll
@@ -760,10 +783,10 @@ __device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) 
         }
       }
       l += lo_f32(ls) + hi_f32(ls);
-      c->alpha[pb][r] = alpha;
+      c->alpha[ps][r] = alpha;
       fence_proxy_async_smem();  // read by the copy engine
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c->p_staged[pb]);
+      if (lane == 0) mbar_arrive(&c->p_staged[ps]);
     }
 
     // both groups' sums go to the value CTA relative to the final maximum,
@@ -791,18 +814,19 @@ __device__ void weight_copier(uint8_t* smem, Ctl* c) {
   uint32_t j = 0;
   for_pieces(c, [&](const Piece& pc) {
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
-      const uint32_t pb = j % kPBufs;
-      if (!wait_warp(&c->p_staged[pb], (j / kPBufs) & 1u, c, kSitePStaged)) return false;
-      if (!leader) continue;
-      const uint32_t bar = mapa_shared(smem_u32(&c->p_full[pb]), 1);
-      bulk_copy_s2c(mapa_shared(smem_u32(smem + kOffP + pb * kPBytes), 1), smem + kOffP + pb * kPBytes, kPBytes, bar);
-      bulk_copy_s2c(mapa_shared(smem_u32(&c->alpha[pb][0]), 1), &c->alpha[pb][0], kRG * 4, bar);
-      bulk_commit_group();
+      const uint32_t ps = j % kPStages, pb = j % kPBufs;
+      if (!wait_warp(&c->p_staged[ps], (j / kPStages) & 1u, c, kSitePStaged)) return false;
+      if (!wait_warp(&c->p_free[pb], ((j / kPBufs) & 1u) ^ 1u, c, kSitePFree)) return false;
+      if (leader) {
+        const uint32_t bar = mapa_shared(smem_u32(&c->p_full[pb]), 1);
+        bulk_copy_s2c(mapa_shared(smem_u32(smem + kOffPV + pb * kPBytes), 1), smem + kOffPS + ps * kPBytes, kPBytes,
+                      bar);
+        bulk_copy_s2c(mapa_shared(smem_u32(&c->alpha[pb][0]), 1), &c->alpha[ps][0], kRG * 4, bar);
+      }
+      __syncwarp();
     }
     return true;
   });
-  if (leader) bulk_wait_group<0>();
-  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -816,7 +840,7 @@ __device__ void value_mma(uint8_t* smem, Ctl* c) {
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
       const uint32_t par = j & 1u, pb = j % kPBufs;
       if (!wait_warp(&c->o_ready[pb], (j / kPBufs) & 1u, c, kSiteOReady)) return false;
-      const uint32_t da = desc_addr(smem, kOffP + pb * kPBytes) | kDescLoK;
+      const uint32_t da = desc_addr(smem, kOffPV + pb * kPBytes) | kDescLoK;
       const uint32_t dv = desc_addr(smem, par * kStageV) | kDescLoV;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -859,6 +883,7 @@ __device__ void value_rows(const Params& p, Ctl* c) {
       const int pb = j % kPBufs;
       if (w == 0 && lane == 0) mbar_arrive_expect_tx(&c->p_full[pb], kPTxBytes);
       if (!wait_warp(&c->p_full[pb], (uint32_t)(j / kPBufs) & 1u, c, kSitePFull)) return false;
+      if (w == 0 && lane == 0) mbar_arrive_cluster_relaxed(&c->ps_free[j % kPStages], 0);
       if (t != t0) {
         const float a = c->alpha[pb][r];
         if (__any_sync(0xffffffffu, a != 1.f)) {
@@ -949,21 +974,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
   Ctl* c = reinterpret_cast<Ctl*>(smem + kOffCtl);
   if (threadIdx.x == 0) {
     for (int q = 0; q < 4; ++q) {
-      mbar_init(&c->full[q], kGroupWarps);
+      // the score CTA's second halves wait for every lane's rope copies too
+      mbar_init(&c->full[q], kGroupWarps + (rank == 0 && (q & 1) ? 32 * kGroupWarps : 0));
       mbar_init(&c->empty[q], 1);
       mbar_init(&c->m_ready[0][q], 1);
       mbar_init(&c->m_ready[1][q], 1);
     }
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < kSBufs; ++q) {
       mbar_init(&c->s_full[q], 1);
       mbar_init(&c->s_free[q], kRowWarps / 2);
     }
     for (int q = 0; q < kPBufs; ++q) {
-      mbar_init(&c->p_staged[q], kRowWarps / 2);
       mbar_init(&c->p_free[q], 1);
       mbar_init(&c->p_full[q], 1);
       mbar_init(&c->pv_done[q], 1);
       mbar_init(&c->o_ready[q], kRowWarps);
+    }
+    for (int q = 0; q < kPStages; ++q) {
+      mbar_init(&c->p_staged[q], kRowWarps / 2);
+      mbar_init(&c->ps_free[q], 1);
     }
     mbar_init(&c->q_ready, kRowWarps);
     mbar_init(&c->fin_free, 32 * kRowWarps);
