@@ -126,6 +126,7 @@ struct Params {
   void* out;
   float* lse;
   int groups;                  // row groups per sequence
+  int box_rows;                // rows of a query copy: those of a row group, or of a sequence that has fewer
   int clusters;                // clusters launched
   // workspace
   uint32_t* err;               // word 0, and the error words from kErrFirst on
@@ -139,10 +140,14 @@ struct Params {
 // all reads stay in kv_indices[0 .. kv_indptr[B]).
 __device__ __forceinline__ uint32_t check_sequence(const Params& p, int b) {
   const int64_t P = p.prefix_lens[b];
+  int64_t lo = 0, hi = 0;
+  if (p.page_size == 1) {
+    lo = p.kv_indptr[b];
+    hi = p.kv_indptr[b + 1];
+  }
   uint32_t e = P < -1 ? MLA_DEVERR_PREFIX : 0u;
   const int64_t N = P < 0 ? 0 : P + p.Q;
   if (p.page_size == 1) {
-    const int64_t lo = p.kv_indptr[b], hi = p.kv_indptr[b + 1];
     if ((b == 0 && lo != 0) || lo < 0 || hi - lo != N) e |= MLA_DEVERR_INDPTR;
   } else if (N > (int64_t)p.max_pages * p.page_size) {
     e |= MLA_DEVERR_PAGES;

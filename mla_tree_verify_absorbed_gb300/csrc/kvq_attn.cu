@@ -43,6 +43,8 @@
 //
 // Every wait is bounded (2 s); on timeout both CTAs stop issuing, drain what
 // they issued, free their Tensor Memory and report MLA_DEVERR_TIMEOUT.
+#include <cuda.h>
+
 #include <cmath>
 #include <mutex>
 
@@ -54,6 +56,12 @@ namespace kvq {
 using namespace sm100;
 
 mla_status validate_cache(const mla_kvq_cache* c);
+
+// Tensor maps of the queries, [B Q H] rows of 512 and of 64, in boxes of 64
+// elements x Params::box_rows rows.
+struct QueryMaps {
+  CUtensorMap lat, pe;
+};
 
 constexpr int kRG = 128;       // query rows per work item
 constexpr int kTK = 64;        // tokens per tile
@@ -82,7 +90,8 @@ constexpr int kPBytes = kRG * 128;            // weights of a tile, f16
 constexpr int kPBufs = 3;                     // value CTA: weights landed
 constexpr int kPStages = 2;                   // score CTA: weights staged
 constexpr int kRawRow = 336;                  // 256 bytes of codes, two buffers of 32 bytes of scales
-constexpr int kRawWarp = 16 * kRawRow;        // a producer warp's 16 tokens
+constexpr int kTok = kTK / kGroupWarps;       // tokens of a producer warp
+constexpr int kRawWarp = kTok * kRawRow;
 // Offsets: stages first in both CTAs, then the score CTA's staged weights or
 // the value CTA's landed ones, then the raw rows.
 constexpr int kOffPS = 2 * kStageS, kOffPV = 2 * kStageV;
@@ -148,7 +157,8 @@ struct alignas(16) Ctl {
   uint64_t empty[4];           // the MMAs reading it are complete
   uint64_t s_full[kSBufs];     // score: S tile in TMEM
   uint64_t s_free[kSBufs];         // score: softmax has loaded S (4 row warps)
-  uint64_t q_ready;            // score: queries in TMEM (8 row warps)
+  uint64_t q_ready;            // score: queries in TMEM, stages free again (8 row warps)
+  uint64_t q_in;               // score: queries copied (copy bytes)
   uint64_t m_ready[2][4];      // score: running maxima after a tile written (per lane quadrant, 1 warp)
   uint64_t p_free[kPBufs];     // score: the PV MMAs that read rank 1's buffer are complete (its commit)
   uint64_t ps_free[kPStages];  // score: the staged weights have landed in rank 1 (its first row warp)
@@ -167,9 +177,9 @@ struct alignas(16) Ctl {
   float lfin[2][kRG];          // value: each group's row sums of the shifted weights
   float mfin[kRG];             // value: row maxima, base-2 units
   int64_t scan[kThreads / 32];
-  int64_t total;               // units of the whole call
+  int64_t left;                // units of this cluster's interval
   int64_t start_x;             // this cluster's first unit within sequence start_b
-  int start_b;
+  int start_b, start_T;        // that sequence, and its tiles
   uint32_t tmem_base;
   int abort;
   int abort_site;
@@ -184,7 +194,7 @@ static_assert(kOffPS % 1024 == 0 && kOffPV % 1024 == 0 && kStageS % 1024 == 0, "
 enum {
   kSiteEmpty = 1, kSiteQReady, kSiteFullS, kSiteSFree, kSiteSFull, kSitePFree, kSiteFinFree, kSiteFullV,
   kSiteOReady, kSitePFull, kSitePvPrev, kSitePvLast, kSiteFinFull, kSiteMReady, kSitePStaged, kSitePiece,
-  kSitePieceFree, kSitePsFree
+  kSitePieceFree, kSitePsFree, kSiteQIn
 };
 
 __device__ __noinline__ void raise_abort(Ctl* c, int site) {
@@ -255,18 +265,26 @@ __device__ __forceinline__ int cut_tile(int64_t z, int T) {
   return z > kFixed + T - kSnap ? T : (int)(z - kFixed);
 }
 
+// a / b for a >= 0, b > 0: a 32-bit division wherever it will do.
+__device__ __noinline__ int64_t div_long(int64_t a, int b) { return a / b; }
+__device__ __forceinline__ int64_t div_fast(int64_t a, int b) {
+  return a >> 32 ? div_long(a, b) : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // Clusters that share `total` units.
 __device__ __forceinline__ int active_clusters(const Params& p, int64_t total) {
-  const int64_t n = total / (kFixed + kMinTiles);
+  const int64_t n = div_fast(total, kFixed + kMinTiles);
   return (int)(n < 1 ? 1 : n > p.clusters ? p.clusters : n);
 }
-__device__ __forceinline__ int64_t first_unit(int64_t total, int n, int k) { return total * k / n; }
+__device__ __forceinline__ int64_t first_unit(int64_t total, int n, int k) { return div_fast(total * k, n); }
 
-// Where a cluster's interval begins: sequence b and unit x of its
-// groups * (kFixed + T) units, for the merging kernel.
-struct Start {
-  int32_t b, x_lo, x_hi, n;  // n: clusters that share the call (0: nothing to merge)
-  __device__ __forceinline__ int64_t x() const { return (int64_t)(uint32_t)x_lo | (int64_t)x_hi << 32; }
+// Where a cluster's interval begins: unit x of the groups * (kFixed + T) units
+// of sequence b, for the merging kernel.
+struct alignas(16) Start {
+  int64_t x;
+  int32_t b, T;
+  int32_t n;  // clusters that share the call (0: nothing to merge)
+  int32_t pad[3];
 };
 
 // Scheduler warp of each CTA: writes this cluster's pieces in order, then an
@@ -275,8 +293,7 @@ struct Start {
 // last, so two partial slots are enough.
 __device__ void schedule(const Params& p, Ctl* c, int cluster) {
   const int lane = threadIdx.x & 31;
-  const int n = active_clusters(p, c->total);
-  int64_t left = first_unit(c->total, n, cluster + 1) - first_unit(c->total, n, cluster);
+  int64_t left = c->left;
   int64_t x = c->start_x;
   uint32_t seg = 0;
   auto put = [&](const Piece& pc) {
@@ -302,7 +319,7 @@ __device__ void schedule(const Params& p, Ctl* c, int cluster) {
     pc.P = p.prefix_lens[b];
     pc.N = (int32_t)((int64_t)pc.P + p.Q);
     pc.entry = p.page_size == 1 ? (int64_t)p.kv_indptr[b] : (int64_t)b * p.max_pages;
-    for (int g = (int)(x / L); g < p.groups && left > 0; ++g) {
+    for (int g = (int)div_fast(x, L); g < p.groups && left > 0; ++g) {
       const int64_t z = x - (int64_t)g * L;
       const int64_t take = L - z < left ? L - z : left;
       pc.g = g;
@@ -340,45 +357,50 @@ constexpr int kFollowers = kProducerWarps + kRowWarps + 1;
 
 // Block-wide: validates every sequence, sums the units and finds where this
 // cluster's interval begins.  Returns the clusters that share the call, 0 when
-// a table is bad.  Threads take consecutive sequences.
+// a table is bad, -1 when every sequence is unused.  Threads take consecutive
+// sequences.
 __device__ int make_split(const Params& p, Ctl* c, int cluster) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = tid * per, b1 = min(b0 + per, p.B);
   uint32_t e = 0;
   int64_t sum = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const uint32_t eb = check_sequence(p, b);
     e |= eb;
     const int T = eb ? 0 : tiles_of(p, b).T;
     sum += T ? (int64_t)p.groups * (kFixed + T) : 0;
   }
-  int64_t inc = sum;
+  auto warp_scan = [&](int64_t v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  const int64_t inc = warp_scan(sum);
   if (lane == 31) c->scan[warp] = inc;
   if (e) atomicOr(&c->err, e);
   __syncthreads();
-  int64_t before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += c->scan[w];
-    total += c->scan[w];
-  }
+  const int64_t warps = warp_scan(lane < kThreads / 32 ? c->scan[lane] : 0);
+  const int64_t total = __shfl_sync(0xffffffffu, warps, 31);
+  int64_t at = __shfl_sync(0xffffffffu, warps, max(warp - 1, 0));  // units before this thread's sequences
+  at = (warp > 0 ? at : 0) + inc - sum;
   if (c->err) return 0;  // the same in every CTA: each has read every sequence
   const int n = active_clusters(p, total);
   if (cluster < n && total > 0) {
     const int64_t w0 = first_unit(total, n, cluster);
-    int64_t at = before + inc - sum;
     if (w0 >= at && w0 < at + sum) {
+      c->left = first_unit(total, n, cluster + 1) - w0;
+#pragma unroll 1
       for (int b = b0; b < b1; ++b) {
         const int T = tiles_of(p, b).T;
         const int64_t u = T ? (int64_t)p.groups * (kFixed + T) : 0;
         if (w0 < at + u) {
           c->start_b = b;
+          c->start_T = T;
           c->start_x = w0 - at;
           break;
         }
@@ -386,15 +408,16 @@ __device__ int make_split(const Params& p, Ctl* c, int cluster) {
       }
     }
   }
-  if (tid == 0) c->total = total;
   __syncthreads();
-  return total > 0 ? n : -1;  // -1: every sequence is unused
+  return total > 0 ? n : -1;
 }
 
 // ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
-// Converts 64 codes with their 4 scales into the 8 pieces of an operand row.
+// Converts 64 codes with their 4 scales into the 8 pieces of an operand row;
+// piece q goes to dst ^ 16 q (dst: the row's address plus 16 times the row's
+// place in its swizzle group).
 template <class To>
 __device__ __forceinline__ void convert_chunk(const uint32_t (&code)[8], uint32_t scale, uint32_t dst, int r7) {
 #pragma unroll
@@ -425,9 +448,9 @@ __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
   return v;
 }
 
-// One warp of producer group `grp`: tokens 16 pw .. + 15 of the tiles of that
+// One warp of producer group `grp`: tokens kTok pw .. of the tiles of that
 // parity.  The packed rows (codes and scales, 288 bytes) come by cp.async into
-// 16 rows of shared memory that the warp has to itself; a half tile's codes are
+// rows of shared memory that the warp has to itself; a half tile's codes are
 // fetched as soon as the tile before has been converted that far, so they have
 // about two tile periods to arrive.  (Loads into registers pass through the
 // small L1 that this much shared memory leaves, and its lines, not the latency,
@@ -440,30 +463,33 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
   const int lane = threadIdx.x & 31;
   const int grp = warp / kGroupWarps, pw = warp % kGroupWarps;
   const int r7 = lane & 7, ch = lane >> 3;
-  const int r = 16 * pw + r7;  // token row of the first set of 8 within the tile
+  const int r = kTok * pw + r7;  // token row of the first set of 8 within the tile
   const uint32_t stage = smem_u32(smem) + grp * (kScore ? kStageS : kStageV);
   const uint32_t raw = smem_u32(smem) + kOffRaw + warp * kRawWarp;
   uint32_t err = 0;
-  uint32_t j = 0;
+  uint32_t j = 0, seg = 0;
   for_pieces(c, [&](const Piece& pc) {
     int t = pc.t0 + (int)((grp ^ j) & 1u);
     j += (uint32_t)(pc.t1 - pc.t0);
-    if (t >= pc.t1) return true;
+    const uint32_t q_phase = seg++ & 1u;
+    // every warp waits for every piece's queries: a phase left out could be
+    // taken for the next one
+    if (t >= pc.t1) return !kScore || wait_warp(&c->q_ready, q_phase, c, kSiteQReady);
     uint32_t turn = (j - (uint32_t)(pc.t1 - t)) >> 1;  // tiles this group has taken before
     const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
-    // Pool row of token 16 pw + (lane & 15) of tile v, in two steps: the table
+    // Pool row of token kTok pw + lane % kTok of tile v, in two steps: the table
     // entry (a slot, or a page; -2 where no node sees the position), and, a
     // tile later, the slot.  Positions that no node sees read slot 0, under a
     // weight of zero.
     auto entry_of = [&](int v) -> int32_t {
-      const int pos = pc.tile(v) * kTK + 16 * pw + (lane & 15);
+      const int pos = pc.tile(v) * kTK + kTok * pw + lane % kTok;
       if (v >= pc.t1 || pos >= pc.N || (pos < pc.lo && pos >= p.sinks)) return -2;
       return __ldg(idx + (p.page_size == 1 ? (uint32_t)pos : (uint32_t)pos / (uint32_t)p.page_size));
     };
     auto slot_of = [&](int32_t e, int v) -> uint32_t {
       int64_t s = e;
       if (p.page_size > 1) {
-        const uint32_t pos = (uint32_t)(pc.tile(v) * kTK + 16 * pw + (lane & 15));
+        const uint32_t pos = (uint32_t)(pc.tile(v) * kTK + kTok * pw + lane % kTok);
         s = s * p.page_size + pos % (uint32_t)p.page_size;
       }
       if (e < 0 || s >= p.slots) {
@@ -475,19 +501,19 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     auto row_of = [&](uint32_t slot, int token) {
       return p.cache + (uint64_t)__shfl_sync(0xffffffffu, slot, token) * (uint32_t)p.row_stride;
     };
-    // 16-byte piece lane & 7 of tokens lane >> 3, + 4, + 8, + 12 of half h, and
+    // 16-byte piece lane & 7 of tokens lane >> 3, + 4, .. of half h, and
     // with the first half all scales, into the buffer of this turn's parity.
     // Past the piece's last tile nothing is fetched: what the next piece
     // fetches first must not race with it.
     auto fetch = [&](uint32_t slot, int h, uint32_t turn, bool more) {
 #pragma unroll
-      for (int i = 0; more && i < 4; ++i) {
+      for (int i = 0; more && i < kTok / 4; ++i) {
         const int token = 4 * i + ch;
         cp_async_16(raw + token * kRawRow + 128 * h + 16 * r7, row_of(slot, token) + 128 * h + 16 * r7);
       }
       const int token = lane >> 1;
-      const uint8_t* row = row_of(slot, token);
-      if (more && h == 0)
+      const uint8_t* row = row_of(slot, token % kTok);
+      if (more && h == 0 && token < kTok)
         cp_async_16(raw + token * kRawRow + kScaleOff + 32 * (turn & 1u) + 16 * (lane & 1),
                     row + kScaleOff + 16 * (lane & 1));
       cp_async_commit();
@@ -496,6 +522,8 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) fetch(slot, h, turn, true);
     int32_t ent = entry_of(t + 2);
+    // until then the queries pass through the stages
+    if (kScore && !wait_warp(&c->q_ready, q_phase, c, kSiteQReady)) return false;
 #pragma unroll 1
     for (int h = 0; t < pc.t1; h ^= 1) {
       cp_async_wait_group<1>();  // this half's pieces, of this lane
@@ -504,8 +532,8 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
       if (!wait_warp(&c->empty[full], (turn & 1u) ^ 1u, c, kSiteEmpty)) return false;
       if (kScore && h) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int token = 4 * i + ch, row = 16 * pw + token;
+        for (int i = 0; i < kTok / 4; ++i) {
+          const int token = 4 * i + ch, row = kTok * pw + token;
           cp_async_16(stage + 8 * kChunk + row * 128 + ((r7 ^ (row & 7)) << 4),
                       row_of(slot, token) + kRopeOff + 16 * r7);
         }
@@ -513,7 +541,7 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
       }
       uint32_t src = raw + r7 * kRawRow, dst = stage + h * kHalf + ch * kChunk + r * 128;
 #pragma unroll 1
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < kTok / 8; ++s) {
         uint32_t code[8];
         ld_shared_v4(src + 128 * h + 32 * ch, code[0], code[1], code[2], code[3]);
         ld_shared_v4(src + 128 * h + 32 * ch + 16, code[4], code[5], code[6], code[7]);
@@ -594,44 +622,48 @@ __device__ void score_mma(uint8_t* smem, Ctl* c) {
   drain_mmas(c, leader);
 }
 
-// Stages query row `row` into Tensor Memory: half h of the row's two threads
-// takes columns [144 h, 144 h + 144) (column c holds elements 2c, 2c + 1 of
-// 512 latent and 64 rope ones), 48 columns of loads in flight at a time.
-__device__ __forceinline__ void stage_query_row(const Params& p, int b, int row, bool live, int h, uint32_t tQ) {
-  const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat) + ((int64_t)b * p.rows + row) * (kDl / 8);
-  const uint4* qp = reinterpret_cast<const uint4*>(p.q_pe) + ((int64_t)b * p.rows + row) * (kDr / 8);
+// Brings a piece's query rows into Tensor Memory (column c holds elements 2c,
+// 2c + 1 of 512 latent and 64 rope ones), all row warps together.  Nine tensor
+// copies, 64 elements of the rows each, fill the two stages, which are free
+// between pieces (the producers wait for q_ready before they fill them); the
+// copies' 128-byte swizzle puts the 8 rows that a quarter warp reads at once
+// into different banks.  (For 128 rows, a thread loading its own row took 14 us,
+// cp.async of 16 bytes a lane 9, a bulk copy per row 9.)
+static_assert(9 * kPBytes <= 2 * kStageS, "queries fit the stages");
+__device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* smem, Ctl* c, const Piece& pc, int warp,
+                              uint32_t seg) {
+  const int lane = threadIdx.x & 31;
+  const int wq = warp & 3, wg = (warp - kWarpRows) >> 2;
+  const int r = wq * 32 + lane;
+  const int rows = min(kRG, p.rows - pc.g * kRG);
   const uint32_t mul = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(p.qpe_mul)) * 0x10001u;  // a power of two
+  if (warp == kWarpRows && elect_one()) {
+    fence_proxy_async_smem();  // the stages were written through the generic proxy
+    mbar_arrive_expect_tx(&c->q_in, 9u * 128u * (uint32_t)p.box_rows);
+    const int y = pc.b * p.rows + pc.g * kRG;
 #pragma unroll 1
-  for (int c0 = 144 * h; c0 < 144 * h + 144; c0 += 48) {
-    uint4 x[12];
+    for (int ck = 0; ck < 9; ++ck)
+      tensor_copy_2d(smem + ck * kPBytes, ck < 8 ? &maps.lat : &maps.pe, ck < 8 ? 64 * ck : 0, y, &c->q_in);
+  }
+  __syncwarp();
+  if (!wait_warp(&c->q_in, seg & 1u, c, kSiteQIn)) return false;
+#pragma unroll 1
+  for (int ck = 0; ck < 9; ++ck) {
+    const uint32_t src = smem_u32(smem) + ck * kPBytes + r * 128;
+    uint32_t w[16];
 #pragma unroll
-    for (int v = 0; v < 12; ++v) {
-      const int col = c0 + 4 * v;
-      x[v] = make_uint4(0, 0, 0, 0);
-      if (live) x[v] = col < 256 ? __ldg(ql + col / 4) : __ldg(qp + (col - 256) / 4);
+    for (int i = 0; i < 4; ++i)
+      ld_shared_v4(src + (((4 * wg + i) ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (r >= rows) w[i] = 0u;  // another sequence's rows, or none
+      if (ck == 8) w[i] = hmul2_bf16(w[i], mul);
     }
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {
-      uint32_t w[16];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        uint4 y = x[4 * s + v];
-        if (c0 + 16 * s + 4 * v >= 256) {
-          y.x = hmul2_bf16(y.x, mul);
-          y.y = hmul2_bf16(y.y, mul);
-          y.z = hmul2_bf16(y.z, mul);
-          y.w = hmul2_bf16(y.w, mul);
-        }
-        w[4 * v + 0] = y.x;
-        w[4 * v + 1] = y.y;
-        w[4 * v + 2] = y.z;
-        w[4 * v + 3] = y.w;
-      }
-      __syncwarp();
-      tmem_st_32x32b_x16(tQ + c0 + 16 * s, w);
-    }
+    __syncwarp();
+    tmem_st_32x32b_x16(((uint32_t)(wq * 32) << 16) + kColQ + 32 * ck + 16 * wg, w);
   }
   tmem_wait_st();
+  return true;
 }
 
 // Pairs of fp32 in a 64-bit register: one instruction for both.
@@ -671,7 +703,7 @@ __device__ __forceinline__ void mask32(uint32_t (&u)[32], uint32_t vis) {
 // the tiles of its parity, all 64 columns of a row in one thread.  The running
 // maximum passes from group to group, warp to warp of the same rows, before
 // the exponentials; each group sums its own weights.
-__device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
+__device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* smem, Ctl* c, int warp) {
   const int lane = threadIdx.x & 31;
   const int wq = warp & 3, wg = (warp - kWarpRows) >> 2;
   const int r = wq * 32 + lane;
@@ -686,7 +718,7 @@ __device__ void score_softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) 
     const int row = pc.g * kRG + r;
     const bool live = row < p.rows;
     const int P = pc.P;
-    stage_query_row(p, pc.b, row, live, wg, lane_off + kColQ);
+    if (!stage_queries(p, maps, smem, c, pc, warp, seg)) return false;
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&c->q_ready);
@@ -966,72 +998,82 @@ __device__ void value_rows(const Params& p, Ctl* c) {
   });
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_attn_kernel(const Params p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_attn_kernel(const Params p,
+                                                                                              const __grid_constant__ QueryMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t rank = cluster_ctarank();
   const int warp = threadIdx.x >> 5;
   const int cluster = blockIdx.x / 2;
   Ctl* c = reinterpret_cast<Ctl*>(smem + kOffCtl);
-  if (threadIdx.x == 0) {
-    for (int q = 0; q < 4; ++q) {
+  // Barriers, a few per warp.
+  if ((threadIdx.x & 31) == 0) {
+    if (warp < 4) {
       // the score CTA's second halves wait for every lane's rope copies too
-      mbar_init(&c->full[q], kGroupWarps + (rank == 0 && (q & 1) ? 32 * kGroupWarps : 0));
-      mbar_init(&c->empty[q], 1);
-      mbar_init(&c->m_ready[0][q], 1);
-      mbar_init(&c->m_ready[1][q], 1);
-    }
-    for (int q = 0; q < kSBufs; ++q) {
-      mbar_init(&c->s_full[q], 1);
-      mbar_init(&c->s_free[q], kRowWarps / 2);
-    }
-    for (int q = 0; q < kPBufs; ++q) {
+      mbar_init(&c->full[warp], kGroupWarps + (rank == 0 && (warp & 1) ? 32 * kGroupWarps : 0));
+      mbar_init(&c->empty[warp], 1);
+      mbar_init(&c->m_ready[0][warp], 1);
+      mbar_init(&c->m_ready[1][warp], 1);
+    } else if (warp < 4 + kSBufs) {
+      mbar_init(&c->s_full[warp - 4], 1);
+      mbar_init(&c->s_free[warp - 4], kRowWarps / 2);
+    } else if (warp < 4 + kSBufs + kPBufs) {
+      const int q = warp - 4 - kSBufs;
       mbar_init(&c->p_free[q], 1);
       mbar_init(&c->p_full[q], 1);
       mbar_init(&c->pv_done[q], 1);
       mbar_init(&c->o_ready[q], kRowWarps);
-    }
-    for (int q = 0; q < kPStages; ++q) {
+    } else if (warp < 4 + kSBufs + kPBufs + kPStages) {
+      const int q = warp - 4 - kSBufs - kPBufs;
       mbar_init(&c->p_staged[q], kRowWarps / 2);
       mbar_init(&c->ps_free[q], 1);
+    } else if (warp == 12) {
+      mbar_init(&c->q_ready, kRowWarps);
+      mbar_init(&c->q_in, 1);
+      mbar_init(&c->fin_free, 32 * kRowWarps);
+      mbar_init(&c->fin_full, 32 * kRowWarps);
+      mbar_init(&c->drain, 1);
+    } else if (warp == 13) {
+      for (int q = 0; q < kPieces; ++q) {
+        mbar_init(&c->piece_full[q], 1);
+        mbar_init(&c->piece_empty[q], kFollowers + (rank == 0 ? 1 : 0));
+      }
+    } else if (warp == 14) {
+      c->abort = 0;
+      c->abort_site = 0;
+      c->start_b = p.B;
+      c->start_x = 0;
+      c->start_T = 0;
+      c->left = 0;
+      c->err = (smem_u32(smem) & 1023u) ? MLA_DEVERR_LAYOUT : 0u;
     }
-    mbar_init(&c->q_ready, kRowWarps);
-    mbar_init(&c->fin_free, 32 * kRowWarps);
-    mbar_init(&c->fin_full, 32 * kRowWarps);
-    mbar_init(&c->drain, 1);
-    for (int q = 0; q < kPieces; ++q) {
-      mbar_init(&c->piece_full[q], 1);
-      mbar_init(&c->piece_empty[q], kFollowers + (rank == 0 ? 1 : 0));
-    }
-    c->abort = 0;
-    c->abort_site = 0;
-    c->start_b = p.B;
-    c->start_x = 0;
-    c->err = (smem_u32(smem) & 1023u) ? MLA_DEVERR_LAYOUT : 0u;
     fence_mbar_init();
   }
-  __syncthreads();
-  const int n = make_split(p, c, cluster);  // the same n in every CTA
-  const bool work = cluster < n;
-  if (threadIdx.x == 0) {
-    if (rank == 0) {
-      Start* st = reinterpret_cast<Start*>(p.starts) + cluster;
-      *st = Start{c->start_b, (int32_t)c->start_x, (int32_t)(c->start_x >> 32), n > 0 ? n : 0};
-    }
-    if (blockIdx.x == 0) p.err[0] = gridDim.x;
-  }
-  if (!work) {
-    // both CTAs of the cluster leave here
-    grid_dep_launch();
-    if (threadIdx.x == 0) p.err[kErrFirst + blockIdx.x] = c->err;
-    return;
-  }
+  static_assert(4 + kSBufs + kPBufs + kPStages <= 12 && kPStages == 2, "barriers per warp");
   if (warp == kWarpAux) {
     tmem_alloc_cta(&c->tmem_base, kTmemCols);
     tmem_relinquish_cta();
   }
   tc_fence_before();
-  cluster_sync();  // barriers of both CTAs initialised before any remote use
+  __syncthreads();
+  cluster_arrive();  // barriers initialised; the peer's are waited for after the split
+  const int n = make_split(p, c, cluster);  // the same n in every CTA
+  const bool work = cluster < n;
+  if (threadIdx.x == 0) {
+    if (rank == 0) {
+      Start* st = reinterpret_cast<Start*>(p.starts) + cluster;
+      *st = Start{c->start_x, c->start_b, c->start_T, n > 0 ? n : 0, {0, 0, 0}};
+    }
+    if (blockIdx.x == 0) p.err[0] = gridDim.x;
+  }
+  cluster_wait();
   tc_fence_after();
+  if (!work) {
+    // both CTAs of the cluster leave here
+    grid_dep_launch();
+    if (threadIdx.x == 0) p.err[kErrFirst + blockIdx.x] = c->err;
+    if (warp == kWarpAux) tmem_dealloc_cta(c->tmem_base, kTmemCols);
+    return;
+  }
 
   const bool base0 = c->tmem_base == 0;  // all columns are allocated
   if (!base0 && threadIdx.x == 0) c->err = MLA_DEVERR_LAYOUT;
@@ -1045,7 +1087,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
   } else if (warp < kWarpRows + kRowWarps) {
     if (!base0) {
     } else if (rank == 0) {
-      score_softmax(p, smem, c, warp);
+      score_softmax(p, maps, smem, c, warp);
     } else {
       value_rows(p, c);
     }
@@ -1077,81 +1119,105 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
 // The pieces of a row group that several clusters shared:
 //   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k.
 // Row k of the grid looks at the boundary between clusters k - 1 and k; the
-// first boundary inside a row group merges it.  One warp per (row, quarter of
-// the columns), four pieces in flight.
-constexpr int kMergeThreads = 256;
-__global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const Params p) {
+// first boundary inside a row group merges it.  A block takes four rows: it
+// first gathers every piece's slot and weights, then each warp sums one half of
+// a row's columns with six pieces' loads in flight.
+constexpr int kMergeThreads = 256, kMergeRows = 4;
+constexpr int kMaxClusters = 128;
+static_assert(2 * kMaxClusters <= kErrMax, "an error word per CTA");
+__global__ void __launch_bounds__(kMergeThreads, 3) kvq_merge_kernel(const Params p) {
+  __shared__ int slot[kMaxClusters];                   // -1: an empty piece
+  __shared__ float weight[kMergeRows][kMaxClusters];   // lse, then exp(lse - max)
   grid_dep_wait();
   const Start* st = reinterpret_cast<const Start*>(p.starts);
-  const int k = (int)blockIdx.y + 1;
-  const Start s0 = st[k - 1], s = st[k];
+  const int k = (int)blockIdx.y + 1, tid = threadIdx.x;
+  // every load of this phase at once: the two clusters at the boundary, and
+  // for thread i the two around piece i, that of cluster k - 1 + i
+  const int c = min(k - 1 + tid, p.clusters - 1);
+  const Start s0 = st[k - 1], s = st[k], me = st[c], next = st[min(c + 1, p.clusters - 1)];
   if (k >= s.n) return;
-  const Tiles tl = tiles_of(p, s.b);
-  const int L = kFixed + tl.T;
-  const int64_t g = s.x() / L;
+  const int T = s.T;
+  const int L = kFixed + T;
+  const int64_t g = div_fast(s.x, L);
   const int64_t base = g * L;
-  if (s.x() == base) return;                      // the boundary lies between two row groups
-  if (s0.b == s.b && s0.x() > base) return;       // not the first inside this one
-  const int lane = threadIdx.x & 31;
-  const int wi = (int)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  const int r = wi >> 2, col = (wi & 3) * 128 + 4 * lane;
-  const int64_t row = g * kRG + r;
-  if (r >= kRG || row >= p.rows) return;
-  // pieces: cluster k - 1 holds units [0, x_k), cluster i >= k units [x_i, x_{i+1})
-  auto unit = [&](int i) -> int64_t {
-    if (i < k) return 0;
-    if (i >= s.n) return L;
-    const Start q = st[i];
-    return q.b != s.b || q.x() - base > L ? L : q.x() - base;
+  if (s.x == base) return;                 // the boundary lies between two row groups
+  if (s0.b == s.b && s0.x > base) return;  // not the first inside this one
+  const int r0 = (int)blockIdx.x * kMergeRows;
+  const int rows = (int)min((int64_t)kRG, p.rows - g * kRG) - r0;
+  if (rows <= 0) return;
+  // pieces: cluster k - 1 has units [0, x_k) of the row group, cluster i >= k [x_i, x_{i+1})
+  auto unit = [&](int i, const Start& q) -> int64_t {
+    return i < k ? 0 : i >= s.n || q.b != s.b || q.x - base > L ? L : q.x - base;
   };
-  float M = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  int64_t z0 = 0;
-  for (int i = k - 1; z0 < L;) {
-    // up to four pieces at once
-    float4 v[4];
-    float ls[4];
+  int n = 0;
+  bool whole = false;
+  if (tid < kMaxClusters && k - 1 + tid < s.n) {
+    const int64_t z0 = unit(c, me), z1 = unit(c + 1, next);
+    if (z0 < L) {
+      const int t0 = cut_tile(z0, T), t1 = cut_tile(z1, T);
+      whole = t0 == 0 && t1 == T;
+      slot[tid] = t1 > t0 ? 2 * c + (t0 == 0) : -1;
+      n = 1;
+    }
+  }
+  n = __syncthreads_count(n);
+  if (__syncthreads_or(whole)) return;  // one cluster has it all: it stored the results
+  for (int i = tid; i < n * kMergeRows; i += kMergeThreads) {
+    const int pc = i >> 2, r = i & 3;
+    weight[r][pc] = slot[pc] >= 0 && r < rows ? p.part_lse[(int64_t)slot[pc] * kRG + r0 + r] : -INFINITY;
+  }
+  __syncthreads();
+  const int warp = tid >> 5, lane = tid & 31;
+  const int r = warp >> 1;
+  float m = -INFINITY, sum = 0.f;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, weight[r][i]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      ls[q] = -INFINITY;
-      if (z0 >= L) continue;
-      const int64_t z1 = unit(i + 1);
-      const int t0 = cut_tile(z0, tl.T), t1 = cut_tile(z1, tl.T);
-      if (t0 == 0 && t1 == tl.T) return;  // one cluster has it all: it stored the results
-      if (t1 > t0) {
-        const int64_t prow = (int64_t)(2 * i + (t0 == 0)) * kRG + r;
-        ls[q] = p.part_lse[prow];
-        v[q] = *reinterpret_cast<const float4*>(p.part_o + prow * kDl + col);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int i = lane; i < n; i += 32) sum += __expf(weight[r][i] - m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (r >= rows) return;
+  // 256 columns: two float4 a lane
+  const int col = (warp & 1) * 256 + 4 * lane;
+  const float* part = p.part_o + (int64_t)(r0 + r) * kDl + col;
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  constexpr int kDeep = 6;
+  for (int i0 = 0; i0 < n; i0 += kDeep) {
+    float4 v[kDeep][2];
+    float w[kDeep];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int i = i0 + d, sl = i < n ? slot[i] : -1;
+      w[d] = sl >= 0 ? __expf(weight[r][i] - m) : 0.f;
+      if (sl >= 0) {
+        const float4* src = reinterpret_cast<const float4*>(part + (int64_t)sl * kRG * kDl);
+        v[d][0] = src[0];
+        v[d][1] = src[32];
+      } else {
+        v[d][0] = v[d][1] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      z0 = z1;
-      ++i;
-    }
-    float mb = fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3]));
-    mb = fmaxf(mb, M);
-    if (mb != -INFINITY) {
-      const float a = __expf(M - mb);  // 0 for the first pieces
-      sum *= a;
-      acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
-      M = mb;
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (ls[q] == -INFINITY) continue;
-      const float wt = __expf(ls[q] - M);
-      sum += wt;
-      acc.x = fmaf(wt, v[q].x, acc.x);
-      acc.y = fmaf(wt, v[q].y, acc.y);
-      acc.z = fmaf(wt, v[q].z, acc.z);
-      acc.w = fmaf(wt, v[q].w, acc.w);
+    for (int d = 0; d < kDeep; ++d) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        acc[h].x = fmaf(w[d], v[d][h].x, acc[h].x);
+        acc[h].y = fmaf(w[d], v[d][h].y, acc[h].y);
+        acc[h].z = fmaf(w[d], v[d][h].z, acc[h].z);
+        acc[h].w = fmaf(w[d], v[d][h].w, acc[h].w);
+      }
     }
   }
   const float inv = 1.f / sum;
-  const int64_t orow = (int64_t)s.b * p.rows + row;
-  uint2 o;
-  o.x = pack_bf16(acc.x * inv, acc.y * inv);
-  o.y = pack_bf16(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + col) = o;
-  if (p.lse && (wi & 3) == 0 && lane == 0) p.lse[orow] = M + logf(sum);
+  const int64_t orow = (int64_t)s.b * p.rows + g * kRG + r0 + r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint2 o;
+    o.x = pack_bf16(acc[h].x * inv, acc[h].y * inv);
+    o.y = pack_bf16(acc[h].z * inv, acc[h].w * inv);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + col + 128 * h) = o;
+  }
+  if (p.lse && (warp & 1) == 0 && lane == 0) p.lse[orow] = m + logf(sum);
 }
 
 namespace {
@@ -1162,7 +1228,8 @@ mla_status validate_shape(const mla_kvq_attn_args* a) {
   if (!a) return MLA_ERR_INVALID_ARG;
   if (a->B < 0 || a->Q < 0 || a->H < 1) return MLA_ERR_INVALID_ARG;
   if (a->Q > MLA_MAX_Q) return MLA_ERR_UNSUPPORTED;
-  if ((int64_t)a->H * a->Q > (int64_t)1 << 24) return MLA_ERR_UNSUPPORTED;
+  // row numbers of the whole batch are 32-bit coordinates of the query copies
+  if ((int64_t)a->H * a->Q > (int64_t)1 << 24 || (int64_t)a->H * a->Q * a->B > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
 
@@ -1213,9 +1280,37 @@ int clusters_per_gpu() {
     cudaGetLastError();
     n = sms / 2;
   }
-  if (2 * n > kErrMax) n = kErrMax / 2;
+  if (n > kMaxClusters) n = kMaxClusters;
   cached[dev] = n;
   return n;
+}
+
+// The driver's encoder of tensor maps, looked up once.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+  static std::mutex mu;
+  static EncodeTiledFn fn = nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    void* f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+    else
+      cudaGetLastError();
+  }
+  return fn;
+}
+bool query_map(CUtensorMap* m, const void* base, int64_t rows, int width, int box_rows) {
+  const EncodeTiledFn f = encode_tiled();
+  const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return f && f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Layout {
@@ -1224,7 +1319,7 @@ struct Layout {
 Layout layout(int clusters) {
   Layout l;
   size_t o = MLA_KVQ_WORKSPACE_BYTES;
-  l.starts = o;    o = align256(o + 16 * ((size_t)clusters + 1));
+  l.starts = o;    o = align256(o + sizeof(Start) * ((size_t)clusters + 1));
   l.part_lse = o;  o = align256(o + sizeof(float) * 2 * (size_t)clusters * kRG);
   l.part_o = o;    o = align256(o + sizeof(float) * 2 * (size_t)clusters * kRG * kDl);
   l.total = o;
@@ -1258,6 +1353,7 @@ Params make_params(const mla_kvq_attn_args* a, void* ws, int clusters) {
   p.out = a->out;
   p.lse = a->lse;
   p.groups = (p.rows + kRG - 1) / kRG;
+  p.box_rows = p.rows < kRG ? p.rows : kRG;
   p.clusters = clusters;
   const Layout l = layout(clusters);
   char* base = static_cast<char*>(ws);
@@ -1296,9 +1392,13 @@ extern "C" mla_status mla_kvq_attn(const mla_kvq_attn_args* a, void* workspace, 
   // per call: the attribute belongs to the context, which may be a new one
   if (cudaFuncSetAttribute(kvq_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc) != cudaSuccess)
     return MLA_ERR_CUDA;
-  if (launch_kernel(kvq_attn_kernel, dim3(2 * n), dim3(kThreads), kSmemAlloc, s, false, p) != cudaSuccess)
+  QueryMaps maps;
+  const int64_t rows = (int64_t)p.B * p.rows;
+  if (!query_map(&maps.lat, p.q_lat, rows, kDl, p.box_rows) || !query_map(&maps.pe, p.q_pe, rows, kDr, p.box_rows))
     return MLA_ERR_CUDA;
-  if (n > 1 && launch_kernel(kvq_merge_kernel, dim3(4 * kRG / (kMergeThreads / 32), n - 1), dim3(kMergeThreads), 0, s,
+  if (launch_kernel(kvq_attn_kernel, dim3(2 * n), dim3(kThreads), kSmemAlloc, s, false, p, maps) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  if (n > 1 && launch_kernel(kvq_merge_kernel, dim3(((p.rows < kRG ? p.rows : kRG) + kMergeRows - 1) / kMergeRows, n - 1), dim3(kMergeThreads), 0, s,
                              true, p) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;

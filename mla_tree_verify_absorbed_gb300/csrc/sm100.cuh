@@ -178,6 +178,16 @@ __device__ __forceinline__ void bulk_copy_s2c(uint32_t dst, const void* src, uin
       "r"(smem_u32(src)), "r"(bytes), "r"(cbar)
       : "memory");
 }
+// Tensor copy of the box at (x, y) of a 2-d tensor map into this CTA's shared
+// memory; the box's bytes (elements outside the tensor count, and read 0)
+// complete_tx the mbarrier.  x times the element size must be a multiple of 16.
+__device__ __forceinline__ void tensor_copy_2d(void* dst, const void* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Waits until at most `n` of this thread's committed bulk groups are still pending.
 template <int n>
@@ -345,6 +355,9 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The two halves of cluster_sync(), for work in between.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Shared-memory address of the same offset in CTA `cta` of the cluster.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t cta) {
   uint32_t r;
