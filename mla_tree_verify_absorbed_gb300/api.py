@@ -628,9 +628,9 @@ class QuantCache:
 
     def c_struct(self) -> MlaKvqCache:
         r = self.rows
+        n = r.size(0)
         # the row stride of a one-row tensor is whatever its maker left there
-        stride = r.stride(0) if r.shape[0] > 1 else KVQ_ROW_BYTES
-        return MlaKvqCache(r.data_ptr(), stride, r.shape[0], self.exponent)
+        return MlaKvqCache(r.data_ptr(), r.stride(0) if n > 1 else KVQ_ROW_BYTES, n, self.exponent)
 
 
 def kvq_alloc(slots: int, exponent: int = 0, device="cuda") -> QuantCache:
@@ -652,13 +652,17 @@ def _one_device(**tensors):
 def _kvq_launch(what: str, f, dev, stream, *args):
     """Calls f(*args, stream) with the tensors' device current."""
     import torch
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"{what}: stream on {stream.device}, tensors on {dev}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"{what}: stream on {stream.device}, tensors on {dev}")
+        raw = stream.cuda_stream
+    else:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
     if dev.index == torch.cuda.current_device():
-        st = f(*args, _stream(stream))
+        st = f(*args, raw)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _stream(stream))
+            st = f(*args, raw)
     if st != MLA_OK:
         raise MlaError(st, what)
 
@@ -681,11 +685,10 @@ def _kvq_rows(what: str, f, cache: QuantCache, kv_c, k_pe, slots, workspace, str
     dev = cache.rows.device
     if workspace is None:
         workspace = alloc_workspace(KVQ_WORKSPACE_BYTES, dev)
-    n = kv_c.shape[0]
-    r = MlaKvqRows(n, MLA_BF16 if kv_c.dtype == torch.bfloat16 else MLA_FP32, kv_c.data_ptr(), k_pe.data_ptr(),
+    n = kv_c.size(0)
+    r = MlaKvqRows(n, MLA_BF16 if kv_c.dtype is torch.bfloat16 else MLA_FP32, kv_c.data_ptr(), k_pe.data_ptr(),
                    kv_c.stride(0) if n > 1 else 512, k_pe.stride(0) if n > 1 else 64, slots.data_ptr())
-    _kvq_launch(what, f, dev, stream, ctypes.byref(cache.c_struct()), ctypes.byref(r), workspace.data_ptr(),
-                _ws_bytes(workspace))
+    _kvq_launch(what, f, dev, stream, cache.c_struct(), r, workspace.data_ptr(), workspace.nbytes)
     return workspace
 
 
@@ -704,11 +707,12 @@ def kvq_read(cache: QuantCache, slots, dtype: str = "bf16", kv_c=None, k_pe=None
     -1 keep what the given arrays hold (zeros in arrays made here).  Returns
     (kv_c [n][512], k_pe [n][64], workspace)."""
     import torch
-    dt = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype] if kv_c is None else kv_c.dtype
-    if kv_c is None:
-        kv_c = torch.zeros((slots.shape[0], 512), dtype=dt, device=cache.rows.device)
-    if k_pe is None:
-        k_pe = torch.zeros((slots.shape[0], 64), dtype=dt, device=cache.rows.device)
+    if kv_c is None or k_pe is None:
+        dt = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype] if kv_c is None else kv_c.dtype
+        if kv_c is None:
+            kv_c = torch.zeros((slots.shape[0], 512), dtype=dt, device=cache.rows.device)
+        if k_pe is None:
+            k_pe = torch.zeros((slots.shape[0], 64), dtype=dt, device=cache.rows.device)
     ws = _kvq_rows("mla_kvq_read", load().mla_kvq_read, cache, kv_c, k_pe, slots, workspace, stream, check)
     return kv_c, k_pe, ws
 
@@ -759,11 +763,14 @@ class KvqInputs:
             raise ValueError("block_table must be a contiguous [B][max_pages] int32 tensor")
 
     def c_args(self, out=None, lse=None) -> MlaKvqAttnArgs:
+        table, tree = self.block_table, self.tree_parent
+        paged = self.page_size > 1
         return MlaKvqAttnArgs(
-            self.B, self.Q, self.H, self.cache.c_struct(), _ptr(self.q_lat), _ptr(self.q_pe), self.page_size,
-            _ptr(self.kv_indptr), _ptr(self.kv_indices), _ptr(self.block_table),
-            0 if self.block_table is None else self.block_table.shape[1], _ptr(self.prefix_lens),
-            _ptr(self.tree_parent), self.window, self.sinks, self.scale, _ptr(out), _ptr(lse))
+            self.B, self.Q, self.H, self.cache.c_struct(), self.q_lat.data_ptr(), self.q_pe.data_ptr(), self.page_size,
+            None if paged else _ptr(self.kv_indptr), None if paged else _ptr(self.kv_indices),
+            _ptr(table) if paged else None, table.shape[1] if paged and table is not None else 0,
+            self.prefix_lens.data_ptr(), None if tree is None else tree.data_ptr(), self.window, self.sinks,
+            self.scale, None if out is None else out.data_ptr(), None if lse is None else lse.data_ptr())
 
 
 def kvq_workspace_size(ki: KvqInputs) -> int:
@@ -794,8 +801,8 @@ def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, che
         _one_device(out=out, lse=lse, workspace=workspace, **ki.tensors())
     if workspace is None:
         workspace = alloc_workspace(kvq_workspace_size(ki), dev)
-    _kvq_launch("mla_kvq_attn", load().mla_kvq_attn, dev, stream, ctypes.byref(ki.c_args(out, lse)),
-                workspace.data_ptr(), _ws_bytes(workspace))
+    _kvq_launch("mla_kvq_attn", load().mla_kvq_attn, dev, stream, ki.c_args(out, lse), workspace.data_ptr(),
+                workspace.nbytes)
     return out, lse
 
 

@@ -98,7 +98,10 @@ constexpr int kOffPS = 2 * kStageS, kOffPV = 2 * kStageV;
 constexpr int kOffRaw = kOffPS + kPStages * kPBytes > kOffPV + kPBufs * kPBytes ? kOffPS + kPStages * kPBytes
                                                                                 : kOffPV + kPBufs * kPBytes;
 constexpr int kOffCtl = kOffRaw + kProducerWarps * kRawWarp;
-constexpr uint32_t kPTxBytes = kPBytes + kRG * 4;        // weights + rescale factors
+// A row group with few rows (decoding with few heads) leaves whole lane
+// quadrants of 32 rows unused: their softmax, weights and outputs are left out.
+__device__ __forceinline__ int live_quads(int rows, int g) { return min(4, (rows - g * kRG + 31) >> 5); }
+__device__ __forceinline__ uint32_t weight_bytes(int quads) { return (uint32_t)quads * 32u * 128u; }
 
 // Tensor Memory columns: score CTA, three S tiles and the queries (bf16 pairs);
 // value CTA, O from column 0
@@ -135,8 +138,8 @@ constexpr float kWeightShift = 7.f;
 
 // Cost of starting a row group or a piece of one, in tiles, and the fewest
 // tiles worth a cluster of its own.
-constexpr int kFixed = 8;
-constexpr int kMinTiles = 6;
+constexpr int kFixed = 4;
+constexpr int kMinTiles = 8;
 
 // One cluster's share of a row group, as the roles need it.
 struct alignas(16) Piece {
@@ -666,25 +669,6 @@ __device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* s
   return true;
 }
 
-// Pairs of fp32 in a 64-bit register: one instruction for both.
-__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
-__device__ __forceinline__ float lo_f32(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float hi_f32(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -717,6 +701,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
     const int t0 = pc.t0, t1 = pc.t1;
     const int row = pc.g * kRG + r;
     const bool live = row < p.rows;
+    const bool idle = wq >= live_quads(p.rows, pc.g);  // none of the warp's rows exists
     const int P = pc.P;
     if (!stage_queries(p, maps, smem, c, pc, warp, seg)) return false;
     tc_fence_before();
@@ -738,6 +723,17 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
     for (int t = t0 + (int)(i - j); t < t1; t += 2, i += 2) {
       const uint32_t sb = i % kSBufs;
       if (!wait_warp(&c->s_full[sb], (i / kSBufs) & 1u, c, kSiteSFull)) return false;
+      const uint32_t ps = i % kPStages;
+      if (idle) {
+        // every barrier's phases count on: the next piece may use the rows
+        if (lane == 0) {
+          mbar_arrive(&c->s_free[sb]);
+          mbar_arrive(&c->m_ready[wg][wq]);
+        }
+        if (!wait_warp(&c->ps_free[ps], ((i / kPStages) & 1u) ^ 1u, c, kSitePsFree)) return false;
+        if (lane == 0) mbar_arrive(&c->p_staged[ps]);
+        continue;
+      }
       tc_fence_after();
       // which of the tile's 64 tokens the row sees, where not all of them
       const int pos0 = pc.tile(t) * kTK;
@@ -785,7 +781,6 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
       }
       const float nmu = m == -INFINITY ? 0.f : kWeightShift - m;
 
-      const uint32_t ps = i % kPStages;
       if (!wait_warp(&c->ps_free[ps], ((i / kPStages) & 1u) ^ 1u, c, kSitePsFree)) return false;
       const uint32_t pst = smem_u32(smem) + kOffPS + ps * kPBytes + r * 128;
       uint64_t ls = 0;  // two fp32 sums
@@ -823,7 +818,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
 
     // both groups' sums go to the value CTA relative to the final maximum,
     // which the group of the last tile has
-    if ((jl & 1u) != (uint32_t)wg) {
+    if ((jl & 1u) != (uint32_t)wg && !idle) {
       if (!wait_warp(&c->m_ready[wg ^ 1][wq], (jl >> 1) & 1u, c, kSiteMReady)) return false;
       const float mn = c->m_run[wg ^ 1][r];
       if (mn != m) l *= exp2f(m - mn);
@@ -841,7 +836,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
 
 // One warp of the score CTA, one thread of it copying: ships each tile's weights and factors to the
 // value CTA, where their bytes complete p_full.
-__device__ void weight_copier(uint8_t* smem, Ctl* c) {
+__device__ void weight_copier(const Params& p, uint8_t* smem, Ctl* c) {
   const bool leader = elect_one();
   uint32_t j = 0;
   for_pieces(c, [&](const Piece& pc) {
@@ -851,8 +846,8 @@ __device__ void weight_copier(uint8_t* smem, Ctl* c) {
       if (!wait_warp(&c->p_free[pb], ((j / kPBufs) & 1u) ^ 1u, c, kSitePFree)) return false;
       if (leader) {
         const uint32_t bar = mapa_shared(smem_u32(&c->p_full[pb]), 1);
-        bulk_copy_s2c(mapa_shared(smem_u32(smem + kOffPV + pb * kPBytes), 1), smem + kOffPS + ps * kPBytes, kPBytes,
-                      bar);
+        bulk_copy_s2c(mapa_shared(smem_u32(smem + kOffPV + pb * kPBytes), 1), smem + kOffPS + ps * kPBytes,
+                      weight_bytes(live_quads(p.rows, pc.g)), bar);
         bulk_copy_s2c(mapa_shared(smem_u32(&c->alpha[pb][0]), 1), &c->alpha[ps][0], kRG * 4, bar);
       }
       __syncwarp();
@@ -911,12 +906,13 @@ __device__ void value_rows(const Params& p, Ctl* c) {
   int j = 0, seg = 0;
   for_pieces(c, [&](const Piece& pc) {
     const int slot = pc.slot, b = pc.b, g = pc.g, t0 = pc.t0;
+    const int quads = live_quads(p.rows, g);
     for (int t = t0; t < pc.t1; ++t, ++j) {
       const int pb = j % kPBufs;
-      if (w == 0 && lane == 0) mbar_arrive_expect_tx(&c->p_full[pb], kPTxBytes);
+      if (w == 0 && lane == 0) mbar_arrive_expect_tx(&c->p_full[pb], weight_bytes(quads) + kRG * 4);
       if (!wait_warp(&c->p_full[pb], (uint32_t)(j / kPBufs) & 1u, c, kSitePFull)) return false;
       if (w == 0 && lane == 0) mbar_arrive_cluster_relaxed(&c->ps_free[j % kPStages], 0);
-      if (t != t0) {
+      if (t != t0 && wq < quads) {
         const float a = c->alpha[pb][r];
         if (__any_sync(0xffffffffu, a != 1.f)) {
           if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c, kSitePvPrev)) return false;
@@ -944,6 +940,7 @@ __device__ void value_rows(const Params& p, Ctl* c) {
     const float l = c->lfin[0][r] + c->lfin[1][r], m = c->mfin[r];
     mbar_arrive_cluster_relaxed(&c->fin_free, 0);
     ++seg;
+    if (wq >= quads) return true;
     const int row = g * kRG + r;
     const bool live = row < p.rows;
     // a row that sees nothing of this piece has l = 0 and O = 0
@@ -1097,7 +1094,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
       if (rank == 0) score_mma(smem, c);
       else value_mma(smem, c);
     } else if (warp == kWarpAux) {
-      if (rank == 0) weight_copier(smem, c);
+      if (rank == 0) weight_copier(p, smem, c);
     } else if (warp == kWarpSched) {
       schedule(p, c, cluster);
     }

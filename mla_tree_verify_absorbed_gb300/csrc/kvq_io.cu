@@ -19,6 +19,8 @@
 // warp takes a row, lane l its scale block l, two rows in flight per warp.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "kvq.cuh"
 #include "sm100.cuh"
 
@@ -37,6 +39,7 @@ struct IoParams {
   void* kv_c;
   void* k_pe;
   int64_t kv_c_stride, k_pe_stride;  // elements
+  bool wide;                         // kv_c rows are 32-byte aligned
   uint32_t* err;
 };
 
@@ -55,36 +58,73 @@ __device__ __forceinline__ void put_block_err(uint32_t* err, uint32_t e) {
   }
 }
 
-// The 16 latents of one scale block as fp32.
-template <class T>
-struct Block16;
-template <>
-struct Block16<__nv_bfloat16> {
-  uint4 v[2];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    v[0] = __ldcs(reinterpret_cast<const uint4*>(p));
-    v[1] = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+// Eight 32-bit words at once, a whole sector when the caller's rows are 32-byte
+// aligned (`wide`, the same for the whole call), else as two halves.  Rows pass
+// once, so they are kept out of L1.
+__device__ __forceinline__ void ld_words(const void* p, bool wide, uint32_t (&v)[8]) {
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldcs(static_cast<const uint4*>(p)), b = __ldcs(static_cast<const uint4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
-  __device__ __forceinline__ float at(int i) const {
-    const uint32_t w = (&v[i >> 3].x)[(i >> 1) & 3];
-    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+}
+__device__ __forceinline__ void st_words(void* p, bool wide, const uint32_t (&v)[8]) {
+  if (wide) {
+    sm100::st_global_v8(static_cast<uint32_t*>(p), v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+  } else {
+    __stcs(static_cast<uint4*>(p), make_uint4(v[0], v[1], v[2], v[3]));
+    __stcs(static_cast<uint4*>(p) + 1, make_uint4(v[4], v[5], v[6], v[7]));
   }
-};
-template <>
-struct Block16<float> {
-  float4 v[4];
-  __device__ __forceinline__ void load(const float* p) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __ldcs(reinterpret_cast<const float4*>(p) + i);
-  }
-  __device__ __forceinline__ float at(int i) const { return (&v[i >> 2].x)[i & 3]; }
-};
+}
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// The 16 latents of one scale block: as fp32, two by two, and the largest
+// magnitude (NaN when there is one).
+template <class T>
+struct Block16;
+template <>
+struct Block16<__nv_bfloat16> {
+  uint32_t v[8];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool wide) { ld_words(p, wide, v); }
+  __device__ __forceinline__ uint64_t two(int i) const { return sm100::pair(v[i] << 16, v[i] & 0xffff0000u); }
+  __device__ __forceinline__ float largest() const {
+    uint32_t m = v[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_nan_bf16x2(m, v[i] & 0x7fff7fffu);
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
+template <>
+struct Block16<float> {
+  uint32_t v[2][8];
+  __device__ __forceinline__ void load(const float* p, bool wide) {
+    ld_words(p, wide, v[0]);
+    ld_words(p + 8, wide, v[1]);
+  }
+  __device__ __forceinline__ uint64_t two(int i) const {
+    return sm100::pair(v[i >> 2][2 * (i & 3)], v[i >> 2][2 * (i & 3) + 1]);
+  }
+  __device__ __forceinline__ float largest() const {
+    float m = fabsf(__uint_as_float(v[0][0]));
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = max_nan(m, fabsf(__uint_as_float(v[i >> 3][i & 7])));
+    return m;
+  }
+};
 
 // The number whose fp32 bits end in the 4-bit code of q = x / s: adding
 // 1.5 * 2^23 + 8 rounds q to an integer, ties to even, in the low bits.
@@ -100,9 +140,7 @@ constexpr uint32_t kRoundSum = kRoundBits * 0x11111111u;
 template <class T>
 __device__ __forceinline__ void quantise(const Block16<T>& x, float mul, float inv_mul, uint32_t (&w)[2],
                                          uint32_t& byte, bool* finite) {
-  float a = fabsf(x.at(0));
-#pragma unroll
-  for (int i = 1; i < 16; ++i) a = max_nan(a, fabsf(x.at(i)));
+  const float a = x.largest();
   const float as = a * inv_mul;
   byte = (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(fminf(as, 4096.f), 7.f), __NV_SATFINITE, __NV_E4M3);
   w[0] = w[1] = 0u - kRoundSum;
@@ -110,12 +148,15 @@ __device__ __forceinline__ void quantise(const Block16<T>& x, float mul, float i
     // a normal scale is within 1/16 of max|x| / 7, so |q| < 7.5 without a clamp
     const float s = __uint_as_float((byte << 20) + (120u << 23)) * mul;  // e4m3 normal as fp32
     const float inv = __frcp_rn(s);
+    const uint64_t s2 = sm100::pair(-s, -s), inv2 = sm100::pair(inv, inv), round2 = sm100::pair(kRound, kRound);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float v = x.at(i);
-      const float q0 = v * inv;
-      const float q1 = fmaf(fmaf(-q0, s, v), inv, q0);
-      w[i >> 3] += __float_as_uint(q1 + kRound) << nib_shift(i & 7);
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t v = x.two(i);
+      const uint64_t q0 = sm100::mul_f32x2(v, inv2);
+      const uint64_t q1 = sm100::fma_f32x2(sm100::fma_f32x2(q0, s2, v), inv2, q0);
+      const uint64_t c = sm100::add_f32x2(q1, round2);
+      w[i >> 2] += (uint32_t)c << nib_shift(2 * (i & 3));
+      w[i >> 2] += (uint32_t)(c >> 32) << nib_shift(2 * (i & 3) + 1);
     }
     return;
   }
@@ -124,13 +165,13 @@ __device__ __forceinline__ void quantise(const Block16<T>& x, float mul, float i
     *finite = false;
     float m = 0.f;  // the block's maximum without NaN
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x.at(i)));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(sm100::lo_f32(x.two(i))), fabsf(sm100::hi_f32(x.two(i)))));
     byte = (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(fminf(m * inv_mul, 4096.f), 7.f), __NV_SATFINITE, __NV_E4M3);
   }
   const float s = byte >= 8u ? __uint_as_float((byte << 20) + (120u << 23)) : (float)byte * 0.001953125f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    float v = x.at(i) * inv_mul;
+    float v = ((i & 1) ? sm100::hi_f32(x.two(i >> 1)) : sm100::lo_f32(x.two(i >> 1))) * inv_mul;
     v = v == v ? fminf(fmaxf(v, -4096.f), 4096.f) : 0.f;
     const float q = byte ? fminf(fmaxf(__fdiv_rn(v, s), -7.f), 7.f) : 0.f;
     w[i >> 3] += __float_as_uint(q + kRound) << nib_shift(i & 7);
@@ -170,7 +211,7 @@ __global__ void __launch_bounds__(kIoThreads) kvq_write_kernel(const IoParams p)
         slot[d] = -1;
       }
       if (slot[d] >= 0) {
-        x[d].load(static_cast<const T*>(p.kv_c) + i * p.kv_c_stride + 16 * lane);
+        x[d].load(static_cast<const T*>(p.kv_c) + i * p.kv_c_stride + 16 * lane, p.wide);
         rope[d] = rope_pair(static_cast<const T*>(p.k_pe) + i * p.k_pe_stride + 2 * lane);
       }
     }
@@ -190,16 +231,20 @@ __global__ void __launch_bounds__(kIoThreads) kvq_write_kernel(const IoParams p)
   put_block_err(p.err, e);
 }
 
-__device__ __forceinline__ void put_latents(__nv_bfloat16* dst, const uint32_t (&v)[8], float) {
-  __stcs(reinterpret_cast<uint4*>(dst), make_uint4(v[0], v[1], v[2], v[3]));
-  __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(v[4], v[5], v[6], v[7]));
+__device__ __forceinline__ void put_latents(__nv_bfloat16* dst, const uint32_t (&v)[8], float, bool wide) {
+  st_words(dst, wide, v);
 }
-__device__ __forceinline__ void put_latents(float* dst, const uint32_t (&v)[8], float mul) {
+__device__ __forceinline__ void put_latents(float* dst, const uint32_t (&v)[8], float mul, bool wide) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    __stcs(reinterpret_cast<float4*>(dst) + i,
-           make_float4(__uint_as_float(v[2 * i] << 16) * mul, __uint_as_float(v[2 * i] & 0xffff0000u) * mul,
-                       __uint_as_float(v[2 * i + 1] << 16) * mul, __uint_as_float(v[2 * i + 1] & 0xffff0000u) * mul));
+  for (int h = 0; h < 2; ++h) {
+    uint32_t f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __float_as_uint(__uint_as_float(v[4 * h + i] << 16) * mul);
+      f[2 * i + 1] = __float_as_uint(__uint_as_float(v[4 * h + i] & 0xffff0000u) * mul);
+    }
+    st_words(dst + 8 * h, wide, f);
+  }
 }
 __device__ __forceinline__ void put_rope(__nv_bfloat16* dst, uint32_t v) { *reinterpret_cast<uint32_t*>(dst) = v; }
 __device__ __forceinline__ void put_rope(float* dst, uint32_t v) {
@@ -248,7 +293,7 @@ __global__ void __launch_bounds__(kIoThreads) kvq_read_kernel(const IoParams p) 
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = hmul2_bf16(v[q], mul2);
       }
-      put_latents(static_cast<T*>(p.kv_c) + i * p.kv_c_stride + 16 * lane, v, p.mul);
+      put_latents(static_cast<T*>(p.kv_c) + i * p.kv_c_stride + 16 * lane, v, p.mul, p.wide);
       put_rope(static_cast<T*>(p.k_pe) + i * p.k_pe_stride + 2 * lane, rope[d]);
     }
   }
@@ -302,6 +347,7 @@ mla_status make_io(const mla_kvq_cache* c, const mla_kvq_rows* r, void* ws, size
   p->k_pe = r->k_pe;
   p->kv_c_stride = r->kv_c_stride;
   p->k_pe_stride = r->k_pe_stride;
+  p->wide = aligned(r->kv_c, 32) && (r->kv_c_stride * el) % 32 == 0;
   p->err = static_cast<uint32_t*>(ws);
   return MLA_OK;
 }
@@ -309,10 +355,16 @@ mla_status make_io(const mla_kvq_cache* c, const mla_kvq_rows* r, void* ws, size
 // Blocks for n rows: one row per warp while they fit the GPU, then a
 // persistent grid of kPerSm blocks per SM.
 mla_status io_grid(int64_t n, int per_sm, int* grid) {
+  // looked up once per device: the two queries took as long as the launch
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> cached[kMaxDevices];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return MLA_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_CUDA;
+  sms = cached[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MLA_ERR_CUDA;
+    cached[dev].store(sms, std::memory_order_relaxed);
+  }
   int64_t g = (n + kIoWarps - 1) / kIoWarps;
   if (g > (int64_t)sms * per_sm) g = (int64_t)sms * per_sm;
   if (g > kErrMax) g = kErrMax;
@@ -351,7 +403,7 @@ extern "C" mla_status mla_kvq_read(const mla_kvq_cache* cache, const mla_kvq_row
   mla_status st = make_io(cache, dst, workspace, ws_bytes, &p, &noop);
   if (st != MLA_OK || noop) return st;
   int grid = 0;
-  st = io_grid(p.n, 8, &grid);
+  st = io_grid(p.n, 16, &grid);
   if (st != MLA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dst->dtype == MLA_BF16)

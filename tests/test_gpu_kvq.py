@@ -385,6 +385,14 @@ def test_rising_maximum():
     check_attn(p)
 
 
+@pytest.mark.parametrize("rows", [129, 150, 198, 225, 1, 33])
+def test_row_groups_with_few_rows_between_full_ones(rows):
+    # many sequences of one or two row groups, the last of them a fraction of 128 rows, so that a cluster's pieces
+    # alternate between groups that use all rows and groups that leave most out
+    n = 24
+    check_attn(problem(B=n, Q=1, H=rows, lens=[(97 * i) % 700 for i in range(n)], page=16, seed=25, tree="null"))
+
+
 WINDOWS = [
     dict(B=1, Q=1, H=4, lens=[500], window=1, sinks=0),
     dict(B=1, Q=1, H=4, lens=[500], window=1, sinks=1),
