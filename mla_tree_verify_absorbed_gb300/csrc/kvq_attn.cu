@@ -1105,6 +1105,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) p.err[kErrFirst + blockIdx.x] = c->err | (c->abort ? MLA_DEVERR_TIMEOUT : 0u);
+  // after an abort nobody has waited for the last copies into the value CTA:
+  // give them far longer than they take
+  if (c->abort) __nanosleep(100000);
   tc_fence_after();
   cluster_sync();  // no CTA leaves while its peer may still touch its shared memory
   if (warp == kWarpAux) tmem_dealloc_cta(c->tmem_base, kTmemCols);
