@@ -1118,106 +1118,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
 // ---------------------------------------------------------------------------
 // The pieces of a row group that several clusters shared:
 //   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k.
-// Row k of the grid looks at the boundary between clusters k - 1 and k; the
-// first boundary inside a row group merges it.  A block takes four rows: it
-// first gathers every piece's slot and weights, then each warp sums one half of
-// a row's columns with six pieces' loads in flight.
-constexpr int kMergeThreads = 256, kMergeRows = 4;
+// Every block reads where the clusters' intervals begin and lists the row
+// groups that a boundary cuts; the blocks then take these eight rows at a time.
+// For eight rows a block gathers every piece's slot and weights, and each warp
+// sums one half of a row's columns with four pieces' loads in flight.  (A block
+// for every eight rows behind every boundary, most of which find nothing to do,
+// took 6 us longer: several waves of blocks that wait for one load each.)
+constexpr int kMergeThreads = 512, kMergeRows = 8;
 constexpr int kMaxClusters = 128;
 static_assert(2 * kMaxClusters <= kErrMax, "an error word per CTA");
-__global__ void __launch_bounds__(kMergeThreads, 3) kvq_merge_kernel(const Params p) {
+__global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Params p, int chunks) {
+  __shared__ Start start[kMaxClusters + 1];
+  __shared__ int cut[kMaxClusters];                    // boundaries that are the first inside a row group
+  __shared__ int cuts;
   __shared__ int slot[kMaxClusters];                   // -1: an empty piece
-  __shared__ float weight[kMergeRows][kMaxClusters];   // lse, then exp(lse - max)
+  __shared__ float weight[kMergeRows][kMaxClusters];   // lse of each piece
+  const int tid = threadIdx.x;
+  if (tid == 0) cuts = 0;
   grid_dep_wait();
-  const Start* st = reinterpret_cast<const Start*>(p.starts);
-  const int k = (int)blockIdx.y + 1, tid = threadIdx.x;
-  // every load of this phase at once: the two clusters at the boundary, and
-  // for thread i the two around piece i, that of cluster k - 1 + i
-  const int c = min(k - 1 + tid, p.clusters - 1);
-  const Start s0 = st[k - 1], s = st[k], me = st[c], next = st[min(c + 1, p.clusters - 1)];
-  if (k >= s.n) return;
-  const int T = s.T;
-  const int L = kFixed + T;
-  const int64_t g = div_fast(s.x, L);
-  const int64_t base = g * L;
-  if (s.x == base) return;                 // the boundary lies between two row groups
-  if (s0.b == s.b && s0.x > base) return;  // not the first inside this one
-  const int r0 = (int)blockIdx.x * kMergeRows;
-  const int rows = (int)min((int64_t)kRG, p.rows - g * kRG) - r0;
-  if (rows <= 0) return;
-  // pieces: cluster k - 1 has units [0, x_k) of the row group, cluster i >= k [x_i, x_{i+1})
-  auto unit = [&](int i, const Start& q) -> int64_t {
-    return i < k ? 0 : i >= s.n || q.b != s.b || q.x - base > L ? L : q.x - base;
-  };
-  int n = 0;
-  bool whole = false;
-  if (tid < kMaxClusters && k - 1 + tid < s.n) {
-    const int64_t z0 = unit(c, me), z1 = unit(c + 1, next);
-    if (z0 < L) {
-      const int t0 = cut_tile(z0, T), t1 = cut_tile(z1, T);
-      whole = t0 == 0 && t1 == T;
-      slot[tid] = t1 > t0 ? 2 * c + (t0 == 0) : -1;
-      n = 1;
-    }
-  }
-  n = __syncthreads_count(n);
-  if (__syncthreads_or(whole)) return;  // one cluster has it all: it stored the results
-  for (int i = tid; i < n * kMergeRows; i += kMergeThreads) {
-    const int pc = i >> 2, r = i & 3;
-    weight[r][pc] = slot[pc] >= 0 && r < rows ? p.part_lse[(int64_t)slot[pc] * kRG + r0 + r] : -INFINITY;
+  if (tid < p.clusters) start[tid] = reinterpret_cast<const Start*>(p.starts)[tid];
+  __syncthreads();
+  const int clusters = start[0].n;
+  if (tid > 0 && tid < clusters) {
+    const Start s0 = start[tid - 1], s = start[tid];
+    const int64_t base = div_fast(s.x, kFixed + s.T) * (kFixed + s.T);
+    if (s.x > base && (s0.b != s.b || s0.x <= base)) cut[atomicAdd(&cuts, 1)] = tid;
   }
   __syncthreads();
   const int warp = tid >> 5, lane = tid & 31;
-  const int r = warp >> 1;
-  float m = -INFINITY, sum = 0.f;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, weight[r][i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  for (int i = lane; i < n; i += 32) sum += __expf(weight[r][i] - m);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (r >= rows) return;
-  // 256 columns: two float4 a lane
-  const int col = (warp & 1) * 256 + 4 * lane;
-  const float* part = p.part_o + (int64_t)(r0 + r) * kDl + col;
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  constexpr int kDeep = 6;
-  for (int i0 = 0; i0 < n; i0 += kDeep) {
-    float4 v[kDeep][2];
-    float w[kDeep];
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      const int i = i0 + d, sl = i < n ? slot[i] : -1;
-      w[d] = sl >= 0 ? __expf(weight[r][i] - m) : 0.f;
-      if (sl >= 0) {
-        const float4* src = reinterpret_cast<const float4*>(part + (int64_t)sl * kRG * kDl);
-        v[d][0] = src[0];
-        v[d][1] = src[32];
-      } else {
-        v[d][0] = v[d][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // tasks in an order that depends on the atomics, results not
+  for (int task = blockIdx.x; task < cuts * chunks; task += gridDim.x) {
+    const int k = cut[task / chunks], r0 = (task % chunks) * kMergeRows;
+    const Start s = start[k];
+    const int T = s.T, L = kFixed + T;
+    const int64_t g = div_fast(s.x, L), base = g * L;
+    const int rows = (int)min((int64_t)kRG, p.rows - g * kRG) - r0;
+    // pieces: cluster k - 1 has units [0, x_k) of the row group, cluster i >= k [x_i, x_{i+1})
+    auto unit = [&](int i) -> int64_t {
+      return i < k ? 0 : i >= clusters || start[i].b != s.b || start[i].x - base > L ? L : start[i].x - base;
+    };
+    bool mine = false, whole = false;
+    const int c = k - 1 + tid;
+    if (c < clusters) {
+      const int64_t z0 = unit(c), z1 = unit(c + 1);
+      mine = z0 < L;
+      if (mine) {
+        const int t0 = cut_tile(z0, T), t1 = cut_tile(z1, T);
+        whole = t0 == 0 && t1 == T;
+        slot[tid] = t1 > t0 ? 2 * c + (t0 == 0) : -1;
       }
     }
+    const int n = __syncthreads_count(mine);
+    // when one cluster has it all it stored the results
+    if (__syncthreads_or(whole) || rows <= 0) continue;
+    for (int i = tid; i < n * kMergeRows; i += kMergeThreads) {
+      const int pc = i / kMergeRows, r = i % kMergeRows;
+      weight[r][pc] = slot[pc] >= 0 && r < rows ? p.part_lse[(int64_t)slot[pc] * kRG + r0 + r] : -INFINITY;
+    }
+    __syncthreads();
+    const int r = warp >> 1;
+    if (r < rows) {
+      float m = -INFINITY, sum = 0.f;
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, weight[r][i]);
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int i = lane; i < n; i += 32) sum += __expf(weight[r][i] - m);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      // 256 columns: two float4 a lane
+      const int col = (warp & 1) * 256 + 4 * lane;
+      const float* part = p.part_o + (int64_t)(r0 + r) * kDl + col;
+      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      constexpr int kDeep = 4;
+      for (int i0 = 0; i0 < n; i0 += kDeep) {
+        float4 v[kDeep][2];
+        float w[kDeep];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+          const int i = i0 + d, sl = i < n ? slot[i] : -1;
+          w[d] = sl >= 0 ? __expf(weight[r][i] - m) : 0.f;
+          v[d][0] = v[d][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (sl >= 0) {
+            const float4* src = reinterpret_cast<const float4*>(part + (int64_t)sl * kRG * kDl);
+            v[d][0] = src[0];
+            v[d][1] = src[32];
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            acc[h].x = fmaf(w[d], v[d][h].x, acc[h].x);
+            acc[h].y = fmaf(w[d], v[d][h].y, acc[h].y);
+            acc[h].z = fmaf(w[d], v[d][h].z, acc[h].z);
+            acc[h].w = fmaf(w[d], v[d][h].w, acc[h].w);
+          }
+        }
+      }
+      const float inv = 1.f / sum;
+      const int64_t orow = (int64_t)s.b * p.rows + g * kRG + r0 + r;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        acc[h].x = fmaf(w[d], v[d][h].x, acc[h].x);
-        acc[h].y = fmaf(w[d], v[d][h].y, acc[h].y);
-        acc[h].z = fmaf(w[d], v[d][h].z, acc[h].z);
-        acc[h].w = fmaf(w[d], v[d][h].w, acc[h].w);
+        uint2 o;
+        o.x = pack_bf16(acc[h].x * inv, acc[h].y * inv);
+        o.y = pack_bf16(acc[h].z * inv, acc[h].w * inv);
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + col + 128 * h) = o;
       }
+      if (p.lse && (warp & 1) == 0 && lane == 0) p.lse[orow] = m + logf(sum);
     }
+    __syncthreads();  // slot and weight are reused
   }
-  const float inv = 1.f / sum;
-  const int64_t orow = (int64_t)s.b * p.rows + g * kRG + r0 + r;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint2 o;
-    o.x = pack_bf16(acc[h].x * inv, acc[h].y * inv);
-    o.y = pack_bf16(acc[h].z * inv, acc[h].w * inv);
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + col + 128 * h) = o;
-  }
-  if (p.lse && (warp & 1) == 0 && lane == 0) p.lse[orow] = m + logf(sum);
 }
 
 namespace {
@@ -1398,8 +1408,10 @@ extern "C" mla_status mla_kvq_attn(const mla_kvq_attn_args* a, void* workspace, 
     return MLA_ERR_CUDA;
   if (launch_kernel(kvq_attn_kernel, dim3(2 * n), dim3(kThreads), kSmemAlloc, s, false, p, maps) != cudaSuccess)
     return MLA_ERR_CUDA;
-  if (n > 1 && launch_kernel(kvq_merge_kernel, dim3(((p.rows < kRG ? p.rows : kRG) + kMergeRows - 1) / kMergeRows, n - 1), dim3(kMergeThreads), 0, s,
-                             true, p) != cudaSuccess)
+  // two blocks per SM of the clusters, fewer when even n - 1 cut row groups make fewer tasks
+  const int chunks = ((p.rows < kRG ? p.rows : kRG) + kMergeRows - 1) / kMergeRows;
+  const int blocks = (n - 1) * chunks < 4 * n ? (n - 1) * chunks : 4 * n;
+  if (n > 1 && launch_kernel(kvq_merge_kernel, dim3(blocks), dim3(kMergeThreads), 0, s, true, p, chunks) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }
