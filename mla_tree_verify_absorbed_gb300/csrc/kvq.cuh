@@ -135,24 +135,32 @@ struct Params {
   float* part_o;               // [2 clusters][rows of a group][512], normalised
 };
 
-// MLA_DEVERR_* bits of sequence b's tables, read before anything of the call
-// is.  With kv_indptr[0] == 0 and every span equal to its sequence's length,
-// all reads stay in kv_indices[0 .. kv_indptr[B]).
-__device__ __forceinline__ uint32_t check_sequence(const Params& p, int b) {
-  const int64_t P = p.prefix_lens[b];
+// What a call needs of sequence b's tables before anything else, and the
+// MLA_DEVERR_* bits they deserve.  With kv_indptr[0] == 0 and every span equal
+// to its sequence's length, all reads stay in kv_indices[0 .. kv_indptr[B]).
+struct Sequence {
+  int32_t P;      // prefix length; -1: unused
+  int64_t entry;  // its first table entry
+  uint32_t err;
+};
+__device__ __forceinline__ Sequence read_sequence(const Params& p, int b) {
+  Sequence s;
+  s.P = p.prefix_lens[b];
   int64_t lo = 0, hi = 0;
   if (p.page_size == 1) {
     lo = p.kv_indptr[b];
     hi = p.kv_indptr[b + 1];
   }
-  uint32_t e = P < -1 ? MLA_DEVERR_PREFIX : 0u;
-  const int64_t N = P < 0 ? 0 : P + p.Q;
+  s.err = s.P < -1 ? MLA_DEVERR_PREFIX : 0u;
+  const int64_t N = s.P < 0 ? 0 : (int64_t)s.P + p.Q;
   if (p.page_size == 1) {
-    if ((b == 0 && lo != 0) || lo < 0 || hi - lo != N) e |= MLA_DEVERR_INDPTR;
-  } else if (N > (int64_t)p.max_pages * p.page_size) {
-    e |= MLA_DEVERR_PAGES;
+    s.entry = lo;
+    if ((b == 0 && lo != 0) || lo < 0 || hi - lo != N) s.err |= MLA_DEVERR_INDPTR;
+  } else {
+    s.entry = (int64_t)b * p.max_pages;
+    if (N > (int64_t)p.max_pages * p.page_size) s.err |= MLA_DEVERR_PAGES;
   }
-  return e;
+  return s;
 }
 
 // What one node sees of the tree: the mask of its visible nodes and its depth.

@@ -182,7 +182,9 @@ struct alignas(16) Ctl {
   int64_t scan[kThreads / 32];
   int64_t left;                // units of this cluster's interval
   int64_t start_x;             // this cluster's first unit within sequence start_b
-  int start_b, start_T;        // that sequence, and its tiles
+  int start_b, start_T;        // that sequence, its tiles,
+  int start_P;                 // its prefix length
+  int64_t start_entry;         // and its first table entry
   uint32_t tmem_base;
   int abort;
   int abort_site;
@@ -242,9 +244,8 @@ struct Tiles {
   int64_t lo;  // positions in [sinks, lo) are seen by no node
   __device__ __forceinline__ int at(int v) const { return v < ns ? v : v - ns + tw; }
 };
-__device__ __forceinline__ Tiles tiles_of(const Params& p, int b) {
+__device__ __forceinline__ Tiles tiles_of(const Params& p, int64_t P) {
   Tiles t;
-  const int64_t P = p.prefix_lens[b];
   t.lo = 0;
   t.ns = t.tw = t.T = 0;
   if (P < 0) return t;
@@ -310,8 +311,10 @@ __device__ void schedule(const Params& p, Ctl* c, int cluster) {
     ++seg;
     return true;
   };
+  Sequence sq{c->start_P, c->start_entry, 0u};
   for (int b = c->start_b; left > 0 && b < p.B; ++b, x = 0) {
-    const Tiles tl = tiles_of(p, b);
+    if (b != c->start_b) sq = read_sequence(p, b);
+    const Tiles tl = tiles_of(p, sq.P);
     if (tl.T == 0) continue;
     const int L = kFixed + tl.T;
     Piece pc;
@@ -319,9 +322,9 @@ __device__ void schedule(const Params& p, Ctl* c, int cluster) {
     pc.ns = tl.ns;
     pc.tw = tl.tw;
     pc.lo = (int32_t)tl.lo;
-    pc.P = p.prefix_lens[b];
+    pc.P = sq.P;
     pc.N = (int32_t)((int64_t)pc.P + p.Q);
-    pc.entry = p.page_size == 1 ? (int64_t)p.kv_indptr[b] : (int64_t)b * p.max_pages;
+    pc.entry = sq.entry;
     for (int g = (int)div_fast(x, L); g < p.groups && left > 0; ++g) {
       const int64_t z = x - (int64_t)g * L;
       const int64_t take = L - z < left ? L - z : left;
@@ -368,12 +371,17 @@ __device__ int make_split(const Params& p, Ctl* c, int cluster) {
   const int b0 = tid * per, b1 = min(b0 + per, p.B);
   uint32_t e = 0;
   int64_t sum = 0;
+  Sequence q;
+  int T = 0;
+  auto units = [&](int b) -> int64_t {  // and q, T
+    q = read_sequence(p, b);
+    T = q.err ? 0 : tiles_of(p, q.P).T;
+    return T ? (int64_t)p.groups * (kFixed + T) : 0;
+  };
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const uint32_t eb = check_sequence(p, b);
-    e |= eb;
-    const int T = eb ? 0 : tiles_of(p, b).T;
-    sum += T ? (int64_t)p.groups * (kFixed + T) : 0;
+    sum += units(b);
+    e |= q.err;
   }
   auto warp_scan = [&](int64_t v) {
 #pragma unroll
@@ -397,18 +405,20 @@ __device__ int make_split(const Params& p, Ctl* c, int cluster) {
     const int64_t w0 = first_unit(total, n, cluster);
     if (w0 >= at && w0 < at + sum) {
       c->left = first_unit(total, n, cluster + 1) - w0;
+      int b = b0;
+      if (per > 1) {  // q and T are those of the thread's last sequence
 #pragma unroll 1
-      for (int b = b0; b < b1; ++b) {
-        const int T = tiles_of(p, b).T;
-        const int64_t u = T ? (int64_t)p.groups * (kFixed + T) : 0;
-        if (w0 < at + u) {
-          c->start_b = b;
-          c->start_T = T;
-          c->start_x = w0 - at;
-          break;
+        for (;; ++b) {
+          const int64_t u = units(b);
+          if (w0 < at + u) break;
+          at += u;
         }
-        at += u;
       }
+      c->start_b = b;
+      c->start_x = w0 - at;
+      c->start_T = T;
+      c->start_P = q.P;
+      c->start_entry = q.entry;
     }
   }
   __syncthreads();
@@ -508,11 +518,13 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     // with the first half all scales, into the buffer of this turn's parity.
     // Past the piece's last tile nothing is fetched: what the next piece
     // fetches first must not race with it.
+    const uint8_t* rows[kTok / 4];  // of the tile fetched last: piece r7 of tokens ch, ch + 4, ..
     auto fetch = [&](uint32_t slot, int h, uint32_t turn, bool more) {
 #pragma unroll
-      for (int i = 0; more && i < kTok / 4; ++i) {
+      for (int i = 0; i < kTok / 4; ++i) {
         const int token = 4 * i + ch;
-        cp_async_16(raw + token * kRawRow + 128 * h + 16 * r7, row_of(slot, token) + 128 * h + 16 * r7);
+        if (h == 0) rows[i] = row_of(slot, token) + 16 * r7;
+        if (more) cp_async_16(raw + token * kRawRow + 128 * h + 16 * r7, rows[i] + 128 * h);
       }
       const int token = lane >> 1;
       const uint8_t* row = row_of(slot, token % kTok);
@@ -650,7 +662,7 @@ __device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* s
   }
   __syncwarp();
   if (!wait_warp(&c->q_in, seg & 1u, c, kSiteQIn)) return false;
-#pragma unroll 1
+#pragma unroll 3
   for (int ck = 0; ck < 9; ++ck) {
     const uint32_t src = smem_u32(smem) + ck * kPBytes + r * 128;
     uint32_t w[16];
