@@ -96,10 +96,11 @@ mla_status mla_kvq_read(const mla_kvq_cache *cache, const mla_kvq_rows *dst, voi
 typedef struct {
     int B;                      /* sequences, >= 0 (0 = no-op) */
     int Q;                      /* nodes per sequence, 0..64 (0 = no-op) */
-    int H;                      /* heads, >= 1 */
+    int H;                      /* heads, >= 1; Q * H up to 2^24 and B * Q * H up to INT32_MAX */
     mla_kvq_cache cache;
     const void *q_lat;          /* bf16 [B][Q][H][512], contiguous */
-    const void *q_pe;           /* bf16 [B][Q][H][64], contiguous */
+    const void *q_pe;           /* bf16 [B][Q][H][64], contiguous; times 2^-exponent in bf16, which is exact
+                                   for magnitudes 2^-94 .. 2^95 (and for any with exponent 0) */
     int page_size;              /* 1: kv_indptr/kv_indices;  > 1: block_table */
     const int32_t *kv_indptr;   /* [B+1]; kv_indptr[0] == 0, spans prefix_lens[b]+Q (0 for an unused sequence) */
     const int32_t *kv_indices;  /* [kv_indptr[B]] pool slots */
@@ -110,7 +111,7 @@ typedef struct {
     const int32_t *tree_parent; /* [B][Q], parent[i] in [-1, i-1]; NULL: each node's parent is the node before */
     int window;                 /* 0: none; W > 0: see below */
     int sinks;                  /* first tokens that stay visible under a window, >= 0; 0 without a window */
-    float scale;                /* score scale, finite and > 0 */
+    float scale;                /* score scale, > 0; scale * 2^exponent * log2(e) must be a normal fp32 number */
     void *out;                  /* bf16 [B][Q][H][512] */
     float *lse;                 /* [B][Q][H], natural log; may be NULL */
 } mla_kvq_attn_args;
@@ -127,10 +128,12 @@ typedef struct {
  * enter the products exactly, the softmax weights rounded to 11 bits.  lse is
  * natural-log; equal arguments give equal bytes.  Enqueues the attention
  * kernel and a kernel that merges the pieces of rows that several clusters
- * shared. A bad table (MLA_DEVERR_PREFIX, _INDPTR, _PAGES: found before any
+ * shared.  A bad table (MLA_DEVERR_PREFIX, _INDPTR, _PAGES: found before any
  * work) leaves out and lse as they were; a slot outside the pool or a parent
  * outside [-1, i-1] (MLA_DEVERR_SLOT, _PARENT) is read as slot 0 or -1 and
- * leaves that sequence's outputs unspecified. No access leaves the pool. */
+ * leaves that sequence's outputs unspecified. No access leaves the pool. A wait
+ * that outlasts two seconds ends the kernel with MLA_DEVERR_TIMEOUT; the
+ * outputs are then unspecified. */
 mla_status mla_kvq_attn(const mla_kvq_attn_args *args, void *workspace, size_t ws_bytes, mla_stream_t stream);
 
 /* Bytes of workspace that mla_kvq_attn needs on the current device, 256-byte

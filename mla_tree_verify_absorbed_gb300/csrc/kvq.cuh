@@ -130,7 +130,7 @@ struct Params {
   int clusters;                // clusters launched
   // workspace
   uint32_t* err;               // word 0, and the error words from kErrFirst on
-  int32_t* starts;             // [clusters + 1][4]: see Start
+  void* starts;                // [clusters]: see Start
   float* part_lse;             // [2 clusters][rows of a group], natural log
   float* part_o;               // [2 clusters][rows of a group][512], normalised
 };

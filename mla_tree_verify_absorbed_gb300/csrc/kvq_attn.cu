@@ -160,7 +160,7 @@ struct alignas(16) Ctl {
   uint64_t empty[4];           // the MMAs reading it are complete
   uint64_t s_full[kSBufs];     // score: S tile in TMEM
   uint64_t s_free[kSBufs];         // score: softmax has loaded S (4 row warps)
-  uint64_t q_ready;            // score: queries in TMEM, stages free again (8 row warps)
+  uint64_t q_ready[2];         // score: queries in TMEM, stages free again (8 row warps); by piece parity
   uint64_t q_in;               // score: queries copied (copy bytes)
   uint64_t m_ready[2][4];      // score: running maxima after a tile written (per lane quadrant, 1 warp)
   uint64_t p_free[kPBufs];     // score: the PV MMAs that read rank 1's buffer are complete (its commit)
@@ -484,10 +484,13 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
   for_pieces(c, [&](const Piece& pc) {
     int t = pc.t0 + (int)((grp ^ j) & 1u);
     j += (uint32_t)(pc.t1 - pc.t0);
-    const uint32_t q_phase = seg++ & 1u;
-    // every warp waits for every piece's queries: a phase left out could be
-    // taken for the next one
-    if (t >= pc.t1) return !kScore || wait_warp(&c->q_ready, q_phase, c, kSiteQReady);
+    const uint32_t q_bar = seg & 1u, q_phase = (seg >> 1) & 1u;
+    ++seg;
+    // Every warp waits for every piece's queries: a phase left out could be
+    // taken for the next one.  A group without a tile in a piece may come late
+    // to that wait, but it has the tile of the next piece, so the queries of
+    // the piece after that, which use the same barrier, cannot overtake it.
+    if (t >= pc.t1) return !kScore || wait_warp(&c->q_ready[q_bar], q_phase, c, kSiteQReady);
     uint32_t turn = (j - (uint32_t)(pc.t1 - t)) >> 1;  // tiles this group has taken before
     const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
     // Pool row of token kTok pw + lane % kTok of tile v, in two steps: the table
@@ -495,14 +498,14 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     // tile later, the slot.  Positions that no node sees read slot 0, under a
     // weight of zero.
     auto entry_of = [&](int v) -> int32_t {
-      const int pos = pc.tile(v) * kTK + kTok * pw + lane % kTok;
-      if (v >= pc.t1 || pos >= pc.N || (pos < pc.lo && pos >= p.sinks)) return -2;
-      return __ldg(idx + (p.page_size == 1 ? (uint32_t)pos : (uint32_t)pos / (uint32_t)p.page_size));
+      const uint32_t pos = (uint32_t)pc.tile(v) * kTK + kTok * pw + lane % kTok;
+      if (v >= pc.t1 || pos >= (uint32_t)pc.N || (pos < (uint32_t)pc.lo && pos >= (uint32_t)p.sinks)) return -2;
+      return __ldg(idx + (p.page_size == 1 ? pos : pos / (uint32_t)p.page_size));
     };
     auto slot_of = [&](int32_t e, int v) -> uint32_t {
       int64_t s = e;
       if (p.page_size > 1) {
-        const uint32_t pos = (uint32_t)(pc.tile(v) * kTK + kTok * pw + lane % kTok);
+        const uint32_t pos = (uint32_t)pc.tile(v) * kTK + kTok * pw + lane % kTok;
         s = s * p.page_size + pos % (uint32_t)p.page_size;
       }
       if (e < 0 || s >= p.slots) {
@@ -538,7 +541,7 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     for (int h = 0; h < 2; ++h) fetch(slot, h, turn, true);
     int32_t ent = entry_of(t + 2);
     // until then the queries pass through the stages
-    if (kScore && !wait_warp(&c->q_ready, q_phase, c, kSiteQReady)) return false;
+    if (kScore && !wait_warp(&c->q_ready[q_bar], q_phase, c, kSiteQReady)) return false;
 #pragma unroll 1
     for (int h = 0; t < pc.t1; h ^= 1) {
       cp_async_wait_group<1>();  // this half's pieces, of this lane
@@ -606,7 +609,7 @@ __device__ void score_mma(uint8_t* smem, Ctl* c) {
   const bool leader = elect_one();
   uint32_t j = 0, seg = 0;
   for_pieces(c, [&](const Piece& pc) {
-    if (!wait_warp(&c->q_ready, seg & 1u, c, kSiteQReady)) return false;
+    if (!wait_warp(&c->q_ready[seg & 1u], (seg >> 1) & 1u, c, kSiteQReady)) return false;
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
       const uint32_t par = j & 1u, turn = j >> 1, sb = j % kSBufs;
@@ -718,13 +721,14 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
     if (!stage_queries(p, maps, smem, c, pc, warp, seg)) return false;
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&c->q_ready);
+    if (lane == 0) mbar_arrive(&c->q_ready[seg & 1u]);
     // rows past the last take the last one's mask: their results are dropped
     const NodeView nv = node_view_warp(p, pc.b, (live ? row : p.rows - 1) / p.H, P, &bad);
-    // prefix positions up to this one are outside the window (unless sinks);
-    // lengths fit 32 bits with the nodes counted, so these do too
-    const int past = p.window > 0 ? P - p.window + nv.depth : -1;
-    const int past_any = p.window > 0 ? P - p.window + nq - 1 : -1;
+    // Prefix positions up to this one are outside the window (unless sinks).
+    // Lengths fit 32 bits with the nodes counted, so these do too, and so do
+    // their differences from a position as long as they are not below -1.
+    const int past = p.window > 0 ? max(P - p.window + nv.depth, -1) : -1;
+    const int past_any = p.window > 0 ? max(P - p.window + nq - 1, -1) : -1;
 
     // m: running maximum of the scaled scores (base-2 units) as of this
     // group's last tile; l: its sum of the shifted weights before rounding
@@ -739,8 +743,8 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
       if (idle) {
         // every barrier's phases count on: the next piece may use the rows
         if (lane == 0) {
-          mbar_arrive(&c->s_free[sb]);
           mbar_arrive(&c->m_ready[wg][wq]);
+          mbar_arrive(&c->s_free[sb]);
         }
         if (!wait_warp(&c->ps_free[ps], ((i / kPStages) & 1u) ^ 1u, c, kSitePsFree)) return false;
         if (lane == 0) mbar_arrive(&c->p_staged[ps]);
@@ -1036,7 +1040,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
       mbar_init(&c->p_staged[q], kRowWarps / 2);
       mbar_init(&c->ps_free[q], 1);
     } else if (warp == 12) {
-      mbar_init(&c->q_ready, kRowWarps);
+      mbar_init(&c->q_ready[0], kRowWarps);
+      mbar_init(&c->q_ready[1], kRowWarps);
       mbar_init(&c->q_in, 1);
       mbar_init(&c->fin_free, 32 * kRowWarps);
       mbar_init(&c->fin_full, 32 * kRowWarps);
@@ -1069,7 +1074,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
   const bool work = cluster < n;
   if (threadIdx.x == 0) {
     if (rank == 0) {
-      Start* st = reinterpret_cast<Start*>(p.starts) + cluster;
+      Start* st = static_cast<Start*>(p.starts) + cluster;
       *st = Start{c->start_x, c->start_b, c->start_T, n > 0 ? n : 0, {0, 0, 0}};
     }
     if (blockIdx.x == 0) p.err[0] = gridDim.x;
@@ -1140,7 +1145,7 @@ constexpr int kMergeThreads = 512, kMergeRows = 8;
 constexpr int kMaxClusters = 128;
 static_assert(2 * kMaxClusters <= kErrMax, "an error word per CTA");
 __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Params p, int chunks) {
-  __shared__ Start start[kMaxClusters + 1];
+  __shared__ Start start[kMaxClusters];
   __shared__ int cut[kMaxClusters];                    // boundaries that are the first inside a row group
   __shared__ int cuts;
   __shared__ int slot[kMaxClusters];                   // -1: an empty piece
@@ -1148,7 +1153,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
   const int tid = threadIdx.x;
   if (tid == 0) cuts = 0;
   grid_dep_wait();
-  if (tid < p.clusters) start[tid] = reinterpret_cast<const Start*>(p.starts)[tid];
+  if (tid < p.clusters) start[tid] = static_cast<const Start*>(p.starts)[tid];
   __syncthreads();
   const int clusters = start[0].n;
   if (tid > 0 && tid < clusters) {
@@ -1246,6 +1251,10 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+float score_factor(const mla_kvq_attn_args& a) {
+  return (float)std::ldexp((double)a.scale * 1.4426950408889634, a.cache.exponent);
+}
+
 mla_status validate_shape(const mla_kvq_attn_args* a) {
   if (!a) return MLA_ERR_INVALID_ARG;
   if (a->B < 0 || a->Q < 0 || a->H < 1) return MLA_ERR_INVALID_ARG;
@@ -1270,8 +1279,9 @@ mla_status validate_call(const mla_kvq_attn_args* a) {
     if ((int64_t)a->max_pages * a->page_size > INT32_MAX) return MLA_ERR_INVALID_ARG;
   }
   if (a->window < 0 || a->sinks < 0 || (a->window == 0 && a->sinks != 0)) return MLA_ERR_INVALID_ARG;
-  // a zero scale would turn masked scores of -inf into NaN
-  if (!std::isfinite(a->scale) || !(a->scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  // the factor of the scores in base-2 units: rounded to zero or infinity it
+  // would turn masked scores of -inf, or scores of 0, into NaN
+  if (!std::isfinite(a->scale) || !(a->scale > 0.f) || !std::isnormal(score_factor(*a))) return MLA_ERR_INVALID_ARG;
   return MLA_OK;
 }
 
@@ -1341,7 +1351,7 @@ struct Layout {
 Layout layout(int clusters) {
   Layout l;
   size_t o = MLA_KVQ_WORKSPACE_BYTES;
-  l.starts = o;    o = align256(o + sizeof(Start) * ((size_t)clusters + 1));
+  l.starts = o;    o = align256(o + sizeof(Start) * (size_t)clusters);
   l.part_lse = o;  o = align256(o + sizeof(float) * 2 * (size_t)clusters * kRG);
   l.part_o = o;    o = align256(o + sizeof(float) * 2 * (size_t)clusters * kRG * kDl);
   l.total = o;
@@ -1370,7 +1380,7 @@ Params make_params(const mla_kvq_attn_args* a, void* ws, int clusters) {
   p.sinks = a->sinks;
   const int e = a->cache.exponent;
   p.qpe_mul = (float)std::ldexp(1.0, -e);
-  p.scale_log2 = (float)std::ldexp((double)a->scale * 1.4426950408889634, e);
+  p.scale_log2 = score_factor(*a);
   p.out_mul = (float)std::ldexp(1.0, e);
   p.out = a->out;
   p.lse = a->lse;
@@ -1380,7 +1390,7 @@ Params make_params(const mla_kvq_attn_args* a, void* ws, int clusters) {
   const Layout l = layout(clusters);
   char* base = static_cast<char*>(ws);
   p.err = reinterpret_cast<uint32_t*>(base);
-  p.starts = reinterpret_cast<int32_t*>(base + l.starts);
+  p.starts = base + l.starts;
   p.part_lse = reinterpret_cast<float*>(base + l.part_lse);
   p.part_o = reinterpret_cast<float*>(base + l.part_o);
   return p;
