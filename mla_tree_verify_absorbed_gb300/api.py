@@ -7,6 +7,7 @@ is loaded on first use and a missing build raises -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -640,13 +641,23 @@ def kvq_alloc(slots: int, exponent: int = 0, device="cuda") -> QuantCache:
     return QuantCache(rows, exponent)
 
 
-def _one_device(**tensors):
-    """Every tensor on the same CUDA device; returns it."""
+def _one_device(workspace=None, **tensors):
+    """Every tensor on the same CUDA device, the workspace in one piece."""
+    tensors["workspace"] = workspace
     _on_cuda(**tensors)
     devs = {t.device for t in tensors.values() if t is not None}
     if len(devs) != 1:
         raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    return devs.pop()
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
+def _made_on(stream):
+    """Where arrays that a call makes are allocated and filled: on its stream,
+    so that the fill precedes the kernels and the memory, once released, is not
+    given to another stream's work before they are done."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _kvq_launch(what: str, f, dev, stream, *args):
@@ -684,7 +695,8 @@ def _kvq_rows(what: str, f, cache: QuantCache, kv_c, k_pe, slots, workspace, str
         _one_device(rows=cache.rows, kv_c=kv_c, k_pe=k_pe, slots=slots, workspace=workspace)
     dev = cache.rows.device
     if workspace is None:
-        workspace = alloc_workspace(KVQ_WORKSPACE_BYTES, dev)
+        with _made_on(stream):
+            workspace = alloc_workspace(KVQ_WORKSPACE_BYTES, dev)
     n = kv_c.size(0)
     r = MlaKvqRows(n, MLA_BF16 if kv_c.dtype is torch.bfloat16 else MLA_FP32, kv_c.data_ptr(), k_pe.data_ptr(),
                    kv_c.stride(0) if n > 1 else 512, k_pe.stride(0) if n > 1 else 64, slots.data_ptr())
@@ -694,8 +706,9 @@ def _kvq_rows(what: str, f, cache: QuantCache, kv_c, k_pe, slots, workspace, str
 
 def kvq_write(cache: QuantCache, kv_c, k_pe, slots, workspace=None, stream=None, check: bool = True):
     """Run mla_kvq_write: quantise row i of kv_c [n][512] and k_pe [n][64]
-    (bf16 or fp32, any row stride) into pool slot slots[i] (int32; -1 skips).
-    Returns the workspace (kvq_check reads its error bits).  check=False skips
+    (bf16 or fp32; rows 16-byte aligned, any such row stride) into pool slot
+    slots[i] (int32; -1 skips, the others differ from each other).  Returns the
+    workspace (kvq_check reads its error bits).  check=False skips
     the tensor checks, for a loop that already passed them."""
     return _kvq_rows("mla_kvq_write", load().mla_kvq_write, cache, kv_c, k_pe, slots, workspace, stream, check)
 
@@ -704,15 +717,20 @@ def kvq_read(cache: QuantCache, slots, dtype: str = "bf16", kv_c=None, k_pe=None
              check: bool = True):
     """Run mla_kvq_read: the rows that pool slots ``slots`` stand for, exactly,
     as ``dtype`` ("bf16" or "fp32"; that of kv_c when given).  Rows with slot
-    -1 keep what the given arrays hold (zeros in arrays made here).  Returns
-    (kv_c [n][512], k_pe [n][64], workspace)."""
+    -1 keep what the given arrays hold (zeros in arrays made here, on
+    ``stream``).  Returns (kv_c [n][512], k_pe [n][64], workspace)."""
     import torch
+    if check:
+        cache.check()
+        if dtype not in ("bf16", "fp32"):
+            raise ValueError(f'dtype {dtype!r}, expected "bf16" or "fp32"')
     if kv_c is None or k_pe is None:
         dt = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype] if kv_c is None else kv_c.dtype
-        if kv_c is None:
-            kv_c = torch.zeros((slots.shape[0], 512), dtype=dt, device=cache.rows.device)
-        if k_pe is None:
-            k_pe = torch.zeros((slots.shape[0], 64), dtype=dt, device=cache.rows.device)
+        with _made_on(stream):
+            if kv_c is None:
+                kv_c = torch.zeros((slots.shape[0], 512), dtype=dt, device=cache.rows.device)
+            if k_pe is None:
+                k_pe = torch.zeros((slots.shape[0], 64), dtype=dt, device=cache.rows.device)
     ws = _kvq_rows("mla_kvq_read", load().mla_kvq_read, cache, kv_c, k_pe, slots, workspace, stream, check)
     return kv_c, k_pe, ws
 
@@ -748,6 +766,9 @@ class KvqInputs:
         import torch
         B, Q, H = self.B, self.Q, self.H
         self.cache.check()
+        for name in ("page_size", "window", "sinks"):
+            if not -2 ** 31 <= getattr(self, name) < 2 ** 31:
+                raise ValueError(f"{name} {getattr(self, name)} outside 32 bits")
         _need(self.q_lat, "q_lat", torch.bfloat16, (B, Q, H, 512))
         _need(self.q_pe, "q_pe", torch.bfloat16, (B, Q, H, 64))
         _need(self.prefix_lens, "prefix_lens", torch.int32, (B,))
@@ -786,21 +807,24 @@ def kvq_workspace_size(ki: KvqInputs) -> int:
 def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, check: bool = True):
     """Run mla_kvq_attn; returns (out [B,Q,H,512] bf16, lse [B,Q,H] fp32).
     Rows of unused sequences keep what the given arrays hold (zeros in arrays
-    made here).  check=False skips the tensor checks (a loop that already
-    passed them)."""
+    made here, on ``stream``).  check=False skips the tensor checks (a loop
+    that already passed them)."""
     import torch
     dev = ki.q_lat.device
-    if out is None:
-        out = torch.zeros((ki.B, ki.Q, ki.H, 512), dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.zeros((ki.B, ki.Q, ki.H), dtype=torch.float32, device=dev)
+    if out is None or lse is None:
+        with _made_on(stream):
+            if out is None:
+                out = torch.zeros((ki.B, ki.Q, ki.H, 512), dtype=torch.bfloat16, device=dev)
+            if lse is None:
+                lse = torch.zeros((ki.B, ki.Q, ki.H), dtype=torch.float32, device=dev)
     if check:
         ki.check_layout()
         _need(out, "out", torch.bfloat16, (ki.B, ki.Q, ki.H, 512))
         _need(lse, "lse", torch.float32, (ki.B, ki.Q, ki.H))
         _one_device(out=out, lse=lse, workspace=workspace, **ki.tensors())
     if workspace is None:
-        workspace = alloc_workspace(kvq_workspace_size(ki), dev)
+        with _made_on(stream):
+            workspace = alloc_workspace(kvq_workspace_size(ki), dev)
     _kvq_launch("mla_kvq_attn", load().mla_kvq_attn, dev, stream, ki.c_args(out, lse), workspace.data_ptr(),
                 workspace.nbytes)
     return out, lse
@@ -809,8 +833,10 @@ def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, che
 def kvq_check(workspace, stream=None) -> int:
     """Synchronise and return the device error bits that the last kvq call on
     this workspace left."""
+    import torch
     bits = ctypes.c_uint32(0)
-    st = load().mla_kvq_check(ctypes.c_void_p(_ptr(workspace)), _stream(stream), ctypes.byref(bits))
+    with torch.cuda.device(workspace.device):
+        st = load().mla_kvq_check(ctypes.c_void_p(_ptr(workspace)), _stream(stream), ctypes.byref(bits))
     if st not in (MLA_OK, MLA_ERR_DEVICE_CHECK):
         raise MlaError(st, "mla_kvq_check")
     return int(bits.value)

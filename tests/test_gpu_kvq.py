@@ -518,6 +518,41 @@ def test_lse_may_be_null_and_streams_and_repeats_agree():
         assert torch.equal(out, o) and torch.equal(lse, l)
 
 
+def test_arrays_made_by_a_call_on_another_stream():
+    # the current stream is kept busy: a fill or a reuse of the memory on it would come at another time
+    p = problem(B=4, Q=3, H=8, lens=[-1, 200, 900, 65], seed=38)
+    out, lse = run(p.ki)
+    at = torch.tensor([5, -1, 3], dtype=torch.int32).cuda()
+    c0, k0, _ = api.kvq_read(p.ki.cache, at)
+    big = torch.randn(6000, 6000, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        big @ big
+        o2, l2 = api.kvq_attn(p.ki, stream=s)
+        c, k, ws = api.kvq_read(p.ki.cache, at, stream=s)
+        junk = [torch.full((1 << 20,), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(40)]
+        s.synchronize()
+        got = [t.cpu() for t in (o2, l2, c, k)]
+        assert api.kvq_check(ws, s) == 0
+        del junk
+        for a, b in zip(got, (out, lse, c0, k0)):
+            assert torch.equal(a, b.cpu())
+    with pytest.raises(ValueError, match="contiguous"):
+        api.kvq_attn(p.ki, workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 30))
+
+
+def test_short_pieces_one_after_another():
+    # one tile to a row group: the two producer groups take turns by piece
+    p = problem(B=600, Q=1, H=20, lens=[(7 * i) % 60 for i in range(600)], tree="null", seed=39)
+    check_attn(p)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1), (2 ** 31 - 2, 7)])
+def test_largest_windows_and_sinks(window, sinks):
+    check_attn(problem(B=3, Q=9, H=7, lens=[0, 500, 61], seed=40, window=window, sinks=sinks))
+
+
 @pytest.mark.parametrize("page", [1, 16])
 def test_bad_tables_are_reported(page):
     def go(**kw):

@@ -162,6 +162,17 @@ def test_attn_argument_refusals(lib, field, value):
     assert attn_call(lib, attn_struct(**{field: value})) == api.MLA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("scale,exponent", [(1e-38, -32), (1e-30, -32), (3e38, 0), (1e30, 32), (1e-40, 0)])
+def test_attn_refuses_a_scale_that_leaves_fp32(lib, scale, exponent):
+    # with the cache's exponent and log2(e) it would round to a subnormal, 0 or infinity
+    assert attn_call(lib, attn_struct(scale=scale, cache=cache_struct(exponent=exponent))) == api.MLA_ERR_INVALID_ARG
+    assert attn_call(lib, attn_struct(scale=scale, cache=cache_struct(exponent=exponent)), ws=0) \
+        == api.MLA_ERR_INVALID_ARG
+    # the exponent that brings it back into range is taken
+    back = 20 if scale < 1 else -20
+    assert attn_call(lib, attn_struct(scale=scale, cache=cache_struct(exponent=back)), ws=0) == api.MLA_ERR_WORKSPACE
+
+
 def test_attn_cache_and_table_refusals(lib):
     for k, v in BAD_CACHE:
         assert attn_call(lib, attn_struct(cache=cache_struct(**{k: v}))) == api.MLA_ERR_INVALID_ARG, (k, v)
@@ -213,3 +224,8 @@ def test_binding_refuses_wrong_tensors(lib):
                 dict(tree_parent=torch.zeros(2, 2, dtype=torch.int32))):
         with pytest.raises(ValueError):
             api.kvq_attn(dataclasses.replace(ki, **bad))
+    for bad in (dict(window=2 ** 32 + 5), dict(window=4, sinks=2 ** 31), dict(page_size=2 ** 32 + 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            api.kvq_attn(dataclasses.replace(ki, **bad))
+    with pytest.raises(ValueError, match="dtype"):
+        api.kvq_read(cache, s, "fp16")
