@@ -1147,23 +1147,32 @@ static_assert(2 * kMaxClusters <= kErrMax, "an error word per CTA");
 __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Params p, int chunks) {
   __shared__ Start start[kMaxClusters];
   __shared__ int cut[kMaxClusters];                    // boundaries that are the first inside a row group
-  __shared__ int cuts;
+  __shared__ uint32_t cut_mask[kMaxClusters / 32];
   __shared__ int slot[kMaxClusters];                   // -1: an empty piece
   __shared__ float weight[kMergeRows][kMaxClusters];   // lse of each piece
   const int tid = threadIdx.x;
-  if (tid == 0) cuts = 0;
+  const int warp = tid >> 5, lane = tid & 31;
   grid_dep_wait();
   if (tid < p.clusters) start[tid] = static_cast<const Start*>(p.starts)[tid];
   __syncthreads();
   const int clusters = start[0].n;
+  bool first = false;
   if (tid > 0 && tid < clusters) {
     const Start s0 = start[tid - 1], s = start[tid];
     const int64_t base = div_fast(s.x, kFixed + s.T) * (kFixed + s.T);
-    if (s.x > base && (s0.b != s.b || s0.x <= base)) cut[atomicAdd(&cuts, 1)] = tid;
+    first = s.x > base && (s0.b != s.b || s0.x <= base);
+  }
+  const uint32_t mask = __ballot_sync(0xffffffffu, first);
+  if (lane == 0 && warp < kMaxClusters / 32) cut_mask[warp] = mask;
+  __syncthreads();
+  // every block lists them in the same order: they share the list
+  int cuts = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxClusters / 32; ++w) {
+    if (w == warp && first) cut[cuts + __popc(mask & ((1u << lane) - 1u))] = tid;
+    cuts += __popc(cut_mask[w]);
   }
   __syncthreads();
-  const int warp = tid >> 5, lane = tid & 31;
-  // tasks in an order that depends on the atomics, results not
   for (int task = blockIdx.x; task < cuts * chunks; task += gridDim.x) {
     const int k = cut[task / chunks], r0 = (task % chunks) * kMergeRows;
     const Start s = start[k];

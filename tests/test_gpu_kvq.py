@@ -518,6 +518,17 @@ def test_lse_may_be_null_and_streams_and_repeats_agree():
         assert torch.equal(out, o) and torch.equal(lse, l)
 
 
+@pytest.mark.parametrize("B", [40, 61, 76, 130])
+def test_many_cut_row_groups(B):
+    # more boundaries inside row groups than a warp counts: every one of them is merged, in every call
+    p = problem(B=B, Q=1, H=3, lens=[1000 + (337 * i) % 1000 for i in range(B)], tree="null", seed=41)
+    out, lse = check_attn(p)
+    ws = api.alloc_workspace(api.kvq_workspace_size(p.ki))
+    for _ in range(20):
+        o2, l2 = run(p.ki, workspace=ws.fill_(0xee))
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
 def test_arrays_made_by_a_call_on_another_stream():
     # the current stream is kept busy: a fill or a reuse of the memory on it would come at another time
     p = problem(B=4, Q=3, H=8, lens=[-1, 200, 900, 65], seed=38)
