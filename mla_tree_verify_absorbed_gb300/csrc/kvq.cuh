@@ -132,7 +132,7 @@ struct Params {
   uint32_t* err;               // word 0, and the error words from kErrFirst on
   void* starts;                // [clusters]: see Start
   float* part_lse;             // [2 clusters][rows of a group], natural log
-  float* part_o;               // [2 clusters][rows of a group][512], normalised
+  float* part_o;               // [2 clusters][512 / 8][rows of a group][8], normalised
 };
 
 // What a call needs of sequence b's tables before anything else, and the

@@ -137,9 +137,12 @@ constexpr float kLazy = 8.f;
 constexpr float kWeightShift = 7.f;
 
 // Cost of starting a row group or a piece of one, in tiles, and the fewest
-// tiles worth a cluster of its own.
+// tiles worth a cluster of its own.  Measured, us (64 nodes x 64 heads in a window
+// of 1,000; 16 sequences x 64 heads in a window of 4,096; 128 ragged sequences
+// x 16 heads): kFixed 2: 43.9, 41.7, 130.4; 4: 41.5, 42.0, 124.5; 6: 47.1, 41.1,
+// 128.2; kMinTiles 16 in place of 4: 48.5, 43.9, 124.5.
 constexpr int kFixed = 4;
-constexpr int kMinTiles = 8;
+constexpr int kMinTiles = 4;
 
 // One cluster's share of a row group, as the roles need it.
 struct alignas(16) Piece {
@@ -260,13 +263,9 @@ __device__ __forceinline__ Tiles tiles_of(const Params& p, int64_t P) {
 }
 
 // First tile of what a cut at unit z of a row group (kFixed + T units) leaves
-// to the right: the fixed cost comes first, and a cut that would leave fewer
-// than kSnap tiles on a side moves to that side's end.
-constexpr int kSnap = 3;
+// to the right: the fixed cost comes first.
 __device__ __forceinline__ int cut_tile(int64_t z, int T) {
-  if (z >= kFixed + T) return T;
-  if (z < kFixed + kSnap) return 0;
-  return z > kFixed + T - kSnap ? T : (int)(z - kFixed);
+  return z <= kFixed ? 0 : z >= kFixed + T ? T : (int)(z - kFixed);
 }
 
 // a / b for a >= 0, b > 0: a 32-bit division wherever it will do.
@@ -910,6 +909,13 @@ __device__ void value_mma(uint8_t* smem, Ctl* c) {
   drain_mmas(c, leader);
 }
 
+// Partial results: 8 columns of all rows after each other, so that the rows of
+// a warp, one to a lane, fill whole lines (row after row, a warp's store touches
+// 32 lines; 32 sequences x 128 heads x 8,192 tokens then took 76.7 us, not 74.3).
+__device__ __forceinline__ int64_t part_index(int slot, int block8, int r) {
+  return (((int64_t)slot * (kDl / 8) + block8) * kRG + r) * 8;
+}
+
 // Row warps of the value CTA (warpgroup h: columns [256 h, 256 h + 256)):
 // rescale O where a factor is not 1, and per piece normalise and store it.
 __device__ void value_rows(const Params& p, Ctl* c) {
@@ -988,8 +994,7 @@ __device__ void value_rows(const Params& p, Ctl* c) {
       }
       if (live && p.lse && h == 0) p.lse[orow] = lse;
     } else {
-      const int64_t prow = (int64_t)slot * kRG + r;
-      float* dst = p.part_o + prow * kDl + col0;
+      float* dst = p.part_o + part_index(slot, col0 / 8, r);
 #pragma unroll 1
       for (int c0 = 0; c0 < 256; c0 += 32) {
         uint32_t u[32];
@@ -998,13 +1003,13 @@ __device__ void value_rows(const Params& p, Ctl* c) {
         if (live) {
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            st_global_v8(dst + c0 + 8 * v, __uint_as_float(u[8 * v + 0]) * inv, __uint_as_float(u[8 * v + 1]) * inv,
+            st_global_v8(dst + (c0 / 8 + v) * kRG * 8, __uint_as_float(u[8 * v + 0]) * inv, __uint_as_float(u[8 * v + 1]) * inv,
                          __uint_as_float(u[8 * v + 2]) * inv, __uint_as_float(u[8 * v + 3]) * inv,
                          __uint_as_float(u[8 * v + 4]) * inv, __uint_as_float(u[8 * v + 5]) * inv,
                          __uint_as_float(u[8 * v + 6]) * inv, __uint_as_float(u[8 * v + 7]) * inv);
         }
       }
-      if (live && h == 0) p.part_lse[prow] = lse;
+      if (live && h == 0) p.part_lse[(int64_t)slot * kRG + r] = lse;
     }
     tc_fence_before();
     return true;
@@ -1137,11 +1142,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
 //   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k.
 // Every block reads where the clusters' intervals begin and lists the row
 // groups that a boundary cuts; the blocks then take these eight rows at a time.
-// For eight rows a block gathers every piece's slot and weights, and each warp
-// sums one half of a row's columns with four pieces' loads in flight.  (A block
-// for every eight rows behind every boundary, most of which find nothing to do,
-// took 6 us longer: several waves of blocks that wait for one load each.)
+// For eight rows a block gathers every piece's slot and lse, a warp per row
+// turns them into weights, and each thread sums 8 columns of a row with four
+// pieces' loads in flight.  (A block for every eight rows behind every boundary,
+// most of which find nothing to do, took 6 us longer: several waves of blocks
+// that wait for one load each.)
 constexpr int kMergeThreads = 512, kMergeRows = 8;
+static_assert(kMergeThreads == kMergeRows * (kDl / 8), "a thread per row and 8 columns");
 constexpr int kMaxClusters = 128;
 static_assert(2 * kMaxClusters <= kErrMax, "an error word per CTA");
 __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Params p, int chunks) {
@@ -1149,7 +1156,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
   __shared__ int cut[kMaxClusters];                    // boundaries that are the first inside a row group
   __shared__ uint32_t cut_mask[kMaxClusters / 32];
   __shared__ int slot[kMaxClusters];                   // -1: an empty piece
-  __shared__ float weight[kMergeRows][kMaxClusters];   // lse of each piece
+  __shared__ float weight[kMergeRows][kMaxClusters];   // each piece's lse, then its weight
+  __shared__ float total[kMergeRows];                  // sum of the weights
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   grid_dep_wait();
@@ -1202,55 +1210,52 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
       weight[r][pc] = slot[pc] >= 0 && r < rows ? p.part_lse[(int64_t)slot[pc] * kRG + r0 + r] : -INFINITY;
     }
     __syncthreads();
-    const int r = warp >> 1;
-    if (r < rows) {
+    if (warp < min(rows, kMergeRows)) {
+      float* w = weight[warp];
       float m = -INFINITY, sum = 0.f;
-      for (int i = lane; i < n; i += 32) m = fmaxf(m, weight[r][i]);
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, w[i]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      for (int i = lane; i < n; i += 32) sum += __expf(weight[r][i] - m);
+      for (int i = lane; i < n; i += 32) {
+        w[i] = __expf(w[i] - m);
+        sum += w[i];
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      // 256 columns: two float4 a lane
-      const int col = (warp & 1) * 256 + 4 * lane;
-      const float* part = p.part_o + (int64_t)(r0 + r) * kDl + col;
-      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      if (lane == 0) {
+        total[warp] = sum;
+        if (p.lse) p.lse[(int64_t)s.b * p.rows + g * kRG + r0 + warp] = m + logf(sum);
+      }
+    }
+    __syncthreads();
+    const int r = lane & 7, block8 = 4 * warp + (lane >> 3);
+    if (r < rows) {
+      uint64_t acc[4] = {0, 0, 0, 0};  // 8 columns, two by two
       constexpr int kDeep = 4;
       for (int i0 = 0; i0 < n; i0 += kDeep) {
-        float4 v[kDeep][2];
+        uint32_t v[kDeep][8];
         float w[kDeep];
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
           const int i = i0 + d, sl = i < n ? slot[i] : -1;
-          w[d] = sl >= 0 ? __expf(weight[r][i] - m) : 0.f;
-          v[d][0] = v[d][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (sl >= 0) {
-            const float4* src = reinterpret_cast<const float4*>(part + (int64_t)sl * kRG * kDl);
-            v[d][0] = src[0];
-            v[d][1] = src[32];
-          }
+          w[d] = sl >= 0 ? weight[r][i] : 0.f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[d][q] = 0u;
+          if (sl >= 0) ld_global_v8(p.part_o + part_index(sl, block8, r0 + r), v[d]);
         }
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            acc[h].x = fmaf(w[d], v[d][h].x, acc[h].x);
-            acc[h].y = fmaf(w[d], v[d][h].y, acc[h].y);
-            acc[h].z = fmaf(w[d], v[d][h].z, acc[h].z);
-            acc[h].w = fmaf(w[d], v[d][h].w, acc[h].w);
-          }
+          for (int q = 0; q < 4; ++q) acc[q] = fma_f32x2(pair(w[d], w[d]), pair(v[d][2 * q], v[d][2 * q + 1]), acc[q]);
         }
       }
-      const float inv = 1.f / sum;
+      const float inv = 1.f / total[r];
       const int64_t orow = (int64_t)s.b * p.rows + g * kRG + r0 + r;
+      uint32_t o[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint2 o;
-        o.x = pack_bf16(acc[h].x * inv, acc[h].y * inv);
-        o.y = pack_bf16(acc[h].z * inv, acc[h].w * inv);
-        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + col + 128 * h) = o;
-      }
-      if (p.lse && (warp & 1) == 0 && lane == 0) p.lse[orow] = m + logf(sum);
+      for (int q = 0; q < 4; ++q) o[q] = pack_bf16(lo_f32(acc[q]) * inv, hi_f32(acc[q]) * inv);
+      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + 8 * block8) =
+          make_uint4(o[0], o[1], o[2], o[3]);
     }
     __syncthreads();  // slot and weight are reused
   }

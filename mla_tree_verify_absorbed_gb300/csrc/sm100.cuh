@@ -148,6 +148,14 @@ __device__ __forceinline__ void st_global_v8(uint32_t* ptr, uint32_t a0, uint32_
                : "memory");
 }
 
+// The same eight words loaded.
+__device__ __forceinline__ void ld_global_v8(const void* ptr, uint32_t (&v)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(ptr)
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // asynchronous copies
 // ---------------------------------------------------------------------------
