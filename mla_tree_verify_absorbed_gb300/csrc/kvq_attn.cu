@@ -1152,10 +1152,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
 // groups that a boundary cuts; the blocks then take these eight rows at a time.
 // For eight rows a block gathers every piece's slot and lse, a warp per row
 // turns them into weights, and each thread sums 8 columns of a row with four
-// pieces' loads in flight.  (A block for every eight rows behind every boundary,
-// most of which find nothing to do, took 6 us longer: several waves of blocks
-// that wait for one load each.)
-constexpr int kMergeThreads = 512, kMergeRows = 8;
+// pieces' loads in flight.  Where that makes at most a quarter as many tasks as
+// blocks (few row groups, in many pieces each), a task is a quarter of the
+// columns instead, and a quarter of the threads each takes every fourth piece:
+// two row groups of 38 pieces took 11 us less, but 32 row groups of two or three
+// pieces 10 us more.  (A block for every eight rows behind every boundary, most
+// of which find nothing to do, took 6 us longer: several waves of blocks that
+// wait for one load each.)
+constexpr int kMergeThreads = 512, kMergeRows = 8, kMergeParts = 4;
 static_assert(kMergeThreads == kMergeRows * (kDl / 8), "a thread per row and 8 columns");
 constexpr int kMaxClusters = 128;
 static_assert(2 * kMaxClusters <= kErrMax, "an error word per CTA");
@@ -1166,6 +1170,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
   __shared__ int slot[kMaxClusters];                   // -1: an empty piece
   __shared__ float weight[kMergeRows][kMaxClusters];   // each piece's lse, then its weight
   __shared__ float total[kMergeRows];                  // sum of the weights
+  __shared__ float4 sums[kMergeParts - 1][2][kMergeThreads / kMergeParts];
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   grid_dep_wait();
@@ -1189,8 +1194,11 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
     cuts += __popc(cut_mask[w]);
   }
   __syncthreads();
-  for (int task = blockIdx.x; task < cuts * chunks; task += gridDim.x) {
-    const int k = cut[task / chunks], r0 = (task % chunks) * kMergeRows;
+  const int parts = cuts * chunks * kMergeParts <= (int)gridDim.x ? kMergeParts : 1;
+  const int items = kMergeThreads / parts, item = tid & (items - 1), part = tid / items;
+  for (int task = blockIdx.x; task < cuts * chunks * parts; task += gridDim.x) {
+    const int k = cut[task / parts / chunks], r0 = (task / parts % chunks) * kMergeRows;
+    const int cb = task % parts;
     const Start s = start[k];
     const int T = s.T, L = kFixed + T;
     const int64_t g = div_fast(s.x, L), base = g * L;
@@ -1232,20 +1240,20 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) {
         total[warp] = sum;
-        if (p.lse) p.lse[(int64_t)s.b * p.rows + g * kRG + r0 + warp] = m + logf(sum);
+        if (p.lse && cb == 0) p.lse[(int64_t)s.b * p.rows + g * kRG + r0 + warp] = m + logf(sum);
       }
     }
     __syncthreads();
-    const int r = lane & 7, block8 = 4 * warp + (lane >> 3);
+    const int r = item & 7, block8 = (cb * items + item) >> 3;
+    uint64_t acc[4] = {0, 0, 0, 0};  // 8 columns, two by two
     if (r < rows) {
-      uint64_t acc[4] = {0, 0, 0, 0};  // 8 columns, two by two
       constexpr int kDeep = 4;
-      for (int i0 = 0; i0 < n; i0 += kDeep) {
+      for (int i0 = part; i0 < n; i0 += kDeep * parts) {
         uint32_t v[kDeep][8];
         float w[kDeep];
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
-          const int i = i0 + d, sl = i < n ? slot[i] : -1;
+          const int i = i0 + d * parts, sl = i < n ? slot[i] : -1;
           w[d] = sl >= 0 ? weight[r][i] : 0.f;
 #pragma unroll
           for (int q = 0; q < 8; ++q) v[d][q] = 0u;
@@ -1257,6 +1265,28 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
           for (int q = 0; q < 4; ++q) acc[q] = fma_f32x2(pair(w[d], w[d]), pair(v[d][2 * q], v[d][2 * q + 1]), acc[q]);
         }
       }
+    }
+    if (parts > 1) {
+      if (part > 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          sums[part - 1][h][item] =
+              make_float4(lo_f32(acc[2 * h]), hi_f32(acc[2 * h]), lo_f32(acc[2 * h + 1]), hi_f32(acc[2 * h + 1]));
+      }
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int o = 0; o < kMergeParts - 1; ++o) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 a = sums[o][h][item];
+            acc[2 * h] = add_f32x2(acc[2 * h], pair(a.x, a.y));
+            acc[2 * h + 1] = add_f32x2(acc[2 * h + 1], pair(a.z, a.w));
+          }
+        }
+      }
+    }
+    if (part == 0 && r < rows) {
       const float inv = 1.f / total[r];
       const int64_t orow = (int64_t)s.b * p.rows + g * kRG + r0 + r;
       uint32_t o[4];
@@ -1265,7 +1295,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
       *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + 8 * block8) =
           make_uint4(o[0], o[1], o[2], o[3]);
     }
-    __syncthreads();  // slot and weight are reused
+    __syncthreads();  // slot, weight and sums are reused
   }
 }
 
@@ -1454,7 +1484,8 @@ extern "C" mla_status mla_kvq_attn(const mla_kvq_attn_args* a, void* workspace, 
     return MLA_ERR_CUDA;
   // two blocks per SM of the clusters, fewer when even n - 1 cut row groups make fewer tasks
   const int chunks = ((p.rows < kRG ? p.rows : kRG) + kMergeRows - 1) / kMergeRows;
-  const int blocks = (n - 1) * chunks < 4 * n ? (n - 1) * chunks : 4 * n;
+  const int tasks = (n - 1) * chunks * kMergeParts;
+  const int blocks = tasks < 4 * n ? tasks : 4 * n;
   if (n > 1 && launch_kernel(kvq_merge_kernel, dim3(blocks), dim3(kMergeThreads), 0, s, true, p, chunks) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
