@@ -968,6 +968,10 @@ __device__ void value_rows(const Params& p, Ctl* c) {
     if (!wait_warp(&c->fin_full, (uint32_t)seg & 1u, c, kSiteFinFull)) return false;
     tc_fence_after();
     const float l = c->lfin[0][r] + c->lfin[1][r], m = c->mfin[r];
+    // The sums are read before the score CTA may write the next piece's: without
+    // the fence nothing orders a load before a relaxed arrive, and a load held up
+    // behind it (by a miss of the instruction cache) read the next piece's zero.
+    __threadfence_block();
     mbar_arrive_cluster_relaxed(&c->fin_free, 0);
     ++seg;
     if (wq >= quads) return true;
