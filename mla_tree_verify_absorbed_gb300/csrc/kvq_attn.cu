@@ -468,6 +468,10 @@ __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
   return v;
 }
 
+// Queries of up to 64 rows pass through one stage, that of the piece's second
+// tile, so that its first is converted meanwhile.
+__device__ __forceinline__ bool one_stage(const Params& p) { return p.box_rows <= 64; }
+
 // One warp of producer group `grp`: tokens kTok pw .. of the tiles of that
 // parity.  The packed rows (codes and scales, 288 bytes) come by cp.async into
 // rows of shared memory that the warp has to itself; a half tile's codes are
@@ -490,6 +494,7 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
   uint32_t j = 0, seg = 0;
   for_pieces(c, [&](const Piece& pc) {
     int t = pc.t0 + (int)((grp ^ j) & 1u);
+    const bool ahead = kScore && one_stage(p) && t == pc.t0;  // the queries use the other stage
     j += (uint32_t)(pc.t1 - pc.t0);
     const uint32_t q_bar = seg & 1u, q_phase = (seg >> 1) & 1u;
     ++seg;
@@ -548,7 +553,7 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     for (int h = 0; h < 2; ++h) fetch(slot, h, turn, true);
     int32_t ent = entry_of(t + 2);
     // until then the queries pass through the stages
-    if (kScore && !wait_warp(&c->q_ready[q_bar], q_phase, c, kSiteQReady)) return false;
+    if (kScore && !ahead && !wait_warp(&c->q_ready[q_bar], q_phase, c, kSiteQReady)) return false;
 #pragma unroll 1
     for (int h = 0; t < pc.t1; h ^= 1) {
       cp_async_wait_group<1>();  // this half's pieces, of this lane
@@ -589,7 +594,7 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
         fetch(slot, 1, turn, t < pc.t1);
       }
     }
-    return true;
+    return !ahead || wait_warp(&c->q_ready[q_bar], q_phase, c, kSiteQReady);
   });
   cp_async_wait_all();
   if (err) atomicOr(&c->err, err);
@@ -649,41 +654,44 @@ __device__ void score_mma(uint8_t* smem, Ctl* c) {
 
 // Brings a piece's query rows into Tensor Memory (column c holds elements 2c,
 // 2c + 1 of 512 latent and 64 rope ones), all row warps together.  Nine tensor
-// copies, 64 elements of the rows each, fill the two stages, which are free
-// between pieces (the producers wait for q_ready before they fill them); the
-// copies' 128-byte swizzle puts the 8 rows that a quarter warp reads at once
+// copies, 64 elements of the rows each, fill the two stages, or with up to 64
+// rows that of the second tile (a call of 257 tokens: 17.1 -> 16.6 us); they are
+// free between pieces (the producers wait for q_ready before they fill them).
+// The copies' 128-byte swizzle puts the 8 rows that a quarter warp reads at once
 // into different banks.  (For 128 rows, a thread loading its own row took 14 us,
 // cp.async of 16 bytes a lane 9, a bulk copy per row 9.)
-static_assert(9 * kPBytes <= 2 * kStageS, "queries fit the stages");
+static_assert(9 * kRG * 128 <= 2 * kStageS && 9 * 64 * 128 <= kStageS, "queries fit the stages");
 __device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* smem, Ctl* c, const Piece& pc, int warp,
-                              uint32_t seg) {
+                              uint32_t seg, uint32_t j) {
   const int lane = threadIdx.x & 31;
   const int wq = warp & 3, wg = (warp - kWarpRows) >> 2;
   const int r = wq * 32 + lane;
   const int rows = min(kRG, p.rows - pc.g * kRG);
   const uint32_t mul = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(p.qpe_mul)) * 0x10001u;  // a power of two
+  uint8_t* stage = smem + (one_stage(p) && !(j & 1u) ? kStageS : 0);
+  const uint32_t chunk = one_stage(p) ? 64 * 128 : kRG * 128;
   if (warp == kWarpRows && elect_one()) {
     fence_proxy_async_smem();  // the stages were written through the generic proxy
     mbar_arrive_expect_tx(&c->q_in, 9u * 128u * (uint32_t)p.box_rows);
     const int y = pc.b * p.rows + pc.g * kRG;
 #pragma unroll 1
     for (int ck = 0; ck < 9; ++ck)
-      tensor_copy_2d(smem + ck * kPBytes, ck < 8 ? &maps.lat : &maps.pe, ck < 8 ? 64 * ck : 0, y, &c->q_in);
+      tensor_copy_2d(stage + ck * chunk, ck < 8 ? &maps.lat : &maps.pe, ck < 8 ? 64 * ck : 0, y, &c->q_in);
   }
   __syncwarp();
   if (!wait_warp(&c->q_in, seg & 1u, c, kSiteQIn)) return false;
 #pragma unroll 3
   for (int ck = 0; ck < 9; ++ck) {
-    const uint32_t src = smem_u32(smem) + ck * kPBytes + r * 128;
-    uint32_t w[16];
+    const uint32_t src = smem_u32(stage) + ck * chunk + r * 128;
+    uint32_t w[16] = {};
+    if (r < rows) {  // else another sequence's rows, or none
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      ld_shared_v4(src + (((4 * wg + i) ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (r >= rows) w[i] = 0u;  // another sequence's rows, or none
-      if (ck == 8) w[i] = hmul2_bf16(w[i], mul);
+      for (int i = 0; i < 4; ++i)
+        ld_shared_v4(src + (((4 * wg + i) ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (ck == 8) w[i] = hmul2_bf16(w[i], mul);
     __syncwarp();
     tmem_st_32x32b_x16(((uint32_t)(wq * 32) << 16) + kColQ + 32 * ck + 16 * wg, w);
   }
@@ -725,7 +733,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
     const bool live = row < p.rows;
     const bool idle = wq >= live_quads(p.rows, pc.g);  // none of the warp's rows exists
     const int P = pc.P;
-    if (!stage_queries(p, maps, smem, c, pc, warp, seg)) return false;
+    if (!stage_queries(p, maps, smem, c, pc, warp, seg, j)) return false;
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&c->q_ready[seg & 1u]);
