@@ -171,7 +171,7 @@ struct alignas(16) Ctl {
   uint64_t empty[4];           // the MMAs reading it are complete
   uint64_t s_full[kSBufs];     // score: S tile in TMEM
   uint64_t s_free[kSBufs];         // score: softmax has loaded S (4 row warps)
-  uint64_t q_ready[2];         // score: queries in TMEM, stages free again (8 row warps); by piece parity
+  uint64_t q_ready[kPieces];   // score: a piece's queries in TMEM, stages free again (8 row warps)
   uint64_t q_in;               // score: queries copied (copy bytes)
   uint64_t m_ready[2][4];      // score: running maxima after a tile written (per lane quadrant, 1 warp)
   uint64_t p_free[kPBufs];     // score: the PV MMAs that read rank 1's buffer are complete (its commit)
@@ -496,12 +496,13 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     int t = pc.t0 + (int)((grp ^ j) & 1u);
     const bool ahead = kScore && one_stage(p) && t == pc.t0;  // the queries use the other stage
     j += (uint32_t)(pc.t1 - pc.t0);
-    const uint32_t q_bar = seg & 1u, q_phase = (seg >> 1) & 1u;
+    const uint32_t q_bar = seg % kPieces, q_phase = (seg / kPieces) & 1u;
     ++seg;
     // Every warp waits for every piece's queries: a phase left out could be
-    // taken for the next one.  A group without a tile in a piece may come late
-    // to that wait, but it has the tile of the next piece, so the queries of
-    // the piece after that, which use the same barrier, cannot overtake it.
+    // taken for the next one.  A group whose tiles do not need the wait may come
+    // to it late, but of the two pieces after this one, one at least has a tile
+    // of the group, so the queries of the fourth, which use the same barrier,
+    // cannot overtake it.
     if (t >= pc.t1) return !kScore || wait_warp(&c->q_ready[q_bar], q_phase, c, kSiteQReady);
     uint32_t turn = (j - (uint32_t)(pc.t1 - t)) >> 1;  // tiles this group has taken before
     const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
@@ -621,7 +622,7 @@ __device__ void score_mma(uint8_t* smem, Ctl* c) {
   const bool leader = elect_one();
   uint32_t j = 0, seg = 0;
   for_pieces(c, [&](const Piece& pc) {
-    if (!wait_warp(&c->q_ready[seg & 1u], (seg >> 1) & 1u, c, kSiteQReady)) return false;
+    if (!wait_warp(&c->q_ready[seg % kPieces], (seg / kPieces) & 1u, c, kSiteQReady)) return false;
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
       const uint32_t par = j & 1u, turn = j >> 1, sb = j % kSBufs;
@@ -736,7 +737,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
     if (!stage_queries(p, maps, smem, c, pc, warp, seg, j)) return false;
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&c->q_ready[seg & 1u]);
+    if (lane == 0) mbar_arrive(&c->q_ready[seg % kPieces]);
     // rows past the last take the last one's mask: their results are dropped
     const NodeView nv = node_view_warp(p, pc.b, (live ? row : p.rows - 1) / p.H, P, &bad);
     // Prefix positions up to this one are outside the window (unless sinks).
@@ -1065,14 +1066,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
       mbar_init(&c->p_staged[q], kRowWarps / 2);
       mbar_init(&c->ps_free[q], 1);
     } else if (warp == 12) {
-      mbar_init(&c->q_ready[0], kRowWarps);
-      mbar_init(&c->q_ready[1], kRowWarps);
       mbar_init(&c->q_in, 1);
       mbar_init(&c->fin_free, 32 * kRowWarps);
       mbar_init(&c->fin_full, 32 * kRowWarps);
       mbar_init(&c->drain, 1);
     } else if (warp == 13) {
       for (int q = 0; q < kPieces; ++q) {
+        mbar_init(&c->q_ready[q], kRowWarps);
         mbar_init(&c->piece_full[q], 1);
         mbar_init(&c->piece_empty[q], kFollowers + (rank == 0 ? 1 : 0));
       }
