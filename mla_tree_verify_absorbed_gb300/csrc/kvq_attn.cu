@@ -1233,6 +1233,20 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
     const int n = __syncthreads_count(mine);
     // when one cluster has it all it stored the results
     if (__syncthreads_or(whole) || rows <= 0) continue;
+    // the first pieces' results are on their way while the weights are computed
+    constexpr int kDeep = 4;
+    const int r = item & 7, block8 = (cb * items + item) >> 3;
+    uint32_t v[kDeep][8];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        const int i = i0 + d * parts, sl = i < n && r < rows ? slot[i] : -1;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[d][q] = 0u;
+        if (sl >= 0) ld_global_v8(p.part_o + part_index(sl, block8, r0 + r), v[d]);
+      }
+    };
+    load(part);
     for (int i = tid; i < n * kMergeRows; i += kMergeThreads) {
       const int pc = i / kMergeRows, r = i % kMergeRows;
       weight[r][pc] = slot[pc] >= 0 && r < rows ? p.part_lse[(int64_t)slot[pc] * kRG + r0 + r] : -INFINITY;
@@ -1256,27 +1270,18 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
       }
     }
     __syncthreads();
-    const int r = item & 7, block8 = (cb * items + item) >> 3;
     uint64_t acc[4] = {0, 0, 0, 0};  // 8 columns, two by two
-    if (r < rows) {
-      constexpr int kDeep = 4;
-      for (int i0 = part; i0 < n; i0 += kDeep * parts) {
-        uint32_t v[kDeep][8];
-        float w[kDeep];
+    for (int i0 = part;;) {
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-          const int i = i0 + d * parts, sl = i < n ? slot[i] : -1;
-          w[d] = sl >= 0 ? weight[r][i] : 0.f;
+      for (int d = 0; d < kDeep; ++d) {
+        const int i = i0 + d * parts;
+        const float w = i < n ? weight[r][i] : 0.f;  // 0 for an empty piece
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[d][q] = 0u;
-          if (sl >= 0) ld_global_v8(p.part_o + part_index(sl, block8, r0 + r), v[d]);
-        }
-#pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[q] = fma_f32x2(pair(w[d], w[d]), pair(v[d][2 * q], v[d][2 * q + 1]), acc[q]);
-        }
+        for (int q = 0; q < 4; ++q) acc[q] = fma_f32x2(pair(w, w), pair(v[d][2 * q], v[d][2 * q + 1]), acc[q]);
       }
+      i0 += kDeep * parts;
+      if (i0 >= n) break;
+      load(i0);
     }
     if (parts > 1) {
       if (part > 0) {
