@@ -34,11 +34,14 @@ constexpr int kErrMax = (int)(MLA_KVQ_WORKSPACE_BYTES / 4) - kErrFirst;
 
 // ---------------------------------------------------------------------------
 // Codes to values.  Nibble pair t of a code word (bits 4t.. of both halves) is
-// moved into the mantissa of a number whose exponent is fixed, so that each
+// put into the mantissa of a number whose exponent is fixed, so that each
 // half reads base + code exactly; one fused multiply-add then gives
 // (base + code) * s - (base + 8) * s = (code - 8) * s, exact because the
 // product is formed without rounding and the constant (base + 8) * s is exact
-// too (base 16: 24 s, 5 bits of 8; base 64: 72 s, 8 bits of 11).
+// too: bf16, base 128, 136 s has 5 + 4 bits less one, 8 of 8; f16, bases 1024
+// and 64, 1032 s has 8 + 4 bits less one, 11 of 11, and 72 s 8.  Lowest bits
+// first, a code needs no shift (bf16: one of four; f16, whose mantissa holds two
+// codes: two of four, the others share one).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
   uint32_t d;
@@ -73,28 +76,30 @@ struct ToBf16 {
   __device__ __forceinline__ static uint32_t scales(uint32_t b) {
     return hmul2_bf16((b << 4) & 0x07F007F0u, 0x7B807B80u);  // * 2^120
   }
-  __device__ __forceinline__ static uint32_t offsets(uint32_t s) { return hmul2_bf16(s, 0xC1C0C1C0u); }  // -24 s
-  // the eight values of a code word, in element order
+  __device__ __forceinline__ static uint32_t offsets(uint32_t s) { return hmul2_bf16(s, 0xC308C308u); }  // -136 s
+  // the eight values of a code word, in element order; s one scale twice
   __device__ __forceinline__ static void word(uint32_t w, uint32_t s, uint32_t o, uint32_t (&v)[4]) {
-    v[0] = hfma2_bf16(and_or(w << 3, 0x00780078u, 0x41804180u), s, o);
-    v[1] = hfma2_bf16(and_or(w >> 1, 0x00780078u, 0x41804180u), s, o);
-    v[2] = hfma2_bf16(and_or(w >> 5, 0x00780078u, 0x41804180u), s, o);
-    v[3] = hfma2_bf16(and_or(w >> 9, 0x00780078u, 0x41804180u), s, o);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = hfma2_bf16(and_or(w >> (4 * t), 0x000F000Fu, 0x43004300u), s, o);
   }
 };
 
-// f16 operand values.
+// f16 operand values, times 2^-kF16Shift: 1032 s has to stay below 65504.  The
+// smallest, 2^-13, is still a normal number.
+constexpr int kF16Shift = 4;
 struct ToF16 {
   // the e4m3 field in the f16 exponent and mantissa is the magnitude times 2^-8
   __device__ __forceinline__ static uint32_t scales(uint32_t b) {
-    return hmul2_f16((b << 7) & 0x3F803F80u, 0x5C005C00u);  // * 256
+    return hmul2_f16((b << 7) & 0x3F803F80u, 0x4C004C00u);  // * 2^(8 - kF16Shift)
   }
-  __device__ __forceinline__ static uint32_t offsets(uint32_t s) { return hmul2_f16(s, 0xD480D480u); }  // -72 s
+  __device__ __forceinline__ static uint32_t offsets(uint32_t s) { return hmul2_f16(s, 0xE408E408u); }   // -1032 s
+  __device__ __forceinline__ static uint32_t offsets2(uint32_t s) { return hmul2_f16(s, 0xD480D480u); }  // -72 s
   __device__ __forceinline__ static void word(uint32_t w, uint32_t s, uint32_t o, uint32_t (&v)[4]) {
-    v[0] = hfma2_f16(and_or(w << 4, 0x00F000F0u, 0x54005400u), s, o);
-    v[1] = hfma2_f16(and_or(w, 0x00F000F0u, 0x54005400u), s, o);
-    v[2] = hfma2_f16(and_or(w >> 4, 0x00F000F0u, 0x54005400u), s, o);
-    v[3] = hfma2_f16(and_or(w >> 8, 0x00F000F0u, 0x54005400u), s, o);
+    const uint32_t u = w >> 8, o2 = offsets2(s);
+    v[0] = hfma2_f16(and_or(w, 0x000F000Fu, 0x64006400u), s, o);
+    v[1] = hfma2_f16(and_or(w, 0x00F000F0u, 0x54005400u), s, o2);
+    v[2] = hfma2_f16(and_or(u, 0x000F000Fu, 0x64006400u), s, o);
+    v[3] = hfma2_f16(and_or(u, 0x00F000F0u, 0x54005400u), s, o2);
   }
 };
 
@@ -122,7 +127,7 @@ struct Params {
   int window, sinks;           // window 0: none
   float qpe_mul;               // 2^-exponent, on the rope queries
   float scale_log2;            // scale * 2^exponent * log2(e): scores in base-2 units
-  float out_mul;               // 2^exponent
+  float out_mul;               // 2^(exponent + kF16Shift)
   void* out;
   float* lse;
   int groups;                  // row groups per sequence

@@ -1450,7 +1450,7 @@ Params make_params(const mla_kvq_attn_args* a, void* ws, int clusters) {
   const int e = a->cache.exponent;
   p.qpe_mul = (float)std::ldexp(1.0, -e);
   p.scale_log2 = score_factor(*a);
-  p.out_mul = (float)std::ldexp(1.0, e);
+  p.out_mul = (float)std::ldexp(1.0, e + kF16Shift);
   p.out = a->out;
   p.lse = a->lse;
   p.groups = (p.rows + kRG - 1) / kRG;
