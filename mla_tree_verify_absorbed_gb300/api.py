@@ -663,13 +663,14 @@ def _made_on(stream):
 def _kvq_launch(what: str, f, dev, stream, *args):
     """Calls f(*args, stream) with the tensors' device current."""
     import torch
+    index = dev.index
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"{what}: stream on {stream.device}, tensors on {dev}")
         raw = stream.cuda_stream
     else:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    if dev.index == torch.cuda.current_device():
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
         st = f(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -679,8 +680,8 @@ def _kvq_launch(what: str, f, dev, stream, *args):
 
 
 def _kvq_rows(what: str, f, cache: QuantCache, kv_c, k_pe, slots, workspace, stream, check: bool):
-    import torch
     if check:
+        import torch
         cache.check()
         if kv_c is None or kv_c.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("kv_c must be a bfloat16 or float32 tensor")
@@ -698,7 +699,7 @@ def _kvq_rows(what: str, f, cache: QuantCache, kv_c, k_pe, slots, workspace, str
         with _made_on(stream):
             workspace = alloc_workspace(KVQ_WORKSPACE_BYTES, dev)
     n = kv_c.size(0)
-    r = MlaKvqRows(n, MLA_BF16 if kv_c.dtype is torch.bfloat16 else MLA_FP32, kv_c.data_ptr(), k_pe.data_ptr(),
+    r = MlaKvqRows(n, MLA_BF16 if kv_c.element_size() == 2 else MLA_FP32, kv_c.data_ptr(), k_pe.data_ptr(),
                    kv_c.stride(0) if n > 1 else 512, k_pe.stride(0) if n > 1 else 64, slots.data_ptr())
     _kvq_launch(what, f, dev, stream, cache.c_struct(), r, workspace.data_ptr(), workspace.nbytes)
     return workspace
@@ -719,12 +720,12 @@ def kvq_read(cache: QuantCache, slots, dtype: str = "bf16", kv_c=None, k_pe=None
     as ``dtype`` ("bf16" or "fp32"; that of kv_c when given).  Rows with slot
     -1 keep what the given arrays hold (zeros in arrays made here, on
     ``stream``).  Returns (kv_c [n][512], k_pe [n][64], workspace)."""
-    import torch
     if check:
         cache.check()
         if dtype not in ("bf16", "fp32"):
             raise ValueError(f'dtype {dtype!r}, expected "bf16" or "fp32"')
     if kv_c is None or k_pe is None:
+        import torch
         dt = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype] if kv_c is None else kv_c.dtype
         with _made_on(stream):
             if kv_c is None:
@@ -809,15 +810,16 @@ def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, che
     Rows of unused sequences keep what the given arrays hold (zeros in arrays
     made here, on ``stream``).  check=False skips the tensor checks (a loop
     that already passed them)."""
-    import torch
     dev = ki.q_lat.device
     if out is None or lse is None:
+        import torch
         with _made_on(stream):
             if out is None:
                 out = torch.zeros((ki.B, ki.Q, ki.H, 512), dtype=torch.bfloat16, device=dev)
             if lse is None:
                 lse = torch.zeros((ki.B, ki.Q, ki.H), dtype=torch.float32, device=dev)
     if check:
+        import torch
         ki.check_layout()
         _need(out, "out", torch.bfloat16, (ki.B, ki.Q, ki.H, 512))
         _need(lse, "lse", torch.float32, (ki.B, ki.Q, ki.H))
