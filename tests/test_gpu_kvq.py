@@ -518,6 +518,31 @@ def test_lse_may_be_null_and_streams_and_repeats_agree():
         assert torch.equal(out, o) and torch.equal(lse, l)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=1500, Q=1, H=2, lens=[(7 * i) % 300 - 1 for i in range(1500)], tree="null"),  # more than a block's threads
+    dict(B=641, Q=2, H=1, lens=[-1] * 640 + [900], page=16),
+    dict(B=2, Q=3, H=700, lens=[700, 90]),                                               # 17 row groups, the last of 52 rows
+    dict(B=700, Q=1, H=1, lens=[0] * 700, tree="null", window=1),
+], ids=["1500", "last_of_641", "700_heads", "nothing_but_nodes"])
+def test_many_sequences_and_heads(kw):
+    check_attn(problem(seed=42, **kw))
+
+
+def test_arrays_aligned_to_16_bytes_only():
+    # whole row groups, cut ones, and queries and outputs whose rows do not fall on sectors
+    p = problem(B=5, Q=4, H=40, lens=[70, 3000, 0, 513, 64], seed=43)
+    out, lse = check_attn(p)
+
+    def moved(t):
+        m = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")[8:].view(t.shape)
+        assert m.data_ptr() % 32 == 16
+        return m.copy_(t)
+    o2 = moved(torch.zeros_like(out))
+    l2 = torch.zeros(lse.numel() + 1, device="cuda")[1:].view(lse.shape)
+    run(dataclasses.replace(p.ki, q_lat=moved(p.ki.q_lat), q_pe=moved(p.ki.q_pe)), out=o2, lse=l2)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
 @pytest.mark.parametrize("B", [40, 61, 76, 130])
 def test_many_cut_row_groups(B):
     # more boundaries inside row groups than a warp counts: every one of them is merged, in every call
