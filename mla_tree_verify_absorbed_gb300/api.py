@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -93,6 +94,18 @@ class MlaKvqRows(ctypes.Structure):
     ]
 
 
+def _packer(cls):
+    """The bytes of a struct from its fields' values: a third of the time that
+    making a ctypes.Structure takes, which counts in a call of a few us."""
+    code = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int: "i"}
+    p = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q")
+    assert p.size == ctypes.sizeof(cls)
+    return p.pack
+
+
+_pack_cache, _pack_rows = _packer(MlaKvqCache), _packer(MlaKvqRows)
+
+
 class MlaKvqAttnArgs(ctypes.Structure):
     _fields_ = [
         ("B", ctypes.c_int), ("Q", ctypes.c_int), ("H", ctypes.c_int),
@@ -156,8 +169,7 @@ def load(path: Optional[str] = None):
                                       ctypes.c_void_p]
     for f in (lib.mla_kvq_write, lib.mla_kvq_read):
         f.restype = ctypes.c_int
-        f.argtypes = [ctypes.POINTER(MlaKvqCache), ctypes.POINTER(MlaKvqRows), ctypes.c_void_p, ctypes.c_size_t,
-                      ctypes.c_void_p]
+        f.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.mla_kvq_attn.restype = ctypes.c_int
     lib.mla_kvq_attn.argtypes = [ctypes.POINTER(MlaKvqAttnArgs), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.mla_kvq_attn_workspace_size.restype = ctypes.c_size_t
@@ -694,14 +706,17 @@ def _kvq_rows(what: str, f, cache: QuantCache, kv_c, k_pe, slots, workspace, str
             raise ValueError("kv_c and k_pe must have the same number of rows")
         _need(slots, "slots", torch.int32, (kv_c.shape[0],))
         _one_device(rows=cache.rows, kv_c=kv_c, k_pe=k_pe, slots=slots, workspace=workspace)
-    dev = cache.rows.device
+    pool = cache.rows
+    dev = pool.device
     if workspace is None:
         with _made_on(stream):
             workspace = alloc_workspace(KVQ_WORKSPACE_BYTES, dev)
-    n = kv_c.size(0)
-    r = MlaKvqRows(n, MLA_BF16 if kv_c.element_size() == 2 else MLA_FP32, kv_c.data_ptr(), k_pe.data_ptr(),
-                   kv_c.stride(0) if n > 1 else 512, k_pe.stride(0) if n > 1 else 64, slots.data_ptr())
-    _kvq_launch(what, f, dev, stream, cache.c_struct(), r, workspace.data_ptr(), workspace.nbytes)
+    n, m = kv_c.shape[0], pool.shape[0]
+    # the row stride of a one-row tensor is whatever its maker left there
+    c = _pack_cache(pool.data_ptr(), pool.stride()[0] if m > 1 else KVQ_ROW_BYTES, m, cache.exponent)
+    r = _pack_rows(n, MLA_BF16 if kv_c.element_size() == 2 else MLA_FP32, kv_c.data_ptr(), k_pe.data_ptr(),
+                   kv_c.stride()[0] if n > 1 else 512, k_pe.stride()[0] if n > 1 else 64, slots.data_ptr())
+    _kvq_launch(what, f, dev, stream, c, r, workspace.data_ptr(), workspace.nbytes)
     return workspace
 
 

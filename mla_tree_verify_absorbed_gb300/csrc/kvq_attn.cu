@@ -82,9 +82,12 @@ constexpr uint32_t kTmemCols = 512;
 // the speed).
 constexpr int kProducerWarps = 8, kGroupWarps = 4;
 constexpr int kWarpRows = 8, kRowWarps = 8;
-constexpr int kWarpMma = 16;
+constexpr int kWarpSched = 16;  // the pieces of work
 constexpr int kWarpAux = 17;    // TMEM allocation; rank 0: weight copies
-constexpr int kWarpSched = 18;  // the pieces of work
+// Warps w, w + 4, .. share a scheduler, and issuing a tile's MMAs is work for it:
+// away from the one that has the row warps of few rows (beside them, 128 ragged
+// sequences x 16 heads took 122.9 us, not 118.2).
+constexpr int kWarpMma = 19;
 
 // A tile is staged as two halves, each with its own full / empty barriers:
 // half h holds latent columns [256 h, 256 h + 256) as 4 chunks of 64 columns
