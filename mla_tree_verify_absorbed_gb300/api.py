@@ -94,18 +94,6 @@ class MlaKvqRows(ctypes.Structure):
     ]
 
 
-def _packer(cls):
-    """The bytes of a struct from its fields' values: a third of the time that
-    making a ctypes.Structure takes, which counts in a call of a few us."""
-    code = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int: "i"}
-    p = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q")
-    assert p.size == ctypes.sizeof(cls)
-    return p.pack
-
-
-_pack_cache, _pack_rows = _packer(MlaKvqCache), _packer(MlaKvqRows)
-
-
 class MlaKvqAttnArgs(ctypes.Structure):
     _fields_ = [
         ("B", ctypes.c_int), ("Q", ctypes.c_int), ("H", ctypes.c_int),
@@ -119,6 +107,22 @@ class MlaKvqAttnArgs(ctypes.Structure):
         ("scale", ctypes.c_float),
         ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
     ]
+
+
+def _packer(cls):
+    """The bytes of a struct from its fields' values (a nested struct's in their
+    place): a third of the time that making a ctypes.Structure takes, which
+    counts in a call of a few us."""
+    code = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int: "i", ctypes.c_float: "f"}
+
+    def flat(c):
+        return "".join(code.get(t) or flat(t) for _, t in c._fields_)
+    p = struct.Struct("@" + flat(cls) + "0q")
+    assert p.size == ctypes.sizeof(cls)
+    return p.pack
+
+
+_pack_cache, _pack_rows, _pack_attn = _packer(MlaKvqCache), _packer(MlaKvqRows), _packer(MlaKvqAttnArgs)
 
 
 class MlaError(RuntimeError):
@@ -171,7 +175,7 @@ def load(path: Optional[str] = None):
         f.restype = ctypes.c_int
         f.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.mla_kvq_attn.restype = ctypes.c_int
-    lib.mla_kvq_attn.argtypes = [ctypes.POINTER(MlaKvqAttnArgs), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.mla_kvq_attn.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.mla_kvq_attn_workspace_size.restype = ctypes.c_size_t
     lib.mla_kvq_attn_workspace_size.argtypes = [ctypes.POINTER(MlaKvqAttnArgs)]
     lib.mla_kvq_check.restype = ctypes.c_int
@@ -639,12 +643,6 @@ class QuantCache:
         if not -KVQ_MAX_EXPONENT <= self.exponent <= KVQ_MAX_EXPONENT:
             raise ValueError(f"cache exponent {self.exponent} outside +-{KVQ_MAX_EXPONENT}")
 
-    def c_struct(self) -> MlaKvqCache:
-        r = self.rows
-        n = r.size(0)
-        # the row stride of a one-row tensor is whatever its maker left there
-        return MlaKvqCache(r.data_ptr(), r.stride(0) if n > 1 else KVQ_ROW_BYTES, n, self.exponent)
-
 
 def kvq_alloc(slots: int, exponent: int = 0, device="cuda") -> QuantCache:
     """A cache of ``slots`` rows that all stand for zeros."""
@@ -799,15 +797,23 @@ class KvqInputs:
                 or self.block_table.shape[0] != B or not self.block_table.is_contiguous():
             raise ValueError("block_table must be a contiguous [B][max_pages] int32 tensor")
 
+    def values(self, out=None, lse=None):
+        """The fields of an MlaKvqAttnArgs in their order, the cache's in its place."""
+        pool, table, tree, paged = self.cache.rows, self.block_table, self.tree_parent, self.page_size > 1
+        m = pool.shape[0]
+        return (self.B, self.Q, self.H,
+                pool.data_ptr(), pool.stride()[0] if m > 1 else KVQ_ROW_BYTES, m, self.cache.exponent,
+                self.q_lat.data_ptr(), self.q_pe.data_ptr(), self.page_size,
+                0 if paged or self.kv_indptr is None else self.kv_indptr.data_ptr(),
+                0 if paged or self.kv_indices is None else self.kv_indices.data_ptr(),
+                table.data_ptr() if paged and table is not None else 0,
+                table.shape[1] if paged and table is not None else 0,
+                self.prefix_lens.data_ptr(), 0 if tree is None else tree.data_ptr(), self.window, self.sinks,
+                self.scale, 0 if out is None else out.data_ptr(), 0 if lse is None else lse.data_ptr())
+
     def c_args(self, out=None, lse=None) -> MlaKvqAttnArgs:
-        table, tree = self.block_table, self.tree_parent
-        paged = self.page_size > 1
-        return MlaKvqAttnArgs(
-            self.B, self.Q, self.H, self.cache.c_struct(), self.q_lat.data_ptr(), self.q_pe.data_ptr(), self.page_size,
-            None if paged else _ptr(self.kv_indptr), None if paged else _ptr(self.kv_indices),
-            _ptr(table) if paged else None, table.shape[1] if paged and table is not None else 0,
-            self.prefix_lens.data_ptr(), None if tree is None else tree.data_ptr(), self.window, self.sinks,
-            self.scale, None if out is None else out.data_ptr(), None if lse is None else lse.data_ptr())
+        v = self.values(out, lse)
+        return MlaKvqAttnArgs(*v[:3], MlaKvqCache(*v[3:7]), *v[7:])
 
 
 def kvq_workspace_size(ki: KvqInputs) -> int:
@@ -842,8 +848,8 @@ def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, che
     if workspace is None:
         with _made_on(stream):
             workspace = alloc_workspace(kvq_workspace_size(ki), dev)
-    _kvq_launch("mla_kvq_attn", load().mla_kvq_attn, dev, stream, ki.c_args(out, lse), workspace.data_ptr(),
-                workspace.nbytes)
+    _kvq_launch("mla_kvq_attn", load().mla_kvq_attn, dev, stream, _pack_attn(*ki.values(out, lse)),
+                workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 
