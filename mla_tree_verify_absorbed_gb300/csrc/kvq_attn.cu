@@ -23,12 +23,14 @@
 // the warps that feed it: per tile it takes in 26 KB of packed rows, hands them
 // to the producers, takes back 72 KB of operand, gives that to the MMAs, and
 // passes 16 KB of weights on, about 1,700 cycles of its 128 bytes per cycle
-// with 1,152 cycles of MMA beneath.  Measured on 64 nodes x 64 heads x 200,000
-// tokens: 1.64 ms, 1.09 PFLOP/s, about 2,000 cycles a tile at the 1.6 GHz that
-// the power limit leaves.  With few rows the same conversion serves fewer
-// products: 128 ragged sequences x 16 heads (440,000 tokens) take 124 us, 1.5
-// TB/s.  A call of 257 tokens takes 17 us: cluster launch and split 2.5, queries
-// 5 to 6, first scores 1 to 2, 1.2 a tile, output 1.3, exit 0.9.
+// with 1,152 cycles of MMA beneath.  A half tile takes a producer warp 650
+// cycles to convert in the value CTA, where nothing else uses the schedulers,
+// and 1,100 to 1,400 beside the softmax.  Measured on 64 nodes x 64 heads x
+// 200,000 tokens: 1.62 ms, 1.10 PFLOP/s.  With few rows the same conversion
+// serves fewer products: 128 ragged sequences x 16 heads (440,000 tokens) take
+// 118 us, 1.5 TB/s.  A call of 257 tokens takes 16 us: launch and split 2.2, the
+// first piece 1.1, its queries 1.6, first scores 2.5, first weights 1.6, 1.0 a
+// tile, output 1.5, exit 0.8.
 //
 // Conversion.  8 producer warps per CTA, in each a lane per (token, 64-element
 // chunk): 32 bytes of codes and 4 scales make the 128 bytes of one operand row
@@ -1047,6 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
   const int warp = threadIdx.x >> 5;
   const int cluster = blockIdx.x / 2;
   Ctl* c = reinterpret_cast<Ctl*>(smem + kOffCtl);
+  grid_dep_wait();  // launched before the stream's last kernel has ended
   // Barriers, a few per warp.
   if ((threadIdx.x & 31) == 0) {
     if (warp < 4) {
@@ -1189,6 +1192,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   grid_dep_wait();
+  grid_dep_launch();
   if (tid < p.clusters) start[tid] = static_cast<const Start*>(p.starts)[tid];
   __syncthreads();
   const int clusters = start[0].n;
@@ -1500,7 +1504,7 @@ extern "C" mla_status mla_kvq_attn(const mla_kvq_attn_args* a, void* workspace, 
   const int64_t rows = (int64_t)p.B * p.rows;
   if (!query_map(&maps.lat, p.q_lat, rows, kDl, p.box_rows) || !query_map(&maps.pe, p.q_pe, rows, kDr, p.box_rows))
     return MLA_ERR_CUDA;
-  if (launch_kernel(kvq_attn_kernel, dim3(2 * n), dim3(kThreads), kSmemAlloc, s, false, p, maps) != cudaSuccess)
+  if (launch_kernel(kvq_attn_kernel, dim3(2 * n), dim3(kThreads), kSmemAlloc, s, true, p, maps) != cudaSuccess)
     return MLA_ERR_CUDA;
   // two blocks per SM of the clusters, fewer when even n - 1 cut row groups make fewer tasks
   const int chunks = ((p.rows < kRG ? p.rows : kRG) + kMergeRows - 1) / kMergeRows;

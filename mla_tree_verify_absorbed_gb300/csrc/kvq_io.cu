@@ -17,8 +17,8 @@
 //
 // Bound: HBM.  A bf16 row is 1152 bytes on one side and 416 on the other; one
 // warp takes a row, lane l its scale block l.  Measured on 200,000 rows in
-// random slots (us; GB/s of both sides): bf16 write 64 (4,900), fp32 write 85
-// (6,400), bf16 read 54 (5,800), fp32 read 89 (6,100).  The bf16 write is held
+// random slots (us; GB/s of both sides): bf16 write 61 (5,100), fp32 write 83
+// (6,600), bf16 read 52 (6,000), fp32 read 86 (6,300).  The bf16 write is held
 // by its instructions rather than by HBM.
 #include <cuda_fp8.h>
 
@@ -204,6 +204,8 @@ __global__ void __launch_bounds__(kIoThreads) kvq_write_kernel(const IoParams p)
   const int lane = threadIdx.x & 31;
   const int64_t warp = (int64_t)blockIdx.x * kIoWarps + (threadIdx.x >> 5);
   const int64_t nwarps = (int64_t)gridDim.x * kIoWarps;
+  grid_dep_wait();  // launched before the stream's last kernel has ended
+  grid_dep_launch();
   uint32_t e = 0;
   for (int64_t i0 = warp; i0 < p.n; i0 += kDeep * nwarps) {
     int64_t slot[kDeep];
@@ -268,6 +270,8 @@ __global__ void __launch_bounds__(kIoThreads) kvq_read_kernel(const IoParams p) 
   // the exponent in bf16: a power of two, exact
   const __nv_bfloat16 mb = __float2bfloat16_rn(p.mul);
   const uint32_t mul2 = (uint32_t)__bfloat16_as_ushort(mb) * 0x10001u;
+  grid_dep_wait();  // launched before the stream's last kernel has ended
+  grid_dep_launch();
   uint32_t e = 0;
   for (int64_t i0 = warp; i0 < p.n; i0 += kDeep * nwarps) {
     int64_t slot[kDeep];
@@ -398,12 +402,10 @@ extern "C" mla_status mla_kvq_write(const mla_kvq_cache* cache, const mla_kvq_ro
   int grid = 0;
   st = io_grid(p.n, 8, &grid);
   if (st != MLA_OK) return st;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (src->dtype == MLA_BF16)
-    kvq_write_kernel<__nv_bfloat16, 2><<<grid, kIoThreads, 0, s>>>(p);
-  else
-    kvq_write_kernel<float, 1><<<grid, kIoThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  const auto kernel = src->dtype == MLA_BF16 ? kvq_write_kernel<__nv_bfloat16, 2> : kvq_write_kernel<float, 1>;
+  const cudaError_t e = launch_kernel(kernel, dim3(grid), dim3(kIoThreads), 0, reinterpret_cast<cudaStream_t>(stream),
+                                      true, p);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 extern "C" mla_status mla_kvq_read(const mla_kvq_cache* cache, const mla_kvq_rows* dst, void* workspace,
@@ -415,12 +417,10 @@ extern "C" mla_status mla_kvq_read(const mla_kvq_cache* cache, const mla_kvq_row
   int grid = 0;
   st = io_grid(p.n, 16, &grid);
   if (st != MLA_OK) return st;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dst->dtype == MLA_BF16)
-    kvq_read_kernel<__nv_bfloat16, 2><<<grid, kIoThreads, 0, s>>>(p);
-  else
-    kvq_read_kernel<float, 2><<<grid, kIoThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  const auto kernel = dst->dtype == MLA_BF16 ? kvq_read_kernel<__nv_bfloat16, 2> : kvq_read_kernel<float, 2>;
+  const cudaError_t e = launch_kernel(kernel, dim3(grid), dim3(kIoThreads), 0, reinterpret_cast<cudaStream_t>(stream),
+                                      true, p);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 extern "C" mla_status mla_kvq_check(const void* workspace, mla_stream_t stream, uint32_t* bits) {

@@ -595,6 +595,53 @@ def test_largest_windows_and_sinks(window, sinks):
     check_attn(problem(B=3, Q=9, H=7, lens=[0, 500, 61], seed=40, window=window, sinks=sinks))
 
 
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "graph"])
+def test_calls_that_follow_each_other_see_each_other(captured):
+    # rows written, attended to, read back and written over, one call right behind the other: each starts
+    # before the last has ended, none may look before it has
+    p = problem(B=6, Q=4, H=16, lens=[700, 90, 1300, 5, 64, 250], seed=44)
+    n = sum(v + 4 for v in p.lens)
+    at = p.ki.kv_indices[:n].contiguous()
+    both = [latents("normal", n, torch.bfloat16, 45 + i) for i in range(2)]
+    both = [(t.cuda(), k.cuda()) for t, k in both]
+    ws = api.alloc_workspace(api.kvq_workspace_size(p.ki))
+    ws2 = api.alloc_workspace(api.KVQ_WORKSPACE_BYTES)
+
+    def buffers():
+        return (torch.zeros((6, 4, 16, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros((6, 4, 16), device="cuda"),
+                torch.zeros((n, 512), dtype=torch.bfloat16, device="cuda"),
+                torch.zeros((n, 64), dtype=torch.bfloat16, device="cuda"))
+
+    def step(i, o, sync):
+        api.kvq_write(p.ki.cache, *both[i], at, workspace=ws2, check=False)
+        if sync:
+            torch.cuda.synchronize()
+        api.kvq_attn(p.ki, out=o[0], lse=o[1], workspace=ws, check=False)
+        if sync:
+            torch.cuda.synchronize()
+        api.kvq_read(p.ki.cache, at, kv_c=o[2], k_pe=o[3], workspace=ws2, check=False)
+        if sync:
+            torch.cuda.synchronize()
+    want = [buffers() for _ in range(2)]
+    for i in range(2):
+        step(i, want[i], True)
+    got = [buffers() for _ in range(30)]
+    torch.cuda.synchronize()
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for i, o in enumerate(got):
+                step(i % 2, o, False)
+        g.replay()
+    else:
+        for i, o in enumerate(got):
+            step(i % 2, o, False)
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        for a, b in zip(o, want[i % 2]):
+            assert torch.equal(a, b), i
+
+
 @pytest.mark.parametrize("page", [1, 16])
 def test_bad_tables_are_reported(page):
     def go(**kw):
