@@ -118,6 +118,8 @@ struct Params {
   const void* q_lat;
   const void* q_pe;
   int page_size;
+  uint32_t page_mul;  // pos / page_size = pos * page_mul >> page_shift
+  int page_shift;
   const int32_t* kv_indptr;
   const int32_t* kv_indices;
   const int32_t* block_table;

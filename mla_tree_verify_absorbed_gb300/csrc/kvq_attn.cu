@@ -28,7 +28,7 @@
 // and 1,100 to 1,400 beside the softmax.  Measured on 64 nodes x 64 heads x
 // 200,000 tokens: 1.62 ms, 1.10 PFLOP/s.  With few rows the same conversion
 // serves fewer products: 128 ragged sequences x 16 heads (440,000 tokens) take
-// 118 us, 1.5 TB/s.  A call of 257 tokens takes 16 us: launch and split 2.2, the
+// 113 us, 1.6 TB/s.  A call of 257 tokens takes 16 us: launch and split 2.2, the
 // first piece 1.1, its queries 1.6, first scores 2.5, first weights 1.6, 1.0 a
 // tile, output 1.5, exit 0.8.
 //
@@ -473,6 +473,14 @@ __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
   return v;
 }
 
+// pos / page_size by a multiplication that the host prepares: for page_size in
+// (2^(L-1), 2^L], ceil(2^(31+L) / page_size) fits 32 bits and is off by less than
+// 2^L over 2^(31+L), too little to matter for pos < 2^31.  Page size 1 needs no
+// branch, and the producers' loops stay short.
+__device__ __forceinline__ uint32_t page_of(const Params& p, uint32_t pos) {
+  return (uint32_t)(((uint64_t)pos * p.page_mul) >> p.page_shift);
+}
+
 // Queries of up to 64 rows pass through one stage, that of the piece's second
 // tile, so that its first is converted meanwhile.
 __device__ __forceinline__ bool one_stage(const Params& p) { return p.box_rows <= 64; }
@@ -518,14 +526,11 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     auto entry_of = [&](int v) -> int32_t {
       const uint32_t pos = (uint32_t)pc.tile(v) * kTK + kTok * pw + lane % kTok;
       if (v >= pc.t1 || pos >= (uint32_t)pc.N || (pos < (uint32_t)pc.lo && pos >= (uint32_t)p.sinks)) return -2;
-      return __ldg(idx + (p.page_size == 1 ? pos : pos / (uint32_t)p.page_size));
+      return __ldg(idx + page_of(p, pos));
     };
     auto slot_of = [&](int32_t e, int v) -> uint32_t {
-      int64_t s = e;
-      if (p.page_size > 1) {
-        const uint32_t pos = (uint32_t)pc.tile(v) * kTK + kTok * pw + lane % kTok;
-        s = s * p.page_size + pos % (uint32_t)p.page_size;
-      }
+      const uint32_t pos = (uint32_t)pc.tile(v) * kTK + kTok * pw + lane % kTok;
+      int64_t s = (int64_t)e * p.page_size + (pos - page_of(p, pos) * (uint32_t)p.page_size);
       if (e < 0 || s >= p.slots) {
         if (e != -2 && v < pc.t1) err |= MLA_DEVERR_SLOT;
         s = 0;
@@ -774,23 +779,29 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
       tc_fence_after();
       // which of the tile's 64 tokens the row sees, where not all of them
       const int pos0 = pc.tile(t) * kTK;
-      const bool masked = pos0 > P - kTK || pos0 <= past_any;
-      uint64_t vis = ~0ull;
-      if (masked) {
+      const uint32_t tS = lane_off + kColS + sb * kTK;
+      if (pos0 > P - kTK || pos0 <= past_any) {
         const int rel0 = pos0 - P;
-        vis = low_bits(-rel0) & ~(low_bits(past - pos0 + 1) & ~low_bits(p.sinks - pos0));
+        uint64_t vis = low_bits(-rel0) & ~(low_bits(past - pos0 + 1) & ~low_bits(p.sinks - pos0));
         if (rel0 < 64 && rel0 > -64) vis |= rel0 >= 0 ? nv.mask >> rel0 : nv.mask << -rel0;
+        // few tiles need it: the masked scores go back, and the loops below know of no mask
+#pragma unroll 1
+        for (int hc = 0; hc < 2; ++hc) {
+          uint32_t u[32];
+          tmem_ld32_sync(tS + 32 * hc, u);
+          mask32(u, (uint32_t)(vis >> (32 * hc)));
+          tmem_st_32x32b_x32(tS + 32 * hc, u);
+        }
+        tmem_wait_st();
       }
       // Two passes of 32 columns, for the maximum and for the weights: the
       // scores stay in Tensor Memory in between, which halves the registers
       // and the code.
-      const uint32_t tS = lane_off + kColS + sb * kTK;
       float tmax = -INFINITY;
 #pragma unroll 1
       for (int hc = 0; hc < 2; ++hc) {
         uint32_t u[32];
         tmem_ld32_sync(tS + 32 * hc, u);
-        if (masked) mask32(u, (uint32_t)(vis >> (32 * hc)));
         float mx[2] = {tmax, __uint_as_float(u[31])};
 #pragma unroll
         for (int q = 0; q < 30; q += 2)
@@ -830,7 +841,6 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
           __syncwarp();
           if (lane == 0) mbar_arrive(&c->s_free[sb]);
         }
-        if (masked) mask32(u, (uint32_t)(vis >> (32 * hc)));
 #pragma unroll
         for (int q8 = 0; q8 < 4; ++q8) {
           uint32_t wv[4];
@@ -1446,6 +1456,10 @@ Params make_params(const mla_kvq_attn_args* a, void* ws, int clusters) {
   p.q_lat = a->q_lat;
   p.q_pe = a->q_pe;
   p.page_size = a->page_size;
+  int L = 0;
+  while (((int64_t)1 << L) < a->page_size) ++L;
+  p.page_shift = 31 + L;
+  p.page_mul = (uint32_t)((((uint64_t)1 << (31 + L)) + (uint64_t)a->page_size - 1) / (uint64_t)a->page_size);
   p.kv_indptr = a->kv_indptr;
   p.kv_indices = a->kv_indices;
   p.block_table = a->block_table;

@@ -528,6 +528,19 @@ def test_many_sequences_and_heads(kw):
     check_attn(problem(seed=42, **kw))
 
 
+@pytest.mark.parametrize("page", [2, 3, 7, 33, 127, 1000, 4097])
+def test_page_sizes(page):
+    check_attn(problem(B=3, Q=3, H=8, lens=[1400, 2 * page - 3 if page > 1 else 0, 65], page=page, seed=46))
+
+
+@pytest.mark.parametrize("page", [2 ** 31 - 1, 2 ** 30, 2 ** 30 + 1])
+def test_a_page_larger_than_the_pool(page):
+    # page 0 holds every position: slots are positions
+    p = problem(B=1, Q=2, H=8, lens=[900], seed=47)
+    ki = dataclasses.replace(p.ki, page_size=page, block_table=torch.zeros((1, 1), dtype=torch.int32, device="cuda"))
+    check_attn(dataclasses.replace(p, ki=ki, slots=[np.arange(902)]))
+
+
 def test_arrays_aligned_to_16_bytes_only():
     # whole row groups, cut ones, and queries and outputs whose rows do not fall on sectors
     p = problem(B=5, Q=4, H=40, lens=[70, 3000, 0, 513, 64], seed=43)

@@ -173,6 +173,22 @@ def test_attn_refuses_a_scale_that_leaves_fp32(lib, scale, exponent):
     assert attn_call(lib, attn_struct(scale=scale, cache=cache_struct(exponent=back)), ws=0) == api.MLA_ERR_WORKSPACE
 
 
+def test_page_of_a_position_by_multiplication():
+    # the kernel's pos * ceil(2^(31 + L) / page) >> (31 + L), 2^(L - 1) < page <= 2^L, for every border that could fail
+    rng = np.random.default_rng(5)
+    pages = {1, 2, 3, 7, 2 ** 30, 2 ** 30 + 1, 2 ** 31 - 1}
+    pages |= {int(2 ** e) for e in rng.uniform(0, 31, 400)} | {2 ** k + d for k in range(2, 31) for d in (-1, 0, 1)}
+    for page in pages:
+        L = (page - 1).bit_length()
+        mul = -(-2 ** (31 + L) // page)
+        assert mul < 2 ** 32
+        last = (2 ** 31 - 1) // page
+        for k in {0, 1, 2, last // 2, last, *map(int, rng.integers(0, last + 1, 20))}:
+            for pos in (k * page - 1, k * page, k * page + page - 1):
+                if 0 <= pos < 2 ** 31:
+                    assert pos * mul >> (31 + L) == pos // page
+
+
 def test_attn_cache_and_table_refusals(lib):
     for k, v in BAD_CACHE:
         assert attn_call(lib, attn_struct(cache=cache_struct(**{k: v}))) == api.MLA_ERR_INVALID_ARG, (k, v)
