@@ -710,11 +710,6 @@ __device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* s
   return true;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 // The low n bits, n clamped to [0, 64].
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : ~0ull >> (64 - n); }
 // Scores of the tokens whose bit is 0 become -inf, whatever they were.
@@ -796,18 +791,12 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
       }
       // Two passes of 32 columns, for the maximum and for the weights: the
       // scores stay in Tensor Memory in between, which halves the registers
-      // and the code.
+      // and the code.  The maximum comes with the load (by instructions of its
+      // own, 64 nodes x 64 heads x 200,000 tokens took 1,624 us, not 1,603).  A
+      // NaN score makes the row's sum NaN whichever way the maximum takes it.
       float tmax = -INFINITY;
 #pragma unroll 1
-      for (int hc = 0; hc < 2; ++hc) {
-        uint32_t u[32];
-        tmem_ld32_sync(tS + 32 * hc, u);
-        float mx[2] = {tmax, __uint_as_float(u[31])};
-#pragma unroll
-        for (int q = 0; q < 30; q += 2)
-          mx[(q >> 1) & 1] = max3(mx[(q >> 1) & 1], __uint_as_float(u[q]), __uint_as_float(u[q + 1]));
-        tmax = max3(mx[0], mx[1], __uint_as_float(u[30]));
-      }
+      for (int hc = 0; hc < 2; ++hc) tmax = fmaxf(tmax, tmem_max32(tS + 32 * hc));
       // the scale is positive: the scaled maximum is the maximum of the scaled scores
       tmax *= sl2;
       // the maximum after the tile before, from the other group (in the first
