@@ -26,9 +26,9 @@
 // with 1,152 cycles of MMA beneath.  A half tile takes a producer warp 650
 // cycles to convert in the value CTA, where nothing else uses the schedulers,
 // and 1,100 to 1,400 beside the softmax.  Measured on 64 nodes x 64 heads x
-// 200,000 tokens: 1.62 ms, 1.10 PFLOP/s.  With few rows the same conversion
+// 200,000 tokens: 1.60 ms, 1.11 PFLOP/s.  With few rows the same conversion
 // serves fewer products: 128 ragged sequences x 16 heads (440,000 tokens) take
-// 113 us, 1.6 TB/s.  A call of 257 tokens takes 16 us: launch and split 2.2, the
+// 108 us, 1.7 TB/s.  A call of 257 tokens takes 15 us: launch and split 2.2, the
 // first piece 1.1, its queries 1.6, first scores 2.5, first weights 1.6, 1.0 a
 // tile, output 1.5, exit 0.8.
 //
@@ -88,7 +88,7 @@ constexpr int kWarpSched = 16;  // the pieces of work
 constexpr int kWarpAux = 17;    // TMEM allocation; rank 0: weight copies
 // Warps w, w + 4, .. share a scheduler, and issuing a tile's MMAs is work for it:
 // away from the one that has the row warps of few rows (beside them, 128 ragged
-// sequences x 16 heads took 122.9 us, not 118.2).
+// sequences x 16 heads took 4% longer).
 constexpr int kWarpMma = 19;
 
 // A tile is staged as two halves, each with its own full / empty barriers:
