@@ -152,8 +152,8 @@ constexpr float kWeightShift = 7.f;
 // Cost of starting a row group or a piece of one, in tiles, and the fewest
 // tiles worth a cluster of its own.  Measured, us (64 nodes x 64 heads in a window
 // of 1,000; 16 sequences x 64 heads in a window of 4,096; 128 ragged sequences
-// x 16 heads): kFixed 2: 43.9, 41.7, 130.4; 4: 41.5, 42.0, 124.5; 6: 47.1, 41.1,
-// 128.2; kMinTiles 16 in place of 4: 48.5, 43.9, 124.5.
+// x 16 heads): kFixed 3: 43.2, 42.0, 110.7; 4: 40.7, 40.5, 109.1; 5: 45.5, 39.1,
+// 111.4; kMinTiles 6 in place of 4: 43.9, 40.7, 109.3.
 constexpr int kFixed = 4;
 constexpr int kMinTiles = 4;
 
