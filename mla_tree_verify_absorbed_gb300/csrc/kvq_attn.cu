@@ -203,7 +203,6 @@ struct alignas(16) Ctl {
   int64_t start_entry;         // and its first table entry
   uint32_t tmem_base;
   int abort;
-  int abort_site;
   uint32_t err;
 };
 constexpr int kSmemBytes = kOffCtl + (int)sizeof(Ctl);
@@ -212,29 +211,19 @@ static_assert(kSmemAlloc <= 232448, "shared memory budget");
 static_assert(offsetof(Ctl, alpha) % 16 == 0 && kOffCtl % 16 == 0, "bulk-copy alignment");
 static_assert(kOffPS % 1024 == 0 && kOffPV % 1024 == 0 && kStageS % 1024 == 0, "swizzle atoms");
 
-enum {
-  kSiteEmpty = 1, kSiteQReady, kSiteFullS, kSiteSFree, kSiteSFull, kSitePFree, kSiteFinFree, kSiteFullV,
-  kSiteOReady, kSitePFull, kSitePvPrev, kSitePvLast, kSiteFinFull, kSiteMReady, kSitePStaged, kSitePiece,
-  kSitePieceFree, kSitePsFree, kSiteQIn
-};
-
-__device__ __noinline__ void raise_abort(Ctl* c, int site) {
-  if (*reinterpret_cast<volatile int*>(&c->abort) == 0) atomicCAS(&c->abort_site, 0, site);
-  for (uint32_t rk = 0; rk < 2; ++rk) st_cluster_u32(mapa_shared(smem_u32(&c->abort), rk), 1u);
-}
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* c, int site) {
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* c) {
   if (mbar_wait(bar, parity, &c->abort, kWaitLimitNs, true)) return true;
-  raise_abort(c, site);
+  for (uint32_t rk = 0; rk < 2; ++rk) st_cluster_u32(mapa_shared(smem_u32(&c->abort), rk), 1u);
   return false;
 }
 // The first try is inline, everything after it one shared copy: the roles'
 // loops have to fit the instruction cache together.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* c, int site) {
-  return mbar_try_wait_cluster(bar, parity) || wait_slow(bar, parity, c, site);
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* c) {
+  return mbar_try_wait_cluster(bar, parity) || wait_slow(bar, parity, c);
 }
 // Every lane waits; the result is warp-uniform and the warp converged.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c, int site) {
-  return __all_sync(0xffffffffu, wait(bar, parity, c, site));
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c) {
+  return __all_sync(0xffffffffu, wait(bar, parity, c));
 }
 
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -258,7 +247,6 @@ struct Tiles {
   int ns, tw;
   int T;  // ns + te - tw; 0 for an unused sequence
   int64_t lo;  // positions in [sinks, lo) are seen by no node
-  __device__ __forceinline__ int at(int v) const { return v < ns ? v : v - ns + tw; }
 };
 __device__ __forceinline__ Tiles tiles_of(const Params& p, int64_t P) {
   Tiles t;
@@ -314,7 +302,7 @@ __device__ void schedule(const Params& p, Ctl* c, int cluster) {
   uint32_t seg = 0;
   auto put = [&](const Piece& pc) {
     const uint32_t q = seg % kPieces;
-    if (!wait_warp(&c->piece_empty[q], ((seg / kPieces) & 1u) ^ 1u, c, kSitePieceFree)) return false;
+    if (!wait_warp(&c->piece_empty[q], ((seg / kPieces) & 1u) ^ 1u, c)) return false;
     if (lane == 0) {
       c->piece[q] = pc;
       mbar_arrive(&c->piece_full[q]);
@@ -361,7 +349,7 @@ __device__ __forceinline__ void for_pieces(Ctl* c, F&& f) {
 #pragma unroll 1
   for (uint32_t seg = 0;; ++seg) {
     const uint32_t q = seg % kPieces;
-    if (!wait_warp(&c->piece_full[q], (seg / kPieces) & 1u, c, kSitePiece)) return;
+    if (!wait_warp(&c->piece_full[q], (seg / kPieces) & 1u, c)) return;
     const Piece pc = c->piece[q];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&c->piece_empty[q]);
@@ -516,7 +504,7 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     // to it late, but of the two pieces after this one, one at least has a tile
     // of the group, so the queries of the fourth, which use the same barrier,
     // cannot overtake it.
-    if (t >= pc.t1) return !kScore || wait_warp(&c->q_ready[q_bar], q_phase, c, kSiteQReady);
+    if (t >= pc.t1) return !kScore || wait_warp(&c->q_ready[q_bar], q_phase, c);
     uint32_t turn = (j - (uint32_t)(pc.t1 - t)) >> 1;  // tiles this group has taken before
     const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
     // Pool row of token kTok pw + lane % kTok of tile v, in two steps: the table
@@ -564,13 +552,13 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     for (int h = 0; h < 2; ++h) fetch(slot, h, turn, true);
     int32_t ent = entry_of(t + 2);
     // until then the queries pass through the stages
-    if (kScore && !ahead && !wait_warp(&c->q_ready[q_bar], q_phase, c, kSiteQReady)) return false;
+    if (kScore && !ahead && !wait_warp(&c->q_ready[q_bar], q_phase, c)) return false;
 #pragma unroll 1
     for (int h = 0; t < pc.t1; h ^= 1) {
       cp_async_wait_group<1>();  // this half's pieces, of this lane
       __syncwarp();              // of every lane
       const uint32_t full = 2 * grp + h;
-      if (!wait_warp(&c->empty[full], (turn & 1u) ^ 1u, c, kSiteEmpty)) return false;
+      if (!wait_warp(&c->empty[full], (turn & 1u) ^ 1u, c)) return false;
       if (kScore && h) {
 #pragma unroll
         for (int i = 0; i < kTok / 4; ++i) {
@@ -605,7 +593,7 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
         fetch(slot, 1, turn, t < pc.t1);
       }
     }
-    return !ahead || wait_warp(&c->q_ready[q_bar], q_phase, c, kSiteQReady);
+    return !ahead || wait_warp(&c->q_ready[q_bar], q_phase, c);
   });
   cp_async_wait_all();
   if (err) atomicOr(&c->err, err);
@@ -632,15 +620,15 @@ __device__ void score_mma(uint8_t* smem, Ctl* c) {
   const bool leader = elect_one();
   uint32_t j = 0, seg = 0;
   for_pieces(c, [&](const Piece& pc) {
-    if (!wait_warp(&c->q_ready[seg % kPieces], (seg / kPieces) & 1u, c, kSiteQReady)) return false;
+    if (!wait_warp(&c->q_ready[seg % kPieces], (seg / kPieces) & 1u, c)) return false;
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
       const uint32_t par = j & 1u, turn = j >> 1, sb = j % kSBufs;
-      if (!wait_warp(&c->s_free[sb], ((j / kSBufs) & 1u) ^ 1u, c, kSiteSFree)) return false;
+      if (!wait_warp(&c->s_free[sb], ((j / kSBufs) & 1u) ^ 1u, c)) return false;
       const uint32_t lo = desc_addr(smem, par * kStageS) | kDescLoK;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (!wait_warp(&c->full[2 * par + h], turn & 1u, c, kSiteFullS)) return false;
+        if (!wait_warp(&c->full[2 * par + h], turn & 1u, c)) return false;
         if (h) fence_proxy_async_smem();  // the rope keys came by cp.async, without a fence of their writers
         tc_fence_after();
         if (leader) {
@@ -690,7 +678,7 @@ __device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* s
       tensor_copy_2d(stage + ck * chunk, ck < 8 ? &maps.lat : &maps.pe, ck < 8 ? 64 * ck : 0, y, &c->q_in);
   }
   __syncwarp();
-  if (!wait_warp(&c->q_in, seg & 1u, c, kSiteQIn)) return false;
+  if (!wait_warp(&c->q_in, seg & 1u, c)) return false;
 #pragma unroll 3
   for (int ck = 0; ck < 9; ++ck) {
     const uint32_t src = smem_u32(stage) + ck * chunk + r * 128;
@@ -759,7 +747,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
 #pragma unroll 1
     for (int t = t0 + (int)(i - j); t < t1; t += 2, i += 2) {
       const uint32_t sb = i % kSBufs;
-      if (!wait_warp(&c->s_full[sb], (i / kSBufs) & 1u, c, kSiteSFull)) return false;
+      if (!wait_warp(&c->s_full[sb], (i / kSBufs) & 1u, c)) return false;
       const uint32_t ps = i % kPStages;
       if (idle) {
         // every barrier's phases count on: the next piece may use the rows
@@ -767,7 +755,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
           mbar_arrive(&c->m_ready[wg][wq]);
           mbar_arrive(&c->s_free[sb]);
         }
-        if (!wait_warp(&c->ps_free[ps], ((i / kPStages) & 1u) ^ 1u, c, kSitePsFree)) return false;
+        if (!wait_warp(&c->ps_free[ps], ((i / kPStages) & 1u) ^ 1u, c)) return false;
         if (lane == 0) mbar_arrive(&c->p_staged[ps]);
         continue;
       }
@@ -803,7 +791,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
       // tile of a piece the wait only keeps the groups in step)
       float mp = -INFINITY;
       if (i > 0) {
-        if (!wait_warp(&c->m_ready[wg ^ 1][wq], ((i - 1) >> 1) & 1u, c, kSiteMReady)) return false;
+        if (!wait_warp(&c->m_ready[wg ^ 1][wq], ((i - 1) >> 1) & 1u, c)) return false;
         if (t > t0) mp = c->m_run[wg ^ 1][r];
       }
       // it moves only when this tile beats it by 2^kLazy
@@ -818,7 +806,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
       }
       const float nmu = m == -INFINITY ? 0.f : kWeightShift - m;
 
-      if (!wait_warp(&c->ps_free[ps], ((i / kPStages) & 1u) ^ 1u, c, kSitePsFree)) return false;
+      if (!wait_warp(&c->ps_free[ps], ((i / kPStages) & 1u) ^ 1u, c)) return false;
       const uint32_t pst = smem_u32(smem) + kOffPS + ps * kPBytes + r * 128;
       uint64_t ls = 0;  // two fp32 sums
 #pragma unroll 1
@@ -855,11 +843,11 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
     // both groups' sums go to the value CTA relative to the final maximum,
     // which the group of the last tile has
     if ((jl & 1u) != (uint32_t)wg && !idle) {
-      if (!wait_warp(&c->m_ready[wg ^ 1][wq], (jl >> 1) & 1u, c, kSiteMReady)) return false;
+      if (!wait_warp(&c->m_ready[wg ^ 1][wq], (jl >> 1) & 1u, c)) return false;
       const float mn = c->m_run[wg ^ 1][r];
       if (mn != m) l *= exp2f(m - mn);
     }
-    if (!wait_warp(&c->fin_free, (seg & 1u) ^ 1u, c, kSiteFinFree)) return false;
+    if (!wait_warp(&c->fin_free, (seg & 1u) ^ 1u, c)) return false;
     st_cluster_f32(mapa_shared(smem_u32(&c->lfin[wg][r]), 1), l);
     if ((jl & 1u) == (uint32_t)wg) st_cluster_f32(mapa_shared(smem_u32(&c->mfin[r]), 1), m);
     mbar_arrive_cluster(&c->fin_full, 1);
@@ -878,8 +866,8 @@ __device__ void weight_copier(const Params& p, uint8_t* smem, Ctl* c) {
   for_pieces(c, [&](const Piece& pc) {
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
       const uint32_t ps = j % kPStages, pb = j % kPBufs;
-      if (!wait_warp(&c->p_staged[ps], (j / kPStages) & 1u, c, kSitePStaged)) return false;
-      if (!wait_warp(&c->p_free[pb], ((j / kPBufs) & 1u) ^ 1u, c, kSitePFree)) return false;
+      if (!wait_warp(&c->p_staged[ps], (j / kPStages) & 1u, c)) return false;
+      if (!wait_warp(&c->p_free[pb], ((j / kPBufs) & 1u) ^ 1u, c)) return false;
       if (leader) {
         const uint32_t bar = mapa_shared(smem_u32(&c->p_full[pb]), 1);
         bulk_copy_s2c(mapa_shared(smem_u32(smem + kOffPV + pb * kPBytes), 1), smem + kOffPS + ps * kPBytes,
@@ -902,12 +890,12 @@ __device__ void value_mma(uint8_t* smem, Ctl* c) {
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
       const uint32_t par = j & 1u, pb = j % kPBufs;
-      if (!wait_warp(&c->o_ready[pb], (j / kPBufs) & 1u, c, kSiteOReady)) return false;
+      if (!wait_warp(&c->o_ready[pb], (j / kPBufs) & 1u, c)) return false;
       const uint32_t da = desc_addr(smem, kOffPV + pb * kPBytes) | kDescLoK;
       const uint32_t dv = desc_addr(smem, par * kStageV) | kDescLoV;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        if (!wait_warp(&c->full[2 * par + h], (j >> 1) & 1u, c, kSiteFullV)) return false;
+        if (!wait_warp(&c->full[2 * par + h], (j >> 1) & 1u, c)) return false;
         tc_fence_after();
         if (leader) {
           // 8-token groups 1 KB apart along K
@@ -953,12 +941,12 @@ __device__ void value_rows(const Params& p, Ctl* c) {
     for (int t = t0; t < pc.t1; ++t, ++j) {
       const int pb = j % kPBufs;
       if (w == 0 && lane == 0) mbar_arrive_expect_tx(&c->p_full[pb], weight_bytes(quads) + kRG * 4);
-      if (!wait_warp(&c->p_full[pb], (uint32_t)(j / kPBufs) & 1u, c, kSitePFull)) return false;
+      if (!wait_warp(&c->p_full[pb], (uint32_t)(j / kPBufs) & 1u, c)) return false;
       if (w == 0 && lane == 0) mbar_arrive_cluster_relaxed(&c->ps_free[j % kPStages], 0);
       if (t != t0 && wq < quads) {
         const float a = c->alpha[pb][r];
         if (__any_sync(0xffffffffu, a != 1.f)) {
-          if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c, kSitePvPrev)) return false;
+          if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < 256; c0 += 32) {
@@ -977,8 +965,8 @@ __device__ void value_rows(const Params& p, Ctl* c) {
       if (lane == 0) mbar_arrive(&c->o_ready[pb]);
     }
 
-    if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c, kSitePvLast)) return false;
-    if (!wait_warp(&c->fin_full, (uint32_t)seg & 1u, c, kSiteFinFull)) return false;
+    if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c)) return false;
+    if (!wait_warp(&c->fin_full, (uint32_t)seg & 1u, c)) return false;
     tc_fence_after();
     const float l = c->lfin[0][r] + c->lfin[1][r], m = c->mfin[r];
     // The sums are read before the score CTA may write the next piece's: without
@@ -1083,7 +1071,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
       }
     } else if (warp == 14) {
       c->abort = 0;
-      c->abort_site = 0;
       c->start_b = p.B;
       c->start_x = 0;
       c->start_T = 0;
