@@ -969,11 +969,14 @@ __device__ void value_rows(const Params& p, Ctl* c) {
     if (!wait_warp(&c->fin_full, (uint32_t)seg & 1u, c)) return false;
     tc_fence_after();
     const float l = c->lfin[0][r] + c->lfin[1][r], m = c->mfin[r];
-    // The sums are read before the score CTA may write the next piece's: without
-    // the fence nothing orders a load before a relaxed arrive, and a load held up
-    // behind it (by a miss of the instruction cache) read the next piece's zero.
-    __threadfence_block();
-    mbar_arrive_cluster_relaxed(&c->fin_free, 0);
+    // The sums are read before the score CTA may write the next piece's.  Its
+    // remote stores are ordered behind these loads by a release at cluster scope
+    // only: behind a relaxed arrive, a load held up by a miss of the instruction
+    // cache has read the next piece's zero.  The release takes 0.4 us, so a piece
+    // that is known to be the cluster's last goes without: nothing waits for it.
+    const uint32_t nq = (uint32_t)(seg + 1) % kPieces;
+    const bool last = mbar_test_wait_cluster(&c->piece_full[nq], ((uint32_t)(seg + 1) / kPieces) & 1u) && c->piece[nq].b < 0;
+    if (!last) mbar_arrive_cluster(&c->fin_free, 0);
     ++seg;
     if (wq >= quads) return true;
     const int row = g * kRG + r;

@@ -1,6 +1,8 @@
 """The 4-bit latent cache without a GPU: the oracle's pins, and what the
 library and its binding refuse before anything is launched."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -245,3 +247,17 @@ def test_binding_refuses_wrong_tensors(lib):
             api.kvq_attn(dataclasses.replace(ki, **bad))
     with pytest.raises(ValueError, match="dtype"):
         api.kvq_read(cache, s, "fp16")
+
+
+# ---------------------------------------------------------------------------
+# orderings that a run on one chip cannot show
+# ---------------------------------------------------------------------------
+def test_relaxed_cluster_arrivals_follow_no_loads():
+    # A relaxed arrive on another CTA's barrier orders none of the thread's own loads and stores before it, so it may
+    # only pass on what another barrier has said: that a bulk copy has read its source (ps_free).  Every other signal
+    # to the peer, fin_free (the row sums have been read) and fin_full (they are written), releases.
+    src = open(os.path.join(B.CSRC, "kvq_attn.cu")).read()
+    relaxed = re.findall(r"mbar_arrive_cluster_relaxed\(&c->(\w+)", src)
+    release = re.findall(r"mbar_arrive_cluster\(&c->(\w+)", src)
+    assert set(relaxed) == {"ps_free"}
+    assert set(release) == {"fin_free", "fin_full"}
