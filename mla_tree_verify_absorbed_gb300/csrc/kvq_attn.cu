@@ -508,19 +508,23 @@ __device__ __forceinline__ void producer(const Params& p, uint8_t* smem, Ctl* c,
     uint32_t turn = (j - (uint32_t)(pc.t1 - t)) >> 1;  // tiles this group has taken before
     const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
     // Pool row of token kTok pw + lane % kTok of tile v, in two steps: the table
-    // entry (a slot, or a page; -2 where no node sees the position), and, a
-    // tile later, the slot.  Positions that no node sees read slot 0, under a
-    // weight of zero.
+    // entry (a slot, or a page), and, a tile later, the slot.  Positions that no
+    // node sees have the entry -1 and read slot 0, under a weight of zero; a
+    // table's own entries may be any number, so a bad one is told from those by
+    // its position.
+    auto pos_of = [&](int v) { return (uint32_t)pc.tile(v) * kTK + kTok * pw + lane % kTok; };
+    auto seen = [&](int v, uint32_t pos) {
+      return v < pc.t1 && pos < (uint32_t)pc.N && (pos >= (uint32_t)pc.lo || pos < (uint32_t)p.sinks);
+    };
     auto entry_of = [&](int v) -> int32_t {
-      const uint32_t pos = (uint32_t)pc.tile(v) * kTK + kTok * pw + lane % kTok;
-      if (v >= pc.t1 || pos >= (uint32_t)pc.N || (pos < (uint32_t)pc.lo && pos >= (uint32_t)p.sinks)) return -2;
-      return __ldg(idx + page_of(p, pos));
+      const uint32_t pos = pos_of(v);
+      return seen(v, pos) ? __ldg(idx + page_of(p, pos)) : -1;
     };
     auto slot_of = [&](int32_t e, int v) -> uint32_t {
-      const uint32_t pos = (uint32_t)pc.tile(v) * kTK + kTok * pw + lane % kTok;
+      const uint32_t pos = pos_of(v);
       int64_t s = (int64_t)e * p.page_size + (pos - page_of(p, pos) * (uint32_t)p.page_size);
       if (e < 0 || s >= p.slots) {
-        if (e != -2 && v < pc.t1) err |= MLA_DEVERR_SLOT;
+        if (seen(v, pos)) err |= MLA_DEVERR_SLOT;
         s = 0;
       }
       return (uint32_t)s;

@@ -692,6 +692,25 @@ def test_bad_tables_are_reported(page):
         assert e == PARENT and torch.equal(out[1:], out0[1:]) and torch.equal(lse[1:], lse0[1:])
 
 
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("value", [-2, -3, -17, -2 ** 31])
+def test_every_negative_table_entry_is_reported(page, value):
+    # at the first and the last position of the prefix and at a node's, of a whole row group and of a cut one
+    p = problem(B=3, Q=4, H=8, lens=[150, 2900, 10], page=page, seed=48)
+    out0, lse0 = check_attn(p)
+    first = [0, 154, 154 + 2904] if page == 1 else [b * p.ki.block_table.shape[1] for b in range(3)]
+    for b, pos in ((0, 0), (0, 149), (1, 2899), (1, 2903), (2, 9), (2, 13)):
+        name = "kv_indices" if page == 1 else "block_table"
+        t = getattr(p.ki, name).clone()
+        t.view(-1)[first[b] + pos // page] = value
+        ki = dataclasses.replace(p.ki, **{name: t})
+        ws = api.alloc_workspace(api.kvq_workspace_size(ki))
+        out, lse = run(ki, workspace=ws)
+        assert api.kvq_check(ws) == SLOT, (b, pos)
+        for o in {0, 1, 2} - {b}:
+            assert torch.equal(out[o], out0[o]) and torch.equal(lse[o], lse0[o]), (b, pos, o)
+
+
 def test_captured_call_follows_its_inputs():
     p = problem(B=3, Q=4, H=16, lens=[900, 300, 64], page=16, seed=37, window=128, sinks=5)
     ws = api.alloc_workspace(api.kvq_workspace_size(p.ki))
