@@ -126,7 +126,8 @@ typedef struct {
  *
  * The softmax statistics and both products accumulate in fp32; keys and values
  * enter the products exactly, the softmax weights rounded to 11 bits.  lse is
- * natural-log; equal arguments give equal bytes.  Enqueues the attention
+ * natural-log, -infinity with a row of zeros in out where every visible score
+ * is -infinity; equal arguments give equal bytes.  Enqueues the attention
  * kernel and a kernel that merges the pieces of rows that several clusters
  * shared.  A bad table (MLA_DEVERR_PREFIX, _INDPTR, _PAGES: found before any
  * work) leaves out and lse as they were; a slot outside the pool or a parent

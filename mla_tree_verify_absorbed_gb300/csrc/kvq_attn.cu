@@ -1258,6 +1258,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
       for (int i = lane; i < n; i += 32) m = fmaxf(m, w[i]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (m == -INFINITY) m = 0.f;  // no piece has any weight
       for (int i = lane; i < n; i += 32) {
         w[i] = __expf(w[i] - m);
         sum += w[i];
@@ -1265,7 +1266,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) {
-        total[warp] = sum;
+        total[warp] = sum == 0.f ? 1.f : sum;  // then a row of zeros, as from one piece
         if (p.lse && cb == 0) p.lse[(int64_t)s.b * p.rows + g * kRG + r0 + warp] = m + logf(sum);
       }
     }

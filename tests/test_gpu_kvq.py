@@ -711,6 +711,24 @@ def test_every_negative_table_entry_is_reported(page, value):
             assert torch.equal(out[o], out0[o]) and torch.equal(lse[o], lse0[o]), (b, pos, o)
 
 
+def test_scores_of_minus_infinity():
+    # rope keys of -infinity: tokens without weight, and rows that have no others, whole or cut into pieces
+    p = problem(B=4, Q=1, H=4, lens=[3000, 200, 5, 2500], seed=49, tree="null")
+    p.ki.q_pe[..., 0] = 1.0
+    dead = np.concatenate([p.slots[0], p.slots[1][:150], p.slots[2], p.slots[3][:2490]]).astype(np.int64)
+    p.ki.cache.rows[torch.from_numpy(dead).cuda(), 288] = 0x80
+    p.ki.cache.rows[torch.from_numpy(dead).cuda(), 289] = 0xff
+    ws = api.alloc_workspace(api.kvq_workspace_size(p.ki))
+    out, lse = run(p.ki, workspace=ws)
+    assert api.kvq_check(ws) == 0
+    for b in (0, 2):
+        assert bool((out[b] == 0).all()), b
+        assert bool((lse[b] == -float("inf")).all()), b
+    # the others are those of the tokens with weight
+    compare(dataclasses.replace(p, lens=[-1, 50, -1, 10],
+                                slots=[None, p.slots[1][150:], None, p.slots[3][2490:]]), out, lse)
+
+
 def test_captured_call_follows_its_inputs():
     p = problem(B=3, Q=4, H=16, lens=[900, 300, 64], page=16, seed=37, window=128, sinks=5)
     ws = api.alloc_workspace(api.kvq_workspace_size(p.ki))
