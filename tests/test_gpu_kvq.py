@@ -729,6 +729,42 @@ def test_scores_of_minus_infinity():
                                 slots=[None, p.slots[1][150:], None, p.slots[3][2490:]]), out, lse)
 
 
+@pytest.mark.parametrize("exponent", [0, 4])
+def test_attention_over_every_scale(exponent):
+    # block i holds the scale bytes 4i .. 4i + 3 (zero, subnormals, .., 0x7f), with and without bit 7; the queries
+    # make up for it, so that every block has its share of the scores
+    p = problem(B=2, Q=3, H=8, lens=[333, 900], seed=50, exponent=exponent, scale=0.003)
+    r = np.random.default_rng(51)
+    p.rows[:, 256:288] = 4 * np.arange(32) + r.integers(0, 4, (len(p.rows), 32)) + 128 * r.integers(0, 2, (len(p.rows), 32))
+    p.ki.cache.rows.copy_(torch.from_numpy(p.rows))
+    up = 2.0 ** (9 - np.arange(32) // 2 - exponent)
+    p.ki.q_lat.mul_(torch.from_numpy(up.repeat(16)).to(torch.bfloat16).cuda())
+    check_attn(p)
+
+
+@pytest.mark.parametrize("page", [1, 64])
+def test_long_prefix(page):
+    # 200,000 tokens, a head that sees them all alike, an ordinary one and a sharp one
+    p = problem(B=1, Q=2, H=3, lens=[200_000], page=page, seed=52)
+    for h, f in ((0, 2.0 ** -8), (2, 4.0)):
+        p.ki.q_lat[:, :, h] *= f
+        p.ki.q_pe[:, :, h] *= f
+    out, lse = check_attn(p)
+    # compare() allows the normaliser as many roundings as there are tokens.  It has fewer: a term passes the 31 + 1
+    # additions of its tile, at most one for each of the 3,126 tiles and one for each of the fewer than 256 partial
+    # results (the same again for their rescaling).  So a lost tile, 64 / 200,000 of the flat head's sum, would show.
+    lat, rope = O.unpack_rows(p.rows[p.slots[0]])
+    for i in range(2):
+        pos = O.visible(p.parent[0], i, 200_000)
+        q = p.ki.q_lat[0, i, 0].double().cpu().numpy(), p.ki.q_pe[0, i, 0].double().cpu().numpy()
+        s = p.ki.scale * (lat[pos] @ q[0] + rope[pos] @ q[1])
+        ds = 584 * 2.0 ** -24 * p.ki.scale * (np.abs(lat[pos]) @ np.abs(q[0]) + np.abs(rope[pos]) @ np.abs(q[1])).max()
+        want = np.log(np.exp(s).sum())
+        tol = ds + 2.0 ** -21 + (32 + 3126 + 2 * 256) * 2.0 ** -24 + 2.0 ** -22 * want
+        assert tol < 64 / 200_000 * np.exp(s.min() - s.max())
+        assert abs(float(lse[0, i, 0]) - want) <= tol
+
+
 def test_captured_call_follows_its_inputs():
     p = problem(B=3, Q=4, H=16, lens=[900, 300, 64], page=16, seed=37, window=128, sinks=5)
     ws = api.alloc_workspace(api.kvq_workspace_size(p.ki))
