@@ -142,6 +142,18 @@ mla_status mla_kvq_attn(const mla_kvq_attn_args *args, void *workspace, size_t w
  * arguments are invalid or no CUDA device can be queried. */
 size_t mla_kvq_attn_workspace_size(const mla_kvq_attn_args *args);
 
+/* Failure-detection self-test, as mla_verify_selftest_timeout.  Runs mla_kvq_attn
+ * with every device wait limited to hold_ns (0 < hold_ns <= 1e9) and the value
+ * product held back on a barrier that nothing completes: the parts of the
+ * kernel before it fill their buffers, wait for it, give up, drain what they
+ * issued and free their Tensor Memory, and the call completes with
+ * MLA_DEVERR_TIMEOUT; out and lse are unspecified.  The context stays usable:
+ * the next call on the same workspace runs normally.  Returns
+ * MLA_ERR_INVALID_ARG for a zero or larger hold_ns or an empty problem,
+ * otherwise as mla_kvq_attn. */
+mla_status mla_kvq_selftest_timeout(const mla_kvq_attn_args *args, void *workspace, size_t ws_bytes,
+                                    uint64_t hold_ns, mla_stream_t stream);
+
 /* Synchronises `stream`, then reads the error bits that the last call of this
  * header on this workspace left (a call with nothing to do launches nothing
  * and leaves them as they were).  Returns MLA_OK or MLA_ERR_DEVICE_CHECK (or

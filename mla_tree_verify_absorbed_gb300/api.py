@@ -34,7 +34,8 @@ EXPORTS = ("mla_verify_workspace_size", "mla_verify_attn", "mla_verify_attn_noal
            "mla_verify_build_meta", "mla_verify_check", "mla_verify_splits_used", "mla_status_str",
            "mla_verify_abi_version",
            "mla_verify_selftest_timeout", "mla_kv_compact", "mla_ddtree_build", "mla_ddtree_accept",
-           "mla_kvq_write", "mla_kvq_read", "mla_kvq_attn", "mla_kvq_attn_workspace_size", "mla_kvq_check")
+           "mla_kvq_write", "mla_kvq_read", "mla_kvq_attn", "mla_kvq_attn_workspace_size", "mla_kvq_check",
+           "mla_kvq_selftest_timeout")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 DDTREE_WORKSPACE_BYTES = 256
 KVQ_ROW_BYTES = 416
@@ -176,6 +177,9 @@ def load(path: Optional[str] = None):
         f.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.mla_kvq_attn.restype = ctypes.c_int
     lib.mla_kvq_attn.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.mla_kvq_selftest_timeout.restype = ctypes.c_int
+    lib.mla_kvq_selftest_timeout.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint64,
+                                             ctypes.c_void_p]
     lib.mla_kvq_attn_workspace_size.restype = ctypes.c_size_t
     lib.mla_kvq_attn_workspace_size.argtypes = [ctypes.POINTER(MlaKvqAttnArgs)]
     lib.mla_kvq_check.restype = ctypes.c_int
@@ -851,6 +855,22 @@ def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, che
     _kvq_launch("mla_kvq_attn", load().mla_kvq_attn, dev, stream, _pack_attn(*ki.values(out, lse)),
                 workspace.data_ptr(), workspace.nbytes)
     return out, lse
+
+
+def kvq_selftest_timeout(ki: KvqInputs, out, lse, workspace, hold_ns: int, stream=None):
+    """Run mla_kvq_selftest_timeout: the attention call with its waits limited
+    to hold_ns and one of its products held back; read the outcome with
+    kvq_check()."""
+    import torch
+    ki.check_layout()
+    _need(out, "out", torch.bfloat16, (ki.B, ki.Q, ki.H, 512))
+    _need(lse, "lse", torch.float32, (ki.B, ki.Q, ki.H))
+    _one_device(out=out, lse=lse, workspace=workspace, **ki.tensors())
+
+    def f(args, ws, n, raw):
+        return load().mla_kvq_selftest_timeout(args, ws, n, ctypes.c_uint64(int(hold_ns)), raw)
+    _kvq_launch("mla_kvq_selftest_timeout", f, ki.q_lat.device, stream, _pack_attn(*ki.values(out, lse)),
+                workspace.data_ptr(), workspace.nbytes)
 
 
 def kvq_check(workspace, stream=None) -> int:

@@ -135,6 +135,8 @@ struct Params {
   int groups;                  // row groups per sequence
   int box_rows;                // rows of a query copy: those of a row group, or of a sequence that has fewer
   int clusters;                // clusters launched
+  uint64_t wait_ns;            // how long a device wait may take
+  bool hold;                   // failure-detection self-test only: the value product never starts
   // workspace
   uint32_t* err;               // word 0, and the error words from kErrFirst on
   void* starts;                // [clusters]: see Start

@@ -51,8 +51,9 @@
 // tiles that need one.  Masked scores are -inf by selection, and any bytes in
 // the cache stand for finite latents, so 0 * V is 0 whatever V holds.
 //
-// Every wait is bounded (2 s); on timeout both CTAs stop issuing, drain what
-// they issued, free their Tensor Memory and report MLA_DEVERR_TIMEOUT.
+// Every wait is bounded (2 s, less in the self-test); on timeout both CTAs stop
+// issuing, drain what they issued, free their Tensor Memory and report
+// MLA_DEVERR_TIMEOUT.
 #include <cuda.h>
 
 #include <cmath>
@@ -201,6 +202,7 @@ struct alignas(16) Ctl {
   int start_b, start_T;        // that sequence, its tiles,
   int start_P;                 // its prefix length
   int64_t start_entry;         // and its first table entry
+  uint64_t wait_ns;            // Params::wait_ns
   uint32_t tmem_base;
   int abort;
   uint32_t err;
@@ -212,7 +214,7 @@ static_assert(offsetof(Ctl, alpha) % 16 == 0 && kOffCtl % 16 == 0, "bulk-copy al
 static_assert(kOffPS % 1024 == 0 && kOffPV % 1024 == 0 && kStageS % 1024 == 0, "swizzle atoms");
 
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* c) {
-  if (mbar_wait(bar, parity, &c->abort, kWaitLimitNs, true)) return true;
+  if (mbar_wait(bar, parity, &c->abort, c->wait_ns, true)) return true;
   for (uint32_t rk = 0; rk < 2; ++rk) st_cluster_u32(mapa_shared(smem_u32(&c->abort), rk), 1u);
   return false;
 }
@@ -887,9 +889,12 @@ __device__ void weight_copier(const Params& p, uint8_t* smem, Ctl* c) {
 // ---------------------------------------------------------------------------
 // value CTA
 // ---------------------------------------------------------------------------
-__device__ void value_mma(uint8_t* smem, Ctl* c) {
+__device__ void value_mma(const Params& p, uint8_t* smem, Ctl* c) {
   const bool leader = elect_one();
   uint32_t j = 0;
+  // the self-test: nothing completes this barrier, so the roles before this one
+  // fill every buffer and wait, each on its own barrier
+  if (p.hold && !wait_warp(&c->drain, 0u, c)) return;
   for_pieces(c, [&](const Piece& pc) {
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
@@ -1082,6 +1087,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
       c->start_x = 0;
       c->start_T = 0;
       c->left = 0;
+      c->wait_ns = p.wait_ns;
       c->err = (smem_u32(smem) & 1023u) ? MLA_DEVERR_LAYOUT : 0u;
     }
     fence_mbar_init();
@@ -1133,7 +1139,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
     if (!base0) {
     } else if (warp == kWarpMma) {
       if (rank == 0) score_mma(smem, c);
-      else value_mma(smem, c);
+      else value_mma(p, smem, c);
     } else if (warp == kWarpAux) {
       if (rank == 0) weight_copier(p, smem, c);
     } else if (warp == kWarpSched) {
@@ -1483,17 +1489,21 @@ extern "C" size_t mla_kvq_attn_workspace_size(const mla_kvq_attn_args* a) {
   return n > 0 ? layout(n).total : 0;
 }
 
-extern "C" mla_status mla_kvq_attn(const mla_kvq_attn_args* a, void* workspace, size_t ws_bytes, mla_stream_t stream) {
+namespace {
+mla_status run_attn(const mla_kvq_attn_args* a, void* workspace, size_t ws_bytes, mla_stream_t stream,
+                    uint64_t hold_ns) {
   mla_status st = validate_shape(a);
   if (st != MLA_OK) return st;
-  if (a->B == 0 || a->Q == 0) return MLA_OK;
+  if (a->B == 0 || a->Q == 0) return hold_ns ? MLA_ERR_INVALID_ARG : MLA_OK;  // the self-test needs a launch
   st = validate_call(a);
   if (st != MLA_OK) return st;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < MLA_KVQ_WORKSPACE_BYTES) return MLA_ERR_WORKSPACE;
   const int n = clusters_per_gpu();
   if (n < 1) return MLA_ERR_CUDA;
   if (ws_bytes < layout(n).total) return MLA_ERR_WORKSPACE;
-  const kvq::Params p = make_params(a, workspace, n);
+  kvq::Params p = make_params(a, workspace, n);
+  p.hold = hold_ns != 0;
+  p.wait_ns = p.hold ? hold_ns : kWaitLimitNs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // per call: the attribute belongs to the context, which may be a new one
   if (cudaFuncSetAttribute(kvq_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc) != cudaSuccess)
@@ -1511,4 +1521,15 @@ extern "C" mla_status mla_kvq_attn(const mla_kvq_attn_args* a, void* workspace, 
   if (n > 1 && launch_kernel(kvq_merge_kernel, dim3(blocks), dim3(kMergeThreads), 0, s, true, p, chunks) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
+}
+}  // namespace
+
+extern "C" mla_status mla_kvq_attn(const mla_kvq_attn_args* a, void* workspace, size_t ws_bytes, mla_stream_t stream) {
+  return run_attn(a, workspace, ws_bytes, stream, 0);
+}
+
+extern "C" mla_status mla_kvq_selftest_timeout(const mla_kvq_attn_args* a, void* workspace, size_t ws_bytes,
+                                               uint64_t hold_ns, mla_stream_t stream) {
+  if (hold_ns == 0 || hold_ns > 1000000000ull) return MLA_ERR_INVALID_ARG;
+  return run_attn(a, workspace, ws_bytes, stream, hold_ns);
 }

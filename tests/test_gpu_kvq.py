@@ -13,6 +13,7 @@ products exactly and everything accumulates in fp32, so against float64:
 lse: ds + 2^-21 + n * 2^-24 from the normaliser, and fp32 rounding 2^-22 |lse|.
 """
 import dataclasses
+import time
 
 import numpy as np
 import pytest
@@ -23,7 +24,7 @@ from oracle import kvq as O
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-SLOT, NONFINITE, PREFIX, INDPTR, PARENT, PAGES = 0x4, 0x200, 0x1, 0x2, 0x8, 0x10
+SLOT, NONFINITE, PREFIX, INDPTR, PARENT, PAGES, TIMEOUT = 0x4, 0x200, 0x1, 0x2, 0x8, 0x10, 0x40
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -763,6 +764,28 @@ def test_long_prefix(page):
         tol = ds + 2.0 ** -21 + (32 + 3126 + 2 * 256) * 2.0 ** -24 + 2.0 ** -22 * want
         assert tol < 64 / 200_000 * np.exp(s.min() - s.max())
         assert abs(float(lse[0, i, 0]) - want) <= tol
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=2, Q=16, H=64, lens=[900, 2100]),             # several row groups, cut ones among them
+    dict(B=1, Q=1, H=16, lens=[0], tree="null"),         # one tile in one cluster
+    dict(B=1, Q=1, H=128, lens=[200], tree="null"),
+    dict(B=300, Q=1, H=20, lens=[(7 * i) % 60 for i in range(300)], tree="null"),  # pieces of one tile, rows left out
+], ids=["groups", "one_tile", "four_tiles", "short_pieces"])
+def test_timeout_is_reported_and_the_context_recovers(kw):
+    p = problem(seed=53, **kw)
+    ws = api.alloc_workspace(api.kvq_workspace_size(p.ki))
+    out, lse = run(p.ki)
+    o2, l2 = torch.zeros_like(out), torch.zeros_like(lse)
+    for _ in range(2):
+        t0 = time.monotonic()
+        api.kvq_selftest_timeout(p.ki, o2, l2, ws, hold_ns=20_000_000)
+        assert api.kvq_check(ws) == TIMEOUT
+        assert time.monotonic() - t0 < 10
+        o3, l3 = run(p.ki, workspace=ws)
+        assert api.kvq_check(ws) == 0
+        assert torch.equal(out, o3) and torch.equal(lse, l3)
+    compare(p, out, lse)
 
 
 def test_captured_call_follows_its_inputs():

@@ -210,6 +210,19 @@ def test_attn_workspace_and_noop(lib):
     assert lib.mla_kvq_check(None, None, None) == api.MLA_ERR_WORKSPACE
 
 
+def test_selftest_timeout_refusals(lib):
+    def call(a, hold, ws=0x700000, n=1 << 40):
+        return lib.mla_kvq_selftest_timeout(ctypes.byref(a), ctypes.c_void_p(ws), ctypes.c_size_t(n),
+                                            ctypes.c_uint64(hold), None)
+    for hold in (0, 1_000_000_001, 2 ** 63):
+        assert call(attn_struct(), hold) == api.MLA_ERR_INVALID_ARG
+    for kw in (dict(B=0), dict(Q=0), dict(H=0), dict(q_lat=None), dict(page_size=0)):
+        assert call(attn_struct(**kw), 1000) == api.MLA_ERR_INVALID_ARG, kw
+    assert call(attn_struct(Q=65), 1000) == api.MLA_ERR_UNSUPPORTED
+    assert call(attn_struct(), 1000, ws=0) == api.MLA_ERR_WORKSPACE
+    assert call(attn_struct(), 1000, n=100) == api.MLA_ERR_WORKSPACE
+
+
 def test_binding_refuses_wrong_tensors(lib):
     torch = pytest.importorskip("torch")
     import dataclasses
