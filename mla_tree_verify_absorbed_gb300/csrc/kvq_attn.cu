@@ -313,11 +313,33 @@ __device__ void schedule(const Params& p, Ctl* c, int cluster) {
     ++seg;
     return true;
   };
+  // The last unused sequence from b on before a used one.  Unused ones are passed
+  // 128 at a time: one after the other they took 0.18 us each, 204 us for 1,024
+  // between two short sequences, and the roles' waits ran out behind ten million.
+  auto last_unused = [&](int b) {
+    for (; b < p.B; b += 128) {
+      bool used[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = b + 32 * q + lane;
+        used[q] = i < p.B && p.prefix_lens[i] >= 0;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t mask = __ballot_sync(0xffffffffu, used[q]);
+        if (mask) return b + 32 * q + __ffs(mask) - 2;
+      }
+    }
+    return p.B;
+  };
   Sequence sq{c->start_P, c->start_entry, 0u};
   for (int b = c->start_b; left > 0 && b < p.B; ++b, x = 0) {
     if (b != c->start_b) sq = read_sequence(p, b);
     const Tiles tl = tiles_of(p, sq.P);
-    if (tl.T == 0) continue;
+    if (tl.T == 0) {
+      b = last_unused(b);
+      continue;
+    }
     const int L = kFixed + tl.T;
     Piece pc;
     pc.b = b;

@@ -491,6 +491,34 @@ def test_unused_sequences_are_left_as_they_were():
     assert bool((out == 3).all())
 
 
+@pytest.mark.parametrize("gap", [1, 2, 31, 32, 33, 127, 128, 129, 130, 500])
+def test_unused_sequences_between_used_ones(gap):
+    # three short sequences of one cluster, the gaps of every length around the scheduler's steps, and some behind
+    lens = [70] + [-1] * gap + [5] + [-1] * (2 * gap) + [130] + [-1] * gap
+    p = problem(B=len(lens), Q=2, H=3, lens=lens, seed=54)
+    out = torch.full((len(lens), 2, 3, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    check_attn(p, out=out)
+    assert bool((out[torch.tensor(lens, device="cuda") < 0] == 3).all())
+
+
+def test_many_unused_sequences_between_used_ones():
+    # one after the other, 14 million would outlast the two seconds that a wait may take
+    B = 14_000_000
+    lens = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    lens[0], lens[-1] = 70, 9
+    table = torch.zeros((B, 1), dtype=torch.int32, device="cuda")  # page 0 holds every position
+    p = problem(B=2, Q=1, H=1, lens=[70, 9], seed=55, tree="null")
+    big = {n: torch.zeros((B, 1, 1, w), dtype=torch.bfloat16, device="cuda") for n, w in (("q_lat", 512), ("q_pe", 64))}
+    for n, t in big.items():
+        t[[0, -1]] = getattr(p.ki, n)
+    ki = dataclasses.replace(p.ki, B=B, prefix_lens=lens, page_size=1 << 20, block_table=table, **big)
+    ws = api.alloc_workspace(api.kvq_workspace_size(ki))
+    out, lse = run(ki, workspace=ws)
+    assert api.kvq_check(ws) == 0
+    compare(dataclasses.replace(p, slots=[np.arange(71), np.arange(10)]), out[[0, -1]], lse[[0, -1]])
+    assert not bool(out[1:-1].any()) and not bool(lse[1:-1].any())
+
+
 def test_lse_may_be_null_and_streams_and_repeats_agree():
     p = problem(B=2, Q=8, H=16, lens=[1500, 700], seed=35)
     ws = api.alloc_workspace(api.kvq_workspace_size(p.ki))
