@@ -293,6 +293,27 @@ struct alignas(16) Start {
   int32_t pad[3];
 };
 
+// The last unused sequence from b on before a used one.  Unused ones are passed
+// 128 at a time: one after the other they took 0.18 us each, 204 us for 1,024
+// between two short sequences, and the roles' waits ran out behind ten million.
+__device__ __noinline__ int last_unused(const int32_t* prefix_lens, int B, int b) {
+  const int lane = threadIdx.x & 31;
+  for (; b < B; b += 128) {
+    bool used[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = b + 32 * q + lane;
+      used[q] = i < B && prefix_lens[i] >= 0;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t mask = __ballot_sync(0xffffffffu, used[q]);
+      if (mask) return b + 32 * q + __ffs(mask) - 2;
+    }
+  }
+  return B;
+}
+
 // Scheduler warp of each CTA: writes this cluster's pieces in order, then an
 // end mark, into the ring that the other roles follow.  A piece that does not
 // begin its row group is the cluster's first, one that does not end it the
@@ -313,31 +334,12 @@ __device__ void schedule(const Params& p, Ctl* c, int cluster) {
     ++seg;
     return true;
   };
-  // The last unused sequence from b on before a used one.  Unused ones are passed
-  // 128 at a time: one after the other they took 0.18 us each, 204 us for 1,024
-  // between two short sequences, and the roles' waits ran out behind ten million.
-  auto last_unused = [&](int b) {
-    for (; b < p.B; b += 128) {
-      bool used[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = b + 32 * q + lane;
-        used[q] = i < p.B && p.prefix_lens[i] >= 0;
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t mask = __ballot_sync(0xffffffffu, used[q]);
-        if (mask) return b + 32 * q + __ffs(mask) - 2;
-      }
-    }
-    return p.B;
-  };
   Sequence sq{c->start_P, c->start_entry, 0u};
   for (int b = c->start_b; left > 0 && b < p.B; ++b, x = 0) {
     if (b != c->start_b) sq = read_sequence(p, b);
     const Tiles tl = tiles_of(p, sq.P);
     if (tl.T == 0) {
-      b = last_unused(b);
+      b = last_unused(p.prefix_lens, p.B, b);
       continue;
     }
     const int L = kFixed + tl.T;
