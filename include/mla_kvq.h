@@ -103,7 +103,7 @@ typedef struct {
                                    for magnitudes 2^-94 .. 2^95 (and for any with exponent 0) */
     int page_size;              /* 1: kv_indptr/kv_indices;  > 1: block_table */
     const int32_t *kv_indptr;   /* [B+1]; kv_indptr[0] == 0, spans prefix_lens[b]+Q (0 for an unused sequence) */
-    const int32_t *kv_indices;  /* [kv_indptr[B]] pool slots */
+    const int32_t *kv_indices;  /* [kv_indptr[B]] pool slots; not NULL, even when that is 0 */
     const int32_t *block_table; /* [B][max_pages] page ids */
     int max_pages;              /* columns of block_table */
     const int32_t *prefix_lens; /* [B], >= 0; -1 marks an unused sequence of a padded batch: nothing of it is
@@ -116,8 +116,9 @@ typedef struct {
     float *lse;                 /* [B][Q][H], natural log; may be NULL */
 } mla_kvq_attn_args;
 
-/* Node i sees the prefix, itself and its ancestors.  A window W > 0 keeps of
- * those the tokens less than W places back and the first `sinks` tokens: with
+/* Node i sees the prefix, itself and its ancestors.  A window W > 0
+ * (mla_verify_attn, over the bf16 and fp32 caches, has none) keeps of those the
+ * tokens less than W places back and the first `sinks` tokens: with
  * a prefix token's place its position and a node's place prefix_lens[b] + its
  * depth (0 for a node without parent), node i sees place p when
  *     p < sinks  or  place(i) - p < W.

@@ -769,7 +769,7 @@ class KvqInputs:
     page_size: int
     tree_parent: object = None   # [B, Q] int32
     kv_indptr: object = None     # [B + 1] int32    (page_size 1)
-    kv_indices: object = None    # int32            (page_size 1)
+    kv_indices: object = None    # int32, not empty (page_size 1)
     block_table: object = None   # [B, max_pages] int32  (page_size > 1)
     window: int = 0
     sinks: int = 0
@@ -833,8 +833,9 @@ def kvq_workspace_size(ki: KvqInputs) -> int:
 def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, check: bool = True):
     """Run mla_kvq_attn; returns (out [B,Q,H,512] bf16, lse [B,Q,H] fp32).
     Rows of unused sequences keep what the given arrays hold (zeros in arrays
-    made here, on ``stream``).  check=False skips the tensor checks (a loop
-    that already passed them)."""
+    made here, on ``stream``).  kvq_check reads the call's error bits from a
+    workspace that was given; one made here is gone with the call.  check=False
+    skips the tensor checks (a loop that already passed them)."""
     dev = ki.q_lat.device
     if out is None or lse is None:
         import torch

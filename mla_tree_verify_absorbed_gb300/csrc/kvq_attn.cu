@@ -26,9 +26,9 @@
 // with 1,152 cycles of MMA beneath.  A half tile takes a producer warp 650
 // cycles to convert in the value CTA, where nothing else uses the schedulers,
 // and 1,100 to 1,400 beside the softmax.  Measured on 64 nodes x 64 heads x
-// 200,000 tokens: 1.60 ms, 1.11 PFLOP/s.  With few rows the same conversion
-// serves fewer products: 128 ragged sequences x 16 heads (440,000 tokens) take
-// 108 us, 1.7 TB/s.  A call of 257 tokens takes 15 us: launch and split 2.2, the
+// 200,000 tokens: 1.58 ms, 1.13 PFLOP/s.  With few rows the same conversion
+// serves fewer products: 128 ragged sequences x 16 heads (429,667 tokens) take
+// 109 us, 1.7 TB/s.  A call of 257 tokens takes 16 us: launch and split 2.2, the
 // first piece 1.1, its queries 1.6, first scores 2.5, first weights 1.6, 1.0 a
 // tile, output 1.5, exit 0.8.
 //
@@ -150,11 +150,17 @@ constexpr uint64_t kDrainLimitNs = 20000000ull;
 constexpr float kLazy = 8.f;
 constexpr float kWeightShift = 7.f;
 
-// Cost of starting a row group or a piece of one, in tiles, and the fewest
-// tiles worth a cluster of its own.  Measured, us (64 nodes x 64 heads in a window
-// of 1,000; 16 sequences x 64 heads in a window of 4,096; 128 ragged sequences
-// x 16 heads): kFixed 3: 43.2, 42.0, 110.7; 4: 40.7, 40.5, 109.1; 5: 45.5, 39.1,
-// 111.4; kMinTiles 6 in place of 4: 43.9, 40.7, 109.3.
+// What the split counts for a row group or a piece of one, in tiles, beside its
+// own, and the fewest tiles worth a cluster of its own.  Chosen by the times of
+// whole calls: a piece of 128 rows spends longer (queries 5 to 6 us, fp32 output
+// 4.4, at 1.0 to 1.2 a tile), but the even cut makes two pieces of an interval
+// wherever it crosses a border, and a larger count moves the cuts without saving
+// any.  Single sizes jump by 10% with where the cuts fall, so these are means, us:
+// 64 nodes x 64 heads in windows of 1,000 .. 1,256; 16 sequences x 64 heads in
+// windows of 4,096 .. 4,352; 128 ragged sequences x 16 heads, three sets of
+// lengths.  kFixed 3: 43.4, 41.9, 101.7; 4: 44.5, 40.8, 99.7; 5: 45.3, 39.9, 101.9;
+// 6: 46.5, 40.3, 103.3; 8: 48.9, 43.2, 106.5; kMinTiles 6 in place of 4: 45.3, 40.8,
+// 100.4.  Row groups in long pieces (32 sequences x 128 heads, trees) move by 1%.
 constexpr int kFixed = 4;
 constexpr int kMinTiles = 4;
 
@@ -296,6 +302,7 @@ struct alignas(16) Start {
 // The last unused sequence from b on before a used one.  Unused ones are passed
 // 128 at a time: one after the other they took 0.18 us each, 204 us for 1,024
 // between two short sequences, and the roles' waits ran out behind ten million.
+// Not inlined: the smallest calls pay for cold code between the hot (15.6 -> 15.8).
 __device__ __noinline__ int last_unused(const int32_t* prefix_lens, int B, int b) {
   const int lane = threadIdx.x & 31;
   for (; b < B; b += 128) {
@@ -1008,7 +1015,8 @@ __device__ void value_rows(const Params& p, Ctl* c) {
     // cache has read the next piece's zero.  The release takes 0.4 us, so a piece
     // that is known to be the cluster's last goes without: nothing waits for it.
     const uint32_t nq = (uint32_t)(seg + 1) % kPieces;
-    const bool last = mbar_test_wait_cluster(&c->piece_full[nq], ((uint32_t)(seg + 1) / kPieces) & 1u) && c->piece[nq].b < 0;
+    const bool last =
+        mbar_test_wait_cluster(&c->piece_full[nq], ((uint32_t)(seg + 1) / kPieces) & 1u) && c->piece[nq].b < 0;
     if (!last) mbar_arrive_cluster(&c->fin_free, 0);
     ++seg;
     if (wq >= quads) return true;

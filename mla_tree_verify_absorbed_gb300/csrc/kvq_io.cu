@@ -17,8 +17,8 @@
 //
 // Bound: HBM.  A bf16 row is 1152 bytes on one side and 416 on the other; one
 // warp takes a row, lane l its scale block l.  Measured on 200,000 rows in
-// random slots (us; GB/s of both sides): bf16 write 61 (5,100), fp32 write 83
-// (6,600), bf16 read 52 (6,000), fp32 read 86 (6,300).  The bf16 write is held
+// random slots (us; GB/s of both sides): bf16 write 60 (5,270), fp32 write 82
+// (6,660), bf16 read 52 (6,100), fp32 read 86 (6,350).  The bf16 write is held
 // by its instructions rather than by HBM.
 #include <cuda_fp8.h>
 
@@ -63,9 +63,9 @@ __device__ __forceinline__ void put_block_err(uint32_t* err, uint32_t e) {
 
 // Eight 32-bit words at once, a whole sector when the caller's rows are 32-byte
 // aligned (`wide`, the same for the whole call), else as two halves, which for
-// 200,000 rows takes 68 us in place of 65 for a bf16 write, 65 for 54 for a bf16
-// read and 162 for 89 for an fp32 read.  Rows pass once, so they are kept out of
-// L1.
+// 200,000 rows takes 63 us in place of 60 for a bf16 write, 86 for 82 for an fp32
+// write, 64 for 52 for a bf16 read and 168 for 86 for an fp32 read, whose stores
+// then fill half sectors.  Rows pass once, so they are kept out of L1.
 __device__ __forceinline__ void ld_words(const void* p, bool wide, uint32_t (&v)[8]) {
   if (wide) {
     asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -197,7 +197,7 @@ __device__ __forceinline__ uint32_t rope_pair(const float* p) {
 }
 
 // One warp per row, kDeep rows in flight per warp: for 200,000 rows 1, 2 and 4
-// took 67, 64 and 78 us from bf16, 85, 89 and 131 from fp32, whose rows are
+// took 63, 60 and 72 us from bf16, 82, 85 and 123 from fp32, whose rows are
 // twice as long and at 4 leave too few warps.
 template <class T, int kDeep>
 __global__ void __launch_bounds__(kIoThreads) kvq_write_kernel(const IoParams p) {
@@ -260,8 +260,8 @@ __device__ __forceinline__ void put_rope(float* dst, uint32_t v) {
   *reinterpret_cast<float2*>(dst) = make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-// Two rows in flight per warp: for 200,000 rows 1, 2 and 4 took 66, 54 and 56 us
-// to bf16, 89 to 90 each to fp32.
+// Two rows in flight per warp: for 200,000 rows 1, 2 and 4 took 63, 52 and 53 us
+// to bf16, 86 each to fp32.
 template <class T, int kDeep>
 __global__ void __launch_bounds__(kIoThreads) kvq_read_kernel(const IoParams p) {
   const int lane = threadIdx.x & 31;
@@ -366,8 +366,9 @@ mla_status make_io(const mla_kvq_cache* c, const mla_kvq_rows* r, void* ws, size
 }
 
 // Blocks for n rows: one row per warp while they fit the GPU, then a
-// persistent grid of per_sm blocks per SM (8 for writes: 4 and 16 took 1 to 2 us
-// longer for 200,000 rows; 16 for reads: 4 and 8 took 2 to 12 us longer).
+// persistent grid of per_sm blocks per SM (for 200,000 rows 4, 8 and 16 took 59,
+// 60 and 61 us for a bf16 write, 82 each for an fp32 one, 54, 55 and 52 for a bf16
+// read, 103, 90 and 86 for an fp32 one: 8 for writes, 16 for reads).
 mla_status io_grid(int64_t n, int per_sm, int* grid) {
   // looked up once per device: the two queries took as long as the launch
   constexpr int kMaxDevices = 64;

@@ -210,6 +210,18 @@ def test_attn_workspace_and_noop(lib):
     assert lib.mla_kvq_check(None, None, None) == api.MLA_ERR_WORKSPACE
 
 
+def test_empty_kv_indices_are_refused(lib):
+    # a batch without a used sequence needs none, but an empty tensor has no address
+    torch = pytest.importorskip("torch")
+    ki = api.KvqInputs(B=1, Q=1, H=1, scale=0.1, q_lat=torch.zeros(1, 1, 1, 512, dtype=torch.bfloat16),
+                       q_pe=torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16), cache=api.kvq_alloc(4, device="cpu"),
+                       prefix_lens=torch.full((1,), -1, dtype=torch.int32), page_size=1,
+                       kv_indptr=torch.zeros(2, dtype=torch.int32), kv_indices=torch.zeros(0, dtype=torch.int32))
+    ki.check_layout()
+    out, lse = torch.zeros(1, 1, 1, 512, dtype=torch.bfloat16), torch.zeros(1, 1, 1)
+    assert attn_call(lib, ki.c_args(out, lse)) == api.MLA_ERR_INVALID_ARG
+
+
 def test_selftest_timeout_refusals(lib):
     def call(a, hold, ws=0x700000, n=1 << 40):
         return lib.mla_kvq_selftest_timeout(ctypes.byref(a), ctypes.c_void_p(ws), ctypes.c_size_t(n),
