@@ -557,6 +557,25 @@ def test_many_sequences_and_heads(kw):
     check_attn(problem(seed=42, **kw))
 
 
+def test_queries_and_outputs_beyond_32_bit_offsets():
+    # 2 sequences x 4 nodes x 2^20 heads: 4.3 billion elements; some heads of each row of nodes against the oracle
+    B, Q, H = 2, 4, 1 << 20
+    heads = [0, 127, 128, 524_287, 1_000_003, H - 1]
+    p = problem(B=B, Q=Q, H=len(heads), lens=[100, 61], seed=56)
+    g = torch.Generator(device="cuda").manual_seed(57)
+    q = {n: torch.empty((B, Q, H, w), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+         for n, w in (("q_lat", 512), ("q_pe", 64))}
+    for n, t in q.items():
+        getattr(p.ki, n).copy_(t[:, :, heads])
+    ki = dataclasses.replace(p.ki, H=H, **q)
+    ws = api.alloc_workspace(api.kvq_workspace_size(ki))
+    out, lse = run(ki, workspace=ws)
+    assert api.kvq_check(ws) == 0
+    compare(p, out[:, :, heads], lse[:, :, heads])
+    # every row was written: weights sum to one, so no row of these latents is zeros, and no lse is 0
+    assert bool((lse != 0).all()) and bool((out.view(torch.int32) != 0).any(-1).all())
+
+
 @pytest.mark.parametrize("page", [2, 3, 7, 33, 127, 1000, 4097])
 def test_page_sizes(page):
     check_attn(problem(B=3, Q=3, H=8, lens=[1400, 2 * page - 3 if page > 1 else 0, 65], page=page, seed=46))
