@@ -208,7 +208,7 @@ def _prepare_tables(case, st, g, dev):
     live = [p >= 0 for p in _lens(case)]
     total = sum(p + n for p, n, u in zip(_lens(case), new, live) if u)
     st.update(block_table=table, pages_held=torch.tensor(held, dtype=torch.int32, device=dev), free_ring=ring,
-              free_state=torch.tensor([head, head + free], dtype=torch.int64, device=dev),
+              free_state=torch.tensor([head, head + free, 0], dtype=torch.int64, device=dev),
               prefix_lens=torch.tensor(_lens(case), dtype=torch.int32, device=dev), num_pages=count,
               new_lens=torch.tensor(new, dtype=torch.int32, device=dev) if case["ragged"] else None)
     rows = sum(n for n, u in zip(new, live) if u) + 29 if case["ragged"] else B * case["Q"]
@@ -382,7 +382,7 @@ def _plain_tables(st):
         b = torch.searchsorted(m, row, right=True)
         p = P[b] + row - (m[b] - n[b])
         slots[:len(row)] = (table[b, p // ps] * ps + p % ps).int()
-    state = torch.stack([head + take.sum(), tail + drop.sum()])
+    state = torch.stack([head + take.sum(), tail + drop.sum(), st["free_state"][2]])
     return table, need.int(), ring, state, slots, ptr.int(), idx, scales
 
 
@@ -603,7 +603,7 @@ def _exact_append(case, st):
 def _exact_tables(case, st):
     ps, ring = case["page"], st["free_ring"].tolist()
     cap = len(ring)
-    head, tail = st["free_state"].tolist()
+    head, tail, zero = st["free_state"].tolist()
     table, held = st["block_table"].tolist(), st["pages_held"].tolist()
     scales, slots, ptr, idx = st["scales"].tolist(), [], [0], []
     lens, new = _lens(case), _new(case)
@@ -626,7 +626,7 @@ def _exact_tables(case, st):
     idx += [0] * (st["kv_indices"].numel() - len(idx))
     dev = st["slots"].device
     ints = [torch.tensor(v, dtype=torch.int32, device=dev) for v in (table, held, ring, slots, ptr, idx, scales)]
-    return (*ints[:3], torch.tensor([head, tail], dtype=torch.int64, device=dev), *ints[3:])
+    return (*ints[:3], torch.tensor([head, tail, zero], dtype=torch.int64, device=dev), *ints[3:])
 
 
 def exact(case, seed):
