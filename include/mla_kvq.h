@@ -165,4 +165,7 @@ mla_status mla_kvq_check(const void *workspace, mla_stream_t stream, uint32_t *b
 }
 #endif
 
+/* the paged 8-bit latent cache, whose calls use the types above */
+#include "mla_kv8.h"
+
 #endif /* MLA_KVQ_H */

@@ -1,5 +1,5 @@
-"""ctypes binding of the C ABI in include/mla_verify.h, include/mla_ddtree.h and
-include/mla_kvq.h.
+"""ctypes binding of the C ABI in include/mla_verify.h, include/mla_ddtree.h,
+include/mla_kvq.h, include/mla_kv8.h and include/mla_kv_tables.h.
 
 Argument marshalling only: torch tensors give device pointers, sizes and
 strides; every step of the computation runs in the CUDA library.  The library
@@ -35,12 +35,19 @@ EXPORTS = ("mla_verify_workspace_size", "mla_verify_attn", "mla_verify_attn_noal
            "mla_verify_abi_version",
            "mla_verify_selftest_timeout", "mla_kv_compact", "mla_ddtree_build", "mla_ddtree_accept",
            "mla_kvq_write", "mla_kvq_read", "mla_kvq_attn", "mla_kvq_attn_workspace_size", "mla_kvq_check",
-           "mla_kvq_selftest_timeout")
+           "mla_kvq_selftest_timeout",
+           "mla_kv8_write", "mla_kv8_read", "mla_kv8_attn", "mla_kv8_attn_workspace_size", "mla_kv8_check",
+           "mla_kv8_selftest_timeout", "mla_kv_tables")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 DDTREE_WORKSPACE_BYTES = 256
 KVQ_ROW_BYTES = 416
 KVQ_MAX_EXPONENT = 32
 KVQ_WORKSPACE_BYTES = 16384
+KV8_ROW_BYTES = 640
+KV8_MAX_SCALE = 15
+KV8_MAX_EXPONENT = 32
+KV8_WORKSPACE_BYTES = 16384
+KV_TABLES_WORKSPACE_BYTES = 16384
 
 
 class MlaVerifyArgs(ctypes.Structure):
@@ -110,6 +117,29 @@ class MlaKvqAttnArgs(ctypes.Structure):
     ]
 
 
+class MlaKv8Cache(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("slots", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("block", ctypes.c_int), ("exponent", ctypes.c_int)]
+
+
+class MlaKv8AttnArgs(ctypes.Structure):
+    _fields_ = [(n, MlaKv8Cache if n == "cache" else t) for n, t in MlaKvqAttnArgs._fields_]
+
+
+class MlaKvTablesArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("Q", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("prefix_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("pages_held", ctypes.c_void_p),
+        ("free_ring", ctypes.c_void_p), ("free_state", ctypes.c_void_p), ("ring", ctypes.c_int),
+        ("slots", ctypes.c_void_p), ("slots_len", ctypes.c_int64),
+        ("kv_indptr", ctypes.c_void_p),
+        ("kv_indices", ctypes.c_void_p), ("indices_len", ctypes.c_int64),
+        ("scales", ctypes.c_void_p), ("block", ctypes.c_int),
+    ]
+
+
 def _packer(cls):
     """The bytes of a struct from its fields' values (a nested struct's in their
     place): a third of the time that making a ctypes.Structure takes, which
@@ -124,6 +154,7 @@ def _packer(cls):
 
 
 _pack_cache, _pack_rows, _pack_attn = _packer(MlaKvqCache), _packer(MlaKvqRows), _packer(MlaKvqAttnArgs)
+_pack_cache8, _pack_attn8, _pack_tables = _packer(MlaKv8Cache), _packer(MlaKv8AttnArgs), _packer(MlaKvTablesArgs)
 
 
 class MlaError(RuntimeError):
@@ -184,6 +215,19 @@ def load(path: Optional[str] = None):
     lib.mla_kvq_attn_workspace_size.argtypes = [ctypes.POINTER(MlaKvqAttnArgs)]
     lib.mla_kvq_check.restype = ctypes.c_int
     lib.mla_kvq_check.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]
+    for f in (lib.mla_kv8_write, lib.mla_kv8_read):
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    for f in (lib.mla_kv8_attn, lib.mla_kv_tables):
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.mla_kv8_selftest_timeout.restype = ctypes.c_int
+    lib.mla_kv8_selftest_timeout.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint64,
+                                             ctypes.c_void_p]
+    lib.mla_kv8_attn_workspace_size.restype = ctypes.c_size_t
+    lib.mla_kv8_attn_workspace_size.argtypes = [ctypes.POINTER(MlaKv8AttnArgs)]
+    lib.mla_kv8_check.restype = ctypes.c_int
+    lib.mla_kv8_check.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]
     lib.mla_verify_check.restype = ctypes.c_int
     lib.mla_verify_check.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]
     lib.mla_status_str.restype = ctypes.c_char_p
@@ -647,6 +691,16 @@ class QuantCache:
         if not -KVQ_MAX_EXPONENT <= self.exponent <= KVQ_MAX_EXPONENT:
             raise ValueError(f"cache exponent {self.exponent} outside +-{KVQ_MAX_EXPONENT}")
 
+    def values(self):
+        """The fields of an MlaKvqCache."""
+        r = self.rows
+        m = r.shape[0]
+        # the row stride of a one-row tensor is whatever its maker left there
+        return r.data_ptr(), r.stride()[0] if m > 1 else KVQ_ROW_BYTES, m, self.exponent
+
+    def tensors(self):
+        return dict(rows=self.rows)
+
 
 def kvq_alloc(slots: int, exponent: int = 0, device="cuda") -> QuantCache:
     """A cache of ``slots`` rows that all stand for zeros."""
@@ -693,7 +747,7 @@ def _kvq_launch(what: str, f, dev, stream, *args):
         raise MlaError(st, what)
 
 
-def _kvq_rows(what: str, f, cache: QuantCache, kv_c, k_pe, slots, workspace, stream, check: bool):
+def _cache_rows(what: str, f, cache, pack, kv_c, k_pe, slots, workspace, stream, check: bool):
     if check:
         import torch
         cache.check()
@@ -707,15 +761,13 @@ def _kvq_rows(what: str, f, cache: QuantCache, kv_c, k_pe, slots, workspace, str
         if k_pe.shape[0] != kv_c.shape[0]:
             raise ValueError("kv_c and k_pe must have the same number of rows")
         _need(slots, "slots", torch.int32, (kv_c.shape[0],))
-        _one_device(rows=cache.rows, kv_c=kv_c, k_pe=k_pe, slots=slots, workspace=workspace)
-    pool = cache.rows
-    dev = pool.device
+        _one_device(kv_c=kv_c, k_pe=k_pe, slots=slots, workspace=workspace, **cache.tensors())
+    dev = cache.rows.device
     if workspace is None:
         with _made_on(stream):
             workspace = alloc_workspace(KVQ_WORKSPACE_BYTES, dev)
-    n, m = kv_c.shape[0], pool.shape[0]
-    # the row stride of a one-row tensor is whatever its maker left there
-    c = _pack_cache(pool.data_ptr(), pool.stride()[0] if m > 1 else KVQ_ROW_BYTES, m, cache.exponent)
+    n = kv_c.shape[0]
+    c = pack(*cache.values())
     r = _pack_rows(n, MLA_BF16 if kv_c.element_size() == 2 else MLA_FP32, kv_c.data_ptr(), k_pe.data_ptr(),
                    kv_c.stride()[0] if n > 1 else 512, k_pe.stride()[0] if n > 1 else 64, slots.data_ptr())
     _kvq_launch(what, f, dev, stream, c, r, workspace.data_ptr(), workspace.nbytes)
@@ -728,15 +780,11 @@ def kvq_write(cache: QuantCache, kv_c, k_pe, slots, workspace=None, stream=None,
     slots[i] (int32; -1 skips, the others differ from each other).  Returns the
     workspace (kvq_check reads its error bits).  check=False skips
     the tensor checks, for a loop that already passed them."""
-    return _kvq_rows("mla_kvq_write", load().mla_kvq_write, cache, kv_c, k_pe, slots, workspace, stream, check)
+    return _cache_rows("mla_kvq_write", load().mla_kvq_write, cache, _pack_cache, kv_c, k_pe, slots, workspace, stream,
+                       check)
 
 
-def kvq_read(cache: QuantCache, slots, dtype: str = "bf16", kv_c=None, k_pe=None, workspace=None, stream=None,
-             check: bool = True):
-    """Run mla_kvq_read: the rows that pool slots ``slots`` stand for, exactly,
-    as ``dtype`` ("bf16" or "fp32"; that of kv_c when given).  Rows with slot
-    -1 keep what the given arrays hold (zeros in arrays made here, on
-    ``stream``).  Returns (kv_c [n][512], k_pe [n][64], workspace)."""
+def _cache_read(what: str, f, cache, pack, slots, dtype, kv_c, k_pe, workspace, stream, check: bool):
     if check:
         cache.check()
         if dtype not in ("bf16", "fp32"):
@@ -749,8 +797,17 @@ def kvq_read(cache: QuantCache, slots, dtype: str = "bf16", kv_c=None, k_pe=None
                 kv_c = torch.zeros((slots.shape[0], 512), dtype=dt, device=cache.rows.device)
             if k_pe is None:
                 k_pe = torch.zeros((slots.shape[0], 64), dtype=dt, device=cache.rows.device)
-    ws = _kvq_rows("mla_kvq_read", load().mla_kvq_read, cache, kv_c, k_pe, slots, workspace, stream, check)
-    return kv_c, k_pe, ws
+    return kv_c, k_pe, _cache_rows(what, f, cache, pack, kv_c, k_pe, slots, workspace, stream, check)
+
+
+def kvq_read(cache: QuantCache, slots, dtype: str = "bf16", kv_c=None, k_pe=None, workspace=None, stream=None,
+             check: bool = True):
+    """Run mla_kvq_read: the rows that pool slots ``slots`` stand for, exactly,
+    as ``dtype`` ("bf16" or "fp32"; that of kv_c when given).  Rows with slot
+    -1 keep what the given arrays hold (zeros in arrays made here, on
+    ``stream``).  Returns (kv_c [n][512], k_pe [n][64], workspace)."""
+    return _cache_read("mla_kvq_read", load().mla_kvq_read, cache, _pack_cache, slots, dtype, kv_c, k_pe, workspace,
+                       stream, check)
 
 
 @dataclass
@@ -775,9 +832,9 @@ class KvqInputs:
     sinks: int = 0
 
     def tensors(self):
-        return dict(q_lat=self.q_lat, q_pe=self.q_pe, rows=self.cache.rows, prefix_lens=self.prefix_lens,
-                    tree_parent=self.tree_parent, kv_indptr=self.kv_indptr, kv_indices=self.kv_indices,
-                    block_table=self.block_table)
+        return dict(q_lat=self.q_lat, q_pe=self.q_pe, prefix_lens=self.prefix_lens, tree_parent=self.tree_parent,
+                    kv_indptr=self.kv_indptr, kv_indices=self.kv_indices, block_table=self.block_table,
+                    **self.cache.tensors())
 
     def check_layout(self):
         """What the C ABI cannot see from pointers.  Raises ValueError."""
@@ -803,10 +860,8 @@ class KvqInputs:
 
     def values(self, out=None, lse=None):
         """The fields of an MlaKvqAttnArgs in their order, the cache's in its place."""
-        pool, table, tree, paged = self.cache.rows, self.block_table, self.tree_parent, self.page_size > 1
-        m = pool.shape[0]
-        return (self.B, self.Q, self.H,
-                pool.data_ptr(), pool.stride()[0] if m > 1 else KVQ_ROW_BYTES, m, self.cache.exponent,
+        table, tree, paged = self.block_table, self.tree_parent, self.page_size > 1
+        return (self.B, self.Q, self.H, *self.cache.values(),
                 self.q_lat.data_ptr(), self.q_pe.data_ptr(), self.page_size,
                 0 if paged or self.kv_indptr is None else self.kv_indptr.data_ptr(),
                 0 if paged or self.kv_indices is None else self.kv_indices.data_ptr(),
@@ -820,22 +875,21 @@ class KvqInputs:
         return MlaKvqAttnArgs(*v[:3], MlaKvqCache(*v[3:7]), *v[7:])
 
 
-def kvq_workspace_size(ki: KvqInputs) -> int:
+def _attn_workspace_size(what: str, f, ki) -> int:
     import torch
     a = ki.c_args()
     with torch.cuda.device(ki.q_lat.device):
-        n = load().mla_kvq_attn_workspace_size(ctypes.byref(a))
+        n = f(ctypes.byref(a))
     if n == 0:
-        raise MlaError(MLA_ERR_INVALID_ARG, "mla_kvq_attn_workspace_size")
+        raise MlaError(MLA_ERR_INVALID_ARG, what)
     return int(n)
 
 
-def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, check: bool = True):
-    """Run mla_kvq_attn; returns (out [B,Q,H,512] bf16, lse [B,Q,H] fp32).
-    Rows of unused sequences keep what the given arrays hold (zeros in arrays
-    made here, on ``stream``).  kvq_check reads the call's error bits from a
-    workspace that was given; one made here is gone with the call.  check=False
-    skips the tensor checks (a loop that already passed them)."""
+def kvq_workspace_size(ki: KvqInputs) -> int:
+    return _attn_workspace_size("mla_kvq_attn_workspace_size", load().mla_kvq_attn_workspace_size, ki)
+
+
+def _cache_attn(what: str, f, pack, size, ki, out, lse, workspace, stream, check: bool):
     dev = ki.q_lat.device
     if out is None or lse is None:
         import torch
@@ -852,35 +906,251 @@ def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, che
         _one_device(out=out, lse=lse, workspace=workspace, **ki.tensors())
     if workspace is None:
         with _made_on(stream):
-            workspace = alloc_workspace(kvq_workspace_size(ki), dev)
-    _kvq_launch("mla_kvq_attn", load().mla_kvq_attn, dev, stream, _pack_attn(*ki.values(out, lse)),
-                workspace.data_ptr(), workspace.nbytes)
+            workspace = alloc_workspace(size(ki), dev)
+    _kvq_launch(what, f, dev, stream, pack(*ki.values(out, lse)), workspace.data_ptr(), workspace.nbytes)
     return out, lse
+
+
+def _attn_selftest(what: str, f, pack, ki, out, lse, workspace, hold_ns: int, stream):
+    import torch
+    ki.check_layout()
+    _need(out, "out", torch.bfloat16, (ki.B, ki.Q, ki.H, 512))
+    _need(lse, "lse", torch.float32, (ki.B, ki.Q, ki.H))
+    _one_device(out=out, lse=lse, workspace=workspace, **ki.tensors())
+    _kvq_launch(what, lambda args, ws, n, raw: f(args, ws, n, ctypes.c_uint64(int(hold_ns)), raw), ki.q_lat.device,
+                stream, pack(*ki.values(out, lse)), workspace.data_ptr(), workspace.nbytes)
+
+
+def _cache_check(what: str, f, workspace, stream) -> int:
+    import torch
+    bits = ctypes.c_uint32(0)
+    with torch.cuda.device(workspace.device):
+        st = f(ctypes.c_void_p(_ptr(workspace)), _stream(stream), ctypes.byref(bits))
+    if st not in (MLA_OK, MLA_ERR_DEVICE_CHECK):
+        raise MlaError(st, what)
+    return int(bits.value)
+
+
+def kvq_attn(ki: KvqInputs, out=None, lse=None, workspace=None, stream=None, check: bool = True):
+    """Run mla_kvq_attn; returns (out [B,Q,H,512] bf16, lse [B,Q,H] fp32).
+    Rows of unused sequences keep what the given arrays hold (zeros in arrays
+    made here, on ``stream``).  kvq_check reads the call's error bits from a
+    workspace that was given; one made here is gone with the call.  check=False
+    skips the tensor checks (a loop that already passed them)."""
+    return _cache_attn("mla_kvq_attn", load().mla_kvq_attn, _pack_attn, kvq_workspace_size, ki, out, lse, workspace,
+                       stream, check)
 
 
 def kvq_selftest_timeout(ki: KvqInputs, out, lse, workspace, hold_ns: int, stream=None):
     """Run mla_kvq_selftest_timeout: the attention call with its waits limited
     to hold_ns and one of its products held back; read the outcome with
     kvq_check()."""
-    import torch
-    ki.check_layout()
-    _need(out, "out", torch.bfloat16, (ki.B, ki.Q, ki.H, 512))
-    _need(lse, "lse", torch.float32, (ki.B, ki.Q, ki.H))
-    _one_device(out=out, lse=lse, workspace=workspace, **ki.tensors())
-
-    def f(args, ws, n, raw):
-        return load().mla_kvq_selftest_timeout(args, ws, n, ctypes.c_uint64(int(hold_ns)), raw)
-    _kvq_launch("mla_kvq_selftest_timeout", f, ki.q_lat.device, stream, _pack_attn(*ki.values(out, lse)),
-                workspace.data_ptr(), workspace.nbytes)
+    _attn_selftest("mla_kvq_selftest_timeout", load().mla_kvq_selftest_timeout, _pack_attn, ki, out, lse, workspace,
+                   hold_ns, stream)
 
 
 def kvq_check(workspace, stream=None) -> int:
     """Synchronise and return the device error bits that the last kvq call on
     this workspace left."""
+    return _cache_check("mla_kvq_check", load().mla_kvq_check, workspace, stream)
+
+
+# ----------------------------------------------------------------------------
+# paged 8-bit latent cache (include/mla_kv8.h)
+# ----------------------------------------------------------------------------
+@dataclass
+class BlockCache:
+    """A pool of 8-bit cache rows under one scale per block of ``block`` slots:
+    ``rows`` is a uint8 [slots][640] tensor or view (row stride a multiple of 32
+    bytes), ``scales`` an int32 [ceil(slots / block)] tensor of scale words (0: the
+    block holds no rows), ``exponent`` the power of two the latents are scaled by."""
+    rows: object
+    scales: object
+    block: int = 64
+    exponent: int = 0
+
+    def check(self):
+        import torch
+        r, s = self.rows, self.scales
+        if r is None or r.dtype != torch.uint8 or r.dim() != 2 or r.shape[1] != KV8_ROW_BYTES or r.stride(1) != 1:
+            raise ValueError(f"cache rows must be a [slots][{KV8_ROW_BYTES}] uint8 view with unit column stride")
+        if r.shape[0] > 1 and r.stride(0) < KV8_ROW_BYTES:
+            raise ValueError("cache rows overlap")
+        if not 1 <= self.block < 2 ** 31:
+            raise ValueError(f"cache block {self.block}, expected at least one slot")
+        _need(s, "scales", torch.int32, (-(-r.shape[0] // self.block),))
+        if not -KV8_MAX_EXPONENT <= self.exponent <= KV8_MAX_EXPONENT:
+            raise ValueError(f"cache exponent {self.exponent} outside +-{KV8_MAX_EXPONENT}")
+
+    def values(self):
+        """The fields of an MlaKv8Cache."""
+        r = self.rows
+        m = r.shape[0]
+        # the row stride of a one-row tensor is whatever its maker left there
+        return (r.data_ptr(), r.stride()[0] if m > 1 else KV8_ROW_BYTES, m, self.scales.data_ptr(), self.block,
+                self.exponent)
+
+    def tensors(self):
+        return dict(rows=self.rows, scales=self.scales)
+
+
+def kv8_alloc(slots: int, block: int = 64, exponent: int = 0, device="cuda") -> BlockCache:
+    """An empty cache of ``slots`` rows."""
     import torch
-    bits = ctypes.c_uint32(0)
-    with torch.cuda.device(workspace.device):
-        st = load().mla_kvq_check(ctypes.c_void_p(_ptr(workspace)), _stream(stream), ctypes.byref(bits))
-    if st not in (MLA_OK, MLA_ERR_DEVICE_CHECK):
-        raise MlaError(st, "mla_kvq_check")
-    return int(bits.value)
+    return BlockCache(torch.zeros((slots, KV8_ROW_BYTES), dtype=torch.uint8, device=device),
+                      torch.zeros((-(-slots // block),), dtype=torch.int32, device=device), block, exponent)
+
+
+def kv8_write(cache: BlockCache, kv_c, k_pe, slots, workspace=None, stream=None, check: bool = True):
+    """Run mla_kv8_write: quantise row i of kv_c [n][512] and k_pe [n][64] (bf16 or
+    fp32; rows 16-byte aligned, any such row stride) into pool slot slots[i] (int32;
+    -1 skips, the others differ from each other), raising the scales of the blocks
+    they go to as far as they need.  Returns the workspace (kv8_check reads its
+    error bits).  check=False skips the tensor checks, for a loop that already
+    passed them."""
+    return _cache_rows("mla_kv8_write", load().mla_kv8_write, cache, _pack_cache8, kv_c, k_pe, slots, workspace,
+                       stream, check)
+
+
+def kv8_read(cache: BlockCache, slots, dtype: str = "bf16", kv_c=None, k_pe=None, workspace=None, stream=None,
+             check: bool = True):
+    """Run mla_kv8_read: the rows that pool slots ``slots`` stand for, as ``dtype``
+    ("bf16" or "fp32"; that of kv_c when given).  Rows with slot -1 keep what the
+    given arrays hold (zeros in arrays made here, on ``stream``).  Returns
+    (kv_c [n][512], k_pe [n][64], workspace)."""
+    return _cache_read("mla_kv8_read", load().mla_kv8_read, cache, _pack_cache8, slots, dtype, kv_c, k_pe, workspace,
+                       stream, check)
+
+
+@dataclass
+class Kv8Inputs(KvqInputs):
+    """Device tensors of one attention call over an 8-bit cache: the fields of
+    KvqInputs with ``cache`` a BlockCache."""
+
+    def c_args(self, out=None, lse=None) -> MlaKv8AttnArgs:
+        v = self.values(out, lse)
+        return MlaKv8AttnArgs(*v[:3], MlaKv8Cache(*v[3:9]), *v[9:])
+
+
+def kv8_workspace_size(ki: Kv8Inputs) -> int:
+    return _attn_workspace_size("mla_kv8_attn_workspace_size", load().mla_kv8_attn_workspace_size, ki)
+
+
+def kv8_attn(ki: Kv8Inputs, out=None, lse=None, workspace=None, stream=None, check: bool = True):
+    """Run mla_kv8_attn; returns (out [B,Q,H,512] bf16, lse [B,Q,H] fp32); as
+    kvq_attn, with kv8_check for the error bits."""
+    return _cache_attn("mla_kv8_attn", load().mla_kv8_attn, _pack_attn8, kv8_workspace_size, ki, out, lse, workspace,
+                       stream, check)
+
+
+def kv8_selftest_timeout(ki: Kv8Inputs, out, lse, workspace, hold_ns: int, stream=None):
+    """Run mla_kv8_selftest_timeout, as kvq_selftest_timeout."""
+    _attn_selftest("mla_kv8_selftest_timeout", load().mla_kv8_selftest_timeout, _pack_attn8, ki, out, lse, workspace,
+                   hold_ns, stream)
+
+
+def kv8_check(workspace, stream=None) -> int:
+    """Synchronise and return the device error bits that the last kv8 or kv_tables
+    call on this workspace left."""
+    return _cache_check("mla_kv8_check", load().mla_kv8_check, workspace, stream)
+
+
+# ----------------------------------------------------------------------------
+# page tables of a step (include/mla_kv_tables.h)
+# ----------------------------------------------------------------------------
+@dataclass
+class TableInputs:
+    """Device tensors of the page tables: what the requests need (prefix_lens, and
+    new_lens or Q) and the state that a call brings to it (block_table, pages_held,
+    free_ring, free_state)."""
+    page_size: int
+    prefix_lens: object     # [B] int32, -1: unused row
+    block_table: object     # [B, max_pages] int32
+    pages_held: object      # [B] int32
+    free_ring: object       # [ring] int32 page ids
+    free_state: object      # [3] int64: head, tail, 0
+    num_pages: int
+    Q: int = 1              # new tokens of each request, where new_lens is None
+    new_lens: object = None  # [B] int32
+
+    def tensors(self):
+        return dict(prefix_lens=self.prefix_lens, block_table=self.block_table, pages_held=self.pages_held,
+                    free_ring=self.free_ring, free_state=self.free_state, new_lens=self.new_lens)
+
+    def check_layout(self):
+        """What the C ABI cannot see from pointers.  Raises ValueError."""
+        import torch
+        for name in ("page_size", "num_pages", "Q"):
+            if not -2 ** 31 <= getattr(self, name) < 2 ** 31:
+                raise ValueError(f"{name} {getattr(self, name)} outside 32 bits")
+        t = self.block_table
+        if t is None or t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous():
+            raise ValueError("block_table must be a contiguous [B][max_pages] int32 tensor")
+        B = t.shape[0]
+        _need(self.prefix_lens, "prefix_lens", torch.int32, (B,))
+        _need(self.pages_held, "pages_held", torch.int32, (B,))
+        if self.new_lens is not None:
+            _need(self.new_lens, "new_lens", torch.int32, (B,))
+        _need(self.free_state, "free_state", torch.int64, (3,))
+        _flat(self.free_ring, "free_ring")
+
+
+def kv_tables_alloc(B: int, max_pages: int, num_pages: int, page_size: int, device="cuda") -> TableInputs:
+    """The tables of B rows that hold nothing, every page free; prefix_lens are -1."""
+    import torch
+    i32 = dict(dtype=torch.int32, device=device)
+    return TableInputs(page_size=page_size, prefix_lens=torch.full((B,), -1, **i32),
+                       block_table=torch.full((B, max_pages), -1, **i32), pages_held=torch.zeros((B,), **i32),
+                       free_ring=torch.arange(num_pages, **i32),
+                       free_state=torch.tensor([0, num_pages, 0], dtype=torch.int64, device=device),
+                       num_pages=num_pages)
+
+
+def _flat(t, name: str):
+    import torch
+    if t is None or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
+
+
+def kv_tables(ti: TableInputs, slots=None, kv_indptr=None, kv_indices=None, cache: Optional[BlockCache] = None,
+              workspace=None, stream=None, check: bool = True):
+    """Run mla_kv_tables: bring block_table, pages_held and the ring of free pages to
+    this step's lengths, in place, and fill the given outputs: ``slots`` of the new
+    tokens ([B][Q] or flat; with new_lens any flat length, -1 behind the last),
+    ``kv_indptr`` [B+1] and ``kv_indices``, the page-size-1 tables.  With ``cache`` the
+    blocks of pages that are handed out become empty.  Returns the workspace
+    (kv8_check reads its error bits)."""
+    if check:
+        import torch
+        ti.check_layout()
+        B = ti.block_table.shape[0]
+        if slots is not None and (slots.dtype != torch.int32 or not slots.is_contiguous()
+                                  or (ti.new_lens is None and slots.numel() != B * ti.Q)):
+            raise ValueError("slots must be contiguous int32, of B * Q entries where new_lens is not given")
+        if kv_indptr is not None:
+            _need(kv_indptr, "kv_indptr", torch.int32, (B + 1,))
+        if kv_indices is not None:
+            _flat(kv_indices, "kv_indices")
+        scales = None
+        if cache is not None:
+            cache.check()
+            scales = cache.scales
+            if cache.rows.shape[0] < ti.num_pages * ti.page_size:
+                raise ValueError("the cache has fewer slots than the pages")
+        _one_device(slots=slots, kv_indptr=kv_indptr, kv_indices=kv_indices, scales=scales, workspace=workspace,
+                    **ti.tensors())
+    t = ti.block_table
+    dev = t.device
+    if workspace is None:
+        with _made_on(stream):
+            workspace = alloc_workspace(KV_TABLES_WORKSPACE_BYTES, dev)
+
+    def p(x):
+        return 0 if x is None else x.data_ptr()
+    args = _pack_tables(t.shape[0], ti.Q, ti.page_size, t.shape[1], ti.num_pages, p(ti.prefix_lens), p(ti.new_lens),
+                        p(t), p(ti.pages_held), p(ti.free_ring), p(ti.free_state), ti.free_ring.shape[0],
+                        p(slots), 0 if slots is None else slots.numel(), p(kv_indptr), p(kv_indices),
+                        0 if kv_indices is None else kv_indices.shape[0], 0 if cache is None else p(cache.scales),
+                        0 if cache is None else cache.block)
+    _kvq_launch("mla_kv_tables", load().mla_kv_tables, dev, stream, args, workspace.data_ptr(), workspace.nbytes)
+    return workspace

@@ -1,0 +1,993 @@
+// Verify attention and decoding over the paged 8-bit latent cache (mla_kv8_attn)
+// on tcgen05 tensor cores.
+//
+// The work.  32 query rows ((node, head) pairs) against tiles of 128 tokens:
+// S^T = K Q^T, online softmax, O^T += V^T P^T, V the latent part of K.  Tokens are
+// the 128 lanes of the first product and latents those of the second, so that the
+// cache's e4m3 codes, as they lie in shared memory, are the A operand of both: rows
+// of tokens in the first (K-major), columns of latents in the second (MN-major).
+// Nothing is converted, every byte is fetched once, and one CTA does all of it.
+//
+// The other operands are made of several e4m3 terms, each in columns of its own, so
+// that each has its own power of two:
+//   queries  q 2^t = hi + lo, t per row.  bf16 has 8 significant bits and a term 4,
+//            so the sum is exact down to 2^-9 of the row's largest element;
+//   weights  w = hi + lo 2^-5 + third 2^-13 of w rounded to f16: w < 2^5 has 11
+//            significant bits, of which the first two terms take 4 or 5 each, and
+//            the smallest code of the third is 2^-22.
+// The terms' products are added in fp32: queries' as the scores are read, weights'
+// when O is.  The rope product (bf16) is accumulated on the queries' first term.
+//
+// Blocks' scales.  A token's score is s_j = c_r 2^k_j S_jr (c_r: scale, row unit),
+// and its value 2^k_j times its codes, so O takes the weights 2^(s_j + k_j - m): the
+// running maximum m is that of s_j + k_j, a weight's size says what the token can
+// add to the output, and the sum for the normaliser takes 2^-k_j off again.
+//
+// What bounds it.  HBM where few rows share a token: 640 bytes a token and row
+// group.  With many rows the tensor pipe: per tile 20 MMAs of 32 cycles for S and 16
+// of 48 for O.
+//
+// Shared memory: two stages of 80 KB (128 tokens x 640 bytes), 40 KB of queries, 16
+// KB of weights.  Tensor Memory: O 4 x 96 columns (latent block; row half, term,
+// row), two S tiles of 64 columns (row half, term, row).
+//
+// Work split as in split.cuh; pieces of a row group are merged by a second kernel.
+//
+// Masks are applied to scores by selection.  Positions that no node sees are
+// filled with zeros in place of being read, so that whatever lies in the pool under
+// a weight of zero is finite.
+//
+// Every wait is bounded (2 s, less in the self-test); on timeout the roles stop,
+// drain what they issued, free their Tensor Memory and report MLA_DEVERR_TIMEOUT.
+#include <cuda_fp8.h>
+
+#include <cmath>
+#include <cstddef>
+#include <mutex>
+
+#include "kv8.cuh"
+#include "sm100.cuh"
+#include "split.cuh"
+
+namespace mlav {
+namespace kv8 {
+using namespace sm100;
+using kvq::div_fast;
+using kvq::for_pieces;
+using kvq::kErrFirst;
+using kvq::kErrMax;
+using kvq::kPieces;
+using kvq::NodeView;
+using kvq::Piece;
+using kvq::Start;
+
+constexpr int kRG = 32;        // query rows per work item
+constexpr int kHalfRows = 16;  // rows of a group of row warps
+constexpr int kTK = 128;       // tokens per tile
+// Warps 0-7 hold scores (warp w: tokens 32 (w % 4) .., rows 16 (w / 4) ..), 8-11
+// fetch, 12 issues the products, 13 hands out the pieces of work.
+constexpr int kRowWarps = 8, kProducerWarps = 4;
+constexpr int kWarpProd = kRowWarps, kWarpMma = kWarpProd + kProducerWarps, kWarpSched = kWarpMma + 1;
+constexpr int kThreads = 32 * (kWarpSched + 1);
+constexpr uint32_t kTmemCols = 512;
+
+constexpr int kFixed = 3;
+constexpr int kMinTiles = 2;
+using Work = kvq::Split<kTK, kFixed, kMinTiles, kThreads, true>;
+
+constexpr int kChunk = kTK * 128;              // 128 bytes of each token: 128 latents, or the rope key
+constexpr int kChunks = MLA_KV8_ROW_BYTES / 128;
+constexpr int kStage = kChunks * kChunk;       // 80 KB
+constexpr int kStages = 2;
+constexpr int kQRows = 2 * kRG;                // (row half, term, row)
+constexpr int kQChunk = kQRows * 128;          // 8 KB
+constexpr int kOffQ = kStages * kStage;
+constexpr int kOffP = kOffQ + kChunks * kQChunk;
+constexpr int kOffCtl = kOffP + kTK * 128;     // weights: a row of 128 bytes per token, 96 used
+
+// Tensor Memory columns
+constexpr uint32_t kColO = 0, kBlockO = 3 * kRG;  // a block of 128 latents
+constexpr uint32_t kColS = 4 * kBlockO;
+static_assert(kColS + 2 * kQRows <= kTmemCols, "Tensor Memory columns");
+
+// operand descriptors (smem_desc): all have 128-byte rows in groups of 8, 1 KB apart
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (kLayoutSw128 << 29);
+constexpr uint32_t kDescLo = ((uint32_t)kChunk >> 4) << 16;  // no operand reaches beyond one row of 128 bytes
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
+  return d;
+}
+__device__ __forceinline__ uint32_t desc_lo(const uint8_t* smem, uint32_t off) {
+  return (((smem_u32(smem) & 0x3FFFFu) + off) >> 4) | kDescLo;
+}
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 20000000ull;
+
+// Weights are 2^(s + k - max + kWeightShift): a lazy maximum lets them reach 2^kLazy
+// above 2^kWeightShift, and up to 2^5 the third term cannot saturate.
+constexpr float kLazy = 2.f;
+constexpr float kWeightShift = 3.f;
+constexpr float kLoMul = 32.f, kThirdMul = 256.f;  // 2^5, and from there 2^8
+
+struct alignas(16) Ctl {
+  uint64_t full[kStages];      // tile landed (every producer lane's copies, and each warp)
+  uint64_t empty[kStages];     // the products that read it are complete
+  uint64_t s_full[2];          // S tile in Tensor Memory
+  uint64_t q_ready;            // a piece's queries, row constants and masks written (8 row warps)
+  uint64_t m_ready[2];         // a tile's partial maxima written (4 row warps of a half)
+  uint64_t l_ready[2];         // a piece's partial sums written (the same)
+  uint64_t p_ready;            // weights in, O rescaled (8 row warps)
+  uint64_t pv_done;            // a tile's O product complete
+  uint64_t drain;
+  uint64_t piece_full[kPieces];   // piece written (scheduler warp)
+  uint64_t piece_empty[kPieces];  // read by every warp that follows the pieces
+  Piece piece[kPieces];
+  alignas(16) float part_max[2][2][4][kHalfRows];  // tile parity, half, token quadrant, row
+  float part_sum[2][4][kHalfRows];
+  float unit[kRG];             // c_r: score factor of a row
+  uint64_t mask[kRG];          // what the row's node sees of the tree,
+  int depth[kRG];              // and its depth
+  int tok_k[kStages][kTK];     // k of the tokens' blocks
+  int64_t scan[kThreads / 32];
+  int64_t left;                // units of this CTA's interval
+  int64_t start_x;             // its first unit within sequence start_b
+  int start_b, start_T;        // that sequence, its tiles,
+  int start_P;                 // its prefix length
+  int64_t start_entry;         // and its first table entry
+  uint64_t wait_ns;            // Params::wait_ns
+  uint32_t tmem_base;
+  int abort;
+  uint32_t err;
+};
+constexpr int kSmemBytes = kOffCtl + (int)sizeof(Ctl);
+constexpr int kSmemAlloc = (kSmemBytes + 1023) & ~1023;
+static_assert(kSmemAlloc <= 232448, "shared memory budget");
+constexpr int kFollowers = kRowWarps + kProducerWarps + 1;
+
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* c) {
+  if (mbar_wait(bar, parity, &c->abort, c->wait_ns)) return true;
+  c->abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* c) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, c);
+}
+// Every lane waits; the result is warp-uniform and the warp converged.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c) {
+  return __all_sync(0xffffffffu, wait(bar, parity, c));
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two f16 numbers to the nearest e4m3 codes (at most 448) and back.
+__device__ __forceinline__ uint32_t to_e4m3(uint32_t f16x2) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(f16x2));
+  return d;
+}
+__device__ __forceinline__ uint32_t from_e4m3(uint32_t codes) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)codes));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// ---------------------------------------------------------------------------
+// producers
+// ---------------------------------------------------------------------------
+// Warp pw fetches tokens 32 pw .. of every tile: a lane looks up a token, and for
+// each four tokens eight lanes copy 128 bytes of one.
+__device__ void producer(const Params& p, uint8_t* smem, Ctl* c, int pw) {
+  const int lane = threadIdx.x & 31;
+  const int r7 = lane & 7, ch = lane >> 3;
+  uint32_t err = 0, j = 0;
+  for_pieces(c, [&](const Piece& pc) {
+    const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
+    auto pos_of = [&](int v) { return (uint32_t)pc.tile(v) * kTK + 32 * pw + lane; };
+    auto seen = [&](int v, uint32_t pos) {
+      return v < pc.t1 && pos < (uint32_t)pc.N && (pos >= (uint32_t)pc.lo || pos < (uint32_t)p.sinks);
+    };
+    auto entry_of = [&](int v) -> int32_t {
+      const uint32_t pos = pos_of(v);
+      return seen(v, pos) ? __ldg(idx + kvq::page_of(p, pos)) : -1;
+    };
+    // -1: not read
+    auto slot_of = [&](int32_t e, int v) -> int32_t {
+      const uint32_t pos = pos_of(v);
+      const int64_t s = (int64_t)e * p.page_size + (pos - kvq::page_of(p, pos) * (uint32_t)p.page_size);
+      if (e >= 0 && s < p.slots) return (int32_t)s;
+      if (seen(v, pos)) err |= MLA_DEVERR_SLOT;
+      return -1;
+    };
+    auto word_of = [&](int32_t slot) { return slot >= 0 ? (uint32_t)__ldg(p.scales + p.block((uint32_t)slot)) : 0u; };
+    int32_t slot = slot_of(entry_of(pc.t0), pc.t0), ent = entry_of(pc.t0 + 1);
+    uint32_t word = word_of(slot);
+#pragma unroll 1
+    for (int v = pc.t0; v < pc.t1; ++v, ++j) {
+      const int32_t next = slot_of(ent, v + 1);
+      const uint32_t next_word = word_of(next);
+      ent = entry_of(v + 2);
+      const uint32_t st = j % kStages;
+      if (!wait_warp(&c->empty[st], ((j / kStages) & 1u) ^ 1u, c)) return false;
+      const uint32_t stage = smem_u32(smem) + st * kStage;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int token = 4 * i + ch, row = 32 * pw + token;
+        const int32_t s = __shfl_sync(0xffffffffu, slot, token);
+        const uint8_t* src = p.cache + (uint64_t)(uint32_t)max(s, 0) * (uint32_t)p.row_stride + 16 * r7;
+        const uint32_t dst = stage + row * 128 + ((r7 ^ (row & 7)) << 4), bytes = s >= 0 ? 16u : 0u;
+#pragma unroll
+        for (int ck = 0; ck < kChunks; ++ck) cp_async_16_zfill(dst + ck * kChunk, src + 128 * ck, bytes);
+      }
+      cp_async_mbar_arrive(&c->full[st]);  // when they have landed
+      c->tok_k[st][32 * pw + lane] = scale_of(word);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->full[st]);
+      slot = next;
+      word = next_word;
+    }
+    return true;
+  });
+  cp_async_wait_all();
+  if (err) atomicOr(&c->err, err);
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+// One warp: S of a tile is issued as soon as the tile is there, ahead of the O
+// product of the tile before when that has to wait for its weights.
+__device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
+  const bool leader = elect_one();
+  if (p.hold && !wait_warp(&c->drain, 0u, c)) return;
+  uint32_t j = 0, seg = 0;
+  const uint32_t q_lo = desc_lo(smem, kOffQ), p_lo = desc_lo(smem, kOffP);
+  for_pieces(c, [&](const Piece& pc) {
+    if (!wait_warp(&c->q_ready, seg & 1u, c)) return false;
+    ++seg;
+    const int halves = p.rows - pc.g * kRG > kHalfRows ? 2 : 1;
+    const uint32_t is8 = idesc_e4m3_f32(kTK, 32 * halves, 0, 0), is16 = idesc_bf16_f32(kTK, 32 * halves, 0, 0);
+    const uint32_t io = idesc_e4m3_f32(128, 48 * halves, 1, 1);
+    const uint32_t n = (uint32_t)(pc.t1 - pc.t0);
+    uint32_t s = 0;  // S products issued
+    auto issue_s = [&]() {
+      const uint32_t i = j + s, st = i % kStages;
+      tc_fence_after();
+      fence_proxy_async_smem();  // the tile came by cp.async, without a fence of its writers
+      if (leader) {
+        const uint32_t d = kColS + (i & 1u) * kQRows, a = desc_lo(smem, st * kStage);
+#pragma unroll 1
+        for (uint32_t ck = 0; ck < 4; ++ck) {
+#pragma unroll
+          for (uint32_t kk = 0; kk < 4; ++kk)
+            mma_cta_ss_f8(d, desc_at(a + ((ck * kChunk + kk * 32) >> 4)), desc_at(q_lo + ((ck * kQChunk + kk * 32) >> 4)),
+                          is8, ck | kk);
+        }
+#pragma unroll
+        for (uint32_t kk = 0; kk < 4; ++kk)
+          mma_cta_ss(d, desc_at(a + ((4 * kChunk + kk * 32) >> 4)), desc_at(q_lo + ((4 * kQChunk + kk * 32) >> 4)), is16,
+                     1);
+        mma_cta_commit(&c->s_full[i & 1u]);
+      }
+      __syncwarp();
+      ++s;
+    };
+    auto full = [&]() { return &c->full[(j + s) % kStages]; };
+    auto full_parity = [&]() { return ((j + s) / kStages) & 1u; };
+#pragma unroll 1
+    for (uint32_t v = 0; v < n; ++v) {
+      if (s == v) {
+        if (!wait_warp(full(), full_parity(), c)) return false;
+        issue_s();
+      }
+      const uint32_t i = j + v, st = i % kStages;
+      // the other S buffer is free: the O product of the tile before, whose weights came from it, is issued
+      uint64_t t0 = 0;
+      while (!__all_sync(0xffffffffu, mbar_test_wait_cluster(&c->p_ready, i & 1u))) {
+        if (s == v + 1 && s < n && __all_sync(0xffffffffu, mbar_test_wait_cluster(full(), full_parity()))) {
+          issue_s();
+          continue;
+        }
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&c->abort) || now - t0 > c->wait_ns)) {
+          c->abort = 1;
+          return false;
+        }
+      }
+      tc_fence_after();
+      if (leader) {
+        const uint32_t a = desc_lo(smem, st * kStage);
+#pragma unroll 1
+        for (uint32_t kk = 0; kk < 4; ++kk) {  // 32 tokens
+#pragma unroll
+          for (uint32_t m = 0; m < 4; ++m)
+            mma_cta_ss_f8(kColO + m * kBlockO, desc_at(a + ((m * kChunk + kk * 32 * 128) >> 4)),
+                          desc_at(p_lo + ((kk * 32 * 128) >> 4)), io, v | kk);
+        }
+        mma_cta_commit(&c->empty[st]);
+        mma_cta_commit(&c->pv_done);
+      }
+      __syncwarp();
+    }
+    j += n;
+    return true;
+  });
+  __syncwarp();
+  // on abort, outstanding MMAs must finish before Tensor Memory is released
+  if (!__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&c->abort) != 0)) return;
+  if (leader && !p.hold) {
+    mma_cta_commit(&c->drain);
+    mbar_wait_drain(&c->drain, 0, kDrainLimitNs);
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// softmax and output
+// ---------------------------------------------------------------------------
+// Brings a piece's queries into shared memory as two e4m3 terms; each row warp takes
+// four rows.  Rows that do not exist, up to the end of a half, are zeros.
+__device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ctl* c, const Piece& pc, int warp) {
+  const int lane = threadIdx.x & 31;
+  const int rows = min(kRG, p.rows - pc.g * kRG), padded = rows > kHalfRows ? kRG : kHalfRows;
+#pragma unroll 1
+  for (int r = 4 * warp; r < min(4 * warp + 4, padded); ++r) {
+    uint32_t w[8] = {}, pe = 0;
+    if (r < rows) {
+      const int64_t row = (int64_t)pc.b * p.rows + pc.g * kRG + r;
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q_lat) + row * (2 * kDl)) + 2 * lane;
+      const uint4 a = __ldg(q), b = __ldg(q + 1);
+      pe = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.q_pe) + row * (2 * kDr)) + lane);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+    uint32_t big = max(pe & 0x7fffu, (pe >> 16) & 0x7fffu);  // magnitudes compare as their bits
+#pragma unroll
+    for (int i = 0; i < 8; ++i) big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    big = __reduce_max_sync(0xffffffffu, big);
+    const bool finite = big < 0x7f80u;
+    // the largest magnitude goes to [2^7, 2^8), or to [2^8, 448] where its fraction allows it
+    const int t = max(min(((big & 0x7fu) <= 0x60u ? 135 : 134) - (int)(big >> 7), 120), -120);
+    const float mul = pow2(t);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi[i] = lo[i] = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t x = w[2 * i + k];
+        const float f0 = __uint_as_float(x << 16) * mul, f1 = __uint_as_float(x & 0xffff0000u) * mul;
+        const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hf = from_e4m3(h);
+        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+        const uint32_t l =
+            __nv_cvt_float2_to_fp8x2(make_float2(f0 - back.x, f1 - back.y), __NV_SATFINITE, __NV_E4M3);
+        hi[i] |= (finite ? h : 0x7f7fu) << (16 * k);
+        lo[i] |= l << (16 * k);
+      }
+    }
+    const __nv_bfloat162 pm =
+        __floats2bfloat162_rn(__uint_as_float(pe << 16) * mul, __uint_as_float(pe & 0xffff0000u) * mul);
+    const int n = 32 * (r >> 4) + (r & 15);
+    const uint32_t q0 = smem_u32(smem) + kOffQ;
+    const uint32_t at = q0 + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);
+    st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+    st_shared_v4(at + 16 * 128, lo[0], lo[1], lo[2], lo[3]);  // 16 rows on: the same swizzle
+    const uint32_t rope = 4 * kQChunk + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + 4 * (lane & 3);
+    *reinterpret_cast<uint32_t*>(smem + kOffQ + rope) = *reinterpret_cast<const uint32_t*>(&pm);
+    *reinterpret_cast<uint32_t*>(smem + kOffQ + rope + 16 * 128) = 0u;
+    if (lane == 0) c->unit[r] = fminf(p.scale_log2 * pow2(-t), 3.402823466e38f);
+  }
+}
+
+// Multiplies the half's columns of O by a factor per row, in the warp's lanes.
+__device__ __forceinline__ void rescale(uint32_t tO, const float (&a)[kHalfRows]) {
+#pragma unroll 1
+  for (int q = 0; q < 12; ++q) {  // block, term
+    const uint32_t at = tO + (q / 3) * kBlockO + (q % 3) * kHalfRows;
+    uint32_t u[16];
+    tmem_ld16_sync(at, u);
+#pragma unroll
+    for (int r = 0; r < kHalfRows; ++r) u[r] = __float_as_uint(__uint_as_float(u[r]) * a[r]);
+    tmem_st_32x32b_x16(at, u);
+  }
+  tmem_wait_st();
+}
+
+__device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
+  const int lane = threadIdx.x & 31;
+  const int quad = warp & 3, half = warp >> 2;
+  const int token = 32 * quad + lane;
+  const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+  const uint32_t tO = lane_off + kColO + half * 3 * kHalfRows;
+  const uint32_t tP = smem_u32(smem) + kOffP + token * 128;
+  uint32_t j = 0, seg = 0;
+  uint32_t i = 0;  // tiles whose maxima this half has exchanged
+  bool bad = false;
+  for_pieces(c, [&](const Piece& pc) {
+    const int rows = min(kRG, p.rows - pc.g * kRG);
+    const int P = pc.P;
+    // This warp has seen the end of every S product of the piece before, and with
+    // the end of its last O product that no warp needs its masks any more.
+    stage_queries(p, smem, c, pc, warp);
+    if (warp == 0) {
+      const NodeView nv = kvq::node_view_warp(p, pc.b, (pc.g * kRG + min(lane, rows - 1)) / p.H, P, &bad);
+      c->mask[lane] = nv.mask;
+      c->depth[lane] = nv.depth;
+    }
+    fence_proxy_async_smem();  // read by the MMA
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c->q_ready);
+    if (!wait_warp(&c->q_ready, seg & 1u, c)) return false;
+    const bool idle = kHalfRows * half >= rows;
+    // positions up to this one are outside some node's window
+    const int past_any = p.window > 0 ? max(P - p.window + p.Q - 1, -1) : -1;
+    float unit[kHalfRows], m[kHalfRows], l[kHalfRows];
+#pragma unroll
+    for (int r = 0; r < kHalfRows; ++r) {
+      unit[r] = c->unit[kHalfRows * half + r];
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll 1
+    for (int t = pc.t0; t < pc.t1; ++t, ++j) {
+      const uint32_t st = j % kStages, par = (j >> 1) & 1u;
+      if (!wait_warp(&c->s_full[j & 1u], par, c)) return false;
+      if (idle) {
+        // every barrier's phases count on
+        if (j > 0 && !wait_warp(&c->pv_done, (j - 1) & 1u, c)) return false;
+        if (lane == 0) mbar_arrive(&c->p_ready);
+        continue;
+      }
+      if (!wait_warp(&c->full[st], par, c)) return false;  // has passed: the producers' scales are visible
+      tc_fence_after();
+      const int k = c->tok_k[st][token];
+      const float kf = (float)k, kmul = pow2(k), kinv = pow2(-k);
+      float y[kHalfRows];
+      {
+        uint32_t u[32];
+        tmem_ld32_sync(lane_off + kColS + (j & 1u) * kQRows + 32 * half, u);
+#pragma unroll
+        for (int r = 0; r < kHalfRows; ++r)
+          y[r] = fmaf((__uint_as_float(u[r]) + __uint_as_float(u[kHalfRows + r])) * kmul, unit[r], kf);
+      }
+      const int pos0 = pc.tile(t) * kTK;
+      if (pos0 > P - kTK || pos0 <= past_any) {
+        const int pos = pos0 + token, rel = pos - P;
+#pragma unroll
+        for (int r = 0; r < kHalfRows; ++r) {
+          const int rr = kHalfRows * half + r;
+          bool see;
+          if (rel >= 0)
+            see = rel < 64 && ((c->mask[rr] >> rel) & 1u);
+          else
+            see = p.window == 0 || pos < p.sinks || pos > P - p.window + c->depth[rr];
+          if (!see) y[r] = -INFINITY;
+        }
+      }
+      // the tile's maxima: of the warp's tokens, then of the half's four warps
+      float4* pm = reinterpret_cast<float4*>(c->part_max[i & 1u][half][quad]);
+#pragma unroll
+      for (int q = 0; q < kHalfRows / 4; ++q) {
+        const float4 v = make_float4(warp_max(y[4 * q]), warp_max(y[4 * q + 1]), warp_max(y[4 * q + 2]),
+                                     warp_max(y[4 * q + 3]));
+        if (lane == 0) pm[q] = v;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->m_ready[half]);
+      if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
+      float nm[kHalfRows];
+      bool move = false;
+#pragma unroll
+      for (int q = 0; q < kHalfRows / 4; ++q) {
+        float4 v = reinterpret_cast<const float4*>(c->part_max[i & 1u][half][0])[q];
+#pragma unroll
+        for (int o = 1; o < 4; ++o) {
+          const float4 w = reinterpret_cast<const float4*>(c->part_max[i & 1u][half][o])[q];
+          v = make_float4(fmaxf(v.x, w.x), fmaxf(v.y, w.y), fmaxf(v.z, w.z), fmaxf(v.w, w.w));
+        }
+        nm[4 * q] = v.x;
+        nm[4 * q + 1] = v.y;
+        nm[4 * q + 2] = v.z;
+        nm[4 * q + 3] = v.w;
+      }
+      ++i;
+      // a maximum moves only when the tile beats it by 2^kLazy; the same in every lane
+#pragma unroll
+      for (int r = 0; r < kHalfRows; ++r) move |= nm[r] > m[r] + kLazy;
+      if (move) {
+        float a[kHalfRows];
+#pragma unroll
+        for (int r = 0; r < kHalfRows; ++r) {
+          const float mn = nm[r] > m[r] + kLazy ? nm[r] : m[r];
+          a[r] = mn == m[r] ? 1.f : exp2f(m[r] - mn);  // 0 when m was -inf
+          l[r] *= a[r];
+          m[r] = mn;
+        }
+        if (t > pc.t0) {
+          if (!wait_warp(&c->pv_done, (j - 1) & 1u, c)) return false;
+          tc_fence_after();
+          rescale(tO, a);
+        }
+      }
+      // weights, and their three terms
+      uint32_t hi[4], lo[4], third[4];
+#pragma unroll
+      for (int q = 0; q < kHalfRows / 2; ++q) {
+        float e[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 2 * q + h;
+          e[h] = ex2_approx(y[r] + (m[r] == -INFINITY ? 0.f : kWeightShift - m[r]));
+          l[r] = fmaf(e[h], kinv, l[r]);
+        }
+        const uint32_t w = pack_f16(e[0], e[1]);
+        const uint32_t h = to_e4m3(w);
+        const uint32_t r1 = kvq::hmul2_f16(sub_f16(w, from_e4m3(h)), 0x50005000u);  // * 32; exact, as what follows
+        const uint32_t b = to_e4m3(r1);
+        const uint32_t r2 = kvq::hmul2_f16(sub_f16(r1, from_e4m3(b)), 0x5c005c00u);  // * 256
+        const uint32_t d = to_e4m3(r2);
+        if (q & 1) {
+          hi[q >> 1] |= h << 16;
+          lo[q >> 1] |= b << 16;
+          third[q >> 1] |= d << 16;
+        } else {
+          hi[q >> 1] = h;
+          lo[q >> 1] = b;
+          third[q >> 1] = d;
+        }
+      }
+      if (j > 0 && !wait_warp(&c->pv_done, (j - 1) & 1u, c)) return false;  // the weights' place is free
+      st_shared_v4(tP + (((3 * half) ^ (token & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(tP + (((3 * half + 1) ^ (token & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+      st_shared_v4(tP + (((3 * half + 2) ^ (token & 7)) << 4), third[0], third[1], third[2], third[3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->p_ready);
+    }
+
+    // The piece's sums over all tokens, then O: the warp's lanes hold latents
+    // 32 quad + lane of each block of 128.
+    const uint32_t phase = seg & 1u;
+    ++seg;
+    if (!idle) {
+#pragma unroll
+      for (int r = 0; r < kHalfRows; ++r) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+        if (lane == 0) c->part_sum[half][quad][r] = l[r];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->l_ready[half]);
+      if (!wait_warp(&c->l_ready[half], phase, c)) return false;
+    } else if (lane == 0) {
+      mbar_arrive(&c->l_ready[half]);
+    }
+    if (!wait_warp(&c->pv_done, (j - 1) & 1u, c)) return false;
+    if (idle) return true;
+    tc_fence_after();
+    float inv[kHalfRows];
+#pragma unroll
+    for (int r = 0; r < kHalfRows; ++r) {
+      const float (&s)[4][kHalfRows] = c->part_sum[half];
+      l[r] = (s[0][r] + s[1][r]) + (s[2][r] + s[3][r]);
+      inv[r] = l[r] > 0.f ? p.out_mul / l[r] : l[r];  // a row that sees nothing of this piece has l = 0 and O = 0
+    }
+    const int row0 = pc.g * kRG + kHalfRows * half, live = min(kHalfRows, p.rows - row0);
+    const int64_t orow = (int64_t)pc.b * p.rows + row0;
+    const int latent = 32 * quad + lane;
+#pragma unroll 1
+    for (int mb = 0; mb < 4; ++mb) {
+      uint32_t u[16], v[16], w[16];
+      __syncwarp();
+      tmem_ld16_sync(tO + mb * kBlockO, u);
+      tmem_ld16_sync(tO + mb * kBlockO + kHalfRows, v);
+      tmem_ld16_sync(tO + mb * kBlockO + 2 * kHalfRows, w);
+#pragma unroll
+      for (int r = 0; r < kHalfRows; ++r) {
+        const float lo = fmaf(__uint_as_float(w[r]), 1.f / kThirdMul, __uint_as_float(v[r]));
+        const float o = fmaf(lo, 1.f / kLoMul, __uint_as_float(u[r])) * inv[r];
+        if (r < live) {
+          if (pc.slot < 0)
+            static_cast<__nv_bfloat16*>(p.out)[(orow + r) * kDl + 128 * mb + latent] = __float2bfloat16_rn(o);
+          else
+            p.part_o[((int64_t)pc.slot * kRG + kHalfRows * half + r) * kDl + 128 * mb + latent] = o;
+        }
+      }
+    }
+    if (quad == 0 && lane < live) {
+      float ml = 0.f, ll = 0.f;
+#pragma unroll
+      for (int r = 0; r < kHalfRows; ++r)
+        if (lane == r) {
+          ml = m[r];
+          ll = l[r];
+        }
+      const float lse =
+          ll > 0.f ? (ml + log2f(ll) - kWeightShift) * 0.69314718055994530942f : ll == 0.f ? -INFINITY : ll;
+      if (pc.slot >= 0) p.part_lse[(int64_t)pc.slot * kRG + kHalfRows * half + lane] = lse;
+      else if (p.lse) p.lse[orow + lane] = lse;
+    }
+    tc_fence_before();
+    return true;
+  });
+  if (bad) atomicOr(&c->err, MLA_DEVERR_PARENT);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5;
+  Ctl* c = reinterpret_cast<Ctl*>(smem + kOffCtl);
+  grid_dep_wait();  // launched before the stream's last kernel has ended
+  if (threadIdx.x == 0) {
+    for (int q = 0; q < kStages; ++q) {
+      mbar_init(&c->full[q], 33 * kProducerWarps);
+      mbar_init(&c->empty[q], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&c->s_full[q], 1);
+      mbar_init(&c->m_ready[q], 4);
+      mbar_init(&c->l_ready[q], 4);
+    }
+    mbar_init(&c->q_ready, kRowWarps);
+    mbar_init(&c->p_ready, kRowWarps);
+    mbar_init(&c->pv_done, 1);
+    mbar_init(&c->drain, 1);
+    for (int q = 0; q < kPieces; ++q) {
+      mbar_init(&c->piece_full[q], 1);
+      mbar_init(&c->piece_empty[q], kFollowers);
+    }
+    c->abort = 0;
+    c->start_b = p.B;
+    c->start_x = 0;
+    c->start_T = 0;
+    c->left = 0;
+    c->wait_ns = p.wait_ns;
+    c->err = (smem_u32(smem) & 1023u) ? MLA_DEVERR_LAYOUT : 0u;
+    fence_mbar_init();
+  }
+  if (warp == kWarpSched) {
+    tmem_alloc_cta(&c->tmem_base, kTmemCols);
+    tmem_relinquish_cta();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int worker = blockIdx.x;
+  const int n = Work::make_split(p, c, worker);  // the same n in every CTA
+  if (threadIdx.x == 0) {
+    static_cast<Start*>(p.starts)[worker] = Start{c->start_x, c->start_b, c->start_T, n > 0 ? n : 0, {0, 0, 0}};
+    if (worker == 0) p.err[0] = gridDim.x;
+    if (c->tmem_base != 0) c->err = MLA_DEVERR_LAYOUT;  // all columns are allocated
+  }
+  if (worker < n && c->tmem_base == 0) {
+    if (warp < kRowWarps) softmax(p, smem, c, warp);
+    else if (warp < kWarpMma) producer(p, smem, c, warp - kWarpProd);
+    else if (warp == kWarpMma) products(p, smem, c);
+    else Work::schedule(p, c, worker);
+  }
+  __syncwarp();
+  grid_dep_launch();  // the merging kernel may start launching; it waits for this grid
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) p.err[kErrFirst + worker] = c->err | (c->abort ? MLA_DEVERR_TIMEOUT : 0u);
+  tc_fence_after();
+  if (warp == kWarpSched) tmem_dealloc_cta(c->tmem_base, kTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// merge
+// ---------------------------------------------------------------------------
+// The pieces of a row group that several CTAs shared:
+//   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k.
+// Every block reads where the CTAs' intervals begin and lists the row groups that
+// a boundary cuts.  A quarter of the columns of a row goes to a warp.  Few rows in
+// many pieces: four warps share it, every fourth piece each; else each of the four
+// takes a row of its own.
+constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32, kMergeParts = 4;
+constexpr int kMaxWorkers = 256;
+static_assert(kMaxWorkers <= kErrMax && kMaxWorkers <= kMergeThreads, "an error word per CTA");
+__global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Params p) {
+  __shared__ Start start[kMaxWorkers];
+  __shared__ int cut[kMaxWorkers];                   // boundaries that are the first inside a row group
+  __shared__ uint32_t cut_mask[kMaxWorkers / 32];
+  __shared__ int slot[kMaxWorkers];                  // -1: an empty piece
+  __shared__ float weight[kMergeWarps][kMaxWorkers];
+  __shared__ float4 sums[kMergeParts - 1][4][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int quarter = warp & 3, part = warp >> 2;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (tid < p.clusters) start[tid] = static_cast<const Start*>(p.starts)[tid];
+  __syncthreads();
+  const int workers = start[0].n;
+  bool first = false;
+  if (tid > 0 && tid < workers) {
+    const Start s0 = start[tid - 1], s = start[tid];
+    const int64_t base = div_fast(s.x, kFixed + s.T) * (kFixed + s.T);
+    first = s.x > base && (s0.b != s.b || s0.x <= base);
+  }
+  const uint32_t mask = __ballot_sync(0xffffffffu, first);
+  if (lane == 0 && warp < kMaxWorkers / 32) cut_mask[warp] = mask;
+  __syncthreads();
+  // every block lists them in the same order: they share the list
+  int cuts = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxWorkers / 32; ++w) {
+    if (w == warp && first) cut[cuts + __popc(mask & ((1u << lane) - 1u))] = tid;
+    cuts += __popc(cut_mask[w]);
+  }
+  __syncthreads();
+  const int rows_max = min(p.rows, kRG);
+  const bool split = cuts * rows_max <= 2 * (int)gridDim.x;
+  const int per = split ? rows_max : (rows_max + kMergeParts - 1) / kMergeParts;  // tasks of a cut
+  for (int task = blockIdx.x; task < cuts * per; task += gridDim.x) {
+    const int k = cut[task / per];
+    const Start s = start[k];
+    const int T = s.T, L = kFixed + T;
+    const int64_t g = div_fast(s.x, L), base = g * L;
+    // pieces: CTA k - 1 has units [0, x_k) of the row group, CTA i >= k [x_i, x_{i+1})
+    auto unit = [&](int i) -> int64_t {
+      return i < k ? 0 : i >= workers || start[i].b != s.b || start[i].x - base > L ? L : start[i].x - base;
+    };
+    bool mine = false, whole = false;
+    const int w = k - 1 + tid;
+    if (w < workers) {
+      const int64_t z0 = unit(w), z1 = unit(w + 1);
+      mine = z0 < L;
+      if (mine) {
+        const int t0 = Work::cut_tile(z0, T), t1 = Work::cut_tile(z1, T);
+        whole = t0 == 0 && t1 == T;
+        slot[tid] = t1 > t0 ? 2 * w + (t0 == 0) : -1;
+      }
+    }
+    const int n = __syncthreads_count(mine);
+    // when one CTA has it all it stored the results
+    if (__syncthreads_or(whole)) continue;
+    const int r = split ? task % per : (task % per) * kMergeParts + part;
+    const bool live = r < min((int64_t)kRG, p.rows - g * kRG);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float total = 1.f;
+    const int64_t orow = (int64_t)s.b * p.rows + g * kRG + r;
+    if (live) {
+      float* wt = weight[warp];
+      float m = -INFINITY, sum = 0.f;
+      for (int i = lane; i < n; i += 32) {
+        wt[i] = slot[i] >= 0 ? p.part_lse[(int64_t)slot[i] * kRG + r] : -INFINITY;
+        m = fmaxf(m, wt[i]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (m == -INFINITY) m = 0.f;  // no piece has any weight
+      for (int i = lane; i < n; i += 32) {
+        wt[i] = __expf(wt[i] - m);
+        sum += wt[i];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      total = sum == 0.f ? 1.f : sum;  // then a row of zeros, as from one piece
+      if (p.lse && quarter == 0 && lane == 0 && (part == 0 || !split)) p.lse[orow] = m + logf(sum);
+      __syncwarp();
+      const int step = split ? kMergeParts : 1;
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + (int64_t)r * kDl + 128 * quarter) + lane;
+      for (int i0 = split ? part : 0; i0 < n; i0 += 4 * step) {
+        float4 v[4];
+        float f[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int i = i0 + d * step, sl = i < n ? slot[i] : -1;
+          v[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+          f[d] = 0.f;
+          if (sl >= 0) {
+            v[d] = __ldcg(src + (int64_t)sl * (kRG * kDl / 4));
+            f[d] = wt[i];
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          acc.x = fmaf(f[d], v[d].x, acc.x);
+          acc.y = fmaf(f[d], v[d].y, acc.y);
+          acc.z = fmaf(f[d], v[d].z, acc.z);
+          acc.w = fmaf(f[d], v[d].w, acc.w);
+        }
+      }
+    }
+    if (split) {
+      if (part > 0) sums[part - 1][quarter][lane] = acc;
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int o = 0; o < kMergeParts - 1; ++o) {
+          const float4 a = sums[o][quarter][lane];
+          acc.x += a.x;
+          acc.y += a.y;
+          acc.z += a.z;
+          acc.w += a.w;
+        }
+      }
+    }
+    if (live && (part == 0 || !split)) {
+      const float inv = 1.f / total;
+      const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                           b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDl + 128 * quarter)[lane] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+    __syncthreads();  // slot and sums are reused
+  }
+}
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+float score_factor(const mla_kv8_attn_args& a) {
+  return (float)std::ldexp((double)a.scale * 1.4426950408889634, a.cache.exponent);
+}
+
+mla_status validate_shape(const mla_kv8_attn_args* a) {
+  if (!a) return MLA_ERR_INVALID_ARG;
+  if (a->B < 0 || a->Q < 0 || a->H < 1) return MLA_ERR_INVALID_ARG;
+  if (a->Q > MLA_MAX_Q) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)a->H * a->Q > (int64_t)1 << 24 || (int64_t)a->H * a->Q * a->B > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+mla_status validate_call(const mla_kv8_attn_args* a) {
+  mla_status st = validate_cache(&a->cache);
+  if (st != MLA_OK) return st;
+  if (!a->q_lat || !a->q_pe || !a->prefix_lens || !a->out) return MLA_ERR_INVALID_ARG;
+  if (!aligned(a->q_lat, 16) || !aligned(a->q_pe, 16) || !aligned(a->out, 16)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(a->prefix_lens, 4) || !aligned(a->tree_parent, 4) || !aligned(a->lse, 4)) return MLA_ERR_INVALID_ARG;
+  if (a->page_size < 1) return MLA_ERR_INVALID_ARG;
+  if (a->page_size == 1) {
+    if (!a->kv_indptr || !a->kv_indices || !aligned(a->kv_indptr, 4) || !aligned(a->kv_indices, 4))
+      return MLA_ERR_INVALID_ARG;
+  } else {
+    if (!a->block_table || a->max_pages < 1 || !aligned(a->block_table, 4)) return MLA_ERR_INVALID_ARG;
+    if ((int64_t)a->max_pages * a->page_size > INT32_MAX) return MLA_ERR_INVALID_ARG;
+  }
+  if (a->window < 0 || a->sinks < 0 || (a->window == 0 && a->sinks != 0)) return MLA_ERR_INVALID_ARG;
+  // rounded to zero or infinity, the factor would turn scores of -inf or 0 into NaN
+  if (!std::isfinite(a->scale) || !(a->scale > 0.f) || !std::isnormal(score_factor(*a))) return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
+// CTAs of a launch, one per SM of the current device; 0 when it cannot be had.
+int workers_per_gpu() {
+  constexpr int kMaxDevices = 64;
+  static std::mutex mu;
+  static int cached[kMaxDevices] = {};
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return 0;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (cached[dev] > 0) return cached[dev];
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cached[dev] = sms < kMaxWorkers ? sms : kMaxWorkers;
+  return cached[dev];
+}
+
+struct Layout {
+  size_t starts, part_lse, part_o, total;
+};
+Layout layout(int workers) {
+  Layout l;
+  size_t o = MLA_KV8_WORKSPACE_BYTES;
+  l.starts = o;    o = align256(o + sizeof(Start) * (size_t)workers);
+  l.part_lse = o;  o = align256(o + sizeof(float) * 2 * (size_t)workers * kRG);
+  l.part_o = o;    o = align256(o + sizeof(float) * 2 * (size_t)workers * kRG * kDl);
+  l.total = o;
+  return l;
+}
+
+Params make_params(const mla_kv8_attn_args* a, void* ws, int workers) {
+  Params p = {};
+  p.B = a->B;
+  p.Q = a->Q;
+  p.H = a->H;
+  p.rows = a->H * a->Q;
+  p.cache = static_cast<const uint8_t*>(a->cache.rows);
+  p.row_stride = a->cache.row_stride;
+  p.slots = a->cache.slots;
+  p.q_lat = a->q_lat;
+  p.q_pe = a->q_pe;
+  p.page_size = a->page_size;
+  Divider d;
+  d.set(a->page_size);
+  p.page_shift = d.shift;
+  p.page_mul = d.mul;
+  p.kv_indptr = a->kv_indptr;
+  p.kv_indices = a->kv_indices;
+  p.block_table = a->block_table;
+  p.max_pages = a->max_pages;
+  p.prefix_lens = a->prefix_lens;
+  p.tree_parent = a->tree_parent;
+  p.window = a->window;
+  p.sinks = a->sinks;
+  p.scale_log2 = score_factor(*a);
+  p.out_mul = (float)std::ldexp(1.0, a->cache.exponent);
+  p.out = a->out;
+  p.lse = a->lse;
+  p.groups = (p.rows + kRG - 1) / kRG;
+  p.clusters = workers;
+  p.scales = a->cache.scales;
+  p.block.set(a->cache.block);
+  const Layout l = layout(workers);
+  char* base = static_cast<char*>(ws);
+  p.err = reinterpret_cast<uint32_t*>(base);
+  p.starts = base + l.starts;
+  p.part_lse = reinterpret_cast<float*>(base + l.part_lse);
+  p.part_o = reinterpret_cast<float*>(base + l.part_o);
+  return p;
+}
+
+mla_status run_attn(const mla_kv8_attn_args* a, void* workspace, size_t ws_bytes, mla_stream_t stream,
+                    uint64_t hold_ns) {
+  mla_status st = validate_shape(a);
+  if (st != MLA_OK) return st;
+  if (a->B == 0 || a->Q == 0) return hold_ns ? MLA_ERR_INVALID_ARG : MLA_OK;  // the self-test needs a launch
+  st = validate_call(a);
+  if (st != MLA_OK) return st;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < MLA_KV8_WORKSPACE_BYTES) return MLA_ERR_WORKSPACE;
+  const int n = workers_per_gpu();
+  if (n < 1) return MLA_ERR_CUDA;
+  if (ws_bytes < layout(n).total) return MLA_ERR_WORKSPACE;
+  Params p = make_params(a, workspace, n);
+  p.hold = hold_ns != 0;
+  p.wait_ns = p.hold ? hold_ns : kWaitLimitNs;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // per call: the attribute belongs to the context, which may be a new one
+  if (cudaFuncSetAttribute(kv8_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  if (launch_kernel(kv8_attn_kernel, dim3(n), dim3(kThreads), kSmemAlloc, s, true, p) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  if (n > 1 && launch_kernel(kv8_merge_kernel, dim3(2 * n), dim3(kMergeThreads), 0, s, true, p) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+}  // namespace
+}  // namespace kv8
+}  // namespace mlav
+
+using namespace mlav;
+
+extern "C" size_t mla_kv8_attn_workspace_size(const mla_kv8_attn_args* a) {
+  if (kv8::validate_shape(a) != MLA_OK) return 0;
+  const int n = kv8::workers_per_gpu();
+  return n > 0 ? kv8::layout(n).total : 0;
+}
+
+extern "C" mla_status mla_kv8_attn(const mla_kv8_attn_args* a, void* workspace, size_t ws_bytes, mla_stream_t stream) {
+  return kv8::run_attn(a, workspace, ws_bytes, stream, 0);
+}
+
+extern "C" mla_status mla_kv8_selftest_timeout(const mla_kv8_attn_args* a, void* workspace, size_t ws_bytes,
+                                               uint64_t hold_ns, mla_stream_t stream) {
+  if (hold_ns == 0 || hold_ns > 1000000000ull) return MLA_ERR_INVALID_ARG;
+  return kv8::run_attn(a, workspace, ws_bytes, stream, hold_ns);
+}

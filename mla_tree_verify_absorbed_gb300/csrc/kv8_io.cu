@@ -1,0 +1,422 @@
+// Writing rows of the paged 8-bit latent cache and reading them back
+// (mla_kv8_write, mla_kv8_read, mla_kv8_check).
+//
+// Write.  A block's unit depends on all rows that go to it, so a write is three
+// kernels: the first gathers what every block's new rows need (an integer maximum
+// per block, the same in any order), the second moves the rows that grown blocks
+// held to their new unit, and the third quantises the new rows.  Where no block
+// grows, the usual case of decoding, the second finds nothing to do.
+//
+// The need of a row of largest magnitude a = f 2^E (1 <= f < 2):
+//   a <= 448 2^(e+k) = 1.75 2^(e+k+8)   <=>   k >= E - e - 8 + (f > 1.75),
+// so it comes from the exponent bits and one comparison.  x 2^-(e+k) is exact in
+// fp32, and the conversion to e4m3 rounds once.
+//
+// Bound: HBM.
+#include <cuda_fp8.h>
+
+#include "io.cuh"
+#include "kv8.cuh"
+#include "sm100.cuh"
+
+namespace mlav {
+namespace kv8 {
+using kvq::io_grid;
+using kvq::kErrMax;
+using kvq::kIoThreads;
+using kvq::kIoWarps;
+using kvq::put_block_err;
+
+struct IoParams {
+  uint8_t* cache;
+  int64_t row_stride, slots;
+  uint32_t* scales;
+  Divider div;
+  int block, exponent;
+  int64_t n;
+  const int32_t* slot;
+  void* kv_c;
+  void* k_pe;
+  int64_t kv_c_stride, k_pe_stride;  // elements
+  bool wide;                         // kv_c rows are 32-byte aligned
+  int per;                           // growing: rows per block of threads
+  uint32_t* err;
+};
+
+// 2^e for -160 < e < 160, as two factors: no power here is out of range, but for
+// fp32 results.
+__device__ __forceinline__ float scale_by(float x, int e) { return x * pow2(e / 2) * pow2(e - e / 2); }
+
+// Sixteen latents of a row as bits of fp32 (the lane's part).
+template <class T>
+struct Part;
+template <>
+struct Part<__nv_bfloat16> {
+  uint32_t v[8];
+  __device__ __forceinline__ void load(const void* row, int lane, bool wide) {
+    kvq::ld_words(static_cast<const __nv_bfloat16*>(row) + 16 * lane, wide, v);
+  }
+  __device__ __forceinline__ uint32_t bits(int i) const { return (i & 1) ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16; }
+};
+template <>
+struct Part<float> {
+  uint32_t v[2][8];
+  __device__ __forceinline__ void load(const void* row, int lane, bool wide) {
+    const float* p = static_cast<const float*>(row) + 16 * lane;
+    kvq::ld_words(p, wide, v[0]);
+    kvq::ld_words(p + 8, wide, v[1]);
+  }
+  __device__ __forceinline__ uint32_t bits(int i) const { return v[i >> 3][i & 7]; }
+};
+
+__device__ __forceinline__ int64_t slot_at(const IoParams& p, int64_t i, uint32_t* e) {
+  const int64_t s = i < p.n ? p.slot[i] : -1;
+  if (s >= -1 && s < p.slots) return s;
+  *e |= MLA_DEVERR_SLOT;
+  return -1;
+}
+
+// What the new rows need, into the pending bits of their blocks' words.
+template <class T, int kDeep>
+__global__ void __launch_bounds__(kIoThreads) kv8_need_kernel(const IoParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (int64_t)blockIdx.x * kIoWarps + (threadIdx.x >> 5);
+  const int64_t nwarps = (int64_t)gridDim.x * kIoWarps;
+  grid_dep_wait();  // launched before the stream's last kernel has ended
+  grid_dep_launch();
+  uint32_t e = 0;
+  for (int64_t i0 = warp; i0 < p.n; i0 += kDeep * nwarps) {
+    int64_t slot[kDeep];
+    Part<T> x[kDeep];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      slot[d] = slot_at(p, i0 + d * nwarps, &e);
+      if (slot[d] >= 0)
+        x[d].load(static_cast<const T*>(p.kv_c) + (i0 + d * nwarps) * p.kv_c_stride, lane, p.wide);
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      if (slot[d] < 0) continue;
+      uint32_t big = 0;  // magnitudes compare as their bits
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t a = x[d].bits(i) & 0x7fffffffu;
+        if (a >= 0x7f800000u) e |= MLA_DEVERR_NONFINITE;
+        else big = max(big, a);
+      }
+      big = __reduce_max_sync(0xffffffffu, big);
+      const int k = (int)(big >> 23) - 127 - p.exponent - 8 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
+      const uint32_t need = (uint32_t)min(max(k, 0), kMaxK) + 1u;
+      if (lane == 0) {
+        uint32_t* word = p.scales + p.div((uint32_t)slot[d]);
+        const uint32_t w = *reinterpret_cast<volatile uint32_t*>(word), had = w & kScaleMask;
+        if (need > had && (need << kPendingShift | had) > w) atomicMax(word, need << kPendingShift | had);
+      }
+    }
+  }
+  put_block_err(p.err, e);
+}
+
+// k of a word between the kernels of a write.
+__device__ __forceinline__ int grown_scale(uint32_t w) {
+  return scale_of(max(w & kScaleMask, (w >> kPendingShift) & kScaleMask));
+}
+
+constexpr uint32_t kClaimed = 1u << (2 * kPendingShift);
+
+// The rows of blocks that held some and have grown, to the new unit.  A thread
+// block looks at `per` of the new rows, claims the grown blocks that nobody has
+// claimed, and moves all their rows, also those that are overwritten next.
+__global__ void __launch_bounds__(kIoThreads) kv8_grow_kernel(const IoParams p) {
+  __shared__ uint32_t claimed[kIoThreads], word[kIoThreads];
+  __shared__ int count;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) count = 0;
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+  uint32_t e = 0;
+  const int64_t i = (int64_t)blockIdx.x * p.per + threadIdx.x;
+  const int64_t s = (int)threadIdx.x < p.per ? slot_at(p, i, &e) : -1;
+  if (s >= 0) {
+    const uint32_t b = p.div((uint32_t)s), w = *reinterpret_cast<volatile uint32_t*>(p.scales + b);
+    if ((w & kScaleMask) && ((w >> kPendingShift) & kScaleMask) > (w & kScaleMask) && !(w & kClaimed) &&
+        !(atomicOr(p.scales + b, kClaimed) & kClaimed)) {
+      const int at = atomicAdd(&count, 1);
+      claimed[at] = b;
+      word[at] = w;
+    }
+  }
+  __syncthreads();
+  const int64_t rows = (int64_t)count * p.block;
+  constexpr int kDeep = 4;
+  for (int64_t r0 = warp; r0 < rows; r0 += kDeep * kIoWarps) {
+    uint8_t* row[kDeep];
+    int down[kDeep];
+    uint4 c[kDeep];
+    uint32_t rope[kDeep];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int64_t r = r0 + d * kIoWarps;
+      row[d] = nullptr;
+      if (r >= rows) continue;
+      const int at = (int)(r / p.block);
+      const int64_t slot = (int64_t)claimed[at] * p.block + r % p.block;
+      if (slot >= p.slots) continue;
+      row[d] = p.cache + slot * p.row_stride;
+      down[d] = grown_scale(word[at]) - scale_of(word[at]);
+      c[d] = reinterpret_cast<const uint4*>(row[d])[lane];
+      rope[d] = reinterpret_cast<const uint32_t*>(row[d] + kRopeOff)[lane];
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      if (!row[d]) continue;
+      const float mul = pow2(-down[d]);
+      uint32_t v[4] = {c[d].x, c[d].y, c[d].z, c[d].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v[q] >> (16 * h)), __NV_E4M3);
+          const float2 g = __half22float2(__half2(f));
+          o |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(g.x * mul, g.y * mul), __NV_SATFINITE, __NV_E4M3)
+               << (16 * h);
+        }
+        v[q] = o;
+      }
+      reinterpret_cast<uint4*>(row[d])[lane] = make_uint4(v[0], v[1], v[2], v[3]);
+      const __nv_bfloat162 k = __floats2bfloat162_rn(__uint_as_float(rope[d] << 16) * mul,
+                                                     __uint_as_float(rope[d] & 0xffff0000u) * mul);
+      reinterpret_cast<uint32_t*>(row[d] + kRopeOff)[lane] = *reinterpret_cast<const uint32_t*>(&k);
+    }
+  }
+}
+
+__device__ __forceinline__ float2 rope_pair(const __nv_bfloat16* p) {
+  const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ float2 rope_pair(const float* p) { return *reinterpret_cast<const float2*>(p); }
+
+// The new rows, in their blocks' units; a row's warp also puts the block's word
+// into its final form (all of a block's rows store the same word, and whichever
+// form another row reads says the same).
+template <class T, int kDeep>
+__global__ void __launch_bounds__(kIoThreads) kv8_write_kernel(const IoParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (int64_t)blockIdx.x * kIoWarps + (threadIdx.x >> 5);
+  const int64_t nwarps = (int64_t)gridDim.x * kIoWarps;
+  grid_dep_wait();
+  grid_dep_launch();
+  uint32_t e = 0;
+  for (int64_t i0 = warp; i0 < p.n; i0 += kDeep * nwarps) {
+    int64_t slot[kDeep];
+    uint32_t word[kDeep];
+    Part<T> x[kDeep];
+    float2 rope[kDeep];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int64_t i = i0 + d * nwarps;
+      slot[d] = slot_at(p, i, &e);
+      if (slot[d] < 0) continue;
+      word[d] = *reinterpret_cast<volatile uint32_t*>(p.scales + p.div((uint32_t)slot[d]));
+      x[d].load(static_cast<const T*>(p.kv_c) + i * p.kv_c_stride, lane, p.wide);
+      rope[d] = rope_pair(static_cast<const T*>(p.k_pe) + i * p.k_pe_stride + 2 * lane);
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      if (slot[d] < 0) continue;
+      const int k = grown_scale(word[d]), down = -(p.exponent + k);
+      const float mul = pow2(down);
+      uint32_t v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float f[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          f[h] = __uint_as_float(x[d].bits(4 * q + h)) * mul;
+          f[h] = f[h] == f[h] ? f[h] : 0.f;
+        }
+        v[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+      }
+      uint8_t* row = p.cache + slot[d] * p.row_stride;
+      reinterpret_cast<uint4*>(row)[lane] = make_uint4(v[0], v[1], v[2], v[3]);
+      const __nv_bfloat162 r = __floats2bfloat162_rn(rope[d].x * mul, rope[d].y * mul);
+      reinterpret_cast<uint32_t*>(row + kRopeOff)[lane] = *reinterpret_cast<const uint32_t*>(&r);
+      if (lane == 0) {
+        volatile uint32_t* w = p.scales + p.div((uint32_t)slot[d]);
+        if (*w != (uint32_t)k + 1u) *w = (uint32_t)k + 1u;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void put_latents(__nv_bfloat16* dst, const float (&f)[16], bool wide) {
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    v[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  kvq::st_words(dst, wide, v);
+}
+__device__ __forceinline__ void put_latents(float* dst, const float (&f)[16], bool wide) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(f[8 * h + i]);
+    kvq::st_words(dst + 8 * h, wide, v);
+  }
+}
+__device__ __forceinline__ void put_rope(__nv_bfloat16* dst, float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void put_rope(float* dst, float a, float b) {
+  *reinterpret_cast<float2*>(dst) = make_float2(a, b);
+}
+
+template <class T, int kDeep>
+__global__ void __launch_bounds__(kIoThreads) kv8_read_kernel(const IoParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (int64_t)blockIdx.x * kIoWarps + (threadIdx.x >> 5);
+  const int64_t nwarps = (int64_t)gridDim.x * kIoWarps;
+  grid_dep_wait();  // launched before the stream's last kernel has ended
+  grid_dep_launch();
+  uint32_t e = 0;
+  for (int64_t i0 = warp; i0 < p.n; i0 += kDeep * nwarps) {
+    int64_t slot[kDeep];
+    uint4 c[kDeep];
+    uint32_t rope[kDeep], word[kDeep];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      slot[d] = slot_at(p, i0 + d * nwarps, &e);
+      if (slot[d] < 0) continue;
+      const uint8_t* row = p.cache + slot[d] * p.row_stride;
+      c[d] = reinterpret_cast<const uint4*>(row)[lane];
+      rope[d] = reinterpret_cast<const uint32_t*>(row + kRopeOff)[lane];
+      word[d] = p.scales[p.div((uint32_t)slot[d])];
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      if (slot[d] < 0) continue;
+      const int64_t i = i0 + d * nwarps;
+      const float mul = pow2(p.exponent + scale_of(word[d]));
+      const uint32_t v[4] = {c[d].x, c[d].y, c[d].z, c[d].w};
+      float f[16];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v[q >> 1] >> (16 * (q & 1))), __NV_E4M3);
+        const float2 g = __half22float2(__half2(h));
+        f[2 * q] = g.x * mul;
+        f[2 * q + 1] = g.y * mul;
+      }
+      put_latents(static_cast<T*>(p.kv_c) + i * p.kv_c_stride + 16 * lane, f, p.wide);
+      put_rope(static_cast<T*>(p.k_pe) + i * p.k_pe_stride + 2 * lane, __uint_as_float(rope[d] << 16) * mul,
+               __uint_as_float(rope[d] & 0xffff0000u) * mul);
+    }
+  }
+  put_block_err(p.err, e);
+}
+
+mla_status validate_cache(const mla_kv8_cache* c) {
+  if (!c || !c->rows || (reinterpret_cast<uintptr_t>(c->rows) & 31u)) return MLA_ERR_INVALID_ARG;
+  if (c->row_stride < MLA_KV8_ROW_BYTES || (c->row_stride & 31) || c->row_stride > INT32_MAX)
+    return MLA_ERR_INVALID_ARG;
+  if (c->slots < 1 || c->slots > INT32_MAX) return MLA_ERR_INVALID_ARG;
+  if (!c->scales || (reinterpret_cast<uintptr_t>(c->scales) & 3u) || c->block < 1) return MLA_ERR_INVALID_ARG;
+  if (c->exponent < -MLA_KV8_MAX_EXPONENT || c->exponent > MLA_KV8_MAX_EXPONENT) return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Checks shared by both directions; *noop when there is nothing to launch.
+mla_status make_io(const mla_kv8_cache* c, const mla_kvq_rows* r, void* ws, size_t ws_bytes, IoParams* p, bool* noop) {
+  mla_status st = validate_cache(c);
+  if (st != MLA_OK) return st;
+  if (!r || r->n < 0 || r->n > INT32_MAX) return MLA_ERR_INVALID_ARG;
+  if (r->dtype != MLA_BF16 && r->dtype != MLA_FP32) return MLA_ERR_INVALID_ARG;
+  *noop = r->n == 0;
+  if (*noop) return MLA_OK;
+  const int64_t el = r->dtype == MLA_BF16 ? 2 : 4;
+  if (!r->kv_c || !r->k_pe || !r->slots) return MLA_ERR_INVALID_ARG;
+  if (!aligned(r->kv_c, 16) || !aligned(r->k_pe, 16) || !aligned(r->slots, 4)) return MLA_ERR_INVALID_ARG;
+  // row strides beyond 2^31 elements would let row offsets pass 64 bits
+  if (r->kv_c_stride < kDl || r->k_pe_stride < kDr || r->kv_c_stride > INT32_MAX || r->k_pe_stride > INT32_MAX ||
+      (r->kv_c_stride * el) % 16 || (r->k_pe_stride * el) % 16)
+    return MLA_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || ws_bytes < MLA_KV8_WORKSPACE_BYTES) return MLA_ERR_WORKSPACE;
+  p->cache = static_cast<uint8_t*>(c->rows);
+  p->row_stride = c->row_stride;
+  p->slots = c->slots;
+  p->scales = reinterpret_cast<uint32_t*>(c->scales);
+  p->div.set(c->block);
+  p->block = c->block;
+  p->exponent = c->exponent;
+  p->n = r->n;
+  p->slot = r->slots;
+  p->kv_c = r->kv_c;
+  p->k_pe = r->k_pe;
+  p->kv_c_stride = r->kv_c_stride;
+  p->k_pe_stride = r->k_pe_stride;
+  p->wide = aligned(r->kv_c, 32) && (r->kv_c_stride * el) % 32 == 0;
+  p->err = static_cast<uint32_t*>(ws);
+  return MLA_OK;
+}
+
+}  // namespace
+}  // namespace kv8
+}  // namespace mlav
+
+using namespace mlav;
+using namespace mlav::kv8;
+
+extern "C" mla_status mla_kv8_write(const mla_kv8_cache* cache, const mla_kvq_rows* src, void* workspace,
+                                    size_t ws_bytes, mla_stream_t stream) {
+  kv8::IoParams p;
+  bool noop = false;
+  mla_status st = make_io(cache, src, workspace, ws_bytes, &p, &noop);
+  if (st != MLA_OK || noop) return st;
+  int grid = 0;
+  st = io_grid(p.n, 8, &grid);
+  if (st != MLA_OK) return st;
+  const bool bf16 = src->dtype == MLA_BF16;
+  const auto need = bf16 ? kv8_need_kernel<__nv_bfloat16, 2> : kv8_need_kernel<float, 1>;
+  const auto write = bf16 ? kv8_write_kernel<__nv_bfloat16, 2> : kv8_write_kernel<float, 1>;
+  // rows per block of the growing kernel: a few blocks of threads per SM
+  p.per = (int)((p.n + 1023) / 1024);
+  if (p.per < kIoWarps) p.per = kIoWarps;
+  if (p.per > kIoThreads) p.per = kIoThreads;
+  const int64_t growers = (p.n + p.per - 1) / p.per;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_kernel(need, dim3(grid), dim3(kIoThreads), 0, s, true, p) != cudaSuccess ||
+      launch_kernel(kv8_grow_kernel, dim3((unsigned)growers), dim3(kIoThreads), 0, s, true, p) != cudaSuccess ||
+      launch_kernel(write, dim3(grid), dim3(kIoThreads), 0, s, true, p) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+extern "C" mla_status mla_kv8_read(const mla_kv8_cache* cache, const mla_kvq_rows* dst, void* workspace,
+                                   size_t ws_bytes, mla_stream_t stream) {
+  kv8::IoParams p;
+  bool noop = false;
+  mla_status st = make_io(cache, dst, workspace, ws_bytes, &p, &noop);
+  if (st != MLA_OK || noop) return st;
+  int grid = 0;
+  st = io_grid(p.n, 16, &grid);
+  if (st != MLA_OK) return st;
+  const auto kernel = dst->dtype == MLA_BF16 ? kv8_read_kernel<__nv_bfloat16, 2> : kv8_read_kernel<float, 2>;
+  const cudaError_t e = launch_kernel(kernel, dim3(grid), dim3(kIoThreads), 0, reinterpret_cast<cudaStream_t>(stream),
+                                      true, p);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+extern "C" mla_status mla_kv8_check(const void* workspace, mla_stream_t stream, uint32_t* bits) {
+  return mla_kvq_check(workspace, stream, bits);  // the same error words
+}
