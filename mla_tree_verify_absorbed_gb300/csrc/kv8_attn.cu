@@ -12,9 +12,10 @@
 // that each has its own power of two:
 //   queries  q 2^t = hi + lo, t per row.  bf16 has 8 significant bits and a term 4,
 //            so the sum is exact down to 2^-9 of the row's largest element;
-//   weights  w = hi + lo 2^-5 + third 2^-13 of w rounded to f16: w < 2^5 has 11
-//            significant bits, of which the first two terms take 4 or 5 each, and
-//            the smallest code of the third is 2^-22.
+//   weights  w = hi + lo 2^-5 + third 2^-15 of w rounded to f16: of its 11
+//            significant bits the first two terms take 4 or 5 each.  The smallest
+//            code of the third is 2^-24, as f16's.  Its largest, 448 2^-15, cuts off
+//            what is left of weights above 2^3, at most 2^-10 of them.
 // The terms' products are added in fp32: queries' as the scores are read, weights'
 // when O is.  The rope product (bf16) is accumulated on the queries' first term.
 //
@@ -27,8 +28,8 @@
 // group.  With many rows the tensor pipe: per tile 20 MMAs of 32 cycles for S and 16
 // of 48 for O.
 //
-// Shared memory: two stages of 80 KB (128 tokens x 640 bytes), 40 KB of queries, 16
-// KB of weights.  Tensor Memory: O 4 x 96 columns (latent block; row half, term,
+// Shared memory: two stages of 80 KB (128 tokens x 640 bytes; a tile's weights take
+// the place of its rope keys) and 40 KB of queries.  Tensor Memory: O 4 x 96 columns (latent block; row half, term,
 // row), two S tiles of 64 columns (row half, term, row).
 //
 // Work split as in split.cuh; pieces of a row group are merged by a second kernel.
@@ -82,8 +83,10 @@ constexpr int kStages = 2;
 constexpr int kQRows = 2 * kRG;                // (row half, term, row)
 constexpr int kQChunk = kQRows * 128;          // 8 KB
 constexpr int kOffQ = kStages * kStage;
-constexpr int kOffP = kOffQ + kChunks * kQChunk;
-constexpr int kOffCtl = kOffP + kTK * 128;     // weights: a row of 128 bytes per token, 96 used
+constexpr int kOffCtl = kOffQ + kChunks * kQChunk;
+// A tile's weights, a row of 128 bytes per token of which 96 are used, take the
+// place of its rope keys, which only its S product reads.
+constexpr int kOffP = 4 * kChunk;
 
 // Tensor Memory columns
 constexpr uint32_t kColO = 0, kBlockO = 3 * kRG;  // a block of 128 latents
@@ -106,27 +109,31 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 20000000ull;
 
 // Weights are 2^(s + k - max + kWeightShift): a lazy maximum lets them reach 2^kLazy
-// above 2^kWeightShift, and up to 2^5 the third term cannot saturate.
-constexpr float kLazy = 2.f;
-constexpr float kWeightShift = 3.f;
-constexpr float kLoMul = 32.f, kThirdMul = 256.f;  // 2^5, and from there 2^8
+// above 2^kWeightShift, 2^8 in all, below e4m3's 448.  Moving a maximum costs a
+// pass over O, some 4,000 cycles, so it should hold for a whole piece: with 2^2 in
+// place of 2^7, every second tile of 64 nodes x 64 heads x 20,000 tokens moved one of
+// its 16 maxima.
+constexpr float kLazy = 7.f;
+constexpr float kWeightShift = 1.f;
+constexpr float kLoMul = 32.f, kThirdMul = 1024.f;  // 2^5, and from there 2^10
 
 struct alignas(16) Ctl {
   uint64_t full[kStages];      // tile landed (every producer lane's copies, and each warp)
-  uint64_t empty[kStages];     // the products that read it are complete
+  uint64_t empty[kStages][kProducerWarps];  // the products that read a producer warp's tokens are complete
   uint64_t s_full[2];          // S tile in Tensor Memory
   uint64_t q_ready;            // a piece's queries, row constants and masks written (8 row warps)
-  uint64_t m_ready[2];         // a tile's partial maxima written (4 row warps of a half)
+  uint64_t m_ready[2];         // a tile's votes or partial maxima written (4 row warps of a half)
   uint64_t l_ready[2];         // a piece's partial sums written (the same)
-  uint64_t p_ready;            // weights in, O rescaled (8 row warps)
-  uint64_t pv_done;            // a tile's O product complete
+  uint64_t p_ready[2];         // weights in, O rescaled (8 row warps)
+  uint64_t pv_done[2];         // a tile's O product complete
   uint64_t drain;
   uint64_t piece_full[kPieces];   // piece written (scheduler warp)
   uint64_t piece_empty[kPieces];  // read by every warp that follows the pieces
   Piece piece[kPieces];
-  alignas(16) float part_max[2][2][4][kHalfRows];  // tile parity, half, token quadrant, row
+  alignas(16) int vote[2][2][4];         // parity of the exchange, half, token quadrant
+  float part_max[2][2][4][kHalfRows];    // the same, and row
   float part_sum[2][4][kHalfRows];
-  float unit[kRG];             // c_r: score factor of a row
+  alignas(16) float unit[kRG]; // c_r: score factor of a row
   uint64_t mask[kRG];          // what the row's node sees of the tree,
   int depth[kRG];              // and its depth
   int tok_k[kStages][kTK];     // k of the tokens' blocks
@@ -224,7 +231,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Ctl* c, int pw) {
       const uint32_t next_word = word_of(next);
       ent = entry_of(v + 2);
       const uint32_t st = j % kStages;
-      if (!wait_warp(&c->empty[st], ((j / kStages) & 1u) ^ 1u, c)) return false;
+      if (!wait_warp(&c->empty[st][pw], ((j / kStages) & 1u) ^ 1u, c)) return false;
       const uint32_t stage = smem_u32(smem) + st * kStage;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -257,7 +264,7 @@ __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
   const bool leader = elect_one();
   if (p.hold && !wait_warp(&c->drain, 0u, c)) return;
   uint32_t j = 0, seg = 0;
-  const uint32_t q_lo = desc_lo(smem, kOffQ), p_lo = desc_lo(smem, kOffP);
+  const uint32_t q_lo = desc_lo(smem, kOffQ);
   for_pieces(c, [&](const Piece& pc) {
     if (!wait_warp(&c->q_ready, seg & 1u, c)) return false;
     ++seg;
@@ -272,7 +279,7 @@ __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
       fence_proxy_async_smem();  // the tile came by cp.async, without a fence of its writers
       if (leader) {
         const uint32_t d = kColS + (i & 1u) * kQRows, a = desc_lo(smem, st * kStage);
-#pragma unroll 1
+#pragma unroll
         for (uint32_t ck = 0; ck < 4; ++ck) {
 #pragma unroll
           for (uint32_t kk = 0; kk < 4; ++kk)
@@ -299,11 +306,13 @@ __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
       const uint32_t i = j + v, st = i % kStages;
       // the other S buffer is free: the O product of the tile before, whose weights came from it, is issued
       uint64_t t0 = 0;
-      while (!__all_sync(0xffffffffu, mbar_test_wait_cluster(&c->p_ready, i & 1u))) {
+      uint32_t polls = 0;
+      while (!__all_sync(0xffffffffu, mbar_test_wait_cluster(&c->p_ready[i & 1u], (i >> 1) & 1u))) {
         if (s == v + 1 && s < n && __all_sync(0xffffffffu, mbar_test_wait_cluster(full(), full_parity()))) {
           issue_s();
           continue;
         }
+        if (++polls & 63u) continue;
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
         if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&c->abort) || now - t0 > c->wait_ns)) {
@@ -314,15 +323,15 @@ __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
       tc_fence_after();
       if (leader) {
         const uint32_t a = desc_lo(smem, st * kStage);
-#pragma unroll 1
-        for (uint32_t kk = 0; kk < 4; ++kk) {  // 32 tokens
+#pragma unroll
+        for (uint32_t kk = 0; kk < 4; ++kk) {  // the 32 tokens of a producer warp
 #pragma unroll
           for (uint32_t m = 0; m < 4; ++m)
             mma_cta_ss_f8(kColO + m * kBlockO, desc_at(a + ((m * kChunk + kk * 32 * 128) >> 4)),
-                          desc_at(p_lo + ((kk * 32 * 128) >> 4)), io, v | kk);
+                          desc_at(a + ((kOffP + kk * 32 * 128) >> 4)), io, v | kk);
+          mma_cta_commit(&c->empty[st][kk]);
         }
-        mma_cta_commit(&c->empty[st]);
-        mma_cta_commit(&c->pv_done);
+        mma_cta_commit(&c->pv_done[i & 1u]);
       }
       __syncwarp();
     }
@@ -411,6 +420,13 @@ __device__ __forceinline__ void rescale(uint32_t tO, const float (&a)[kHalfRows]
   tmem_wait_st();
 }
 
+// One piece's state of a row warp: per row, two by two, 2^(score + k) is weighted
+// by 2^shift, shift = kWeightShift - the running maximum; sum of the weights.
+struct Rows {
+  uint64_t shift[kHalfRows / 2], sum[kHalfRows / 2];
+};
+constexpr float kNone = 3.402823466e38f;  // shift before the first score: any score beats that maximum
+
 __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
   const int lane = threadIdx.x & 31;
   const int quad = warp & 3, half = warp >> 2;
@@ -419,8 +435,12 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
   const uint32_t tO = lane_off + kColO + half * 3 * kHalfRows;
   const uint32_t tP = smem_u32(smem) + kOffP + token * 128;
   uint32_t j = 0, seg = 0;
-  uint32_t i = 0;  // tiles whose maxima this half has exchanged
+  uint32_t i = 0;  // exchanges among the half's warps
   bool bad = false;
+  auto exchange = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c->m_ready[half]);
+  };
   for_pieces(c, [&](const Piece& pc) {
     const int rows = min(kRG, p.rows - pc.g * kRG);
     const int P = pc.P;
@@ -439,12 +459,11 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
     const bool idle = kHalfRows * half >= rows;
     // positions up to this one are outside some node's window
     const int past_any = p.window > 0 ? max(P - p.window + p.Q - 1, -1) : -1;
-    float unit[kHalfRows], m[kHalfRows], l[kHalfRows];
+    Rows R;
 #pragma unroll
-    for (int r = 0; r < kHalfRows; ++r) {
-      unit[r] = c->unit[kHalfRows * half + r];
-      m[r] = -INFINITY;
-      l[r] = 0.f;
+    for (int r = 0; r < kHalfRows / 2; ++r) {
+      R.shift[r] = pair(kNone, kNone);
+      R.sum[r] = 0;
     }
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
@@ -452,122 +471,142 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
       if (!wait_warp(&c->s_full[j & 1u], par, c)) return false;
       if (idle) {
         // every barrier's phases count on
-        if (j > 0 && !wait_warp(&c->pv_done, (j - 1) & 1u, c)) return false;
-        if (lane == 0) mbar_arrive(&c->p_ready);
+        if (lane == 0) mbar_arrive(&c->p_ready[j & 1u]);
         continue;
       }
       if (!wait_warp(&c->full[st], par, c)) return false;  // has passed: the producers' scales are visible
       tc_fence_after();
       const int k = c->tok_k[st][token];
-      const float kf = (float)k, kmul = pow2(k), kinv = pow2(-k);
-      float y[kHalfRows];
+      const uint64_t k2 = pair((float)k, (float)k), mul2 = pair(pow2(k), pow2(k)), inv2 = pair(pow2(-k), pow2(-k));
+      uint64_t y[kHalfRows / 2];  // score + k, base 2
       {
         uint32_t u[32];
         tmem_ld32_sync(lane_off + kColS + (j & 1u) * kQRows + 32 * half, u);
+        const ulonglong2* unit = reinterpret_cast<const ulonglong2*>(c->unit + kHalfRows * half);
 #pragma unroll
-        for (int r = 0; r < kHalfRows; ++r)
-          y[r] = fmaf((__uint_as_float(u[r]) + __uint_as_float(u[kHalfRows + r])) * kmul, unit[r], kf);
+        for (int q = 0; q < kHalfRows / 4; ++q) {
+          const ulonglong2 f = unit[q];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = 2 * q + h;
+            const uint64_t v = add_f32x2(pair(u[2 * r], u[2 * r + 1]), pair(u[16 + 2 * r], u[17 + 2 * r]));
+            y[r] = fma_f32x2(mul_f32x2(v, mul2), h ? f.y : f.x, k2);
+          }
+        }
       }
       const int pos0 = pc.tile(t) * kTK;
       if (pos0 > P - kTK || pos0 <= past_any) {
         const int pos = pos0 + token, rel = pos - P;
 #pragma unroll
-        for (int r = 0; r < kHalfRows; ++r) {
-          const int rr = kHalfRows * half + r;
-          bool see;
-          if (rel >= 0)
-            see = rel < 64 && ((c->mask[rr] >> rel) & 1u);
-          else
-            see = p.window == 0 || pos < p.sinks || pos > P - p.window + c->depth[rr];
-          if (!see) y[r] = -INFINITY;
+        for (int r = 0; r < kHalfRows / 2; ++r) {
+          bool see[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int rr = kHalfRows * half + 2 * r + h;
+            if (rel >= 0) see[h] = rel < 64 && ((c->mask[rr] >> rel) & 1u);
+            else see[h] = p.window == 0 || pos < p.sinks || pos > P - p.window + c->depth[rr];
+          }
+          y[r] = pair(see[0] ? lo_f32(y[r]) : -INFINITY, see[1] ? hi_f32(y[r]) : -INFINITY);
         }
       }
-      // the tile's maxima: of the warp's tokens, then of the half's four warps
-      float4* pm = reinterpret_cast<float4*>(c->part_max[i & 1u][half][quad]);
+      // A maximum moves only when the tile beats it by 2^kLazy, for the four warps of
+      // the half together; until they have all voted the weights are taken with the
+      // maximum as it is.
+      uint32_t hi[4], lo[4], third[4];
+      uint64_t sum[kHalfRows / 2];
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        uint64_t x[kHalfRows / 2];
+        float top = -INFINITY;
 #pragma unroll
-      for (int q = 0; q < kHalfRows / 4; ++q) {
-        const float4 v = make_float4(warp_max(y[4 * q]), warp_max(y[4 * q + 1]), warp_max(y[4 * q + 2]),
-                                     warp_max(y[4 * q + 3]));
-        if (lane == 0) pm[q] = v;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->m_ready[half]);
-      if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
-      float nm[kHalfRows];
-      bool move = false;
-#pragma unroll
-      for (int q = 0; q < kHalfRows / 4; ++q) {
-        float4 v = reinterpret_cast<const float4*>(c->part_max[i & 1u][half][0])[q];
-#pragma unroll
-        for (int o = 1; o < 4; ++o) {
-          const float4 w = reinterpret_cast<const float4*>(c->part_max[i & 1u][half][o])[q];
-          v = make_float4(fmaxf(v.x, w.x), fmaxf(v.y, w.y), fmaxf(v.z, w.z), fmaxf(v.w, w.w));
+        for (int r = 0; r < kHalfRows / 2; ++r) {
+          x[r] = add_f32x2(y[r], R.shift[r]);
+          top = fmaxf(top, fmaxf(lo_f32(x[r]), hi_f32(x[r])));
         }
-        nm[4 * q] = v.x;
-        nm[4 * q + 1] = v.y;
-        nm[4 * q + 2] = v.z;
-        nm[4 * q + 3] = v.w;
-      }
-      ++i;
-      // a maximum moves only when the tile beats it by 2^kLazy; the same in every lane
+        const bool ahead = !again && t == pc.t0;  // no maximum yet
+        if (!again && !ahead) {
+          const bool move = __any_sync(0xffffffffu, top > kWeightShift + kLazy);
+          if (lane == 0) c->vote[i & 1u][half][quad] = move;
+          exchange();
+        }
+        if (!ahead) {
+          // weights, and their three terms
 #pragma unroll
-      for (int r = 0; r < kHalfRows; ++r) move |= nm[r] > m[r] + kLazy;
-      if (move) {
+          for (int q = 0; q < kHalfRows / 2; ++q) {
+            const float e0 = ex2_approx(lo_f32(x[q])), e1 = ex2_approx(hi_f32(x[q]));
+            sum[q] = fma_f32x2(pair(e0, e1), inv2, R.sum[q]);
+            const uint32_t w = pack_f16(e0, e1);
+            const uint32_t h = to_e4m3(w);
+            const uint32_t r1 = kvq::hmul2_f16(sub_f16(w, from_e4m3(h)), 0x50005000u);  // * 32; exact, as what follows
+            const uint32_t b = to_e4m3(r1);
+            const uint32_t r2 = kvq::hmul2_f16(sub_f16(r1, from_e4m3(b)), 0x64006400u);  // * 1024
+            const uint32_t d = to_e4m3(r2);
+            if (q & 1) {
+              hi[q >> 1] |= h << 16;
+              lo[q >> 1] |= b << 16;
+              third[q >> 1] |= d << 16;
+            } else {
+              hi[q >> 1] = h;
+              lo[q >> 1] = b;
+              third[q >> 1] = d;
+            }
+          }
+        }
+        if (again) break;
+        if (!ahead) {
+          if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
+          const int4 vote = *reinterpret_cast<const int4*>(c->vote[i & 1u][half]);
+          ++i;
+          if (!(vote.x | vote.y | vote.z | vote.w)) break;
+        }
+        // the tile's maxima: of the warp's tokens, then of the half's four warps
+        float2* pm = reinterpret_cast<float2*>(c->part_max[i & 1u][half][quad]);
+#pragma unroll
+        for (int r = 0; r < kHalfRows / 2; ++r) {
+          const float2 v = make_float2(warp_max(lo_f32(y[r])), warp_max(hi_f32(y[r])));
+          if (lane == 0) pm[r] = v;
+        }
+        exchange();
+        if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
         float a[kHalfRows];
 #pragma unroll
         for (int r = 0; r < kHalfRows; ++r) {
-          const float mn = nm[r] > m[r] + kLazy ? nm[r] : m[r];
-          a[r] = mn == m[r] ? 1.f : exp2f(m[r] - mn);  // 0 when m was -inf
-          l[r] *= a[r];
-          m[r] = mn;
+          const float (&m4)[4][kHalfRows] = c->part_max[i & 1u][half];
+          const float m = fmaxf(fmaxf(m4[0][r], m4[1][r]), fmaxf(m4[2][r], m4[3][r]));
+          const float was = r & 1 ? hi_f32(R.shift[r >> 1]) : lo_f32(R.shift[r >> 1]);
+          const bool moves = m + was > kWeightShift + kLazy;
+          const float now = moves ? kWeightShift - m : was;
+          a[r] = moves ? (was == kNone ? 0.f : exp2f(now - was)) : 1.f;
+          R.shift[r >> 1] = r & 1 ? pair(lo_f32(R.shift[r >> 1]), now) : pair(now, hi_f32(R.shift[r >> 1]));
         }
+        ++i;
+#pragma unroll
+        for (int r = 0; r < kHalfRows / 2; ++r) R.sum[r] = mul_f32x2(R.sum[r], pair(a[2 * r], a[2 * r + 1]));
         if (t > pc.t0) {
-          if (!wait_warp(&c->pv_done, (j - 1) & 1u, c)) return false;
+          if (!wait_warp(&c->pv_done[(j - 1) & 1u], ((j - 1) >> 1) & 1u, c)) return false;
           tc_fence_after();
           rescale(tO, a);
         }
       }
-      // weights, and their three terms
-      uint32_t hi[4], lo[4], third[4];
 #pragma unroll
-      for (int q = 0; q < kHalfRows / 2; ++q) {
-        float e[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = 2 * q + h;
-          e[h] = ex2_approx(y[r] + (m[r] == -INFINITY ? 0.f : kWeightShift - m[r]));
-          l[r] = fmaf(e[h], kinv, l[r]);
-        }
-        const uint32_t w = pack_f16(e[0], e[1]);
-        const uint32_t h = to_e4m3(w);
-        const uint32_t r1 = kvq::hmul2_f16(sub_f16(w, from_e4m3(h)), 0x50005000u);  // * 32; exact, as what follows
-        const uint32_t b = to_e4m3(r1);
-        const uint32_t r2 = kvq::hmul2_f16(sub_f16(r1, from_e4m3(b)), 0x5c005c00u);  // * 256
-        const uint32_t d = to_e4m3(r2);
-        if (q & 1) {
-          hi[q >> 1] |= h << 16;
-          lo[q >> 1] |= b << 16;
-          third[q >> 1] |= d << 16;
-        } else {
-          hi[q >> 1] = h;
-          lo[q >> 1] = b;
-          third[q >> 1] = d;
-        }
-      }
-      if (j > 0 && !wait_warp(&c->pv_done, (j - 1) & 1u, c)) return false;  // the weights' place is free
-      st_shared_v4(tP + (((3 * half) ^ (token & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
-      st_shared_v4(tP + (((3 * half + 1) ^ (token & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
-      st_shared_v4(tP + (((3 * half + 2) ^ (token & 7)) << 4), third[0], third[1], third[2], third[3]);
+      for (int r = 0; r < kHalfRows / 2; ++r) R.sum[r] = sum[r];
+      const uint32_t at = tP + st * kStage;
+      st_shared_v4(at + (((3 * half) ^ (token & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(at + (((3 * half + 1) ^ (token & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+      st_shared_v4(at + (((3 * half + 2) ^ (token & 7)) << 4), third[0], third[1], third[2], third[3]);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c->p_ready);
+      if (lane == 0) mbar_arrive(&c->p_ready[j & 1u]);
     }
 
     // The piece's sums over all tokens, then O: the warp's lanes hold latents
     // 32 quad + lane of each block of 128.
     const uint32_t phase = seg & 1u;
     ++seg;
+    float l[kHalfRows];
+#pragma unroll
+    for (int r = 0; r < kHalfRows; ++r) l[r] = r & 1 ? hi_f32(R.sum[r >> 1]) : lo_f32(R.sum[r >> 1]);
     if (!idle) {
 #pragma unroll
       for (int r = 0; r < kHalfRows; ++r) {
@@ -581,7 +620,7 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
     } else if (lane == 0) {
       mbar_arrive(&c->l_ready[half]);
     }
-    if (!wait_warp(&c->pv_done, (j - 1) & 1u, c)) return false;
+    if (!wait_warp(&c->pv_done[(j - 1) & 1u], ((j - 1) >> 1) & 1u, c)) return false;
     if (idle) return true;
     tc_fence_after();
     float inv[kHalfRows];
@@ -618,7 +657,7 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
 #pragma unroll
       for (int r = 0; r < kHalfRows; ++r)
         if (lane == r) {
-          ml = m[r];
+          ml = kWeightShift - (r & 1 ? hi_f32(R.shift[r >> 1]) : lo_f32(R.shift[r >> 1]));
           ll = l[r];
         }
       const float lse =
@@ -640,16 +679,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p) {
   if (threadIdx.x == 0) {
     for (int q = 0; q < kStages; ++q) {
       mbar_init(&c->full[q], 33 * kProducerWarps);
-      mbar_init(&c->empty[q], 1);
+      for (int w = 0; w < kProducerWarps; ++w) mbar_init(&c->empty[q][w], 1);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&c->s_full[q], 1);
+      mbar_init(&c->p_ready[q], kRowWarps);
+      mbar_init(&c->pv_done[q], 1);
       mbar_init(&c->m_ready[q], 4);
       mbar_init(&c->l_ready[q], 4);
     }
     mbar_init(&c->q_ready, kRowWarps);
-    mbar_init(&c->p_ready, kRowWarps);
-    mbar_init(&c->pv_done, 1);
     mbar_init(&c->drain, 1);
     for (int q = 0; q < kPieces; ++q) {
       mbar_init(&c->piece_full[q], 1);
