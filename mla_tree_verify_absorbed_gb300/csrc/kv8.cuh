@@ -48,6 +48,7 @@ struct Divider {
 struct Params : kvq::Params {
   const int32_t* scales;
   Divider block;  // slot -> block
+  int box;        // tokens that lie in a row within a page, at most 32; 0: fewer than 8
 };
 
 mla_status validate_cache(const mla_kv8_cache* c);

@@ -40,6 +40,7 @@
 //
 // Every wait is bounded (2 s, less in the self-test); on timeout the roles stop,
 // drain what they issued, free their Tensor Memory and report MLA_DEVERR_TIMEOUT.
+#include <cuda.h>
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -49,6 +50,7 @@
 #include "kv8.cuh"
 #include "sm100.cuh"
 #include "split.cuh"
+#include "tensor_map.cuh"
 
 namespace mlav {
 namespace kv8 {
@@ -93,6 +95,14 @@ constexpr uint32_t kColO = 0, kBlockO = 3 * kRG;  // a block of 128 latents
 constexpr uint32_t kColS = 4 * kBlockO;
 static_assert(kColS + 2 * kQRows <= kTmemCols, "Tensor Memory columns");
 
+// Chunks that come by cp.async where rows come one by one; the others are gathered.
+constexpr int kCopied = 3;
+
+// Tensor maps of the pool: single rows, and boxes of Params::box rows.
+struct CacheMaps {
+  CUtensorMap row, box;
+};
+
 // operand descriptors (smem_desc): all have 128-byte rows in groups of 8, 1 KB apart
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (kLayoutSw128 << 29);
 constexpr uint32_t kDescLo = ((uint32_t)kChunk >> 4) << 16;  // no operand reaches beyond one row of 128 bytes
@@ -118,8 +128,8 @@ constexpr float kWeightShift = 1.f;
 constexpr float kLoMul = 32.f, kThirdMul = 1024.f;  // 2^5, and from there 2^10
 
 struct alignas(16) Ctl {
-  uint64_t full[kStages];      // tile landed (every producer lane's copies, and each warp)
-  uint64_t empty[kStages][kProducerWarps];  // the products that read a producer warp's tokens are complete
+  uint64_t full[kStages];      // tile landed (each producer warp's copies)
+  uint64_t empty[kStages];     // the products that read it are complete
   uint64_t s_full[2];          // S tile in Tensor Memory
   uint64_t q_ready;            // a piece's queries, row constants and masks written (8 row warps)
   uint64_t m_ready[2];         // a tile's votes or partial maxima written (4 row warps of a half)
@@ -136,6 +146,7 @@ struct alignas(16) Ctl {
   alignas(16) float unit[kRG]; // c_r: score factor of a row
   uint64_t mask[kRG];          // what the row's node sees of the tree,
   int depth[kRG];              // and its depth
+  float shift[kRowWarps][kHalfRows];  // each row warp's copy of Rows::shift, a row to a lane
   int tok_k[kStages][kTK];     // k of the tokens' blocks
   int64_t scan[kThreads / 32];
   int64_t left;                // units of this CTA's interval
@@ -198,11 +209,15 @@ __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
 // ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
-// Warp pw fetches tokens 32 pw .. of every tile: a lane looks up a token, and for
-// each four tokens eight lanes copy 128 bytes of one.
-__device__ void producer(const Params& p, uint8_t* smem, Ctl* c, int pw) {
+// Warp pw fetches tokens 32 pw .. of every tile: each lane looks up a token, a tile
+// ahead.  Where pages hold at least 8 tokens in a row and the tile is seen whole, the
+// rows of up to 32 tokens come by one tensor copy per chunk (128 bytes of a row).  Else they come one by
+// one, by both ways that there are, since neither alone fetches fast enough: a
+// gather of four rows takes the copy engine 30 cycles (17 bytes per cycle), and
+// cp.async of 16 bytes a lane reach 20 to 30 bytes per cycle, whatever the depth,
+// where the tensor pipe takes 40.
+__device__ void producer(const Params& p, const CacheMaps& maps, uint8_t* smem, Ctl* c, int pw) {
   const int lane = threadIdx.x & 31;
-  const int r7 = lane & 7, ch = lane >> 3;
   uint32_t err = 0, j = 0;
   for_pieces(c, [&](const Piece& pc) {
     const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
@@ -214,7 +229,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Ctl* c, int pw) {
       const uint32_t pos = pos_of(v);
       return seen(v, pos) ? __ldg(idx + kvq::page_of(p, pos)) : -1;
     };
-    // -1: not read
+    // -1: a row outside the pool, which reads zeros
     auto slot_of = [&](int32_t e, int v) -> int32_t {
       const uint32_t pos = pos_of(v);
       const int64_t s = (int64_t)e * p.page_size + (pos - kvq::page_of(p, pos) * (uint32_t)p.page_size);
@@ -230,22 +245,45 @@ __device__ void producer(const Params& p, uint8_t* smem, Ctl* c, int pw) {
       const int32_t next = slot_of(ent, v + 1);
       const uint32_t next_word = word_of(next);
       ent = entry_of(v + 2);
-      const uint32_t st = j % kStages;
-      if (!wait_warp(&c->empty[st][pw], ((j / kStages) & 1u) ^ 1u, c)) return false;
-      const uint32_t stage = smem_u32(smem) + st * kStage;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int token = 4 * i + ch, row = 32 * pw + token;
-        const int32_t s = __shfl_sync(0xffffffffu, slot, token);
-        const uint8_t* src = p.cache + (uint64_t)(uint32_t)max(s, 0) * (uint32_t)p.row_stride + 16 * r7;
-        const uint32_t dst = stage + row * 128 + ((r7 ^ (row & 7)) << 4), bytes = s >= 0 ? 16u : 0u;
-#pragma unroll
-        for (int ck = 0; ck < kChunks; ++ck) cp_async_16_zfill(dst + ck * kChunk, src + 128 * ck, bytes);
-      }
-      cp_async_mbar_arrive(&c->full[st]);  // when they have landed
+      const uint32_t st = j % kStages, par = ((j / kStages) & 1u) ^ 1u;
+      uint8_t* to = smem + st * kStage + 32 * pw * 128;
+      const uint32_t dst = smem_u32(to);
+      const bool boxes = p.box > 0 && __all_sync(0xffffffffu, seen(v, pos_of(v)));
+      const int32_t s1 = __shfl_down_sync(0xffffffffu, slot, 1), s2 = __shfl_down_sync(0xffffffffu, slot, 2),
+                    s3 = __shfl_down_sync(0xffffffffu, slot, 3);
+      if (!wait_warp(&c->empty[st], par, c)) return false;
+      uint64_t* full = &c->full[st];
       c->tok_k[st][32 * pw + lane] = scale_of(word);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c->full[st]);
+      if (boxes) {
+        if (lane == 0) mbar_arrive_expect_tx(full, kChunks * 32 * 128);
+        __syncwarp();
+        if ((lane & (p.box - 1)) == 0) {
+#pragma unroll
+          for (int ck = 0; ck < kChunks; ++ck)
+            tensor_copy_2d(to + ck * kChunk + lane * 128, &maps.box, 128 * ck, slot, full);
+        }
+      } else {
+        const int r7 = lane & 7, ch = lane >> 3;
+        if ((lane & 3) == 0) {
+#pragma unroll
+          for (int ck = kCopied; ck < kChunks; ++ck)
+            tensor_gather4(dst + ck * kChunk + lane * 128, &maps.row, 128 * ck, slot, s1, s2, s3, full);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int token = 4 * i + ch;
+          const int32_t s = __shfl_sync(0xffffffffu, slot, token);
+          const uint8_t* src = p.cache + (uint64_t)(uint32_t)max(s, 0) * (uint32_t)p.row_stride + 16 * r7;
+          const uint32_t at = dst + token * 128 + ((r7 ^ (token & 7)) << 4), bytes = s >= 0 ? 16u : 0u;
+#pragma unroll
+          for (int ck = 0; ck < kCopied; ++ck) cp_async_16_zfill(at + ck * kChunk, src + 128 * ck, bytes);
+        }
+        cp_async_mbar_hold(full);  // until they have landed
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(full, (kChunks - kCopied) * 32 * 128);
+      }
       slot = next;
       word = next_word;
     }
@@ -258,8 +296,10 @@ __device__ void producer(const Params& p, uint8_t* smem, Ctl* c, int pw) {
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
-// One warp: S of a tile is issued as soon as the tile is there, ahead of the O
-// product of the tile before when that has to wait for its weights.
+// One warp, which issues what can be issued next: the O product of a tile when its
+// weights are there, else the next S product when its tile is.  (S chunk by chunk as
+// they land, and O freeing them one by one, took longer: each test and each branch
+// into the issuing lane costs some 300 cycles.)
 __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
   const bool leader = elect_one();
   if (p.hold && !wait_warp(&c->drain, 0u, c)) return;
@@ -271,71 +311,66 @@ __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
     const int halves = p.rows - pc.g * kRG > kHalfRows ? 2 : 1;
     const uint32_t is8 = idesc_e4m3_f32(kTK, 32 * halves, 0, 0), is16 = idesc_bf16_f32(kTK, 32 * halves, 0, 0);
     const uint32_t io = idesc_e4m3_f32(128, 48 * halves, 1, 1);
-    const uint32_t n = (uint32_t)(pc.t1 - pc.t0);
-    uint32_t s = 0;  // S products issued
-    auto issue_s = [&]() {
-      const uint32_t i = j + s, st = i % kStages;
-      tc_fence_after();
-      fence_proxy_async_smem();  // the tile came by cp.async, without a fence of its writers
-      if (leader) {
-        const uint32_t d = kColS + (i & 1u) * kQRows, a = desc_lo(smem, st * kStage);
+    const uint32_t end = j + (uint32_t)(pc.t1 - pc.t0), first = j;
+    uint32_t s = j;  // the next S product
+    auto test = [&](uint64_t* bar, uint32_t n) {  // tile n's phase of a barrier that every second tile uses
+      return __all_sync(0xffffffffu, mbar_test_wait(bar, (n >> 1) & 1u));
+    };
+    uint64_t t0 = 0;
+    uint32_t polls = 0;
+    while (j < end) {
+      if (s > j && test(&c->p_ready[j & 1u], j)) {
+        const uint32_t st = j % kStages;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t a = desc_lo(smem, st * kStage);
 #pragma unroll
-        for (uint32_t ck = 0; ck < 4; ++ck) {
+          for (uint32_t kk = 0; kk < 4; ++kk) {  // 32 tokens
+#pragma unroll
+            for (uint32_t m = 0; m < 4; ++m)
+              mma_cta_ss_f8(kColO + m * kBlockO, desc_at(a + ((m * kChunk + kk * 32 * 128) >> 4)),
+                            desc_at(a + ((kOffP + kk * 32 * 128) >> 4)), io, (j - first) | kk);
+          }
+          mma_cta_commit(&c->empty[st]);
+          mma_cta_commit(&c->pv_done[st]);
+        }
+        __syncwarp();
+        ++j;
+        polls = 0;
+        continue;
+      }
+      // The S tile before the last has been read when its weights are there.
+      if (s < end && s <= j + 1 && test(&c->full[s % kStages], s)) {
+        tc_fence_after();
+        fence_proxy_async_smem();  // parts may come by cp.async, without a fence of their writers
+        if (leader) {
+          const uint32_t d = kColS + (s & 1u) * kQRows, a = desc_lo(smem, (s % kStages) * kStage);
+#pragma unroll
+          for (uint32_t ck = 0; ck < 4; ++ck) {
+#pragma unroll
+            for (uint32_t kk = 0; kk < 4; ++kk)
+              mma_cta_ss_f8(d, desc_at(a + ((ck * kChunk + kk * 32) >> 4)), desc_at(q_lo + ((ck * kQChunk + kk * 32) >> 4)),
+                            is8, ck | kk);
+          }
 #pragma unroll
           for (uint32_t kk = 0; kk < 4; ++kk)
-            mma_cta_ss_f8(d, desc_at(a + ((ck * kChunk + kk * 32) >> 4)), desc_at(q_lo + ((ck * kQChunk + kk * 32) >> 4)),
-                          is8, ck | kk);
+            mma_cta_ss(d, desc_at(a + ((4 * kChunk + kk * 32) >> 4)), desc_at(q_lo + ((4 * kQChunk + kk * 32) >> 4)),
+                       is16, 1);
+          mma_cta_commit(&c->s_full[s & 1u]);
         }
-#pragma unroll
-        for (uint32_t kk = 0; kk < 4; ++kk)
-          mma_cta_ss(d, desc_at(a + ((4 * kChunk + kk * 32) >> 4)), desc_at(q_lo + ((4 * kQChunk + kk * 32) >> 4)), is16,
-                     1);
-        mma_cta_commit(&c->s_full[i & 1u]);
+        __syncwarp();
+        ++s;
+        polls = 0;
+        continue;
       }
-      __syncwarp();
-      ++s;
-    };
-    auto full = [&]() { return &c->full[(j + s) % kStages]; };
-    auto full_parity = [&]() { return ((j + s) / kStages) & 1u; };
-#pragma unroll 1
-    for (uint32_t v = 0; v < n; ++v) {
-      if (s == v) {
-        if (!wait_warp(full(), full_parity(), c)) return false;
-        issue_s();
+      if (++polls & 63u) continue;
+      const uint64_t now = globaltimer_ns();
+      if (polls == 64u) t0 = now;
+      if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&c->abort) || now - t0 > c->wait_ns)) {
+        c->abort = 1;
+        return false;
       }
-      const uint32_t i = j + v, st = i % kStages;
-      // the other S buffer is free: the O product of the tile before, whose weights came from it, is issued
-      uint64_t t0 = 0;
-      uint32_t polls = 0;
-      while (!__all_sync(0xffffffffu, mbar_test_wait_cluster(&c->p_ready[i & 1u], (i >> 1) & 1u))) {
-        if (s == v + 1 && s < n && __all_sync(0xffffffffu, mbar_test_wait_cluster(full(), full_parity()))) {
-          issue_s();
-          continue;
-        }
-        if (++polls & 63u) continue;
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&c->abort) || now - t0 > c->wait_ns)) {
-          c->abort = 1;
-          return false;
-        }
-      }
-      tc_fence_after();
-      if (leader) {
-        const uint32_t a = desc_lo(smem, st * kStage);
-#pragma unroll
-        for (uint32_t kk = 0; kk < 4; ++kk) {  // the 32 tokens of a producer warp
-#pragma unroll
-          for (uint32_t m = 0; m < 4; ++m)
-            mma_cta_ss_f8(kColO + m * kBlockO, desc_at(a + ((m * kChunk + kk * 32 * 128) >> 4)),
-                          desc_at(a + ((kOffP + kk * 32 * 128) >> 4)), io, v | kk);
-          mma_cta_commit(&c->empty[st][kk]);
-        }
-        mma_cta_commit(&c->pv_done[i & 1u]);
-      }
-      __syncwarp();
     }
-    j += n;
     return true;
   });
   __syncwarp();
@@ -356,20 +391,28 @@ __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
 __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ctl* c, const Piece& pc, int warp) {
   const int lane = threadIdx.x & 31;
   const int rows = min(kRG, p.rows - pc.g * kRG), padded = rows > kHalfRows ? kRG : kHalfRows;
-#pragma unroll 1
-  for (int r = 4 * warp; r < min(4 * warp + 4, padded); ++r) {
-    uint32_t w[8] = {}, pe = 0;
+  uint4 all[4][2] = {};
+  uint32_t rope_all[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * warp + i;
     if (r < rows) {
       const int64_t row = (int64_t)pc.b * p.rows + pc.g * kRG + r;
       const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q_lat) + row * (2 * kDl)) + 2 * lane;
-      const uint4 a = __ldg(q), b = __ldg(q + 1);
-      pe = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.q_pe) + row * (2 * kDr)) + lane);
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+      all[i][0] = __ldg(q);
+      all[i][1] = __ldg(q + 1);
+      rope_all[i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.q_pe) + row * (2 * kDr)) + lane);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * warp + i;
+    if (r >= padded) break;
+    const uint4 a = all[i][0], b = all[i][1];
+    const uint32_t pe = rope_all[i], w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t big = max(pe & 0x7fffu, (pe >> 16) & 0x7fffu);  // magnitudes compare as their bits
 #pragma unroll
-    for (int i = 0; i < 8; ++i) big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    for (int q = 0; q < 8; ++q) big = max(big, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
     big = __reduce_max_sync(0xffffffffu, big);
     const bool finite = big < 0x7f80u;
     // the largest magnitude goes to [2^7, 2^8), or to [2^8, 448] where its fraction allows it
@@ -377,19 +420,19 @@ __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ct
     const float mul = pow2(t);
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hi[i] = lo[i] = 0;
+    for (int q = 0; q < 4; ++q) {
+      hi[q] = lo[q] = 0;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint32_t x = w[2 * i + k];
+        const uint32_t x = w[2 * q + k];
         const float f0 = __uint_as_float(x << 16) * mul, f1 = __uint_as_float(x & 0xffff0000u) * mul;
         const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1), __NV_SATFINITE, __NV_E4M3);
         const uint32_t hf = from_e4m3(h);
         const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
         const uint32_t l =
             __nv_cvt_float2_to_fp8x2(make_float2(f0 - back.x, f1 - back.y), __NV_SATFINITE, __NV_E4M3);
-        hi[i] |= (finite ? h : 0x7f7fu) << (16 * k);
-        lo[i] |= l << (16 * k);
+        hi[q] |= (finite ? h : 0x7f7fu) << (16 * k);
+        lo[q] |= l << (16 * k);
       }
     }
     const __nv_bfloat162 pm =
@@ -406,17 +449,16 @@ __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ct
   }
 }
 
-// Multiplies the half's columns of O by a factor per row, in the warp's lanes.
-__device__ __forceinline__ void rescale(uint32_t tO, const float (&a)[kHalfRows]) {
-#pragma unroll 1
-  for (int q = 0; q < 12; ++q) {  // block, term
-    const uint32_t at = tO + (q / 3) * kBlockO + (q % 3) * kHalfRows;
-    uint32_t u[16];
-    tmem_ld16_sync(at, u);
+// Multiplies a row's columns of O, in the warp's lanes, by a factor.
+__device__ __forceinline__ void rescale_row(uint32_t tO, float a) {
+  uint32_t u[12];
 #pragma unroll
-    for (int r = 0; r < kHalfRows; ++r) u[r] = __float_as_uint(__uint_as_float(u[r]) * a[r]);
-    tmem_st_32x32b_x16(at, u);
-  }
+  for (int q = 0; q < 12; ++q)  // block, term
+    tmem_ld1(tO + (q / 3) * kBlockO + (q % 3) * kHalfRows, u[q]);
+  tmem_wait_ld(u);
+#pragma unroll
+  for (int q = 0; q < 12; ++q)
+    tmem_st1(tO + (q / 3) * kBlockO + (q % 3) * kHalfRows, __float_as_uint(__uint_as_float(u[q]) * a));
   tmem_wait_st();
 }
 
@@ -465,6 +507,7 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
       R.shift[r] = pair(kNone, kNone);
       R.sum[r] = 0;
     }
+    if (lane < kHalfRows) c->shift[warp][lane] = kNone;
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
       const uint32_t st = j % kStages, par = (j >> 1) & 1u;
@@ -512,54 +555,43 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
       // A maximum moves only when the tile beats it by 2^kLazy, for the four warps of
       // the half together; until they have all voted the weights are taken with the
       // maximum as it is.
-      uint32_t hi[4], lo[4], third[4];
-      uint64_t sum[kHalfRows / 2];
-#pragma unroll 1
-      for (bool again = false;; again = true) {
-        uint64_t x[kHalfRows / 2];
+      uint32_t hi[4] = {}, lo[4] = {}, third[4] = {};
+      uint64_t x[kHalfRows / 2] = {}, sum[kHalfRows / 2];
+      auto weigh = [&](int q) {  // two rows' weights, and their three terms
+        const float e0 = ex2_approx(lo_f32(x[q])), e1 = ex2_approx(hi_f32(x[q]));
+        sum[q] = fma_f32x2(pair(e0, e1), inv2, R.sum[q]);
+        const uint32_t w = pack_f16(e0, e1);
+        const uint32_t h = to_e4m3(w);
+        const uint32_t r1 = kvq::hmul2_f16(sub_f16(w, from_e4m3(h)), 0x50005000u);  // * 32; exact, as what follows
+        const uint32_t b = to_e4m3(r1);
+        const uint32_t r2 = kvq::hmul2_f16(sub_f16(r1, from_e4m3(b)), 0x64006400u);  // * 1024
+        const uint32_t d = to_e4m3(r2);
+        const uint32_t place = q & 1 ? 0x5410u : 0x3254u;  // the pair's half of the word, the other as it is
+        hi[q >> 1] = __byte_perm(hi[q >> 1], h, place);
+        lo[q >> 1] = __byte_perm(lo[q >> 1], b, place);
+        third[q >> 1] = __byte_perm(third[q >> 1], d, place);
+      };
+      uint32_t moved = 0xffffffffu;  // rows; in a piece's first tile all, from no maximum at all
+      bool move = t == pc.t0;
+      if (!move) {
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < kHalfRows / 2; ++r) {
           x[r] = add_f32x2(y[r], R.shift[r]);
           top = fmaxf(top, fmaxf(lo_f32(x[r]), hi_f32(x[r])));
         }
-        const bool ahead = !again && t == pc.t0;  // no maximum yet
-        if (!again && !ahead) {
-          const bool move = __any_sync(0xffffffffu, top > kWeightShift + kLazy);
-          if (lane == 0) c->vote[i & 1u][half][quad] = move;
-          exchange();
-        }
-        if (!ahead) {
-          // weights, and their three terms
+        move = __any_sync(0xffffffffu, top > kWeightShift + kLazy);
+        if (lane == 0) c->vote[i & 1u][half][quad] = move;
+        exchange();
 #pragma unroll
-          for (int q = 0; q < kHalfRows / 2; ++q) {
-            const float e0 = ex2_approx(lo_f32(x[q])), e1 = ex2_approx(hi_f32(x[q]));
-            sum[q] = fma_f32x2(pair(e0, e1), inv2, R.sum[q]);
-            const uint32_t w = pack_f16(e0, e1);
-            const uint32_t h = to_e4m3(w);
-            const uint32_t r1 = kvq::hmul2_f16(sub_f16(w, from_e4m3(h)), 0x50005000u);  // * 32; exact, as what follows
-            const uint32_t b = to_e4m3(r1);
-            const uint32_t r2 = kvq::hmul2_f16(sub_f16(r1, from_e4m3(b)), 0x64006400u);  // * 1024
-            const uint32_t d = to_e4m3(r2);
-            if (q & 1) {
-              hi[q >> 1] |= h << 16;
-              lo[q >> 1] |= b << 16;
-              third[q >> 1] |= d << 16;
-            } else {
-              hi[q >> 1] = h;
-              lo[q >> 1] = b;
-              third[q >> 1] = d;
-            }
-          }
-        }
-        if (again) break;
-        if (!ahead) {
-          if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
-          const int4 vote = *reinterpret_cast<const int4*>(c->vote[i & 1u][half]);
-          ++i;
-          if (!(vote.x | vote.y | vote.z | vote.w)) break;
-        }
-        // the tile's maxima: of the warp's tokens, then of the half's four warps
+        for (int q = 0; q < kHalfRows / 2; ++q) weigh(q);
+        if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
+        const int4 vote = *reinterpret_cast<const int4*>(c->vote[i & 1u][half]);
+        ++i;
+        move = vote.x | vote.y | vote.z | vote.w;
+      }
+      if (move) {
+        // the tile's maxima: of the warp's tokens, then of the half's four warps; a row to a lane
         float2* pm = reinterpret_cast<float2*>(c->part_max[i & 1u][half][quad]);
 #pragma unroll
         for (int r = 0; r < kHalfRows / 2; ++r) {
@@ -568,24 +600,34 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
         }
         exchange();
         if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
-        float a[kHalfRows];
-#pragma unroll
-        for (int r = 0; r < kHalfRows; ++r) {
-          const float (&m4)[4][kHalfRows] = c->part_max[i & 1u][half];
-          const float m = fmaxf(fmaxf(m4[0][r], m4[1][r]), fmaxf(m4[2][r], m4[3][r]));
-          const float was = r & 1 ? hi_f32(R.shift[r >> 1]) : lo_f32(R.shift[r >> 1]);
-          const bool moves = m + was > kWeightShift + kLazy;
-          const float now = moves ? kWeightShift - m : was;
-          a[r] = moves ? (was == kNone ? 0.f : exp2f(now - was)) : 1.f;
-          R.shift[r >> 1] = r & 1 ? pair(lo_f32(R.shift[r >> 1]), now) : pair(now, hi_f32(R.shift[r >> 1]));
-        }
+        const int r = lane % kHalfRows;
+        const float (&m4)[4][kHalfRows] = c->part_max[i & 1u][half];
+        const float m = fmaxf(fmaxf(m4[0][r], m4[1][r]), fmaxf(m4[2][r], m4[3][r])), was = c->shift[warp][r];
         ++i;
-#pragma unroll
-        for (int r = 0; r < kHalfRows / 2; ++r) R.sum[r] = mul_f32x2(R.sum[r], pair(a[2 * r], a[2 * r + 1]));
+        const bool moves = m + was > kWeightShift + kLazy;
+        const float now = moves ? kWeightShift - m : was;
+        const float a = moves ? (was == kNone ? 0.f : exp2f(now - was)) : 1.f;
+        __syncwarp();
+        c->shift[warp][r] = now;
+        moved = __ballot_sync(0xffffffffu, moves) & ((1u << kHalfRows) - 1u);
         if (t > pc.t0) {
           if (!wait_warp(&c->pv_done[(j - 1) & 1u], ((j - 1) >> 1) & 1u, c)) return false;
           tc_fence_after();
-          rescale(tO, a);
+          for (uint32_t left = moved; left; left &= left - 1) {
+            const int q = __ffs(left) - 1;
+            rescale_row(tO + q, __shfl_sync(0xffffffffu, a, q));
+          }
+        } else {
+          moved = (1u << kHalfRows) - 1u;  // no weights yet
+        }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < kHalfRows / 2; ++q) {
+          if (!((moved >> (2 * q)) & 3u)) continue;
+          R.shift[q] = reinterpret_cast<const uint64_t*>(c->shift[warp])[q];
+          R.sum[q] = mul_f32x2(R.sum[q], pair(__shfl_sync(0xffffffffu, a, 2 * q), __shfl_sync(0xffffffffu, a, 2 * q + 1)));
+          x[q] = add_f32x2(y[q], R.shift[q]);
+          weigh(q);
         }
       }
 #pragma unroll
@@ -671,15 +713,15 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
   if (bad) atomicOr(&c->err, MLA_DEVERR_PARENT);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p, const __grid_constant__ CacheMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   Ctl* c = reinterpret_cast<Ctl*>(smem + kOffCtl);
   grid_dep_wait();  // launched before the stream's last kernel has ended
   if (threadIdx.x == 0) {
     for (int q = 0; q < kStages; ++q) {
-      mbar_init(&c->full[q], 33 * kProducerWarps);
-      for (int w = 0; w < kProducerWarps; ++w) mbar_init(&c->empty[q][w], 1);
+      mbar_init(&c->full[q], kProducerWarps);
+      mbar_init(&c->empty[q], 1);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&c->s_full[q], 1);
@@ -719,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p) {
   }
   if (worker < n && c->tmem_base == 0) {
     if (warp < kRowWarps) softmax(p, smem, c, warp);
-    else if (warp < kWarpMma) producer(p, smem, c, warp - kWarpProd);
+    else if (warp < kWarpMma) producer(p, maps, smem, c, warp - kWarpProd);
     else if (warp == kWarpMma) products(p, smem, c);
     else Work::schedule(p, c, worker);
   }
@@ -728,6 +770,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p) {
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) p.err[kErrFirst + worker] = c->err | (c->abort ? MLA_DEVERR_TIMEOUT : 0u);
+  // after an abort nobody has waited for the last copies into shared memory: give
+  // them far longer than they take
+  if (c->abort) __nanosleep(100000);
   tc_fence_after();
   if (warp == kWarpSched) tmem_dealloc_cta(c->tmem_base, kTmemCols);
 }
@@ -930,6 +975,16 @@ int workers_per_gpu() {
   return cached[dev];
 }
 
+// The pool's rows as a tensor of bytes, a chunk of `rows` rows to a box.
+bool cache_map(CUtensorMap* m, const mla_kv8_cache& cache, int rows) {
+  const kvq::EncodeTiledFn f = kvq::encode_tiled();
+  const cuuint64_t dims[2] = {MLA_KV8_ROW_BYTES, (cuuint64_t)cache.slots}, strides[1] = {(cuuint64_t)cache.row_stride};
+  const cuuint32_t box[2] = {128, (cuuint32_t)rows}, step[2] = {1, 1};
+  return f && f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache.rows, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Layout {
   size_t starts, part_lse, part_o, total;
 };
@@ -975,6 +1030,9 @@ Params make_params(const mla_kv8_attn_args* a, void* ws, int workers) {
   p.clusters = workers;
   p.scales = a->cache.scales;
   p.block.set(a->cache.block);
+  p.box = a->page_size & -a->page_size;  // the largest power of two that divides the page size
+  if (p.box > 32) p.box = 32;
+  if (p.box < 8) p.box = 0;
   const Layout l = layout(workers);
   char* base = static_cast<char*>(ws);
   p.err = reinterpret_cast<uint32_t*>(base);
@@ -1002,7 +1060,9 @@ mla_status run_attn(const mla_kv8_attn_args* a, void* workspace, size_t ws_bytes
   // per call: the attribute belongs to the context, which may be a new one
   if (cudaFuncSetAttribute(kv8_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc) != cudaSuccess)
     return MLA_ERR_CUDA;
-  if (launch_kernel(kv8_attn_kernel, dim3(n), dim3(kThreads), kSmemAlloc, s, true, p) != cudaSuccess)
+  CacheMaps maps;
+  if (!cache_map(&maps.row, a->cache, 1) || !cache_map(&maps.box, a->cache, p.box > 0 ? p.box : 1)) return MLA_ERR_CUDA;
+  if (launch_kernel(kv8_attn_kernel, dim3(n), dim3(kThreads), kSmemAlloc, s, true, p, maps) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (n > 1 && launch_kernel(kv8_merge_kernel, dim3(2 * n), dim3(kMergeThreads), 0, s, true, p) != cudaSuccess)
     return MLA_ERR_CUDA;

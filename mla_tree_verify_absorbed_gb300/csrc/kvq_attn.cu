@@ -62,6 +62,7 @@
 #include "kvq.cuh"
 #include "sm100.cuh"
 #include "split.cuh"
+#include "tensor_map.cuh"
 
 namespace mlav {
 namespace kvq {
@@ -1202,25 +1203,6 @@ int clusters_per_gpu() {
   return n;
 }
 
-// The driver's encoder of tensor maps, looked up once.
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static std::mutex mu;
-  static EncodeTiledFn fn = nullptr;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    void* f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-    else
-      cudaGetLastError();
-  }
-  return fn;
-}
 bool query_map(CUtensorMap* m, const void* base, int64_t rows, int width, int box_rows) {
   const EncodeTiledFn f = encode_tiled();
   const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * 2};
