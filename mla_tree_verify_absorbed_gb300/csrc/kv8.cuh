@@ -9,6 +9,9 @@
 // would.
 #pragma once
 
+#include <cuda.h>
+#include <cuda_fp8.h>
+
 #include "../../include/mla_kv8.h"
 #include "kvq.cuh"
 
@@ -43,13 +46,66 @@ struct Divider {
   __device__ __forceinline__ uint32_t operator()(uint32_t x) const { return (uint32_t)(((uint64_t)x * mul) >> shift); }
 };
 
-// The attention's launch parameters: those of the 4-bit cache's, of which
-// qpe_mul and box_rows are not used, and the blocks.
+// The attention's launch parameters: those of the 4-bit cache's, of which qpe_mul is
+// not used, and the blocks.
 struct Params : kvq::Params {
   const int32_t* scales;
   Divider block;  // slot -> block
   int box;        // tokens that lie in a row within a page, at most 32; 0: fewer than 8
 };
+
+// Tensor maps of the pool: single rows, and boxes of Params::box rows; 128 bytes of each.
+struct CacheMaps {
+  CUtensorMap row, box;
+};
+// Tensor maps of the queries, [B Q H] rows of 512 and of 64, in boxes of 64 elements
+// x Params::box_rows rows.
+struct QueryMaps {
+  CUtensorMap lat, pe;
+};
+
+// Two e4m3 codes as f16 numbers.
+__device__ __forceinline__ uint32_t from_e4m3(uint32_t codes) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)codes));
+  return d;
+}
+
+// A query row of largest magnitude `big` (bf16 bits without sign) times 2^t lies
+// within e4m3's 448, its largest element at [2^7, 2^8) or, where its fraction allows
+// it, at [2^8, 448].
+__device__ __forceinline__ int query_unit(uint32_t big) {
+  return max(min(((big & 0x7fu) <= 0x60u ? 135 : 134) - (int)(big >> 7), 120), -120);
+}
+// The factor of that row's scores, kept a normal number: 0 or infinity would turn
+// masked scores of -infinity, or scores of 0, into NaN.
+__device__ __forceinline__ float query_factor(float scale_log2, int t) {
+  return fminf(fmaxf(scale_log2 * pow2(-t), 1.17549435e-38f), 3.402823466e38f);
+}
+// Four bf16 elements x 2^t as two e4m3 terms, hi + lo; hi is NaN in a row that is not
+// finite.
+__device__ __forceinline__ void query_terms(uint32_t x0, uint32_t x1, float mul, bool finite, uint32_t& hi,
+                                            uint32_t& lo) {
+  hi = lo = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t x = k ? x1 : x0;
+    const float f0 = __uint_as_float(x << 16) * mul, f1 = __uint_as_float(x & 0xffff0000u) * mul;
+    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hf = from_e4m3(h);
+    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+    const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(f0 - back.x, f1 - back.y), __NV_SATFINITE, __NV_E4M3);
+    hi |= (finite ? h : 0x7f7fu) << (16 * k);
+    lo |= l << (16 * k);
+  }
+}
+
+// The kernel for many query rows (kv8_rows.cu): clusters that a launch can have on the
+// current device (0 when it cannot be had), and the launch.
+namespace rows {
+int clusters_per_gpu();
+mla_status launch(Params p, const CacheMaps& cache, cudaStream_t stream);
+}  // namespace rows
 
 mla_status validate_cache(const mla_kv8_cache* c);
 

@@ -98,11 +98,6 @@ static_assert(kColS + 2 * kQRows <= kTmemCols, "Tensor Memory columns");
 // Chunks that come by cp.async where rows come one by one; the others are gathered.
 constexpr int kCopied = 3;
 
-// Tensor maps of the pool: single rows, and boxes of Params::box rows.
-struct CacheMaps {
-  CUtensorMap row, box;
-};
-
 // operand descriptors (smem_desc): all have 128-byte rows in groups of 8, 1 KB apart
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (kLayoutSw128 << 29);
 constexpr uint32_t kDescLo = ((uint32_t)kChunk >> 4) << 16;  // no operand reaches beyond one row of 128 bytes
@@ -189,15 +184,10 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Two f16 numbers to the nearest e4m3 codes (at most 448) and back.
+// Two f16 numbers to the nearest e4m3 codes (at most 448).
 __device__ __forceinline__ uint32_t to_e4m3(uint32_t f16x2) {
   uint16_t d;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(f16x2));
-  return d;
-}
-__device__ __forceinline__ uint32_t from_e4m3(uint32_t codes) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)codes));
   return d;
 }
 __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
@@ -415,26 +405,11 @@ __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ct
     for (int q = 0; q < 8; ++q) big = max(big, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
     big = __reduce_max_sync(0xffffffffu, big);
     const bool finite = big < 0x7f80u;
-    // the largest magnitude goes to [2^7, 2^8), or to [2^8, 448] where its fraction allows it
-    const int t = max(min(((big & 0x7fu) <= 0x60u ? 135 : 134) - (int)(big >> 7), 120), -120);
+    const int t = query_unit(big);
     const float mul = pow2(t);
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      hi[q] = lo[q] = 0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t x = w[2 * q + k];
-        const float f0 = __uint_as_float(x << 16) * mul, f1 = __uint_as_float(x & 0xffff0000u) * mul;
-        const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hf = from_e4m3(h);
-        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
-        const uint32_t l =
-            __nv_cvt_float2_to_fp8x2(make_float2(f0 - back.x, f1 - back.y), __NV_SATFINITE, __NV_E4M3);
-        hi[q] |= (finite ? h : 0x7f7fu) << (16 * k);
-        lo[q] |= l << (16 * k);
-      }
-    }
+    for (int q = 0; q < 4; ++q) query_terms(w[2 * q], w[2 * q + 1], mul, finite, hi[q], lo[q]);
     const __nv_bfloat162 pm =
         __floats2bfloat162_rn(__uint_as_float(pe << 16) * mul, __uint_as_float(pe & 0xffff0000u) * mul);
     const int n = 32 * (r >> 4) + (r & 15);
@@ -445,7 +420,7 @@ __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ct
     const uint32_t rope = 4 * kQChunk + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + 4 * (lane & 3);
     *reinterpret_cast<uint32_t*>(smem + kOffQ + rope) = *reinterpret_cast<const uint32_t*>(&pm);
     *reinterpret_cast<uint32_t*>(smem + kOffQ + rope + 16 * 128) = 0u;
-    if (lane == 0) c->unit[r] = fminf(p.scale_log2 * pow2(-t), 3.402823466e38f);
+    if (lane == 0) c->unit[r] = query_factor(p.scale_log2, t);
   }
 }
 
@@ -985,10 +960,26 @@ bool cache_map(CUtensorMap* m, const mla_kv8_cache& cache, int rows) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Which kernel a call takes, by the query rows of a sequence, its workers (CTAs, or
+// clusters of two), and the rows that a worker takes at once.
+constexpr int kFewRows = 64;
+struct Plan {
+  bool many;
+  int workers, group;
+};
+Plan plan(int rows) {
+  Plan pl;
+  pl.many = rows > kFewRows;
+  pl.workers = pl.many ? rows::clusters_per_gpu() : workers_per_gpu();
+  pl.group = pl.many ? kvq::kRows128 : kRG;
+  return pl;
+}
+
 struct Layout {
   size_t starts, part_lse, part_o, total;
 };
-Layout layout(int workers) {
+Layout layout(const Plan& pl) {
+  const int workers = pl.workers, kRG = pl.group;
   Layout l;
   size_t o = MLA_KV8_WORKSPACE_BYTES;
   l.starts = o;    o = align256(o + sizeof(Start) * (size_t)workers);
@@ -998,7 +989,7 @@ Layout layout(int workers) {
   return l;
 }
 
-Params make_params(const mla_kv8_attn_args* a, void* ws, int workers) {
+Params make_params(const mla_kv8_attn_args* a, void* ws, const Plan& pl) {
   Params p = {};
   p.B = a->B;
   p.Q = a->Q;
@@ -1027,13 +1018,13 @@ Params make_params(const mla_kv8_attn_args* a, void* ws, int workers) {
   p.out = a->out;
   p.lse = a->lse;
   p.groups = (p.rows + kRG - 1) / kRG;
-  p.clusters = workers;
+  p.clusters = pl.workers;
   p.scales = a->cache.scales;
   p.block.set(a->cache.block);
   p.box = a->page_size & -a->page_size;  // the largest power of two that divides the page size
   if (p.box > 32) p.box = 32;
   if (p.box < 8) p.box = 0;
-  const Layout l = layout(workers);
+  const Layout l = layout(pl);
   char* base = static_cast<char*>(ws);
   p.err = reinterpret_cast<uint32_t*>(base);
   p.starts = base + l.starts;
@@ -1050,18 +1041,20 @@ mla_status run_attn(const mla_kv8_attn_args* a, void* workspace, size_t ws_bytes
   st = validate_call(a);
   if (st != MLA_OK) return st;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < MLA_KV8_WORKSPACE_BYTES) return MLA_ERR_WORKSPACE;
-  const int n = workers_per_gpu();
-  if (n < 1) return MLA_ERR_CUDA;
-  if (ws_bytes < layout(n).total) return MLA_ERR_WORKSPACE;
-  Params p = make_params(a, workspace, n);
+  const Plan pl = plan(a->H * a->Q);
+  if (pl.workers < 1) return MLA_ERR_CUDA;
+  if (ws_bytes < layout(pl).total) return MLA_ERR_WORKSPACE;
+  Params p = make_params(a, workspace, pl);
   p.hold = hold_ns != 0;
   p.wait_ns = p.hold ? hold_ns : kWaitLimitNs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  CacheMaps maps;
+  if (!cache_map(&maps.row, a->cache, 1) || !cache_map(&maps.box, a->cache, p.box > 0 ? p.box : 1)) return MLA_ERR_CUDA;
+  if (pl.many) return rows::launch(p, maps, s);
+  const int n = pl.workers;
   // per call: the attribute belongs to the context, which may be a new one
   if (cudaFuncSetAttribute(kv8_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc) != cudaSuccess)
     return MLA_ERR_CUDA;
-  CacheMaps maps;
-  if (!cache_map(&maps.row, a->cache, 1) || !cache_map(&maps.box, a->cache, p.box > 0 ? p.box : 1)) return MLA_ERR_CUDA;
   if (launch_kernel(kv8_attn_kernel, dim3(n), dim3(kThreads), kSmemAlloc, s, true, p, maps) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (n > 1 && launch_kernel(kv8_merge_kernel, dim3(2 * n), dim3(kMergeThreads), 0, s, true, p) != cudaSuccess)
@@ -1077,8 +1070,8 @@ using namespace mlav;
 
 extern "C" size_t mla_kv8_attn_workspace_size(const mla_kv8_attn_args* a) {
   if (kv8::validate_shape(a) != MLA_OK) return 0;
-  const int n = kv8::workers_per_gpu();
-  return n > 0 ? kv8::layout(n).total : 0;
+  const kv8::Plan pl = kv8::plan(a->H * a->Q);
+  return pl.workers > 0 ? kv8::layout(pl).total : 0;
 }
 
 extern "C" mla_status mla_kv8_attn(const mla_kv8_attn_args* a, void* workspace, size_t ws_bytes, mla_stream_t stream) {

@@ -76,7 +76,7 @@ struct QueryMaps {
   CUtensorMap lat, pe;
 };
 
-constexpr int kRG = 128;       // query rows per work item
+constexpr int kRG = kRows128;  // query rows per work item
 constexpr int kTK = 64;        // tokens per tile
 constexpr int kThreads = 640;  // 20 warps: 96 registers a thread
 constexpr uint32_t kTmemCols = 512;
@@ -163,7 +163,7 @@ constexpr float kWeightShift = 7.f;
 // lengths.  kFixed 3: 43.4, 41.9, 101.7; 4: 44.5, 40.8, 99.7; 5: 45.3, 39.9, 101.9;
 // 6: 46.5, 40.3, 103.3; 8: 48.9, 43.2, 106.5; kMinTiles 6 in place of 4: 45.3, 40.8,
 // 100.4.  Row groups in long pieces (32 sequences x 128 heads, trees) move by 1%.
-constexpr int kFixed = 4;
+constexpr int kFixed = kFixed128;
 constexpr int kMinTiles = 4;
 
 using Work = Split<kTK, kFixed, kMinTiles, kThreads, false>;
@@ -736,13 +736,6 @@ __device__ void value_mma(const Params& p, uint8_t* smem, Ctl* c) {
   drain_mmas(c, leader);
 }
 
-// Partial results: 8 columns of all rows after each other, so that the rows of
-// a warp, one to a lane, fill whole lines (row after row, a warp's store touches
-// 32 lines; 32 sequences x 128 heads x 8,192 tokens then took 76.7 us, not 74.3).
-__device__ __forceinline__ int64_t part_index(int slot, int block8, int r) {
-  return (((int64_t)slot * (kDl / 8) + block8) * kRG + r) * 8;
-}
-
 // Row warps of the value CTA (warpgroup h: columns [256 h, 256 h + 256)):
 // rescale O where a factor is not 1, and per piece normalise and store it.
 __device__ void value_rows(const Params& p, Ctl* c) {
@@ -988,7 +981,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kvq_att
 // wait for one load each.)
 constexpr int kMergeThreads = 512, kMergeRows = 8, kMergeParts = 4;
 static_assert(kMergeThreads == kMergeRows * (kDl / 8), "a thread per row and 8 columns");
-constexpr int kMaxClusters = 128;
 static_assert(2 * kMaxClusters <= kErrMax, "an error word per CTA");
 __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Params p, int chunks) {
   __shared__ Start start[kMaxClusters];
@@ -1131,6 +1123,13 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
     }
     __syncthreads();  // slot, weight and sums are reused
   }
+}
+
+cudaError_t launch_merge(const Params& p, cudaStream_t s) {
+  // two blocks per SM of the clusters, fewer when even n - 1 cut row groups make fewer tasks
+  const int n = p.clusters, chunks = ((p.rows < kRG ? p.rows : kRG) + kMergeRows - 1) / kMergeRows;
+  const int tasks = (n - 1) * chunks * kMergeParts;
+  return launch_kernel(kvq_merge_kernel, dim3(tasks < 4 * n ? tasks : 4 * n), dim3(kMergeThreads), 0, s, true, p, chunks);
 }
 
 namespace {
@@ -1305,12 +1304,7 @@ mla_status run_attn(const mla_kvq_attn_args* a, void* workspace, size_t ws_bytes
     return MLA_ERR_CUDA;
   if (launch_kernel(kvq_attn_kernel, dim3(2 * n), dim3(kThreads), kSmemAlloc, s, true, p, maps) != cudaSuccess)
     return MLA_ERR_CUDA;
-  // two blocks per SM of the clusters, fewer when even n - 1 cut row groups make fewer tasks
-  const int chunks = ((p.rows < kRG ? p.rows : kRG) + kMergeRows - 1) / kMergeRows;
-  const int tasks = (n - 1) * chunks * kMergeParts;
-  const int blocks = tasks < 4 * n ? tasks : 4 * n;
-  if (n > 1 && launch_kernel(kvq_merge_kernel, dim3(blocks), dim3(kMergeThreads), 0, s, true, p, chunks) != cudaSuccess)
-    return MLA_ERR_CUDA;
+  if (n > 1 && launch_merge(p, s) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 }  // namespace

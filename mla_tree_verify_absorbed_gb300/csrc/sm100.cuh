@@ -346,6 +346,14 @@ __device__ __forceinline__ void mma_cta_ss_f8(uint32_t d_tmem, uint64_t a_desc, 
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ void mma_cta_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Arrive once on this CTA's barrier when the MMAs this thread issued so far
 // have completed; the second form arrives on the barrier at the same offset in
 // every cluster CTA whose bit is set.
@@ -372,6 +380,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn_maj
   return idesc_f16_f32(M, N, a_mn_major, b_mn_major);
 }
 
+// The same with an e5m2 A operand (format 1).
+__host__ __device__ constexpr uint32_t idesc_e5m2_e4m3_f32(int M, int N, int a_mn_major, int b_mn_major) {
+  return (1u << 7) | idesc_f16_f32(M, N, a_mn_major, b_mn_major);
+}
+
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn_major, int b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -387,7 +400,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes
   d |= (uint64_t)(layout & 7u) << 61;
   return d;
 }
-constexpr uint32_t kLayoutSw128 = 2;
+constexpr uint32_t kLayoutSw128 = 2, kLayoutSw64 = 4;
 
 // Byte offset of element (row, k) in a K-major 128-byte-swizzled tile whose
 // rows are 64 bf16 wide (one swizzle atom column); rows are 128 bytes apart.
@@ -460,6 +473,11 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t caddr, float v) {
 // Tensor Memory loads / stores: 32 lanes x N columns of 32 bits; thread t of
 // the warp moves lane (quadrant base + t).
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
