@@ -82,21 +82,19 @@ __device__ __forceinline__ int query_unit(uint32_t big) {
 __device__ __forceinline__ float query_factor(float scale_log2, int t) {
   return fminf(fmaxf(scale_log2 * pow2(-t), 1.17549435e-38f), 3.402823466e38f);
 }
-// Four bf16 elements x 2^t as two e4m3 terms, hi + lo; hi is NaN in a row that is not
-// finite.
+// Four bf16 elements x 2^t as two e4m3 terms: hi the sign, exponent and three bits
+// behind the first of each, lo the other four; hi is NaN in a row that is not finite.
 __device__ __forceinline__ void query_terms(uint32_t x0, uint32_t x1, float mul, bool finite, uint32_t& hi,
                                             uint32_t& lo) {
   hi = lo = 0;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint32_t x = k ? x1 : x0;
-    const float f0 = __uint_as_float(x << 16) * mul, f1 = __uint_as_float(x & 0xffff0000u) * mul;
-    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hf = from_e4m3(h);
-    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
-    const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(f0 - back.x, f1 - back.y), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t x = k ? x1 : x0, a = x << 16, b = x & 0xffff0000u;
+    const float h0 = __uint_as_float(a & 0xfff00000u), h1 = __uint_as_float(b & 0xfff00000u);
+    const float l0 = __uint_as_float(a) - h0, l1 = __uint_as_float(b) - h1;
+    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(h0 * mul, h1 * mul), __NV_SATFINITE, __NV_E4M3);
     hi |= (finite ? h : 0x7f7fu) << (16 * k);
-    lo |= l << (16 * k);
+    lo |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(l0 * mul, l1 * mul), __NV_SATFINITE, __NV_E4M3) << (16 * k);
   }
 }
 

@@ -56,13 +56,13 @@ using kvq::Start;
 
 constexpr int kRG = kvq::kRows128;
 constexpr int kTK = 64;  // tokens per tile
-// Warps 0-7 hold rows, in two groups that take the tiles of one parity; 8 and 9 fetch
-// 32 tokens each.
-constexpr int kRowWarps = 8, kProducerWarps = 2;
+// Warps 0-7 hold rows, in two groups that take the tiles of one parity; 8 to 11 fetch,
+// 8 and 9 by tensor copies, 10 and 11 by cp.async, 32 tokens each.
+constexpr int kRowWarps = 8, kProducerWarps = 4;
 constexpr int kWarpProd = kRowWarps;
-constexpr int kWarpAux = 10;    // TMEM allocation; rank 0: weight copies
-constexpr int kWarpMma = 11;
-constexpr int kWarpSched = 12;  // the pieces of work
+constexpr int kWarpAux = 12;    // TMEM allocation; rank 0: weight copies
+constexpr int kWarpMma = 13;
+constexpr int kWarpSched = 14;  // the pieces of work
 constexpr int kThreads = 32 * (kWarpSched + 1);
 constexpr uint32_t kTmemCols = 512;
 
@@ -211,12 +211,14 @@ constexpr int kFollowers = kRowWarps + kProducerWarps + 1;  // and, in the score
 // producers
 // ---------------------------------------------------------------------------
 // As in kv8_attn.cu: tensor copies of a page's rows where pages allow it, else
-// gathers and cp.async together.
+// gathers and cp.async together, each by warps of their own (a warp that issues
+// gathers waits for the copy engine).
 template <bool kScore>
-__device__ __forceinline__ void producer(const Params& p, const CacheMaps& maps, uint8_t* smem, Ctl* c, int pw) {
+__device__ __forceinline__ void producer(const Params& p, const CacheMaps& maps, uint8_t* smem, Ctl* c, int warp) {
   constexpr int kChunks = kScore ? kChunksS : kChunksV;
   constexpr int kCopied = kScore ? 3 : 2;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, pw = warp & 1;
+  const bool tensor = warp < 2;
   uint32_t err = 0, j = 0, seg = 0;
   for_pieces(c, [&](const Piece& pc) {
     const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
@@ -237,7 +239,7 @@ __device__ __forceinline__ void producer(const Params& p, const CacheMaps& maps,
       return -1;
     };
     auto word_of = [&](int32_t slot) {
-      return kScore && slot >= 0 ? (uint32_t)__ldg(p.scales + p.block((uint32_t)slot)) : 0u;
+      return kScore && tensor && slot >= 0 ? (uint32_t)__ldg(p.scales + p.block((uint32_t)slot)) : 0u;
     };
     int32_t slot = slot_of(entry_of(pc.t0), pc.t0), ent = entry_of(pc.t0 + 1);
     uint32_t word = word_of(slot);
@@ -255,40 +257,44 @@ __device__ __forceinline__ void producer(const Params& p, const CacheMaps& maps,
       const bool boxes = p.box > 0 && __all_sync(0xffffffffu, seen(v, pos_of(v)));
       uint64_t* full = &c->full[st];
       if (!wait_warp(&c->empty[st], ((j / kStages) & 1u) ^ 1u, c)) return false;
-      if (kScore) {
+      if (kScore && tensor) {
         c->inv[j % kInv][32 * pw + lane] = pow2(-scale_of(word));
         __syncwarp();
       }
-      if (boxes) {
-        if (lane == 0) mbar_arrive_expect_tx(full, kChunks * 32 * 128);
+      if (tensor) {
+        if (lane == 0) mbar_arrive_expect_tx(full, (boxes ? kChunks : kChunks - kCopied) * 32 * 128);
         __syncwarp();
-        if ((lane & (p.box - 1)) == 0) {
+        if (boxes) {
+          if ((lane & (p.box - 1)) == 0) {
 #pragma unroll
-          for (int ck = 0; ck < kChunks; ++ck)
-            tensor_copy_2d(to + ck * kChunk + lane * 128, &maps.box, 128 * ck, slot, full);
+            for (int ck = 0; ck < kChunks; ++ck)
+              tensor_copy_2d(to + ck * kChunk + lane * 128, &maps.box, 128 * ck, slot, full);
+          }
+        } else {
+          const int32_t s1 = __shfl_down_sync(0xffffffffu, slot, 1), s2 = __shfl_down_sync(0xffffffffu, slot, 2),
+                        s3 = __shfl_down_sync(0xffffffffu, slot, 3);
+          if ((lane & 3) == 0) {
+#pragma unroll
+            for (int ck = kCopied; ck < kChunks; ++ck)
+              tensor_gather4(dst + ck * kChunk + lane * 128, &maps.row, 128 * ck, slot, s1, s2, s3, full);
+          }
         }
       } else {
-        const int r7 = lane & 7, ch = lane >> 3;
-        const int32_t s1 = __shfl_down_sync(0xffffffffu, slot, 1), s2 = __shfl_down_sync(0xffffffffu, slot, 2),
-                      s3 = __shfl_down_sync(0xffffffffu, slot, 3);
-        if ((lane & 3) == 0) {
+        if (!boxes) {
+          const int r7 = lane & 7, ch = lane >> 3;
 #pragma unroll
-          for (int ck = kCopied; ck < kChunks; ++ck)
-            tensor_gather4(dst + ck * kChunk + lane * 128, &maps.row, 128 * ck, slot, s1, s2, s3, full);
+          for (int i = 0; i < 8; ++i) {
+            const int token = 4 * i + ch;
+            const int32_t s = __shfl_sync(0xffffffffu, slot, token);
+            const uint8_t* src = p.cache + (uint64_t)(uint32_t)max(s, 0) * (uint32_t)p.row_stride + 16 * r7;
+            const uint32_t at = dst + token * 128 + ((r7 ^ (token & 7)) << 4), bytes = s >= 0 ? 16u : 0u;
+#pragma unroll
+            for (int ck = 0; ck < kCopied; ++ck) cp_async_16_zfill(at + ck * kChunk, src + 128 * ck, bytes);
+          }
+          cp_async_mbar_hold(full);  // until they have landed
+          __syncwarp();
         }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int token = 4 * i + ch;
-          const int32_t s = __shfl_sync(0xffffffffu, slot, token);
-          const uint8_t* src = p.cache + (uint64_t)(uint32_t)max(s, 0) * (uint32_t)p.row_stride + 16 * r7;
-          const uint32_t at = dst + token * 128 + ((r7 ^ (token & 7)) << 4), bytes = s >= 0 ? 16u : 0u;
-#pragma unroll
-          for (int ck = 0; ck < kCopied; ++ck) cp_async_16_zfill(at + ck * kChunk, src + 128 * ck, bytes);
-        }
-        cp_async_mbar_hold(full);  // until they have landed
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(full, (kChunks - kCopied) * 32 * 128);
+        if (lane == 0) mbar_arrive(full);
       }
       slot = next;
       word = next_word;
@@ -380,14 +386,15 @@ __device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* s
     for (int i = 0; i < 4; ++i)
       ld_shared_v4(src + (((4 * wg + i) ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   };
-  uint32_t big = 0;  // magnitudes compare as their bits
+  uint32_t big2 = 0;  // magnitudes compare as their bits
 #pragma unroll 1
   for (int ck = 0; ck < 9; ++ck) {
     uint32_t w[16];
     half_chunk(ck, w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    for (int i = 0; i < 16; ++i) big2 = __vmaxu2(big2, w[i] & 0x7fff7fffu);
   }
+  uint32_t big = max(big2 & 0xffffu, big2 >> 16);
   c->q_big[wg][r] = big;
   __syncwarp();
   if (lane == 0) mbar_arrive(&c->q_max);
@@ -703,12 +710,12 @@ __device__ void value_rows(const Params& p, Ctl* c) {
           if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c)) return false;
           tc_fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < 256; c0 += 32) {
-            uint32_t u[32];
-            tmem_ld32_sync(tO + c0, u);
+          for (int c0 = 0; c0 < 256; c0 += 64) {
+            uint32_t u[64];
+            tmem_ld64_sync(tO + c0, u);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) * a);
-            tmem_st_32x32b_x32(tO + c0, u);
+            for (int q = 0; q < 64; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) * a);
+            tmem_st64(tO + c0, u);
           }
           tmem_wait_st();
         }
