@@ -8,16 +8,15 @@
 // of tokens in the first (K-major), columns of latents in the second (MN-major).
 // Nothing is converted, every byte is fetched once, and one CTA does all of it.
 //
-// The other operands are made of several e4m3 terms, each in columns of its own, so
-// that each has its own power of two:
-//   queries  q 2^t = hi + lo, t per row.  bf16 has 8 significant bits and a term 4,
-//            so the sum is exact down to 2^-9 of the row's largest element;
-//   weights  w = hi + lo 2^-5 + third 2^-15 of w rounded to f16: of its 11
-//            significant bits the first two terms take 4 or 5 each.  The smallest
-//            code of the third is 2^-24, as f16's.  Its largest, 448 2^-15, cuts off
-//            what is left of weights above 2^3, at most 2^-10 of them.
-// The terms' products are added in fp32: queries' as the scores are read, weights'
-// when O is.  The rope product (bf16) is accumulated on the queries' first term.
+// The other operands are made of several 8-bit terms, each in columns of its own, whose
+// products are added in fp32: queries' as the scores are read, weights' when O is.
+//   queries  q 2^t = hi + lo, both e4m3, t per row.  bf16 has 8 significant bits and a
+//            term 4, so the sum is exact down to 2^-9 of the row's largest element;
+//   weights  w = t1 + t2 + t3 of w rounded to f16, all e5m2.  An e5m2 number is the
+//            upper byte of an f16 one: t1 and t2 are the upper bytes of w and of what is
+//            left, t3 what is left then, rounded.  3 + 3 + 3 significant bits, off by
+//            at most 2^-9, as bf16.
+// The rope product (bf16) is accumulated on the queries' first term.
 //
 // Blocks' scales.  A token's score is s_j = c_r 2^k_j S_jr (c_r: scale, row unit),
 // and its value 2^k_j times its codes, so O takes the weights 2^(s_j + k_j - m): the
@@ -114,13 +113,12 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 20000000ull;
 
 // Weights are 2^(s + k - max + kWeightShift): a lazy maximum lets them reach 2^kLazy
-// above 2^kWeightShift, 2^8 in all, below e4m3's 448.  Moving a maximum costs a
-// pass over O, some 4,000 cycles, so it should hold for a whole piece: with 2^2 in
-// place of 2^7, every second tile of 64 nodes x 64 heads x 20,000 tokens moved one of
-// its 16 maxima.
-constexpr float kLazy = 7.f;
-constexpr float kWeightShift = 1.f;
-constexpr float kLoMul = 32.f, kThirdMul = 1024.f;  // 2^5, and from there 2^10
+// above 2^kWeightShift, 2^15 in all, below e5m2's 57,344, so that weights down to
+// 2^-15 of the maximum keep 9 bits and down to 2^-23 some.  Moving a maximum costs a
+// pass over a row of O: with 2^2 in place of 2^8, every second tile of 64 nodes x 64
+// heads x 20,000 tokens moved one of its 16 maxima.
+constexpr float kLazy = 8.f;
+constexpr float kWeightShift = 7.f;
 
 struct alignas(16) Ctl {
   uint64_t full[kStages];      // tile landed (each producer warp's copies)
@@ -183,12 +181,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-// Two f16 numbers to the nearest e4m3 codes (at most 448).
-__device__ __forceinline__ uint32_t to_e4m3(uint32_t f16x2) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(f16x2));
-  return d;
 }
 __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -300,7 +292,7 @@ __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
     ++seg;
     const int halves = p.rows - pc.g * kRG > kHalfRows ? 2 : 1;
     const uint32_t is8 = idesc_e4m3_f32(kTK, 32 * halves, 0, 0), is16 = idesc_bf16_f32(kTK, 32 * halves, 0, 0);
-    const uint32_t io = idesc_e4m3_f32(128, 48 * halves, 1, 1);
+    const uint32_t io = idesc_e4m3_e5m2_f32(128, 48 * halves, 1, 1);
     const uint32_t end = j + (uint32_t)(pc.t1 - pc.t0), first = j;
     uint32_t s = j;  // the next S product
     auto test = [&](uint64_t* bar, uint32_t n) {  // tile n's phase of a barrier that every second tile uses
@@ -376,16 +368,18 @@ __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
 // ---------------------------------------------------------------------------
 // softmax and output
 // ---------------------------------------------------------------------------
-// Brings a piece's queries into shared memory as two e4m3 terms; each row warp takes
-// four rows.  Rows that do not exist, up to the end of a half, are zeros.
+// Brings a piece's queries into shared memory as two e4m3 terms, a row to a warp, two
+// of a warp's rows in flight.  Rows that do not exist, up to the end of a half, are zeros.
 __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ctl* c, const Piece& pc, int warp) {
   const int lane = threadIdx.x & 31;
   const int rows = min(kRG, p.rows - pc.g * kRG), padded = rows > kHalfRows ? kRG : kHalfRows;
-  uint4 all[4][2] = {};
-  uint32_t rope_all[4] = {};
+#pragma unroll 1
+  for (int r0 = warp; r0 < padded; r0 += 2 * kRowWarps) {
+  uint4 all[2][2] = {};
+  uint32_t rope_all[2] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * warp + i;
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + kRowWarps * i;
     if (r < rows) {
       const int64_t row = (int64_t)pc.b * p.rows + pc.g * kRG + r;
       const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q_lat) + row * (2 * kDl)) + 2 * lane;
@@ -395,9 +389,8 @@ __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ct
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * warp + i;
-    if (r >= padded) break;
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + kRowWarps * i;
     const uint4 a = all[i][0], b = all[i][1];
     const uint32_t pe = rope_all[i], w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t big = max(pe & 0x7fffu, (pe >> 16) & 0x7fffu);  // magnitudes compare as their bits
@@ -421,6 +414,7 @@ __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ct
     *reinterpret_cast<uint32_t*>(smem + kOffQ + rope) = *reinterpret_cast<const uint32_t*>(&pm);
     *reinterpret_cast<uint32_t*>(smem + kOffQ + rope + 16 * 128) = 0u;
     if (lane == 0) c->unit[r] = query_factor(p.scale_log2, t);
+  }
   }
 }
 
@@ -536,15 +530,12 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
         const float e0 = ex2_approx(lo_f32(x[q])), e1 = ex2_approx(hi_f32(x[q]));
         sum[q] = fma_f32x2(pair(e0, e1), inv2, R.sum[q]);
         const uint32_t w = pack_f16(e0, e1);
-        const uint32_t h = to_e4m3(w);
-        const uint32_t r1 = kvq::hmul2_f16(sub_f16(w, from_e4m3(h)), 0x50005000u);  // * 32; exact, as what follows
-        const uint32_t b = to_e4m3(r1);
-        const uint32_t r2 = kvq::hmul2_f16(sub_f16(r1, from_e4m3(b)), 0x64006400u);  // * 1024
-        const uint32_t d = to_e4m3(r2);
-        const uint32_t place = q & 1 ? 0x5410u : 0x3254u;  // the pair's half of the word, the other as it is
-        hi[q >> 1] = __byte_perm(hi[q >> 1], h, place);
-        lo[q >> 1] = __byte_perm(lo[q >> 1], b, place);
-        third[q >> 1] = __byte_perm(third[q >> 1], d, place);
+        const uint32_t r1 = sub_f16(w, w & 0xff00ff00u);                    // exact
+        const uint32_t r2 = sub_f16(r1, r1 & 0xff00ff00u) + 0x00800080u;    // exact, then rounded at the upper byte
+        const uint32_t place = q & 1 ? 0x7510u : 0x3275u;  // upper bytes into the pair's half of the word
+        hi[q >> 1] = __byte_perm(hi[q >> 1], w, place);
+        lo[q >> 1] = __byte_perm(lo[q >> 1], r1, place);
+        third[q >> 1] = __byte_perm(third[q >> 1], r2, place);
       };
       uint32_t moved = 0xffffffffu;  // rows; in a piece's first tile all, from no maximum at all
       bool move = t == pc.t0;
@@ -659,8 +650,7 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
       tmem_ld16_sync(tO + mb * kBlockO + 2 * kHalfRows, w);
 #pragma unroll
       for (int r = 0; r < kHalfRows; ++r) {
-        const float lo = fmaf(__uint_as_float(w[r]), 1.f / kThirdMul, __uint_as_float(v[r]));
-        const float o = fmaf(lo, 1.f / kLoMul, __uint_as_float(u[r])) * inv[r];
+        const float o = (__uint_as_float(u[r]) + (__uint_as_float(v[r]) + __uint_as_float(w[r]))) * inv[r];
         if (r < live) {
           if (pc.slot < 0)
             static_cast<__nv_bfloat16*>(p.out)[(orow + r) * kDl + 128 * mb + latent] = __float2bfloat16_rn(o);
@@ -757,10 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p, c
 // ---------------------------------------------------------------------------
 // The pieces of a row group that several CTAs shared:
 //   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k.
-// Every block reads where the CTAs' intervals begin and lists the row groups that
-// a boundary cuts.  A quarter of the columns of a row goes to a warp.  Few rows in
-// many pieces: four warps share it, every fourth piece each; else each of the four
-// takes a row of its own.
+// Every block reads where the CTAs' intervals begin and lists the row groups that a
+// boundary cuts.  A warp takes a quarter of the columns of a row; with few rows in many
+// pieces four warps share that, every fourth piece each.
 constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32, kMergeParts = 4;
 constexpr int kMaxWorkers = 256;
 static_assert(kMaxWorkers <= kErrMax && kMaxWorkers <= kMergeThreads, "an error word per CTA");
@@ -768,11 +757,10 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Param
   __shared__ Start start[kMaxWorkers];
   __shared__ int cut[kMaxWorkers];                   // boundaries that are the first inside a row group
   __shared__ uint32_t cut_mask[kMaxWorkers / 32];
-  __shared__ int slot[kMaxWorkers];                  // -1: an empty piece
   __shared__ float weight[kMergeWarps][kMaxWorkers];
-  __shared__ float4 sums[kMergeParts - 1][4][32];
+  __shared__ int16_t slot[kMergeWarps][kMaxWorkers];  // -1: an empty piece
+  __shared__ float4 sums[kMergeWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quarter = warp & 3, part = warp >> 2;
   grid_dep_wait();
   grid_dep_launch();
   if (tid < p.clusters) start[tid] = static_cast<const Start*>(p.starts)[tid];
@@ -795,102 +783,116 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Param
     cuts += __popc(cut_mask[w]);
   }
   __syncthreads();
+  // A task is a quarter of a row's columns, or every fourth piece of it; a block takes
+  // 16 or 4 of them at a time.
   const int rows_max = min(p.rows, kRG);
-  const bool split = cuts * rows_max <= 2 * (int)gridDim.x;
-  const int per = split ? rows_max : (rows_max + kMergeParts - 1) / kMergeParts;  // tasks of a cut
-  for (int task = blockIdx.x; task < cuts * per; task += gridDim.x) {
-    const int k = cut[task / per];
-    const Start s = start[k];
-    const int T = s.T, L = kFixed + T;
-    const int64_t g = div_fast(s.x, L), base = g * L;
-    // pieces: CTA k - 1 has units [0, x_k) of the row group, CTA i >= k [x_i, x_{i+1})
-    auto unit = [&](int i) -> int64_t {
-      return i < k ? 0 : i >= workers || start[i].b != s.b || start[i].x - base > L ? L : start[i].x - base;
-    };
-    bool mine = false, whole = false;
-    const int w = k - 1 + tid;
-    if (w < workers) {
-      const int64_t z0 = unit(w), z1 = unit(w + 1);
-      mine = z0 < L;
-      if (mine) {
-        const int t0 = Work::cut_tile(z0, T), t1 = Work::cut_tile(z1, T);
-        whole = t0 == 0 && t1 == T;
-        slot[tid] = t1 > t0 ? 2 * w + (t0 == 0) : -1;
-      }
-    }
-    const int n = __syncthreads_count(mine);
-    // when one CTA has it all it stored the results
-    if (__syncthreads_or(whole)) continue;
-    const int r = split ? task % per : (task % per) * kMergeParts + part;
-    const bool live = r < min((int64_t)kRG, p.rows - g * kRG);
+  const bool split = cuts * rows_max <= (int)gridDim.x * 2;
+  const int at_once = split ? kMergeWarps / kMergeParts : kMergeWarps;
+  const int part = split ? warp % kMergeParts : 0, step = split ? kMergeParts : 1;
+  const int tasks = cuts * rows_max * 4;
+  for (int t0 = blockIdx.x * at_once; t0 < tasks; t0 += gridDim.x * at_once) {
+    const int task = t0 + (split ? warp / kMergeParts : warp);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float total = 1.f;
-    const int64_t orow = (int64_t)s.b * p.rows + g * kRG + r;
-    if (live) {
+    float total = 0.f;
+    int64_t orow = -1;
+    const int quarter = task & 3, r = (task >> 2) % rows_max;
+    if (task < tasks) {
+      const int k = cut[(task >> 2) / rows_max];
+      const Start s = start[k];
+      const int T = s.T, L = kFixed + T;
+      const int64_t g = div_fast(s.x, L), base = g * L;
+      // pieces: CTA k - 1 has units [0, x_k) of the row group, CTA i >= k [x_i, x_{i+1})
+      auto unit = [&](int i) -> int64_t {
+        return i < k ? 0 : i >= workers || start[i].b != s.b || start[i].x - base > L ? L : start[i].x - base;
+      };
+      int n = 0;
+      bool whole = false;
+      int16_t* sl = slot[warp];
       float* wt = weight[warp];
-      float m = -INFINITY, sum = 0.f;
-      for (int i = lane; i < n; i += 32) {
-        wt[i] = slot[i] >= 0 ? p.part_lse[(int64_t)slot[i] * kRG + r] : -INFINITY;
-        m = fmaxf(m, wt[i]);
+      float m = -INFINITY;
+      for (int i = lane;; i += 32) {
+        const int w = k - 1 + i;
+        const int64_t z0 = w < workers ? unit(w) : L;
+        if (z0 < L) {
+          const int u0 = Work::cut_tile(z0, T), u1 = Work::cut_tile(unit(w + 1), T);
+          whole |= u0 == 0 && u1 == T;
+          sl[i] = (int16_t)(u1 > u0 ? 2 * w + (u0 == 0) : -1);
+          wt[i] = u1 > u0 ? p.part_lse[(int64_t)sl[i] * kRG + r] : -INFINITY;
+          m = fmaxf(m, wt[i]);
+        }
+        const int some = __popc(__ballot_sync(0xffffffffu, z0 < L));
+        n += some;
+        if (some < 32) break;
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (m == -INFINITY) m = 0.f;  // no piece has any weight
-      for (int i = lane; i < n; i += 32) {
-        wt[i] = __expf(wt[i] - m);
-        sum += wt[i];
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      total = sum == 0.f ? 1.f : sum;  // then a row of zeros, as from one piece
-      if (p.lse && quarter == 0 && lane == 0 && (part == 0 || !split)) p.lse[orow] = m + logf(sum);
       __syncwarp();
-      const int step = split ? kMergeParts : 1;
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + (int64_t)r * kDl + 128 * quarter) + lane;
-      for (int i0 = split ? part : 0; i0 < n; i0 += 4 * step) {
-        float4 v[4];
-        float f[4];
+      // when one CTA has it all it stored the results
+      if (r < min((int64_t)kRG, p.rows - g * kRG) && !__any_sync(0xffffffffu, whole)) {
+        orow = (int64_t)s.b * p.rows + g * kRG + r;
+        // the first pieces' results are on their way while the weights are computed
+        constexpr int kDeep = 4;
+        float4 v[kDeep];
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + (int64_t)r * kDl + 128 * quarter) + lane;
+        auto load = [&](int i0) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const int i = i0 + d * step, sl = i < n ? slot[i] : -1;
-          v[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-          f[d] = 0.f;
-          if (sl >= 0) {
-            v[d] = __ldcg(src + (int64_t)sl * (kRG * kDl / 4));
-            f[d] = wt[i];
+          for (int d = 0; d < kDeep; ++d) {
+            const int i = i0 + d * step, at = i < n ? sl[i] : -1;
+            v[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (at >= 0) v[d] = __ldcg(src + (int64_t)at * (kRG * kDl / 4));
           }
+        };
+        load(part);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (m == -INFINITY) m = 0.f;  // no piece has any weight
+        float sum = 0.f;
+        for (int i = lane; i < n; i += 32) {
+          wt[i] = __expf(wt[i] - m);
+          sum += wt[i];
         }
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          acc.x = fmaf(f[d], v[d].x, acc.x);
-          acc.y = fmaf(f[d], v[d].y, acc.y);
-          acc.z = fmaf(f[d], v[d].z, acc.z);
-          acc.w = fmaf(f[d], v[d].w, acc.w);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        total = sum == 0.f ? 1.f : sum;  // then a row of zeros, as from one piece
+        if (p.lse && quarter == 0 && part == 0 && lane == 0) p.lse[orow] = m + logf(sum);
+        __syncwarp();
+        for (int i0 = part;;) {
+#pragma unroll
+          for (int d = 0; d < kDeep; ++d) {
+            const int i = i0 + d * step;
+            const float f = i < n ? wt[i] : 0.f;  // 0 for an empty piece
+            acc.x = fmaf(f, v[d].x, acc.x);
+            acc.y = fmaf(f, v[d].y, acc.y);
+            acc.z = fmaf(f, v[d].z, acc.z);
+            acc.w = fmaf(f, v[d].w, acc.w);
+          }
+          i0 += kDeep * step;
+          if (i0 >= n) break;
+          load(i0);
         }
       }
+      __syncwarp();  // slot and weight are reused
     }
-    if (split) {
-      if (part > 0) sums[part - 1][quarter][lane] = acc;
+    if (split) {  // the same in every block
+      sums[warp][lane] = acc;
       __syncthreads();
       if (part == 0) {
 #pragma unroll
-        for (int o = 0; o < kMergeParts - 1; ++o) {
-          const float4 a = sums[o][quarter][lane];
+        for (int o = 1; o < kMergeParts; ++o) {
+          const float4 a = sums[warp + o][lane];
           acc.x += a.x;
           acc.y += a.y;
           acc.z += a.z;
           acc.w += a.w;
         }
       }
+      __syncthreads();
     }
-    if (live && (part == 0 || !split)) {
+    if (orow >= 0 && part == 0) {
       const float inv = 1.f / total;
       const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
                            b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
       reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDl + 128 * quarter)[lane] =
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
-    __syncthreads();  // slot and sums are reused
   }
 }
 

@@ -380,7 +380,10 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn_maj
   return idesc_f16_f32(M, N, a_mn_major, b_mn_major);
 }
 
-// The same with an e5m2 A operand (format 1).
+// The same with an e5m2 operand (format 1).
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N, int a_mn_major, int b_mn_major) {
+  return (1u << 10) | idesc_f16_f32(M, N, a_mn_major, b_mn_major);
+}
 __host__ __device__ constexpr uint32_t idesc_e5m2_e4m3_f32(int M, int N, int a_mn_major, int b_mn_major) {
   return (1u << 7) | idesc_f16_f32(M, N, a_mn_major, b_mn_major);
 }
