@@ -43,10 +43,6 @@ struct IoParams {
   uint32_t* err;
 };
 
-// 2^e for -160 < e < 160, as two factors: no power here is out of range, but for
-// fp32 results.
-__device__ __forceinline__ float scale_by(float x, int e) { return x * pow2(e / 2) * pow2(e - e / 2); }
-
 // Sixteen latents of a row as bits of fp32 (the lane's part).
 template <class T>
 struct Part;
@@ -76,7 +72,28 @@ __device__ __forceinline__ int64_t slot_at(const IoParams& p, int64_t i, uint32_
   return -1;
 }
 
-// What the new rows need, into the pending bits of their blocks' words.
+// What a row needs of its block, in the form of a scale word; the same in every lane.
+template <class T>
+__device__ __forceinline__ uint32_t need_of(const IoParams& p, const Part<T>& x, uint32_t* e) {
+  uint32_t big = 0;  // magnitudes compare as their bits
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t a = x.bits(i) & 0x7fffffffu;
+    if (a >= 0x7f800000u) *e |= MLA_DEVERR_NONFINITE;
+    else big = max(big, a);
+  }
+  big = __reduce_max_sync(0xffffffffu, big);
+  const int k = (int)(big >> 23) - 127 - p.exponent - 8 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return (uint32_t)min(max(k, 0), kMaxK) + 1u;
+}
+// Into the pending bits of the block's word.
+__device__ __forceinline__ void put_need(const IoParams& p, int64_t slot, uint32_t need) {
+  uint32_t* word = p.scales + p.div((uint32_t)slot);
+  const uint32_t w = *reinterpret_cast<volatile uint32_t*>(word), had = w & kScaleMask;
+  if (need > had && (need << kPendingShift | had) > w) atomicMax(word, need << kPendingShift | had);
+}
+
+// What the new rows need.
 template <class T, int kDeep>
 __global__ void __launch_bounds__(kIoThreads) kv8_need_kernel(const IoParams p) {
   const int lane = threadIdx.x & 31;
@@ -97,21 +114,8 @@ __global__ void __launch_bounds__(kIoThreads) kv8_need_kernel(const IoParams p) 
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
       if (slot[d] < 0) continue;
-      uint32_t big = 0;  // magnitudes compare as their bits
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t a = x[d].bits(i) & 0x7fffffffu;
-        if (a >= 0x7f800000u) e |= MLA_DEVERR_NONFINITE;
-        else big = max(big, a);
-      }
-      big = __reduce_max_sync(0xffffffffu, big);
-      const int k = (int)(big >> 23) - 127 - p.exponent - 8 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
-      const uint32_t need = (uint32_t)min(max(k, 0), kMaxK) + 1u;
-      if (lane == 0) {
-        uint32_t* word = p.scales + p.div((uint32_t)slot[d]);
-        const uint32_t w = *reinterpret_cast<volatile uint32_t*>(word), had = w & kScaleMask;
-        if (need > had && (need << kPendingShift | had) > w) atomicMax(word, need << kPendingShift | had);
-      }
+      const uint32_t need = need_of(p, x[d], &e);
+      if (lane == 0) put_need(p, slot[d], need);
     }
   }
   put_block_err(p.err, e);
@@ -124,40 +128,30 @@ __device__ __forceinline__ int grown_scale(uint32_t w) {
 
 constexpr uint32_t kClaimed = 1u << (2 * kPendingShift);
 
-// The rows of blocks that held some and have grown, to the new unit.  A thread
-// block looks at `per` of the new rows, claims the grown blocks that nobody has
-// claimed, and moves all their rows, also those that are overwritten next.
-__global__ void __launch_bounds__(kIoThreads) kv8_grow_kernel(const IoParams p) {
-  __shared__ uint32_t claimed[kIoThreads], word[kIoThreads];
-  __shared__ int count;
+// Claims slot s's block if it held rows, has grown and nobody has claimed it; *w
+// receives its word.
+__device__ __forceinline__ bool claim(const IoParams& p, int64_t s, uint32_t* w) {
+  uint32_t* word = p.scales + p.div((uint32_t)s);
+  *w = *reinterpret_cast<volatile uint32_t*>(word);
+  return (*w & kScaleMask) && ((*w >> kPendingShift) & kScaleMask) > (*w & kScaleMask) && !(*w & kClaimed) &&
+         !(atomicOr(word, kClaimed) & kClaimed);
+}
+
+// Moves all rows of `count` claimed blocks to their new units, also those that are
+// overwritten next; a block of kWarps warps.
+template <int kWarps>
+__device__ __forceinline__ void grow(const IoParams& p, const uint32_t* claimed, const uint32_t* word, int count) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) count = 0;
-  grid_dep_wait();
-  grid_dep_launch();
-  __syncthreads();
-  uint32_t e = 0;
-  const int64_t i = (int64_t)blockIdx.x * p.per + threadIdx.x;
-  const int64_t s = (int)threadIdx.x < p.per ? slot_at(p, i, &e) : -1;
-  if (s >= 0) {
-    const uint32_t b = p.div((uint32_t)s), w = *reinterpret_cast<volatile uint32_t*>(p.scales + b);
-    if ((w & kScaleMask) && ((w >> kPendingShift) & kScaleMask) > (w & kScaleMask) && !(w & kClaimed) &&
-        !(atomicOr(p.scales + b, kClaimed) & kClaimed)) {
-      const int at = atomicAdd(&count, 1);
-      claimed[at] = b;
-      word[at] = w;
-    }
-  }
-  __syncthreads();
   const int64_t rows = (int64_t)count * p.block;
   constexpr int kDeep = 4;
-  for (int64_t r0 = warp; r0 < rows; r0 += kDeep * kIoWarps) {
+  for (int64_t r0 = warp; r0 < rows; r0 += kDeep * kWarps) {
     uint8_t* row[kDeep];
     int down[kDeep];
     uint4 c[kDeep];
     uint32_t rope[kDeep];
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
-      const int64_t r = r0 + d * kIoWarps;
+      const int64_t r = r0 + d * kWarps;
       row[d] = nullptr;
       if (r >= rows) continue;
       const int at = (int)(r / p.block);
@@ -193,15 +187,63 @@ __global__ void __launch_bounds__(kIoThreads) kv8_grow_kernel(const IoParams p) 
   }
 }
 
+// The rows of blocks that held some and have grown: a thread block looks at `per` of
+// the new rows.
+__global__ void __launch_bounds__(kIoThreads) kv8_grow_kernel(const IoParams p) {
+  __shared__ uint32_t claimed[kIoThreads], word[kIoThreads];
+  __shared__ int count;
+  if (threadIdx.x == 0) count = 0;
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+  uint32_t e = 0, w;
+  const int64_t i = (int64_t)blockIdx.x * p.per + threadIdx.x;
+  const int64_t s = (int)threadIdx.x < p.per ? slot_at(p, i, &e) : -1;
+  if (s >= 0 && claim(p, s, &w)) {
+    const int at = atomicAdd(&count, 1);
+    claimed[at] = p.div((uint32_t)s);
+    word[at] = w;
+  }
+  __syncthreads();
+  grow<kIoWarps>(p, claimed, word, count);
+}
+
 __device__ __forceinline__ float2 rope_pair(const __nv_bfloat16* p) {
   const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 __device__ __forceinline__ float2 rope_pair(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
-// The new rows, in their blocks' units; a row's warp also puts the block's word
-// into its final form (all of a block's rows store the same word, and whichever
+// A new row in its block's unit, by the block's word.  The row's warp also puts the
+// word into its final form (all of a block's rows store the same word, and whichever
 // form another row reads says the same).
+template <class T>
+__device__ __forceinline__ void put_row(const IoParams& p, int64_t slot, uint32_t word, const Part<T>& x, float2 rope) {
+  const int lane = threadIdx.x & 31;
+  const int k = grown_scale(word);
+  const float mul = pow2(-(p.exponent + k));
+  uint32_t v[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float f[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      f[h] = __uint_as_float(x.bits(4 * q + h)) * mul;
+      f[h] = f[h] == f[h] ? f[h] : 0.f;
+    }
+    v[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+  }
+  uint8_t* row = p.cache + slot * p.row_stride;
+  reinterpret_cast<uint4*>(row)[lane] = make_uint4(v[0], v[1], v[2], v[3]);
+  const __nv_bfloat162 r = __floats2bfloat162_rn(rope.x * mul, rope.y * mul);
+  reinterpret_cast<uint32_t*>(row + kRopeOff)[lane] = *reinterpret_cast<const uint32_t*>(&r);
+  if (lane == 0 && word != (uint32_t)k + 1u)
+    *reinterpret_cast<volatile uint32_t*>(p.scales + p.div((uint32_t)slot)) = (uint32_t)k + 1u;
+}
+
+// The new rows, last ones first: the second level cache still holds what the first
+// kernel has read last.
 template <class T, int kDeep>
 __global__ void __launch_bounds__(kIoThreads) kv8_write_kernel(const IoParams p) {
   const int lane = threadIdx.x & 31;
@@ -217,40 +259,76 @@ __global__ void __launch_bounds__(kIoThreads) kv8_write_kernel(const IoParams p)
     float2 rope[kDeep];
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
-      const int64_t i = i0 + d * nwarps;
-      slot[d] = slot_at(p, i, &e);
+      const int64_t i = p.n - 1 - (i0 + d * nwarps);
+      slot[d] = i >= 0 ? slot_at(p, i, &e) : -1;
       if (slot[d] < 0) continue;
       word[d] = *reinterpret_cast<volatile uint32_t*>(p.scales + p.div((uint32_t)slot[d]));
       x[d].load(static_cast<const T*>(p.kv_c) + i * p.kv_c_stride, lane, p.wide);
       rope[d] = rope_pair(static_cast<const T*>(p.k_pe) + i * p.k_pe_stride + 2 * lane);
     }
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      if (slot[d] < 0) continue;
-      const int k = grown_scale(word[d]), down = -(p.exponent + k);
-      const float mul = pow2(down);
-      uint32_t v[4];
+    for (int d = 0; d < kDeep; ++d)
+      if (slot[d] >= 0) put_row(p, slot[d], word[d], x[d], rope[d]);
+  }
+}
+
+// All three steps for few rows: one cluster, whose barrier stands between the steps
+// where the larger calls have a launch (64 rows written and read back: 5.8 -> 3.9 us).
+constexpr int kSmallBlocks = 8, kSmallWarps = 16, kSmallDeep = 2;
+constexpr int kSmallRows = kSmallBlocks * kSmallWarps * kSmallDeep;
+template <class T>
+__global__ void __cluster_dims__(kSmallBlocks, 1, 1) __launch_bounds__(32 * kSmallWarps)
+    kv8_write_small_kernel(const IoParams p) {
+  __shared__ uint32_t claimed[kSmallWarps * kSmallDeep], word[kSmallWarps * kSmallDeep];
+  __shared__ uint32_t found[kSmallWarps];
+  __shared__ int count;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) count = 0;
+  grid_dep_wait();  // launched before the stream's last kernel has ended
+  grid_dep_launch();
+  uint32_t e = 0;
+  int64_t slot[kSmallDeep];
+  Part<T> x[kSmallDeep];
+  float2 rope[kSmallDeep];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float f[4];
+  for (int d = 0; d < kSmallDeep; ++d) {
+    const int64_t i = blockIdx.x + kSmallBlocks * (warp + kSmallWarps * d);
+    slot[d] = slot_at(p, i, &e);
+    if (slot[d] < 0) continue;
+    x[d].load(static_cast<const T*>(p.kv_c) + i * p.kv_c_stride, lane, p.wide);
+    rope[d] = rope_pair(static_cast<const T*>(p.k_pe) + i * p.k_pe_stride + 2 * lane);
+  }
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          f[h] = __uint_as_float(x[d].bits(4 * q + h)) * mul;
-          f[h] = f[h] == f[h] ? f[h] : 0.f;
-        }
-        v[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3) |
-               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3) << 16;
-      }
-      uint8_t* row = p.cache + slot[d] * p.row_stride;
-      reinterpret_cast<uint4*>(row)[lane] = make_uint4(v[0], v[1], v[2], v[3]);
-      const __nv_bfloat162 r = __floats2bfloat162_rn(rope[d].x * mul, rope[d].y * mul);
-      reinterpret_cast<uint32_t*>(row + kRopeOff)[lane] = *reinterpret_cast<const uint32_t*>(&r);
-      if (lane == 0) {
-        volatile uint32_t* w = p.scales + p.div((uint32_t)slot[d]);
-        if (*w != (uint32_t)k + 1u) *w = (uint32_t)k + 1u;
-      }
+  for (int d = 0; d < kSmallDeep; ++d) {
+    if (slot[d] < 0) continue;
+    const uint32_t need = need_of(p, x[d], &e);
+    if (lane == 0) put_need(p, slot[d], need);
+  }
+  const uint32_t any = __reduce_or_sync(0xffffffffu, e);
+  if (lane == 0) found[warp] = any;
+  sm100::cluster_sync();
+  if (threadIdx.x == 0) {
+    uint32_t f = 0;
+    for (int w = 0; w < kSmallWarps; ++w) f |= found[w];
+    p.err[kvq::kErrFirst + blockIdx.x] = f;
+    if (blockIdx.x == 0) p.err[0] = gridDim.x;
+  }
+#pragma unroll
+  for (int d = 0; d < kSmallDeep; ++d) {
+    uint32_t w;
+    if (lane == 0 && slot[d] >= 0 && claim(p, slot[d], &w)) {
+      const int at = atomicAdd(&count, 1);
+      claimed[at] = p.div((uint32_t)slot[d]);
+      word[at] = w;
     }
   }
+  __syncthreads();
+  grow<kSmallWarps>(p, claimed, word, count);
+  sm100::cluster_sync();
+#pragma unroll
+  for (int d = 0; d < kSmallDeep; ++d)
+    if (slot[d] >= 0)
+      put_row(p, slot[d], *reinterpret_cast<volatile uint32_t*>(p.scales + p.div((uint32_t)slot[d])), x[d], rope[d]);
 }
 
 __device__ __forceinline__ void put_latents(__nv_bfloat16* dst, const float (&f)[16], bool wide) {
@@ -383,10 +461,16 @@ extern "C" mla_status mla_kv8_write(const mla_kv8_cache* cache, const mla_kvq_ro
   bool noop = false;
   mla_status st = make_io(cache, src, workspace, ws_bytes, &p, &noop);
   if (st != MLA_OK || noop) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = src->dtype == MLA_BF16;
+  if (p.n <= kSmallRows) {
+    const auto small = bf16 ? kv8_write_small_kernel<__nv_bfloat16> : kv8_write_small_kernel<float>;
+    const cudaError_t e = launch_kernel(small, dim3(kSmallBlocks), dim3(32 * kSmallWarps), 0, s, true, p);
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  }
   int grid = 0;
   st = io_grid(p.n, 8, &grid);
   if (st != MLA_OK) return st;
-  const bool bf16 = src->dtype == MLA_BF16;
   const auto need = bf16 ? kv8_need_kernel<__nv_bfloat16, 2> : kv8_need_kernel<float, 1>;
   const auto write = bf16 ? kv8_write_kernel<__nv_bfloat16, 2> : kv8_write_kernel<float, 1>;
   // rows per block of the growing kernel: a few blocks of threads per SM
@@ -394,7 +478,6 @@ extern "C" mla_status mla_kv8_write(const mla_kv8_cache* cache, const mla_kvq_ro
   if (p.per < kIoWarps) p.per = kIoWarps;
   if (p.per > kIoThreads) p.per = kIoThreads;
   const int64_t growers = (p.n + p.per - 1) / p.per;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (launch_kernel(need, dim3(grid), dim3(kIoThreads), 0, s, true, p) != cudaSuccess ||
       launch_kernel(kv8_grow_kernel, dim3((unsigned)growers), dim3(kIoThreads), 0, s, true, p) != cudaSuccess ||
       launch_kernel(write, dim3(grid), dim3(kIoThreads), 0, s, true, p) != cudaSuccess)
