@@ -133,10 +133,11 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const Params p) {
   const int64_t takes = total[2], drops = total[3];
   uint32_t err = bad;
   if (head < 0 || tail < head || tail - head > a.ring) err |= MLA_DEVERR_PAGES;
-  else if (takes > tail - head || tail - head + drops > a.ring) err |= MLA_DEVERR_CAPACITY;
-  if (total[0] > (N)INT32_MAX || total[1] > (N)INT32_MAX || takes > INT32_MAX || drops > INT32_MAX ||
-      (a.kv_indices && total[0] > a.indices_len) || (a.slots && a.new_lens && total[1] > a.slots_len))
-    err |= MLA_DEVERR_CAPACITY;
+  // with a bad request the sums mean nothing
+  if (!err && (takes > tail - head || tail - head + drops > a.ring || total[0] > (N)INT32_MAX ||
+               total[1] > (N)INT32_MAX || takes > INT32_MAX || drops > INT32_MAX ||
+               (a.kv_indices && total[0] > a.indices_len) || (a.slots && a.new_lens && total[1] > a.slots_len)))
+    err = MLA_DEVERR_CAPACITY;
   uint32_t late = 0;
   if (!err) {  // the same in every block
     for (int b = b0; b < b1; ++b) {
