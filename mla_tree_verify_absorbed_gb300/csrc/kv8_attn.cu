@@ -16,7 +16,7 @@
 //            upper byte of an f16 one: t1 and t2 are the upper bytes of w and of what is
 //            left, t3 what is left then, rounded.  3 + 3 + 3 significant bits, off by
 //            at most 2^-9, as bf16.
-// The rope product (bf16) is accumulated on the queries' first term.
+// The rope product (bf16) is accumulated on the queries' terms, half on each.
 //
 // Blocks' scales.  A token's score is s_j = c_r 2^k_j S_jr (c_r: scale, row unit),
 // and its value 2^k_j times its codes, so O takes the weights 2^(s_j + k_j - m): the
@@ -403,8 +403,10 @@ __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ct
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) query_terms(w[2 * q], w[2 * q + 1], mul, finite, hi[q], lo[q]);
+    // the rope query by halves on both terms: zeros on one of them would make NaN of infinite rope keys
+    const float half = 0.5f * mul;
     const __nv_bfloat162 pm =
-        __floats2bfloat162_rn(__uint_as_float(pe << 16) * mul, __uint_as_float(pe & 0xffff0000u) * mul);
+        __floats2bfloat162_rn(__uint_as_float(pe << 16) * half, __uint_as_float(pe & 0xffff0000u) * half);
     const int n = 32 * (r >> 4) + (r & 15);
     const uint32_t q0 = smem_u32(smem) + kOffQ;
     const uint32_t at = q0 + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);
@@ -412,7 +414,7 @@ __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ct
     st_shared_v4(at + 16 * 128, lo[0], lo[1], lo[2], lo[3]);  // 16 rows on: the same swizzle
     const uint32_t rope = 4 * kQChunk + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + 4 * (lane & 3);
     *reinterpret_cast<uint32_t*>(smem + kOffQ + rope) = *reinterpret_cast<const uint32_t*>(&pm);
-    *reinterpret_cast<uint32_t*>(smem + kOffQ + rope + 16 * 128) = 0u;
+    *reinterpret_cast<uint32_t*>(smem + kOffQ + rope + 16 * 128) = *reinterpret_cast<const uint32_t*>(&pm);
     if (lane == 0) c->unit[r] = query_factor(p.scale_log2, t);
   }
   }

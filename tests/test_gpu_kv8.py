@@ -313,7 +313,8 @@ def problem(B=1, Q=4, H=8, lens=None, page=1, seed=0, tree="tree", window=0, sin
     unit = 2.0 ** (exponent + k)[:, None]
     gain = np.exp(0.4 * r.standard_normal(512))
     rows = np.zeros((pool, 640), np.uint8)
-    rows[:, :512] = O.nearest_codes(r.standard_normal((pool, 512)) * gain * 2.0 ** (exponent + 6) / unit)
+    x = (r.standard_normal((pool, 512)) * gain * 2.0 ** (exponent + 6) / unit).clip(-448, 448)
+    rows[:, :512] = torch.from_numpy(x).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     rows[:, 512:] = O.bf16_bits(r.standard_normal((pool, 64)) / unit).view(np.uint8).reshape(pool, 128)
     # rows that no position names hold anything
     used = np.zeros(pool, bool)
@@ -402,8 +403,8 @@ SHAPES = [
     dict(B=1, Q=4, H=10, lens=[2900], stride=672),
     dict(B=70, Q=1, H=2, lens=[(37 * i) % 400 for i in range(70)], tree="null"),
     dict(B=1, Q=64, H=64, lens=[130], tree="chain"),
-    dict(B=1, Q=7, H=8, lens=[2000], page=1 << 20),
-    dict(B=1, Q=7, H=18, lens=[2000], page=1 << 20),
+    dict(B=1, Q=7, H=8, lens=[2000], page=1 << 13),
+    dict(B=1, Q=7, H=18, lens=[2000], page=1 << 13),
 ]
 
 
