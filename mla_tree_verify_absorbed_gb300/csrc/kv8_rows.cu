@@ -537,8 +537,10 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
         if (!wait_warp(&c->m_ready[wg ^ 1][wq], ((i - 1) >> 1) & 1u, c)) return false;
         if (t > t0) mp = c->m_run[wg ^ 1][r];
       }
-      // it moves only when this tile beats it by 2^kLazy
-      const float mn = tmax > mp + kLazy ? tmax : mp;
+      // It moves only when this tile beats it by 2^kLazy in some row of the warp, and then
+      // in all of them: O's rows are rescaled together, which holds up its products for
+      // 1,300 cycles, and so less often.
+      const float mn = __any_sync(0xffffffffu, tmax > mp + kLazy) ? fmaxf(tmax, mp) : mp;
       c->m_run[wg][r] = mn;
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->m_ready[wg][wq]);
