@@ -54,10 +54,6 @@ struct Params : kvq::Params {
   int box;        // tokens that lie in a row within a page, at most 32; 0: fewer than 8
 };
 
-// Tensor maps of the pool: single rows, and boxes of Params::box rows; 128 bytes of each.
-struct CacheMaps {
-  CUtensorMap row, box;
-};
 // Tensor maps of the queries, [B Q H] rows of 512 and of 64, in boxes of 64 elements
 // x Params::box_rows rows.
 struct QueryMaps {
@@ -102,7 +98,7 @@ __device__ __forceinline__ void query_terms(uint32_t x0, uint32_t x1, float mul,
 // current device (0 when it cannot be had), and the launch.
 namespace rows {
 int clusters_per_gpu();
-mla_status launch(Params p, const CacheMaps& cache, cudaStream_t stream);
+mla_status launch(Params p, const CUtensorMap& cache, cudaStream_t stream);
 }  // namespace rows
 
 mla_status validate_cache(const mla_kv8_cache* c);

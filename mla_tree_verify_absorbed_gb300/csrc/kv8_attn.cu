@@ -94,9 +94,6 @@ constexpr uint32_t kColO = 0, kBlockO = 3 * kRG;  // a block of 128 latents
 constexpr uint32_t kColS = 4 * kBlockO;
 static_assert(kColS + 2 * kQRows <= kTmemCols, "Tensor Memory columns");
 
-// Chunks that come by cp.async where rows come one by one; the others are gathered.
-constexpr int kCopied = 3;
-
 // operand descriptors (smem_desc): all have 128-byte rows in groups of 8, 1 KB apart
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (kLayoutSw128 << 29);
 constexpr uint32_t kDescLo = ((uint32_t)kChunk >> 4) << 16;  // no operand reaches beyond one row of 128 bytes
@@ -193,12 +190,12 @@ __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
 // ---------------------------------------------------------------------------
 // Warp pw fetches tokens 32 pw .. of every tile: each lane looks up a token, a tile
 // ahead.  Where pages hold at least 8 tokens in a row and the tile is seen whole, the
-// rows of up to 32 tokens come by one tensor copy per chunk (128 bytes of a row).  Else they come one by
-// one, by both ways that there are, since neither alone fetches fast enough: a
-// gather of four rows takes the copy engine 30 cycles (17 bytes per cycle), and
-// cp.async of 16 bytes a lane reach 20 to 30 bytes per cycle, whatever the depth,
-// where the tensor pipe takes 40.
-__device__ void producer(const Params& p, const CacheMaps& maps, uint8_t* smem, Ctl* c, int pw) {
+// rows of up to 32 tokens come by one tensor copy per chunk (128 bytes of a row), else
+// row by row by cp.async, eight lanes to 128 bytes, zeros for positions that no node
+// sees.  (Gathers of four rows take the copy engine 30 cycles each, 17 bytes per
+// cycle: with them for two of the five chunks, 8 ragged sequences x 32 nodes x 64
+// heads took 250 us, not 223, in the kernel for many rows.)
+__device__ void producer(const Params& p, const CUtensorMap& map, uint8_t* smem, Ctl* c, int pw) {
   const int lane = threadIdx.x & 31;
   uint32_t err = 0, j = 0;
   for_pieces(c, [&](const Piece& pc) {
@@ -211,7 +208,7 @@ __device__ void producer(const Params& p, const CacheMaps& maps, uint8_t* smem, 
       const uint32_t pos = pos_of(v);
       return seen(v, pos) ? __ldg(idx + kvq::page_of(p, pos)) : -1;
     };
-    // -1: a row outside the pool, which reads zeros
+    // -1: not read, zeros in its place
     auto slot_of = [&](int32_t e, int v) -> int32_t {
       const uint32_t pos = pos_of(v);
       const int64_t s = (int64_t)e * p.page_size + (pos - kvq::page_of(p, pos) * (uint32_t)p.page_size);
@@ -231,8 +228,6 @@ __device__ void producer(const Params& p, const CacheMaps& maps, uint8_t* smem, 
       uint8_t* to = smem + st * kStage + 32 * pw * 128;
       const uint32_t dst = smem_u32(to);
       const bool boxes = p.box > 0 && __all_sync(0xffffffffu, seen(v, pos_of(v)));
-      const int32_t s1 = __shfl_down_sync(0xffffffffu, slot, 1), s2 = __shfl_down_sync(0xffffffffu, slot, 2),
-                    s3 = __shfl_down_sync(0xffffffffu, slot, 3);
       if (!wait_warp(&c->empty[st], par, c)) return false;
       uint64_t* full = &c->full[st];
       c->tok_k[st][32 * pw + lane] = scale_of(word);
@@ -243,16 +238,10 @@ __device__ void producer(const Params& p, const CacheMaps& maps, uint8_t* smem, 
         if ((lane & (p.box - 1)) == 0) {
 #pragma unroll
           for (int ck = 0; ck < kChunks; ++ck)
-            tensor_copy_2d(to + ck * kChunk + lane * 128, &maps.box, 128 * ck, slot, full);
+            tensor_copy_2d(to + ck * kChunk + lane * 128, &map, 128 * ck, slot, full);
         }
       } else {
         const int r7 = lane & 7, ch = lane >> 3;
-        if ((lane & 3) == 0) {
-#pragma unroll
-          for (int ck = kCopied; ck < kChunks; ++ck)
-            tensor_gather4(dst + ck * kChunk + lane * 128, &maps.row, 128 * ck, slot, s1, s2, s3, full);
-        }
-        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int token = 4 * i + ch;
@@ -260,11 +249,11 @@ __device__ void producer(const Params& p, const CacheMaps& maps, uint8_t* smem, 
           const uint8_t* src = p.cache + (uint64_t)(uint32_t)max(s, 0) * (uint32_t)p.row_stride + 16 * r7;
           const uint32_t at = dst + token * 128 + ((r7 ^ (token & 7)) << 4), bytes = s >= 0 ? 16u : 0u;
 #pragma unroll
-          for (int ck = 0; ck < kCopied; ++ck) cp_async_16_zfill(at + ck * kChunk, src + 128 * ck, bytes);
+          for (int ck = 0; ck < kChunks; ++ck) cp_async_16_zfill(at + ck * kChunk, src + 128 * ck, bytes);
         }
         cp_async_mbar_hold(full);  // until they have landed
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(full, (kChunks - kCopied) * 32 * 128);
+        if (lane == 0) mbar_arrive(full);
       }
       slot = next;
       word = next_word;
@@ -324,7 +313,7 @@ __device__ void products(const Params& p, uint8_t* smem, Ctl* c) {
       // The S tile before the last has been read when its weights are there.
       if (s < end && s <= j + 1 && test(&c->full[s % kStages], s)) {
         tc_fence_after();
-        fence_proxy_async_smem();  // parts may come by cp.async, without a fence of their writers
+        fence_proxy_async_smem();  // the tile may have come by cp.async, without a fence of its writers
         if (leader) {
           const uint32_t d = kColS + (s & 1u) * kQRows, a = desc_lo(smem, (s % kStages) * kStage);
 #pragma unroll
@@ -680,7 +669,7 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
   if (bad) atomicOr(&c->err, MLA_DEVERR_PARENT);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p, const __grid_constant__ CacheMaps maps) {
+__global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   Ctl* c = reinterpret_cast<Ctl*>(smem + kOffCtl);
@@ -728,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const Params p, c
   }
   if (worker < n && c->tmem_base == 0) {
     if (warp < kRowWarps) softmax(p, smem, c, warp);
-    else if (warp < kWarpMma) producer(p, maps, smem, c, warp - kWarpProd);
+    else if (warp < kWarpMma) producer(p, map, smem, c, warp - kWarpProd);
     else if (warp == kWarpMma) products(p, smem, c);
     else Work::schedule(p, c, worker);
   }
@@ -1052,14 +1041,14 @@ mla_status run_attn(const mla_kv8_attn_args* a, void* workspace, size_t ws_bytes
   p.hold = hold_ns != 0;
   p.wait_ns = p.hold ? hold_ns : kWaitLimitNs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  CacheMaps maps;
-  if (!cache_map(&maps.row, a->cache, 1) || !cache_map(&maps.box, a->cache, p.box > 0 ? p.box : 1)) return MLA_ERR_CUDA;
-  if (pl.many) return rows::launch(p, maps, s);
+  CUtensorMap map;
+  if (!cache_map(&map, a->cache, p.box > 0 ? p.box : 1)) return MLA_ERR_CUDA;
+  if (pl.many) return rows::launch(p, map, s);
   const int n = pl.workers;
   // per call: the attribute belongs to the context, which may be a new one
   if (cudaFuncSetAttribute(kv8_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc) != cudaSuccess)
     return MLA_ERR_CUDA;
-  if (launch_kernel(kv8_attn_kernel, dim3(n), dim3(kThreads), kSmemAlloc, s, true, p, maps) != cudaSuccess)
+  if (launch_kernel(kv8_attn_kernel, dim3(n), dim3(kThreads), kSmemAlloc, s, true, p, map) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (n > 1 && launch_kernel(kv8_merge_kernel, dim3(2 * n), dim3(kMergeThreads), 0, s, true, p) != cudaSuccess)
     return MLA_ERR_CUDA;

@@ -56,13 +56,13 @@ using kvq::Start;
 
 constexpr int kRG = kvq::kRows128;
 constexpr int kTK = 64;  // tokens per tile
-// Warps 0-7 hold rows, in two groups that take the tiles of one parity; 8 to 11 fetch,
-// 8 and 9 by tensor copies, 10 and 11 by cp.async, 32 tokens each.
-constexpr int kRowWarps = 8, kProducerWarps = 4;
+// Warps 0-7 hold rows, in two groups that take the tiles of one parity; 8 and 9 fetch
+// 32 tokens each.
+constexpr int kRowWarps = 8, kProducerWarps = 2;
 constexpr int kWarpProd = kRowWarps;
-constexpr int kWarpAux = 12;    // TMEM allocation; rank 0: weight copies
-constexpr int kWarpMma = 13;
-constexpr int kWarpSched = 14;  // the pieces of work
+constexpr int kWarpAux = 10;    // TMEM allocation; rank 0: weight copies
+constexpr int kWarpMma = 11;
+constexpr int kWarpSched = 12;  // the pieces of work
 constexpr int kThreads = 32 * (kWarpSched + 1);
 constexpr uint32_t kTmemCols = 512;
 
@@ -210,15 +210,12 @@ constexpr int kFollowers = kRowWarps + kProducerWarps + 1;  // and, in the score
 // ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
-// As in kv8_attn.cu: tensor copies of a page's rows where pages allow it, else
-// gathers and cp.async together, each by warps of their own (a warp that issues
-// gathers waits for the copy engine).
+// As in kv8_attn.cu: tensor copies of a page's rows where pages allow it, else cp.async.
+// (Four warps in place of two: 4% slower.)
 template <bool kScore>
-__device__ __forceinline__ void producer(const Params& p, const CacheMaps& maps, uint8_t* smem, Ctl* c, int warp) {
+__device__ __forceinline__ void producer(const Params& p, const CUtensorMap& map, uint8_t* smem, Ctl* c, int pw) {
   constexpr int kChunks = kScore ? kChunksS : kChunksV;
-  constexpr int kCopied = kScore ? 3 : 2;
-  const int lane = threadIdx.x & 31, pw = warp & 1;
-  const bool tensor = warp < 2;
+  const int lane = threadIdx.x & 31;
   uint32_t err = 0, j = 0, seg = 0;
   for_pieces(c, [&](const Piece& pc) {
     const int32_t* idx = (p.page_size == 1 ? p.kv_indices : p.block_table) + pc.entry;
@@ -230,7 +227,7 @@ __device__ __forceinline__ void producer(const Params& p, const CacheMaps& maps,
       const uint32_t pos = pos_of(v);
       return seen(v, pos) ? __ldg(idx + kvq::page_of(p, pos)) : -1;
     };
-    // -1: a row outside the pool, which reads zeros
+    // -1: not read, zeros in its place
     auto slot_of = [&](int32_t e, int v) -> int32_t {
       const uint32_t pos = pos_of(v);
       const int64_t s = (int64_t)e * p.page_size + (pos - kvq::page_of(p, pos) * (uint32_t)p.page_size);
@@ -239,7 +236,7 @@ __device__ __forceinline__ void producer(const Params& p, const CacheMaps& maps,
       return -1;
     };
     auto word_of = [&](int32_t slot) {
-      return kScore && tensor && slot >= 0 ? (uint32_t)__ldg(p.scales + p.block((uint32_t)slot)) : 0u;
+      return kScore && slot >= 0 ? (uint32_t)__ldg(p.scales + p.block((uint32_t)slot)) : 0u;
     };
     int32_t slot = slot_of(entry_of(pc.t0), pc.t0), ent = entry_of(pc.t0 + 1);
     uint32_t word = word_of(slot);
@@ -257,43 +254,31 @@ __device__ __forceinline__ void producer(const Params& p, const CacheMaps& maps,
       const bool boxes = p.box > 0 && __all_sync(0xffffffffu, seen(v, pos_of(v)));
       uint64_t* full = &c->full[st];
       if (!wait_warp(&c->empty[st], ((j / kStages) & 1u) ^ 1u, c)) return false;
-      if (kScore && tensor) {
+      if (kScore) {
         c->inv[j % kInv][32 * pw + lane] = pow2(-scale_of(word));
         __syncwarp();
       }
-      if (tensor) {
-        if (lane == 0) mbar_arrive_expect_tx(full, (boxes ? kChunks : kChunks - kCopied) * 32 * 128);
+      if (boxes) {
+        if (lane == 0) mbar_arrive_expect_tx(full, kChunks * 32 * 128);
         __syncwarp();
-        if (boxes) {
-          if ((lane & (p.box - 1)) == 0) {
+        if ((lane & (p.box - 1)) == 0) {
 #pragma unroll
-            for (int ck = 0; ck < kChunks; ++ck)
-              tensor_copy_2d(to + ck * kChunk + lane * 128, &maps.box, 128 * ck, slot, full);
-          }
-        } else {
-          const int32_t s1 = __shfl_down_sync(0xffffffffu, slot, 1), s2 = __shfl_down_sync(0xffffffffu, slot, 2),
-                        s3 = __shfl_down_sync(0xffffffffu, slot, 3);
-          if ((lane & 3) == 0) {
-#pragma unroll
-            for (int ck = kCopied; ck < kChunks; ++ck)
-              tensor_gather4(dst + ck * kChunk + lane * 128, &maps.row, 128 * ck, slot, s1, s2, s3, full);
-          }
+          for (int ck = 0; ck < kChunks; ++ck)
+            tensor_copy_2d(to + ck * kChunk + lane * 128, &map, 128 * ck, slot, full);
         }
       } else {
-        if (!boxes) {
-          const int r7 = lane & 7, ch = lane >> 3;
+        const int r7 = lane & 7, ch = lane >> 3;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int token = 4 * i + ch;
-            const int32_t s = __shfl_sync(0xffffffffu, slot, token);
-            const uint8_t* src = p.cache + (uint64_t)(uint32_t)max(s, 0) * (uint32_t)p.row_stride + 16 * r7;
-            const uint32_t at = dst + token * 128 + ((r7 ^ (token & 7)) << 4), bytes = s >= 0 ? 16u : 0u;
+        for (int i = 0; i < 8; ++i) {
+          const int token = 4 * i + ch;
+          const int32_t s = __shfl_sync(0xffffffffu, slot, token);
+          const uint8_t* src = p.cache + (uint64_t)(uint32_t)max(s, 0) * (uint32_t)p.row_stride + 16 * r7;
+          const uint32_t at = dst + token * 128 + ((r7 ^ (token & 7)) << 4), bytes = s >= 0 ? 16u : 0u;
 #pragma unroll
-            for (int ck = 0; ck < kCopied; ++ck) cp_async_16_zfill(at + ck * kChunk, src + 128 * ck, bytes);
-          }
-          cp_async_mbar_hold(full);  // until they have landed
-          __syncwarp();
+          for (int ck = 0; ck < kChunks; ++ck) cp_async_16_zfill(at + ck * kChunk, src + 128 * ck, bytes);
         }
+        cp_async_mbar_hold(full);  // until they have landed
+        __syncwarp();
         if (lane == 0) mbar_arrive(full);
       }
       slot = next;
@@ -329,7 +314,7 @@ __device__ void score_mma(uint8_t* smem, Ctl* c) {
       const uint32_t st = j % kStages, sb = j % kSBufs;
       if (!wait_warp(&c->s_free[sb], ((j / kSBufs) & 1u) ^ 1u, c)) return false;
       if (!wait_warp(&c->full[st], (j / kStages) & 1u, c)) return false;
-      fence_proxy_async_smem();  // parts may come by cp.async, without a fence of their writers
+      fence_proxy_async_smem();  // the tile may have come by cp.async, without a fence of its writers
       tc_fence_after();
       if (leader) {
         const uint32_t lo = desc_addr(smem, st * kStageS) | kDescLoK, d = kColS + sb * kTK;
@@ -661,7 +646,7 @@ __device__ void value_mma(const Params& p, uint8_t* smem, Ctl* c) {
       const uint32_t st = j % kStages, pb = j % kPBufs;
       if (!wait_warp(&c->full[st], (j / kStages) & 1u, c)) return false;
       if (!wait_warp(&c->o_ready[pb], (j / kPBufs) & 1u, c)) return false;
-      fence_proxy_async_smem();  // parts may come by cp.async, without a fence of their writers
+      fence_proxy_async_smem();  // the tile may have come by cp.async, without a fence of its writers
       tc_fence_after();
       if (leader) {
         const uint32_t da = desc_addr(smem, kOffPV + pb * kPBytes) | kDescLoK;
@@ -788,7 +773,7 @@ __device__ void value_rows(const Params& p, Ctl* c) {
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    kv8_rows_kernel(const Params p, const __grid_constant__ CacheMaps cache, const __grid_constant__ QueryMaps queries) {
+    kv8_rows_kernel(const Params p, const __grid_constant__ CUtensorMap cache, const __grid_constant__ QueryMaps queries) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t rank = cluster_ctarank();
   const int warp = threadIdx.x >> 5;
@@ -936,7 +921,7 @@ int clusters_per_gpu() {
   return n;
 }
 
-mla_status launch(Params p, const CacheMaps& cache, cudaStream_t s) {
+mla_status launch(Params p, const CUtensorMap& cache, cudaStream_t s) {
   p.groups = (p.rows + kRG - 1) / kRG;
   p.box_rows = p.rows < kRG ? p.rows : kRG;
   // per call: the attribute belongs to the context, which may be a new one

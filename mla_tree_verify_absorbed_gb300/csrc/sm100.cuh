@@ -216,16 +216,6 @@ __device__ __forceinline__ void tensor_copy_2d(void* dst, const void* map, int x
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-// Rows y0 .. y3 of a 2-d tensor map whose box is one row high, x elements in, one
-// after the other into this CTA's shared memory; a row outside the tensor reads 0.
-__device__ __forceinline__ void tensor_gather4(uint32_t dst, const void* map, int x, int y0, int y1, int y2, int y3,
-                                               uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Waits until at most `n` of this thread's committed bulk groups are still pending.
 template <int n>
