@@ -745,35 +745,13 @@ constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32, kMergeParts
 constexpr int kMaxWorkers = 256;
 static_assert(kMaxWorkers <= kErrMax && kMaxWorkers <= kMergeThreads, "an error word per CTA");
 __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Params p) {
-  __shared__ Start start[kMaxWorkers];
-  __shared__ int cut[kMaxWorkers];                   // boundaries that are the first inside a row group
-  __shared__ uint32_t cut_mask[kMaxWorkers / 32];
+  __shared__ kvq::Cuts<kMaxWorkers> c;
   __shared__ float weight[kMergeWarps][kMaxWorkers];
-  __shared__ int16_t slot[kMergeWarps][kMaxWorkers];  // -1: an empty piece
   __shared__ float4 sums[kMergeWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dep_wait();
   grid_dep_launch();
-  if (tid < p.clusters) start[tid] = static_cast<const Start*>(p.starts)[tid];
-  __syncthreads();
-  const int workers = start[0].n;
-  bool first = false;
-  if (tid > 0 && tid < workers) {
-    const Start s0 = start[tid - 1], s = start[tid];
-    const int64_t base = div_fast(s.x, kFixed + s.T) * (kFixed + s.T);
-    first = s.x > base && (s0.b != s.b || s0.x <= base);
-  }
-  const uint32_t mask = __ballot_sync(0xffffffffu, first);
-  if (lane == 0 && warp < kMaxWorkers / 32) cut_mask[warp] = mask;
-  __syncthreads();
-  // every block lists them in the same order: they share the list
-  int cuts = 0;
-#pragma unroll
-  for (int w = 0; w < kMaxWorkers / 32; ++w) {
-    if (w == warp && first) cut[cuts + __popc(mask & ((1u << lane) - 1u))] = tid;
-    cuts += __popc(cut_mask[w]);
-  }
-  __syncthreads();
+  const int cuts = Work::list_cuts<kRG>(p, &c);
   // A task is a quarter of a row's columns, or every fourth piece of it; a block takes
   // 16 or 4 of them at a time.
   const int rows_max = min(p.rows, kRG);
@@ -788,37 +766,17 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Param
     int64_t orow = -1;
     const int quarter = task & 3, r = (task >> 2) % rows_max;
     if (task < tasks) {
-      const int k = cut[(task >> 2) / rows_max];
-      const Start s = start[k];
-      const int T = s.T, L = kFixed + T;
-      const int64_t g = div_fast(s.x, L), base = g * L;
-      // pieces: CTA k - 1 has units [0, x_k) of the row group, CTA i >= k [x_i, x_{i+1})
-      auto unit = [&](int i) -> int64_t {
-        return i < k ? 0 : i >= workers || start[i].b != s.b || start[i].x - base > L ? L : start[i].x - base;
-      };
-      int n = 0;
-      bool whole = false;
-      int16_t* sl = slot[warp];
+      const auto g = c.group[(task >> 2) / rows_max];
+      const int n = g.n;
       float* wt = weight[warp];
       float m = -INFINITY;
-      for (int i = lane;; i += 32) {
-        const int w = k - 1 + i;
-        const int64_t z0 = w < workers ? unit(w) : L;
-        if (z0 < L) {
-          const int u0 = Work::cut_tile(z0, T), u1 = Work::cut_tile(unit(w + 1), T);
-          whole |= u0 == 0 && u1 == T;
-          sl[i] = (int16_t)(u1 > u0 ? 2 * w + (u0 == 0) : -1);
-          wt[i] = u1 > u0 ? p.part_lse[(int64_t)sl[i] * kRG + r] : -INFINITY;
-          m = fmaxf(m, wt[i]);
-        }
-        const int some = __popc(__ballot_sync(0xffffffffu, z0 < L));
-        n += some;
-        if (some < 32) break;
+      for (int i = lane; i < n; i += 32) {
+        const int at = c.slot_of(g, i);
+        wt[i] = at >= 0 ? p.part_lse[(int64_t)at * kRG + r] : -INFINITY;
+        m = fmaxf(m, wt[i]);
       }
-      __syncwarp();
-      // when one CTA has it all it stored the results
-      if (r < min((int64_t)kRG, p.rows - g * kRG) && !__any_sync(0xffffffffu, whole)) {
-        orow = (int64_t)s.b * p.rows + g * kRG + r;
+      if (r < g.rows) {
+        orow = g.row + r;
         // the first pieces' results are on their way while the weights are computed
         constexpr int kDeep = 4;
         float4 v[kDeep];
@@ -826,7 +784,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Param
         auto load = [&](int i0) {
 #pragma unroll
           for (int d = 0; d < kDeep; ++d) {
-            const int i = i0 + d * step, at = i < n ? sl[i] : -1;
+            const int i = i0 + d * step, at = i < n ? c.slot_of(g, i) : -1;
             v[d] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (at >= 0) v[d] = __ldcg(src + (int64_t)at * (kRG * kDl / 4));
           }
@@ -860,7 +818,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Param
           load(i0);
         }
       }
-      __syncwarp();  // slot and weight are reused
+      __syncwarp();  // weight is reused
     }
     if (split) {  // the same in every block
       sums[warp][lane] = acc;

@@ -28,8 +28,7 @@
 // What bounds it: the tensor pipes.  Per tile 36 MMAs of 32 cycles in the score CTA
 // (the bf16 rate: two terms at twice the rate), 12 of 128 in the value CTA.
 //
-// Work split as in split.cuh; pieces of a row group are merged by the 4-bit cache's
-// merging kernel.  Every wait is bounded (2 s, less in the self-test); on timeout both
+// Work split as in split.cuh; pieces of a row group are merged by a second kernel.  Every wait is bounded (2 s, less in the self-test); on timeout both
 // CTAs stop issuing, drain what they issued, free their Tensor Memory and report
 // MLA_DEVERR_TIMEOUT.
 #include <cuda.h>
@@ -66,7 +65,8 @@ constexpr int kWarpSched = 12;  // the pieces of work
 constexpr int kThreads = 32 * (kWarpSched + 1);
 constexpr uint32_t kTmemCols = 512;
 
-using Work = kvq::Split<kTK, kvq::kFixed128, 4, kThreads, true>;
+constexpr int kFixed = 4, kMinTiles = 4;
+using Work = kvq::Split<kTK, kFixed, kMinTiles, kThreads, true>;
 
 constexpr int kChunk = kTK * 128;             // 128 bytes of each token: 128 latents, or the rope key
 constexpr int kChunksS = 5, kChunksV = 4;     // score CTA: with the rope keys
@@ -127,7 +127,7 @@ struct alignas(16) Ctl {
   uint64_t s_full[kSBufs];     // score: S tile in TMEM, and the MMA warp's word that the tile's scales are there
   uint64_t s_free[kSBufs];     // score: softmax has loaded S (4 row warps)
   uint64_t q_ready[kPieces];   // score: a piece's queries in TMEM, stages free again (8 row warps)
-  uint64_t q_in;               // score: queries copied (copy bytes)
+  uint64_t q_in[3];            // score: three chunks of the queries copied (copy bytes)
   uint64_t q_max;              // score: halves' largest queries written (8 row warps)
   uint64_t m_ready[2][4];      // score: running maxima after a tile written (per lane quadrant, 1 warp)
   uint64_t p_free[kPBufs];     // score: the PV MMAs that read rank 1's buffer are complete (its commit)
@@ -353,14 +353,14 @@ __device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* s
   const uint32_t chunk = (uint32_t)p.box_rows * 128;
   if (warp == 0 && elect_one()) {
     fence_proxy_async_smem();  // parts of the stages may have been read or written through the generic proxy
-    mbar_arrive_expect_tx(&c->q_in, 9u * chunk);
     const int y = pc.b * p.rows + pc.g * kRG;
 #pragma unroll 1
-    for (int ck = 0; ck < 9; ++ck)
-      tensor_copy_2d(smem + ck * kRG * 128, ck < 8 ? &maps.lat : &maps.pe, ck < 8 ? 64 * ck : 0, y, &c->q_in);
+    for (int ck = 0; ck < 9; ++ck) {
+      if (ck % 3 == 0) mbar_arrive_expect_tx(&c->q_in[ck / 3], 3u * chunk);
+      tensor_copy_2d(smem + ck * kRG * 128, ck < 8 ? &maps.lat : &maps.pe, ck < 8 ? 64 * ck : 0, y, &c->q_in[ck / 3]);
+    }
   }
   __syncwarp();
-  if (!wait_warp(&c->q_in, seg & 1u, c)) return false;
   const bool live = r < rows;  // else another sequence's rows, or none
   auto half_chunk = [&](int ck, uint32_t (&w)[16]) {
 #pragma unroll
@@ -374,6 +374,7 @@ __device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* s
   uint32_t big2 = 0;  // magnitudes compare as their bits
 #pragma unroll 1
   for (int ck = 0; ck < 9; ++ck) {
+    if (ck % 3 == 0 && !wait_warp(&c->q_in[ck / 3], seg & 1u, c)) return false;
     uint32_t w[16];
     half_chunk(ck, w);
 #pragma unroll
@@ -803,7 +804,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&c->p_staged[q], kRowWarps / 2);
       mbar_init(&c->ps_free[q], 1);
     } else if (warp == 9) {
-      mbar_init(&c->q_in, 1);
+      for (int k = 0; k < 3; ++k) mbar_init(&c->q_in[k], 1);
       mbar_init(&c->q_max, kRowWarps);
       mbar_init(&c->fin_free, 32 * kRowWarps);
       mbar_init(&c->fin_full, 32 * kRowWarps);
@@ -878,6 +879,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kWarpAux) tmem_dealloc_cta(c->tmem_base, kTmemCols);
 }
 
+// ---------------------------------------------------------------------------
+// merge
+// ---------------------------------------------------------------------------
+// As the few-rows kernel's: the pieces of a row group that several clusters shared,
+//   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k.
+// Partial results lie 8 columns of all rows after each other, so a warp takes 8 rows x
+// 32 columns, a row and 8 columns per lane, and needs nothing of other warps; with few
+// rows in many pieces four warps share that, every fourth piece each.
+constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32, kMergeParts = 4, kMergeRows = 8;
+__global__ void __launch_bounds__(kMergeThreads, 2) kv8_rows_merge_kernel(const Params p) {
+  __shared__ kvq::Cuts<kvq::kMaxClusters> c;
+  __shared__ float sums[kMergeWarps][9][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int cuts = Work::list_cuts<kRG>(p, &c);
+  const int octets = (min(p.rows, kRG) + kMergeRows - 1) / kMergeRows;
+  const int tasks = cuts * octets * (kDl / 32);
+  const bool split = tasks * kMergeParts <= (int)gridDim.x * kMergeWarps;
+  const int at_once = split ? kMergeWarps / kMergeParts : kMergeWarps;
+  const int part = split ? warp % kMergeParts : 0, step = split ? kMergeParts : 1;
+  for (int t0 = blockIdx.x * at_once; t0 < tasks; t0 += gridDim.x * at_once) {
+    const int task = t0 + (split ? warp / kMergeParts : warp);
+    const int block8 = (task % (kDl / 32)) * 4 + (lane >> 3);
+    const int oct = task / (kDl / 32);
+    float acc[8], total = 0.f, m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] = 0.f;
+    int64_t orow = -1;
+    if (task < tasks) {
+      const auto g = c.group[oct / octets];
+      const int n = g.n, r = oct % octets * kMergeRows + (lane & 7);
+      const bool live = r < g.rows;
+      if (live) orow = g.row + r;
+      constexpr int kDeep = 3;
+      uint32_t v[kDeep][8];
+      float e[kDeep];
+      auto lse_of = [&](int i) {
+        const int at = live && i < n ? c.slot_of(g, i) : -1;
+        return at >= 0 ? __ldcg(p.part_lse + (int64_t)at * kRG + r) : -INFINITY;
+      };
+      auto load = [&](int i0) {
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+          const int i = i0 + d * step, at = live && i < n ? c.slot_of(g, i) : -1;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[d][q] = 0u;
+          if (at >= 0) ld_global_v8(p.part_o + kvq::part_index(at, block8, r), v[d]);
+          e[d] = lse_of(i);
+        }
+      };
+      load(part);
+      for (int i = lane >> 3; i < n; i += 4) m = fmaxf(m, lse_of(i));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      if (m == -INFINITY) m = 0.f;  // no piece has any weight
+      for (int i0 = part;;) {
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+          const float f = __expf(e[d] - m);  // 0 for an empty piece
+          total += f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) acc[q] = fmaf(f, __uint_as_float(v[d][q]), acc[q]);
+        }
+        i0 += kDeep * step;
+        if (i0 >= n) break;
+        load(i0);
+      }
+    }
+    if (split) {  // the same in every block
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sums[warp][q][lane] = acc[q];
+      sums[warp][8][lane] = total;
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int o = 1; o < kMergeParts; ++o) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) acc[q] += sums[warp + o][q][lane];
+          total += sums[warp + o][8][lane];
+        }
+      }
+      __syncthreads();
+    }
+    if (orow >= 0 && part == 0) {
+      const float inv = 1.f / (total == 0.f ? 1.f : total);  // then a row of zeros, as from one piece
+      uint4 o;
+      o.x = pack_bf16(acc[0] * inv, acc[1] * inv);
+      o.y = pack_bf16(acc[2] * inv, acc[3] * inv);
+      o.z = pack_bf16(acc[4] * inv, acc[5] * inv);
+      o.w = pack_bf16(acc[6] * inv, acc[7] * inv);
+      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDl + 8 * block8) = o;
+      if (p.lse && block8 == 0) p.lse[orow] = m + logf(total);
+    }
+  }
+}
+
 namespace {
 
 bool query_map(CUtensorMap* m, const void* base, int64_t rows, int width, int box_rows) {
@@ -934,7 +1032,9 @@ mla_status launch(Params p, const CUtensorMap& cache, cudaStream_t s) {
   if (launch_kernel(kv8_rows_kernel, dim3(2 * p.clusters), dim3(kThreads), kSmemAlloc, s, true, p, cache, maps) !=
       cudaSuccess)
     return MLA_ERR_CUDA;
-  if (p.clusters > 1 && kvq::launch_merge(p, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (p.clusters > 1 && launch_kernel(kv8_rows_merge_kernel, dim3(4 * p.clusters), dim3(kMergeThreads), 0, s, true,
+                                      static_cast<const Params&>(p)) != cudaSuccess)
+    return MLA_ERR_CUDA;
   return MLA_OK;
 }
 

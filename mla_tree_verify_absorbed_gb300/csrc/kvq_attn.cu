@@ -163,7 +163,7 @@ constexpr float kWeightShift = 7.f;
 // lengths.  kFixed 3: 43.4, 41.9, 101.7; 4: 44.5, 40.8, 99.7; 5: 45.3, 39.9, 101.9;
 // 6: 46.5, 40.3, 103.3; 8: 48.9, 43.2, 106.5; kMinTiles 6 in place of 4: 45.3, 40.8,
 // 100.4.  Row groups in long pieces (32 sequences x 128 heads, trees) move by 1%.
-constexpr int kFixed = kFixed128;
+constexpr int kFixed = 4;
 constexpr int kMinTiles = 4;
 
 using Work = Split<kTK, kFixed, kMinTiles, kThreads, false>;
@@ -1125,13 +1125,6 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kvq_merge_kernel(const Param
   }
 }
 
-cudaError_t launch_merge(const Params& p, cudaStream_t s) {
-  // two blocks per SM of the clusters, fewer when even n - 1 cut row groups make fewer tasks
-  const int n = p.clusters, chunks = ((p.rows < kRG ? p.rows : kRG) + kMergeRows - 1) / kMergeRows;
-  const int tasks = (n - 1) * chunks * kMergeParts;
-  return launch_kernel(kvq_merge_kernel, dim3(tasks < 4 * n ? tasks : 4 * n), dim3(kMergeThreads), 0, s, true, p, chunks);
-}
-
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -1304,7 +1297,12 @@ mla_status run_attn(const mla_kvq_attn_args* a, void* workspace, size_t ws_bytes
     return MLA_ERR_CUDA;
   if (launch_kernel(kvq_attn_kernel, dim3(2 * n), dim3(kThreads), kSmemAlloc, s, true, p, maps) != cudaSuccess)
     return MLA_ERR_CUDA;
-  if (n > 1 && launch_merge(p, s) != cudaSuccess) return MLA_ERR_CUDA;
+  // two blocks per SM of the clusters, fewer when even n - 1 cut row groups make fewer tasks
+  const int chunks = ((p.rows < kRG ? p.rows : kRG) + kMergeRows - 1) / kMergeRows;
+  const int tasks = (n - 1) * chunks * kMergeParts;
+  const int blocks = tasks < 4 * n ? tasks : 4 * n;
+  if (n > 1 && launch_kernel(kvq_merge_kernel, dim3(blocks), dim3(kMergeThreads), 0, s, true, p, chunks) != cudaSuccess)
+    return MLA_ERR_CUDA;
   return MLA_OK;
 }
 }  // namespace

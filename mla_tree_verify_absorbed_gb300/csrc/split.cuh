@@ -54,6 +54,23 @@ struct alignas(16) Start {
   int32_t pad[3];
 };
 
+// What the 8-bit cache's merging kernels share among a block's threads: the row groups
+// that several workers have pieces of.  A group's pieces are worker k - 1's, which ends
+// there, and those of workers k, k + 1, ..., which begin in it.
+template <int kMax>
+struct Cuts {
+  struct Group {
+    int64_t row;         // first output row
+    int32_t rows;
+    int32_t k, n, head;  // n pieces; the first one's slot (-1: no tiles)
+  };
+  Start start[kMax];
+  Group group[kMax];
+  int16_t slot[kMax];    // of the piece that a worker begins with (-1: no tiles)
+  uint32_t masks[3][kMax / 32];
+  __device__ __forceinline__ int slot_of(const Group& g, int i) const { return i == 0 ? g.head : slot[g.k - 1 + i]; }
+};
+
 // The last unused sequence from b on before a used one.  Unused ones are passed
 // 128 at a time: one after the other they took 0.18 us each, 204 us for 1,024
 // between two short sequences, and the roles' waits ran out behind ten million.
@@ -100,16 +117,14 @@ __device__ __forceinline__ void for_pieces(Ctl* c, F&& f) {
   }
 }
 
-// Kernels that give a cluster of two CTAs 128 query rows share the merging kernel
-// (kvq_attn.cu), and with it the fixed cost, the most clusters, and where partial
-// results lie: 8 columns of all rows after each other, so that the rows of a warp,
-// one to a lane, fill whole lines (row after row, a warp's store touches 32 lines; 32
-// sequences x 128 heads x 8,192 tokens then took 76.7 us, not 74.3).
-constexpr int kRows128 = 128, kFixed128 = 4, kMaxClusters = 128;
+// Kernels that give a cluster of two CTAs 128 query rows: the most clusters, and where
+// partial results lie: 8 columns of all rows after each other, so that the rows of a
+// warp, one to a lane, fill whole lines (row after row, a warp's store touches 32 lines;
+// 32 sequences x 128 heads x 8,192 tokens then took 76.7 us, not 74.3).
+constexpr int kRows128 = 128, kMaxClusters = 128;
 __device__ __forceinline__ int64_t part_index(int slot, int block8, int r) {
   return (((int64_t)slot * (kDl / 8) + block8) * kRows128 + r) * 8;
 }
-cudaError_t launch_merge(const Params& p, cudaStream_t stream);
 
 // kTK tokens per tile, kThreads threads per CTA; kFixed units for a row group or a
 // piece of one beside its tiles, and kMinTiles tiles at least for a cluster.
@@ -268,6 +283,62 @@ struct Split {
     }
     __syncthreads();
     return total > 0 ? n : -1;
+  }
+
+  // Lists in every block, in the same order, the row groups of kRG rows that no worker has
+  // all tiles of (the others' results are stored); returns how many.  All threads call it,
+  // at least kMax of them.
+  template <int kRG, int kMax>
+  __device__ __forceinline__ static int list_cuts(const Params& p, Cuts<kMax>* c) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid < p.clusters) c->start[tid] = static_cast<const Start*>(p.starts)[tid];
+    __syncthreads();
+    const int workers = c->start[0].n;
+    bool first = false, more = false, whole = false;
+    int head = -1;
+    int64_t g = 0;
+    Start s = {};
+    if (tid > 0 && tid < workers) {
+      const Start s0 = c->start[tid - 1], s1 = c->start[min(tid + 1, workers - 1)];
+      s = c->start[tid];
+      const int L = kFixed + s.T;
+      g = div_fast(s.x, L);
+      const int64_t base = g * L;
+      first = s.x > base && (s0.b != s.b || s0.x <= base);  // the group's first boundary
+      more = s.x > base && !first;
+      const bool ends = tid + 1 < workers && s1.b == s.b && s1.x - base <= L;
+      const int u0 = cut_tile(s.x - base, s.T), u1 = cut_tile(ends ? s1.x - base : L, s.T);
+      c->slot[tid] = (int16_t)(u1 > u0 ? 2 * tid + (u0 == 0) : -1);
+      whole = (u0 == 0 && u1 == s.T) || (first && u0 == s.T);
+      head = u0 > 0 ? 2 * tid - 1 : -1;
+    }
+    const uint32_t more_mask = __ballot_sync(0xffffffffu, more), whole_mask = __ballot_sync(0xffffffffu, whole);
+    if (lane == 0 && warp < kMax / 32) {
+      c->masks[0][warp] = more_mask;
+      c->masks[1][warp] = whole_mask;
+    }
+    __syncthreads();
+    int end = tid + 1;
+    if (first) {
+      while (end < workers && (c->masks[0][end >> 5] >> (end & 31)) & 1u) {
+        whole |= (c->masks[1][end >> 5] >> (end & 31)) & 1u;
+        ++end;
+      }
+    }
+    first = first && !whole;
+    const uint32_t mask = __ballot_sync(0xffffffffu, first);
+    if (lane == 0 && warp < kMax / 32) c->masks[2][warp] = mask;
+    __syncthreads();
+    int cuts = 0;
+#pragma unroll
+    for (int w = 0; w < kMax / 32; ++w) {
+      if (w == warp && first)
+        c->group[cuts + __popc(mask & ((1u << lane) - 1u))] = {
+            (int64_t)s.b * p.rows + g * kRG, (int32_t)min((int64_t)kRG, p.rows - g * kRG), tid, end - tid + 1, head};
+      cuts += __popc(c->masks[2][w]);
+    }
+    __syncthreads();
+    return cuts;
   }
 };
 
