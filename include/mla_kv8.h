@@ -66,9 +66,9 @@ typedef struct {
  * that was empty stay as they were.)
  *
  * An infinite latent is stored as the largest magnitude with its sign and does
- * not count for k, NaN is stored as 0, and MLA_DEVERR_NONFINITE is recorded.  A slot outside [-1, slots)
- * writes nothing and records MLA_DEVERR_SLOT; the other rows are written.  The
- * slots >= 0 must differ from each other.  Two calls that write the same block
+ * not count for k, NaN is stored as 0, and MLA_DEVERR_NONFINITE is recorded.  A
+ * slot outside [-1, slots) writes nothing and records MLA_DEVERR_SLOT; the other
+ * rows are written.  The slots >= 0 must differ from each other.  Two calls that write the same block
  * must be ordered, and so must a write and anything that reads the block's rows.
  * kv_c and k_pe must not overlap the cache.  Equal arguments and cache give
  * equal bytes. */
@@ -111,13 +111,14 @@ typedef struct {
 } mla_kv8_attn_args;
 
 /* Both products take the cache's codes as they are and accumulate in fp32.  A
- * query enters as two e4m3 terms in units of a power of two of its row, off by at
- * most 2^-17 of the row's largest magnitude (0 for elements of at least 2^-9 of
- * it); a softmax weight as three, exact from its rounding to 11 bits on for
- * weights (times the block's 2^k) of at least 2^-14 of the row's largest, else off
- * by at most 2^-25 of that.  lse is natural-log, -infinity with a row of zeros in
- * out where every visible score is -infinity; a row whose queries hold an infinity
- * or NaN is NaN.  Equal arguments give equal bytes.
+ * query enters as two e4m3 terms in units of a power of two of its row: exact for
+ * elements of at least 2^-9 of the row's largest magnitude, else off by at most
+ * 2^-16 of that.  A softmax weight enters as three e5m2 terms, off by at most 2^-9
+ * of its rounding to 11 bits, as a bf16 number would be, or, where it is (times the
+ * block's 2^k) below 2^-15 of the row's largest, by 2^-24 of that.
+ * lse is natural-log, -infinity with a row of zeros in out where every visible
+ * score is -infinity; a row whose queries hold an infinity or NaN is NaN.  Equal
+ * arguments give equal bytes.
  *
  * Table entries of prefix positions that no node of a sequence sees are not
  * read.  A bad table (MLA_DEVERR_PREFIX, _INDPTR, _PAGES: found before any work)

@@ -23,13 +23,17 @@
 // running maximum m is that of s_j + k_j, a weight's size says what the token can
 // add to the output, and the sum for the normaliser takes 2^-k_j off again.
 //
-// What bounds it.  HBM where few rows share a token: 640 bytes a token and row
-// group.  With many rows the tensor pipe: per tile 20 MMAs of 32 cycles for S and 16
-// of 48 for O.
+// What bounds it.  HBM where at most 32 rows share a token: 128 ragged sequences of up
+// to 16,384 tokens x 16 heads read their 280 MB in 67.5 us, 4.1 TB/s; the CTAs' loops run at
+// 90% of the measured copy rate, the rest is their start (7 us: the split, the queries,
+// the first tiles), the output (2 us) and the merge (5 us).  With two row groups to a
+// sequence (16 sequences of 100,000 in windows of 4,096 x 64 heads: 33.4 us) that fixed
+// part, and shared memory: a tile's S takes 1,260 cycles and its O 1,200, not the 640 and
+// 768 of the tensor pipe, since both read their A operand, the 64 or 80 KB of the tile.
 //
 // Shared memory: two stages of 80 KB (128 tokens x 640 bytes; a tile's weights take
-// the place of its rope keys) and 40 KB of queries.  Tensor Memory: O 4 x 96 columns (latent block; row half, term,
-// row), two S tiles of 64 columns (row half, term, row).
+// the place of its rope keys) and 40 KB of queries.  Tensor Memory: O 4 x 96 columns
+// (latent block; row half, term, row), two S tiles of 64 columns (row half, term, row).
 //
 // Work split as in split.cuh; pieces of a row group are merged by a second kernel.
 //
@@ -73,6 +77,8 @@ constexpr int kWarpProd = kRowWarps, kWarpMma = kWarpProd + kProducerWarps, kWar
 constexpr int kThreads = 32 * (kWarpSched + 1);
 constexpr uint32_t kTmemCols = 512;
 
+// A piece costs kFixed tiles beside its own.  The mean of 11 sizes (decode of 40 to 200
+// ragged sequences x 16 to 64 heads, windows) took, against 3: 2 2.1% more, 4 1.4%, 5 3.5%.
 constexpr int kFixed = 3;
 constexpr int kMinTiles = 2;
 using Work = kvq::Split<kTK, kFixed, kMinTiles, kThreads, true>;
@@ -364,48 +370,48 @@ __device__ __forceinline__ void stage_queries(const Params& p, uint8_t* smem, Ct
   const int rows = min(kRG, p.rows - pc.g * kRG), padded = rows > kHalfRows ? kRG : kHalfRows;
 #pragma unroll 1
   for (int r0 = warp; r0 < padded; r0 += 2 * kRowWarps) {
-  uint4 all[2][2] = {};
-  uint32_t rope_all[2] = {};
+    uint4 all[2][2] = {};
+    uint32_t rope_all[2] = {};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = r0 + kRowWarps * i;
-    if (r < rows) {
-      const int64_t row = (int64_t)pc.b * p.rows + pc.g * kRG + r;
-      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q_lat) + row * (2 * kDl)) + 2 * lane;
-      all[i][0] = __ldg(q);
-      all[i][1] = __ldg(q + 1);
-      rope_all[i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.q_pe) + row * (2 * kDr)) + lane);
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + kRowWarps * i;
+      if (r < rows) {
+        const int64_t row = (int64_t)pc.b * p.rows + pc.g * kRG + r;
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q_lat) + row * (2 * kDl)) + 2 * lane;
+        all[i][0] = __ldg(q);
+        all[i][1] = __ldg(q + 1);
+        rope_all[i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.q_pe) + row * (2 * kDr)) + lane);
+      }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = r0 + kRowWarps * i;
-    const uint4 a = all[i][0], b = all[i][1];
-    const uint32_t pe = rope_all[i], w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t big = max(pe & 0x7fffu, (pe >> 16) & 0x7fffu);  // magnitudes compare as their bits
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + kRowWarps * i;
+      const uint4 a = all[i][0], b = all[i][1];
+      const uint32_t pe = rope_all[i], w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t big = max(pe & 0x7fffu, (pe >> 16) & 0x7fffu);  // magnitudes compare as their bits
 #pragma unroll
-    for (int q = 0; q < 8; ++q) big = max(big, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
-    big = __reduce_max_sync(0xffffffffu, big);
-    const bool finite = big < 0x7f80u;
-    const int t = query_unit(big);
-    const float mul = pow2(t);
-    uint32_t hi[4], lo[4];
+      for (int q = 0; q < 8; ++q) big = max(big, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
+      big = __reduce_max_sync(0xffffffffu, big);
+      const bool finite = big < 0x7f80u;
+      const int t = query_unit(big);
+      const float mul = pow2(t);
+      uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) query_terms(w[2 * q], w[2 * q + 1], mul, finite, hi[q], lo[q]);
-    // the rope query by halves on both terms: zeros on one of them would make NaN of infinite rope keys
-    const float half = 0.5f * mul;
-    const __nv_bfloat162 pm =
-        __floats2bfloat162_rn(__uint_as_float(pe << 16) * half, __uint_as_float(pe & 0xffff0000u) * half);
-    const int n = 32 * (r >> 4) + (r & 15);
-    const uint32_t q0 = smem_u32(smem) + kOffQ;
-    const uint32_t at = q0 + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);
-    st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-    st_shared_v4(at + 16 * 128, lo[0], lo[1], lo[2], lo[3]);  // 16 rows on: the same swizzle
-    const uint32_t rope = 4 * kQChunk + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + 4 * (lane & 3);
-    *reinterpret_cast<uint32_t*>(smem + kOffQ + rope) = *reinterpret_cast<const uint32_t*>(&pm);
-    *reinterpret_cast<uint32_t*>(smem + kOffQ + rope + 16 * 128) = *reinterpret_cast<const uint32_t*>(&pm);
-    if (lane == 0) c->unit[r] = query_factor(p.scale_log2, t);
-  }
+      for (int q = 0; q < 4; ++q) query_terms(w[2 * q], w[2 * q + 1], mul, finite, hi[q], lo[q]);
+      // the rope query by halves on both terms: zeros on one of them would make NaN of infinite rope keys
+      const float half = 0.5f * mul;
+      const __nv_bfloat162 pm =
+          __floats2bfloat162_rn(__uint_as_float(pe << 16) * half, __uint_as_float(pe & 0xffff0000u) * half);
+      const int n = 32 * (r >> 4) + (r & 15);
+      const uint32_t q0 = smem_u32(smem) + kOffQ;
+      const uint32_t at = q0 + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);
+      st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(at + 16 * 128, lo[0], lo[1], lo[2], lo[3]);  // 16 rows on: the same swizzle
+      const uint32_t rope = 4 * kQChunk + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + 4 * (lane & 3);
+      *reinterpret_cast<uint32_t*>(smem + kOffQ + rope) = *reinterpret_cast<const uint32_t*>(&pm);
+      *reinterpret_cast<uint32_t*>(smem + kOffQ + rope + 16 * 128) = *reinterpret_cast<const uint32_t*>(&pm);
+      if (lane == 0) c->unit[r] = query_factor(p.scale_log2, t);
+    }
   }
 }
 
@@ -912,7 +918,11 @@ bool cache_map(CUtensorMap* m, const mla_kv8_cache& cache, int rows) {
 }
 
 // Which kernel a call takes, by the query rows of a sequence, its workers (CTAs, or
-// clusters of two), and the rows that a worker takes at once.
+// clusters of two), and the rows that a worker takes at once.  Two groups of 32 rows cost
+// less than one of 128 that is half empty, three do not; us, few rows' kernel and many
+// rows', 30 sequences of 4,096 to 8,192 tokens: 40 rows 57.0 and 63.1, 64 59.6 and 66.0, 96 76.9
+// and 70.0, 128 93.1 and 74.2; 16 windows of 4,096: 64 rows 33.6 and 40.1, 128 49.0 and
+// 45.5.
 constexpr int kFewRows = 64;
 struct Plan {
   bool many;

@@ -12,7 +12,11 @@
 // so it comes from the exponent bits and one comparison.  x 2^-(e+k) is exact in
 // fp32, and the conversion to e4m3 rounds once.
 //
-// Bound: HBM.
+// Bound: HBM, and the launches for few rows.  200,000 rows read back to bf16 take 57.1 us
+// (359 MB: 6.3 TB/s, 93% of the measured copy rate).  40,011 fp32 rows of a prompt are
+// written in 27.5 us; their 92 MB are read by the first kernel and the third, whose order
+// finds the last of them in the second level cache (17.3 us if each byte came once).
+
 #include <cuda_fp8.h>
 
 #include "io.cuh"
@@ -272,14 +276,14 @@ __global__ void __launch_bounds__(kIoThreads) kv8_write_kernel(const IoParams p)
   }
 }
 
-// All three steps for few rows: one cluster, whose barrier stands between the steps
-// where the larger calls have a launch (64 rows written and read back: 5.8 -> 3.9 us).
-constexpr int kSmallBlocks = 8, kSmallWarps = 16, kSmallDeep = 2;
-constexpr int kSmallRows = kSmallBlocks * kSmallWarps * kSmallDeep;
+// All three steps for few rows: one cluster, a warp per row, whose barrier stands between
+// the steps where the larger calls have a launch.  One launch and three, us: 16 rows 3.1
+// and 4.0, 64 3.4 and 4.2, 128 3.7 and 4.4; with two rows to a warp 256 rows 5.0 and 4.4.
+constexpr int kSmallBlocks = 8, kSmallWarps = 16, kSmallRows = kSmallBlocks * kSmallWarps;
 template <class T>
 __global__ void __cluster_dims__(kSmallBlocks, 1, 1) __launch_bounds__(32 * kSmallWarps)
     kv8_write_small_kernel(const IoParams p) {
-  __shared__ uint32_t claimed[kSmallWarps * kSmallDeep], word[kSmallWarps * kSmallDeep];
+  __shared__ uint32_t claimed[kSmallWarps], word[kSmallWarps];
   __shared__ uint32_t found[kSmallWarps];
   __shared__ int count;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -287,22 +291,15 @@ __global__ void __cluster_dims__(kSmallBlocks, 1, 1) __launch_bounds__(32 * kSma
   grid_dep_wait();  // launched before the stream's last kernel has ended
   grid_dep_launch();
   uint32_t e = 0;
-  int64_t slot[kSmallDeep];
-  Part<T> x[kSmallDeep];
-  float2 rope[kSmallDeep];
-#pragma unroll
-  for (int d = 0; d < kSmallDeep; ++d) {
-    const int64_t i = blockIdx.x + kSmallBlocks * (warp + kSmallWarps * d);
-    slot[d] = slot_at(p, i, &e);
-    if (slot[d] < 0) continue;
-    x[d].load(static_cast<const T*>(p.kv_c) + i * p.kv_c_stride, lane, p.wide);
-    rope[d] = rope_pair(static_cast<const T*>(p.k_pe) + i * p.k_pe_stride + 2 * lane);
-  }
-#pragma unroll
-  for (int d = 0; d < kSmallDeep; ++d) {
-    if (slot[d] < 0) continue;
-    const uint32_t need = need_of(p, x[d], &e);
-    if (lane == 0) put_need(p, slot[d], need);
+  Part<T> x;
+  float2 rope;
+  const int64_t i = blockIdx.x + kSmallBlocks * warp;
+  const int64_t slot = slot_at(p, i, &e);
+  if (slot >= 0) {
+    x.load(static_cast<const T*>(p.kv_c) + i * p.kv_c_stride, lane, p.wide);
+    rope = rope_pair(static_cast<const T*>(p.k_pe) + i * p.k_pe_stride + 2 * lane);
+    const uint32_t need = need_of(p, x, &e);
+    if (lane == 0) put_need(p, slot, need);
   }
   const uint32_t any = __reduce_or_sync(0xffffffffu, e);
   if (lane == 0) found[warp] = any;
@@ -313,22 +310,17 @@ __global__ void __cluster_dims__(kSmallBlocks, 1, 1) __launch_bounds__(32 * kSma
     p.err[kvq::kErrFirst + blockIdx.x] = f;
     if (blockIdx.x == 0) p.err[0] = gridDim.x;
   }
-#pragma unroll
-  for (int d = 0; d < kSmallDeep; ++d) {
-    uint32_t w;
-    if (lane == 0 && slot[d] >= 0 && claim(p, slot[d], &w)) {
-      const int at = atomicAdd(&count, 1);
-      claimed[at] = p.div((uint32_t)slot[d]);
-      word[at] = w;
-    }
+  uint32_t mine;
+  if (lane == 0 && slot >= 0 && claim(p, slot, &mine)) {
+    const int at = atomicAdd(&count, 1);
+    claimed[at] = p.div((uint32_t)slot);
+    word[at] = mine;
   }
   __syncthreads();
   grow<kSmallWarps>(p, claimed, word, count);
   sm100::cluster_sync();
-#pragma unroll
-  for (int d = 0; d < kSmallDeep; ++d)
-    if (slot[d] >= 0)
-      put_row(p, slot[d], *reinterpret_cast<volatile uint32_t*>(p.scales + p.div((uint32_t)slot[d])), x[d], rope[d]);
+  if (slot >= 0)
+    put_row(p, slot, *reinterpret_cast<volatile uint32_t*>(p.scales + p.div((uint32_t)slot)), x, rope);
 }
 
 __device__ __forceinline__ void put_latents(__nv_bfloat16* dst, const float (&f)[16], bool wide) {

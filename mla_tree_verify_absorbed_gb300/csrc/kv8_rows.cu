@@ -15,9 +15,8 @@
 //   queries  q 2^t = hi + lo, both e4m3, t per row (see kv8_attn.cu);
 //   weights  three e5m2 terms.  An e5m2 number is the upper byte of an f16 one, so the
 //            terms are cut off an f16 weight byte by byte: w = t1 + t2 + t3, t1 and t2
-//            the upper bytes of w and of what is left, t3 what is left then, rounded.
-//            3 + 3 + 3 significant bits, off by at most 2^-9, the same as bf16, down
-//            to 2^-14 and with 57,344 2^16 between the smallest and the largest.
+//            the upper bytes of w and of what is left, t3 what is left then, rounded:
+//            3 + 3 + 3 significant bits, off by at most 2^-9, as bf16.
 // The rope product (bf16) accumulates in the same columns too.
 //
 // Blocks' scales: see kv8_attn.cu.  A row's score is s_j = c_r 2^k_j S_rj, the running
@@ -25,12 +24,18 @@
 // else the scores are replaced by s_j + k_j in Tensor Memory first, as masked ones
 // are by -infinity, so that the softmax's loops know of neither.
 //
-// What bounds it: the tensor pipes.  Per tile 36 MMAs of 32 cycles in the score CTA
-// (the bf16 rate: two terms at twice the rate), 12 of 128 in the value CTA.
+// What bounds it: the value CTA's products.  Per tile they are 12 MMAs of 128 cycles,
+// 1,536, and their operands, the weights' arrival and the latents' loads pass 200 KB
+// through shared memory, 1,590 cycles; measured 1,690.  The score CTA has 36 MMAs of 32
+// cycles (the bf16 rate: two terms at twice the rate) and a softmax of 1,700 for two tiles
+// in turn.  A tree of 64 nodes x 64 heads over 200,000 tokens, 1.78e12 operations:
+// 1,335 us (1,246 at the best clocks), 1.34 PFLOP/s of the 1.93 measured for bf16.  Short work
+// adds a cluster's start, 6 us per piece for the queries' way into Tensor Memory, 4 us for
+// its output, and the merge: 30 sequences of 4,096 to 8,192 tokens x 128 heads 73.9 us.
 //
-// Work split as in split.cuh; pieces of a row group are merged by a second kernel.  Every wait is bounded (2 s, less in the self-test); on timeout both
-// CTAs stop issuing, drain what they issued, free their Tensor Memory and report
-// MLA_DEVERR_TIMEOUT.
+// Work split as in split.cuh; pieces of a row group are merged by a second kernel.  Every
+// wait is bounded (2 s, less in the self-test); on timeout both CTAs stop issuing, drain
+// what they issued, free their Tensor Memory and report MLA_DEVERR_TIMEOUT.
 #include <cuda.h>
 #include <cuda_fp8.h>
 
@@ -65,7 +70,11 @@ constexpr int kWarpSched = 12;  // the pieces of work
 constexpr int kThreads = 32 * (kWarpSched + 1);
 constexpr uint32_t kTmemCols = 512;
 
-constexpr int kFixed = 4, kMinTiles = 4;
+// A piece costs kFixed tiles beside its own: the queries' way into Tensor Memory, the
+// output, its merging.  Single sizes jump by 6% with where the cuts fall; the mean of 14
+// (decode of 7 to 60 sequences x 128 heads, trees of 8 and 32 nodes x 64 heads, windows
+// of 4,096) took, against kFixed 4: 6 1.8% less, 7 1.9%, 8 2.2%, 10 0.8%.
+constexpr int kFixed = 8, kMinTiles = 4;
 using Work = kvq::Split<kTK, kFixed, kMinTiles, kThreads, true>;
 
 constexpr int kChunk = kTK * 128;             // 128 bytes of each token: 128 latents, or the rope key
@@ -114,7 +123,7 @@ constexpr uint64_t kDrainLimitNs = 20000000ull;
 
 // Weights are 2^(s + k - max + kWeightShift): a lazy maximum lets them reach 2^kLazy
 // above 2^kWeightShift, 2^15 in all, below e5m2's 57,344, so that weights down to
-// 2^-21 of the maximum keep 9 bits and down to 2^-31 some.
+// 2^-15 of the maximum keep 9 bits and down to 2^-23 some.
 constexpr float kLazy = 8.f;
 constexpr float kWeightShift = 7.f;
 
@@ -886,7 +895,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 //   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k.
 // Partial results lie 8 columns of all rows after each other, so a warp takes 8 rows x
 // 32 columns, a row and 8 columns per lane, and needs nothing of other warps; with few
-// rows in many pieces four warps share that, every fourth piece each.
+// rows in many pieces four warps share that, every fourth piece each.  The partial
+// results come from the second level cache; of the 9 us that it adds to 30 sequences of
+// 4,096 to 8,192 tokens x 128 heads 2 are for the launch and 2.5 for the data.
 constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32, kMergeParts = 4, kMergeRows = 8;
 __global__ void __launch_bounds__(kMergeThreads, 2) kv8_rows_merge_kernel(const Params p) {
   __shared__ kvq::Cuts<kvq::kMaxClusters> c;

@@ -109,7 +109,7 @@ def test_writes_are_the_oracles_bytes(kind, exponent, block, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("n", [1, 2, 7, 64, 255, 256, 257, 2433, 9001])
+@pytest.mark.parametrize("n", [1, 2, 7, 64, 127, 128, 129, 255, 256, 257, 2433, 9001])
 def test_rows_of_any_count_with_strides(n, dtype):
     # one wide array holds kv_c and k_pe; cache rows 672 bytes apart; the last block is not whole; sizes differ
     slots, block = n + 3, 13
