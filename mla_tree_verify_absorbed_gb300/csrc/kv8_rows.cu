@@ -144,8 +144,8 @@ struct alignas(16) Ctl {
   uint64_t fin_free;           // score: rank 1 consumed lfin / mfin (256 arrivals)
   uint64_t p_staged[kPStages]; // score: weights and factors staged (4 row warps)
   uint64_t p_full[kPBufs];     // value: weights and factors landed (copy bytes)
-  uint64_t pv_done[kPBufs];    // value: PV MMAs of a tile complete
-  uint64_t o_ready[kPBufs];    // value: O rescaled, weights in (8 row warps)
+  uint64_t pv_done[2][kPBufs];  // value: a tile's MMAs into half of O's columns complete
+  uint64_t o_ready[2][kPBufs];  // value: that half rescaled, weights in (4 row warps)
   uint64_t fin_full;           // value: lfin / mfin written (256 remote arrivals)
   uint64_t drain;
   uint64_t piece_full[kPieces];   // piece written (scheduler warp)
@@ -655,28 +655,32 @@ __device__ void value_mma(const Params& p, uint8_t* smem, Ctl* c) {
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
       const uint32_t st = j % kStages, pb = j % kPBufs;
       if (!wait_warp(&c->full[st], (j / kStages) & 1u, c)) return false;
-      if (!wait_warp(&c->o_ready[pb], (j / kPBufs) & 1u, c)) return false;
-      fence_proxy_async_smem();  // the tile may have come by cp.async, without a fence of its writers
-      tc_fence_after();
-      if (leader) {
-        const uint32_t da = desc_addr(smem, kOffPV + pb * kPBytes) | kDescLoK;
-        const uint32_t dv = desc_addr(smem, st * kStageV) | kDescLoV;
+      // Half of the columns after the other: while the products of one are running, the
+      // other can be rescaled.
 #pragma unroll
-        for (uint32_t k = 0; k < 2; ++k) {  // 32 tokens
+      for (uint32_t h = 0; h < 2; ++h) {
+        if (!wait_warp(&c->o_ready[h][pb], (j / kPBufs) & 1u, c)) return false;
+        fence_proxy_async_smem();  // the tile may have come by cp.async, without a fence of its writers
+        tc_fence_after();
+        if (leader) {
+          const uint32_t da = desc_addr(smem, kOffPV + pb * kPBytes) | kDescLoK;
+          const uint32_t dv = desc_addr(smem, st * kStageV + h * 2 * kChunk) | kDescLoV;
 #pragma unroll
-          for (uint32_t term = 0; term < 3; ++term) {
+          for (uint32_t k = 0; k < 2; ++k) {  // 32 tokens
 #pragma unroll
-            for (uint32_t h = 0; h < 2; ++h)
+            for (uint32_t term = 0; term < 3; ++term)
               mma_cta_ss_f8(h * 256, desc_at(da + ((term * kTerm + k * 32) >> 4), kDescHi64),
-                            desc_at(dv + ((h * 2 * kChunk + k * 32 * 128) >> 4), kDescHi128), kIdescPV,
+                            desc_at(dv + ((k * 32 * 128) >> 4), kDescHi128), kIdescPV,
                             k | term | (uint32_t)(t - pc.t0));
           }
+          mma_cta_commit(&c->pv_done[h][pb]);
+          if (h == 1) {
+            mma_cta_commit(&c->empty[st]);
+            mma_cta_commit(&c->p_free[pb], 0x1);
+          }
         }
-        mma_cta_commit(&c->empty[st]);
-        mma_cta_commit(&c->p_free[pb], 0x1);
-        mma_cta_commit(&c->pv_done[pb]);
+        __syncwarp();
       }
-      __syncwarp();
     }
     return true;
   });
@@ -704,7 +708,7 @@ __device__ void value_rows(const Params& p, Ctl* c) {
       if (t != t0 && wq < quads) {
         const float a = c->alpha[pb][r];
         if (__any_sync(0xffffffffu, a != 1.f)) {
-          if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c)) return false;
+          if (!wait_warp(&c->pv_done[h][(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < 256; c0 += 64) {
@@ -720,10 +724,10 @@ __device__ void value_rows(const Params& p, Ctl* c) {
       fence_proxy_async_smem();  // the weights feed the MMA
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c->o_ready[pb]);
+      if (lane == 0) mbar_arrive(&c->o_ready[h][pb]);
     }
 
-    if (!wait_warp(&c->pv_done[(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c)) return false;
+    if (!wait_warp(&c->pv_done[h][(j - 1) % kPBufs], (uint32_t)((j - 1) / kPBufs) & 1u, c)) return false;
     if (!wait_warp(&c->fin_full, (uint32_t)seg & 1u, c)) return false;
     tc_fence_after();
     const float l = c->lfin[0][r] + c->lfin[1][r], m = c->mfin[r];
@@ -806,8 +810,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&c->s_free[q], kRowWarps / 2);
       mbar_init(&c->p_free[q], 1);
       mbar_init(&c->p_full[q], 1);
-      mbar_init(&c->pv_done[q], 1);
-      mbar_init(&c->o_ready[q], kRowWarps);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&c->pv_done[h][q], 1);
+        mbar_init(&c->o_ready[h][q], kRowWarps / 2);
+      }
     } else if (warp < 4 + kSBufs + kPStages) {
       const int q = warp - 4 - kSBufs;
       mbar_init(&c->p_staged[q], kRowWarps / 2);
