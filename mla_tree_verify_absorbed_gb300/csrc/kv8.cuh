@@ -51,7 +51,7 @@ struct Divider {
 struct Params : kvq::Params {
   const int32_t* scales;
   Divider block;  // slot -> block
-  int box;        // tokens that lie in a row within a page, at most 32; 0: fewer than 8
+  int box;        // tokens that lie in a row within a page, 16 or 32; 0: fewer
 };
 
 // Tensor maps of the queries, [B Q H] rows of 512 and of 64, in boxes of 64 elements

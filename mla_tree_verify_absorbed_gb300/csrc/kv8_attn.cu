@@ -195,12 +195,15 @@ __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
 // producers
 // ---------------------------------------------------------------------------
 // Warp pw fetches tokens 32 pw .. of every tile: each lane looks up a token, a tile
-// ahead.  Where pages hold at least 8 tokens in a row and the tile is seen whole, the
-// rows of up to 32 tokens come by one tensor copy per chunk (128 bytes of a row), else
-// row by row by cp.async, eight lanes to 128 bytes, zeros for positions that no node
-// sees.  (Gathers of four rows take the copy engine 30 cycles each, 17 bytes per
-// cycle: with them for two of the five chunks, 8 ragged sequences x 32 nodes x 64
-// heads took 250 us, not 223, in the kernel for many rows.)
+// ahead.  Where pages hold a multiple of 16 tokens and the tile is seen whole, the rows
+// of 16 or 32 tokens come by one tensor copy per chunk (128 bytes of a row), else row by
+// row by cp.async, eight lanes to 128 bytes, zeros for positions that no node sees.
+// Small copies cost the copy engine more than their bytes: 8 ragged sequences x 32 nodes
+// x 64 heads in the kernel for many rows take 170 us in pages of 64, 180 of 16, and of 8
+// 201 by cp.async and 221 by copies of 8 rows; here, where HBM bounds both, 128 ragged
+// sequences x 16 heads in pages of 8 take 67.5 us either way.  (Gathers of four rows take
+// the engine 30 cycles each, 17 bytes per cycle: with them for two of the five chunks
+// those 201 us were 250.)
 __device__ void producer(const Params& p, const CUtensorMap& map, uint8_t* smem, Ctl* c, int pw) {
   const int lane = threadIdx.x & 31;
   uint32_t err = 0, j = 0;
@@ -241,10 +244,15 @@ __device__ void producer(const Params& p, const CUtensorMap& map, uint8_t* smem,
       if (boxes) {
         if (lane == 0) mbar_arrive_expect_tx(full, kChunks * 32 * 128);
         __syncwarp();
-        if ((lane & (p.box - 1)) == 0) {
+        const bool leader = elect_one();
+#pragma unroll 1
+        for (int i = 0; i < 32; i += p.box) {
+          const int32_t s = __shfl_sync(0xffffffffu, slot, i);
+          if (leader) {
 #pragma unroll
-          for (int ck = 0; ck < kChunks; ++ck)
-            tensor_copy_2d(to + ck * kChunk + lane * 128, &map, 128 * ck, slot, full);
+            for (int ck = 0; ck < kChunks; ++ck) tensor_copy_2d(to + ck * kChunk + i * 128, &map, 128 * ck, s, full);
+          }
+          __syncwarp();
         }
       } else {
         const int r7 = lane & 7, ch = lane >> 3;
@@ -982,9 +990,9 @@ Params make_params(const mla_kv8_attn_args* a, void* ws, const Plan& pl) {
   p.clusters = pl.workers;
   p.scales = a->cache.scales;
   p.block.set(a->cache.block);
-  p.box = a->page_size & -a->page_size;  // the largest power of two that divides the page size
+  p.box = a->page_size & -a->page_size;  // the largest power of two that divides the page size; see producer()
   if (p.box > 32) p.box = 32;
-  if (p.box < 8) p.box = 0;
+  if (p.box < 16) p.box = 0;
   const Layout l = layout(pl);
   char* base = static_cast<char*>(ws);
   p.err = reinterpret_cast<uint32_t*>(base);

@@ -29,9 +29,9 @@
 // through shared memory, 1,590 cycles; measured 1,690.  The score CTA has 36 MMAs of 32
 // cycles (the bf16 rate: two terms at twice the rate) and a softmax of 1,700 for two tiles
 // in turn.  A tree of 64 nodes x 64 heads over 200,000 tokens, 1.78e12 operations:
-// 1,335 us (1,246 at the best clocks), 1.34 PFLOP/s of the 1.93 measured for bf16.  Short work
+// 1,310 us (1,225 at the best clocks), 1.36 PFLOP/s of the 1.93 measured for bf16.  Short work
 // adds a cluster's start, 6 us per piece for the queries' way into Tensor Memory, 4 us for
-// its output, and the merge: 30 sequences of 4,096 to 8,192 tokens x 128 heads 73.9 us.
+// its output, and the merge: 30 sequences of 4,096 to 8,192 tokens x 128 heads 67.8 us.
 //
 // Work split as in split.cuh; pieces of a row group are merged by a second kernel.  Every
 // wait is bounded (2 s, less in the self-test); on timeout both CTAs stop issuing, drain
@@ -219,8 +219,9 @@ constexpr int kFollowers = kRowWarps + kProducerWarps + 1;  // and, in the score
 // ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
-// As in kv8_attn.cu: tensor copies of a page's rows where pages allow it, else cp.async.
-// (Four warps in place of two: 4% slower.)
+// As in kv8_attn.cu: tensor copies of a page's rows where pages allow it, else cp.async,
+// which takes the score CTA 3,500 cycles per tile where the products take 1,690.  (Four
+// warps in place of two: 17% slower; tiles in flight one or two in place of four: the same.)
 template <bool kScore>
 __device__ __forceinline__ void producer(const Params& p, const CUtensorMap& map, uint8_t* smem, Ctl* c, int pw) {
   constexpr int kChunks = kScore ? kChunksS : kChunksV;
@@ -270,10 +271,15 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap& map
       if (boxes) {
         if (lane == 0) mbar_arrive_expect_tx(full, kChunks * 32 * 128);
         __syncwarp();
-        if ((lane & (p.box - 1)) == 0) {
+        const bool leader = elect_one();
+#pragma unroll 1
+        for (int i = 0; i < 32; i += p.box) {
+          const int32_t s = __shfl_sync(0xffffffffu, slot, i);
+          if (leader) {
 #pragma unroll
-          for (int ck = 0; ck < kChunks; ++ck)
-            tensor_copy_2d(to + ck * kChunk + lane * 128, &map, 128 * ck, slot, full);
+            for (int ck = 0; ck < kChunks; ++ck) tensor_copy_2d(to + ck * kChunk + i * 128, &map, 128 * ck, s, full);
+          }
+          __syncwarp();
         }
       } else {
         const int r7 = lane & 7, ch = lane >> 3;
