@@ -928,9 +928,9 @@ bool cache_map(CUtensorMap* m, const mla_kv8_cache& cache, int rows) {
 // Which kernel a call takes, by the query rows of a sequence, its workers (CTAs, or
 // clusters of two), and the rows that a worker takes at once.  Two groups of 32 rows cost
 // less than one of 128 that is half empty, three do not; us, few rows' kernel and many
-// rows', 30 sequences of 4,096 to 8,192 tokens: 40 rows 57.0 and 63.1, 64 59.6 and 66.0, 96 76.9
-// and 70.0, 128 93.1 and 74.2; 16 windows of 4,096: 64 rows 33.6 and 40.1, 128 49.0 and
-// 45.5.
+// rows', 30 sequences of 4,096 to 8,192 tokens: 40 rows 57.0 and 63.1, 64 59.6 and 66.0,
+// 96 76.9 and 70.0, 128 93.1 and 74.2; 16 windows of 4,096: 64 rows 33.6 and 40.1, 128
+// 49.0 and 45.5.
 constexpr int kFewRows = 64;
 struct Plan {
   bool many;
