@@ -58,7 +58,6 @@
 namespace mlav {
 namespace kv8 {
 using namespace sm100;
-using kvq::div_fast;
 using kvq::for_pieces;
 using kvq::kErrFirst;
 using kvq::kErrMax;
