@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const Params p) {
                total[1] > (N)INT32_MAX || takes > INT32_MAX || drops > INT32_MAX ||
                (a.kv_indices && total[0] > a.indices_len) || (a.slots && a.new_lens && total[1] > a.slots_len)))
     err = MLA_DEVERR_CAPACITY;
+  // length + page_size - 1 may pass 32 bits
+  auto pages_of = [&](int32_t length) { return length > 0 ? (int)p.page((uint32_t)length - 1u) + 1 : 0; };
   uint32_t late = 0;
   if (!err) {  // the same in every block
     for (int b = b0; b < b1; ++b) {
@@ -165,7 +167,6 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const Params p) {
       late |= MLA_DEVERR_SLOT;
       return false;
     };
-    auto pages_of = [&](int32_t length) { return length > 0 ? (int)p.page((uint32_t)length - 1u) + 1 : 0; };
     const bool wide = (reinterpret_cast<uintptr_t>(a.kv_indices) & 15u) == 0;
     // first slot of page j of request b, -1 where its id is none
     auto page_of = [&](int b, int j) -> int32_t {
@@ -267,8 +268,7 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const Params p) {
   __syncthreads();
   if (!last || err) return;
   __threadfence();
-  for (int b = tid; b < B; b += kThreads)
-    a.pages_held[b] = (s.length[b + 1] - s.length[b] + a.page_size - 1) / a.page_size;
+  for (int b = tid; b < B; b += kThreads) a.pages_held[b] = pages_of(s.length[b + 1] - s.length[b]);
   if (tid == 0) {
     a.free_state[0] = head + takes;
     a.free_state[1] = tail + drops;

@@ -129,6 +129,40 @@ def test_pages_so_large_that_the_sums_take_64_bits():
     s.step([2 ** 28 - 1, 2 ** 28, 3], [2, 0, 1], status=CAPACITY, idx_len=100)
 
 
+@pytest.mark.parametrize("page", [2 ** 31 - 1, 2 ** 30 + 1, 2 ** 31 - 1000])
+def test_pages_of_nearly_2_to_the_31_slots(page):
+    # one page is the pool: length + page_size passes 2^31 in every step, and what is held has to be right for the next
+    s = State(2, 1, 1, page)
+    s.step([0, -1], Q=11)
+    s.step([2000, -1], Q=2)
+    s.step([2000, 0], [0, 1], status=CAPACITY)   # the page is taken
+    s.step([2002, -1], Q=0)
+
+
+def test_pages_of_nearly_2_to_the_31_slots_change_hands():
+    s = State(2, 1, 1, 2 ** 31 - 1)
+    s.step([1, -1], Q=1)
+    s.step([-1, -1], Q=1)
+    s.step([-1, 70], Q=1)
+    assert s.h["held"] == [0, 1]
+
+
+@pytest.mark.parametrize("page,max_pages", [(2 ** 31 - 1, 1), (2 ** 30 + 1, 1), (100, 21_474_836), (4096, 2 ** 19 - 1)])
+def test_lengths_near_2_to_the_31(page, max_pages):
+    # the table's last page is partly used, then full, then all of it comes back; positions are not listed
+    full = page * max_pages
+    ti = api.kv_tables_alloc(1, max_pages, max_pages, page)
+    slots = torch.zeros(1, dtype=torch.int32).cuda()
+    for prefix, pages in ((full - page + 1, max_pages), (full - 9, max_pages), (full - 1, max_pages), (0, 1),
+                          (full - 2, max_pages)):
+        ti.prefix_lens = i32([prefix])
+        assert api.kv8_check(api.kv_tables(ti, slots)) == 0
+        assert ti.pages_held.tolist() == [pages]
+        assert int(ti.free_state[1] - ti.free_state[0]) == max_pages - pages
+        at = int(ti.block_table[0, prefix // page]) * page + prefix % page
+        assert slots.tolist() == [at]
+
+
 def test_tables_that_cannot_be_built_leave_everything():
     s = State(3, 8, 12, 4, block=4, head=7)
     s.step([10, 5, -1], Q=2)
