@@ -114,8 +114,12 @@ typedef struct {
  * query enters as two e4m3 terms in units of a power of two of its row: exact for
  * elements of at least 2^-9 of the row's largest magnitude, else off by at most
  * 2^-16 of that.  A softmax weight enters as three e5m2 terms, off by at most 2^-9
- * of its rounding to 11 bits, as a bf16 number would be, or, where it is (times the
- * block's 2^k) below 2^-15 of the row's largest, by 2^-24 of that.
+ * of its rounding to 11 bits, as a bf16 number would be.  Beside that the small ones
+ * among the weights of a tile are together off by at most 2^-8.6 of its largest, and
+ * none by more than itself, however small the tile's weights are beside others' and
+ * however the scales of its blocks differ; a tile is 64 positions from a multiple of
+ * 64 on, 128 where Q * H is at most 64.  (2^40 below the largest weight times 2^k
+ * that came before, a weight times 2^k may be off by 2^-64 of that.)
  * lse is natural-log, -infinity with a row of zeros in out where every visible
  * score is -infinity; a row whose queries hold an infinity or NaN is NaN.  Equal
  * arguments give equal bytes.

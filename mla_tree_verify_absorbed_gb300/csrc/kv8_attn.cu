@@ -12,16 +12,24 @@
 // products are added in fp32: queries' as the scores are read, weights' when O is.
 //   queries  q 2^t = hi + lo, both e4m3, t per row.  bf16 has 8 significant bits and a
 //            term 4, so the sum is exact down to 2^-9 of the row's largest element;
-//   weights  w = t1 + t2 + t3 of w rounded to f16, all e5m2.  An e5m2 number is the
-//            upper byte of an f16 one: t1 and t2 are the upper bytes of w and of what is
-//            left, t3 what is left then, rounded.  3 + 3 + 3 significant bits, off by
-//            at most 2^-9, as bf16.
+//   weights  w = t1 + 2^-3 t2 + 2^-6 t3 of w rounded to f16, all e5m2.  An e5m2 number
+//            is the upper byte of an f16 one: t1 and t2 are the upper bytes of w and of 2^3
+//            times what is left, t3 2^3 times what is left then, rounded.  3 + 3 + 3
+//            significant bits, off by at most 2^-9, as bf16, or by 2^-23 where that is more.
 // The rope product (bf16) is accumulated on the queries' terms, half on each.
 //
 // Blocks' scales.  A token's score is s_j = c_r 2^k_j S_jr (c_r: scale, row unit),
-// and its value 2^k_j times its codes, so O takes the weights 2^(s_j + k_j - m): the
-// running maximum m is that of s_j + k_j, a weight's size says what the token can
-// add to the output, and the sum for the normaliser takes 2^-k_j off again.
+// and its value 2^k_j times its codes, so O takes the weights 2^(s_j + k_j - m): m
+// follows the largest s_j + k_j, a weight's size says what the token can add to the
+// output, and the sum for the normaliser takes 2^-k_j off again.
+//
+// m follows the tiles, up and down.  Weights end at 2^-23, so behind a token that towers
+// over all others a running maximum would leave nothing of theirs, though the sum counts
+// them: O, in fp32, has room for both.  So m falls where a tile's largest weight T of a
+// row is below 2^F, F = log2 n + d - 14 for n tokens whose k_j differ by d at most.  Beside
+// their 9 bits, they are then off by 2^-23 each (and 2^-25 from f16), as softmax weights by
+// n 2^-22.6 2^d / T <= 2^-8.6 of the tile's largest together.  m is a whole number, so that
+// O and the sums move exactly.
 //
 // What bounds it.  HBM where at most 32 rows share a token: 128 ragged sequences of up
 // to 16,384 tokens x 16 heads read their 280 MB in 67.5 us, 4.1 TB/s; the CTAs' loops run at
@@ -114,13 +122,18 @@ __device__ __forceinline__ uint32_t desc_lo(const uint8_t* smem, uint32_t off) {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 20000000ull;
 
-// Weights are 2^(s + k - max + kWeightShift): a lazy maximum lets them reach 2^kLazy
-// above 2^kWeightShift, 2^15 in all, below e5m2's 57,344, so that weights down to
-// 2^-15 of the maximum keep 9 bits and down to 2^-23 some.  Moving a maximum costs a
-// pass over a row of O: with 2^2 in place of 2^8, every second tile of 64 nodes x 64
-// heads x 20,000 tokens moved one of its 16 maxima.
-constexpr float kLazy = 8.f;
-constexpr float kWeightShift = 7.f;
+// Weights are 2^(s + k - m + kWeightShift), at most 2^kTop, below e5m2's 57,344.  Moving m
+// costs a pass over a row of O (with 2^2 in place of 2^8 to go, every second tile of 64
+// nodes x 64 heads x 20,000 tokens moved one of its 16), so it is lazy: the largest weight
+// of a piece's first tile is put at 2^kWeightShift, one that is too large, and thus rare,
+// at 2^kRisen, a tile whose weights are too small 2^kFallen above the least.
+constexpr float kTop = 15.f, kWeightShift = 7.f, kRisen = 14.f, kFallen = 8.f;
+constexpr int kLossLog2 = 14;
+// m stays within 2^kDeepest of the largest so far: O and the sums stay far from fp32's
+// limits, and what is lost is below 2^-70 of the largest weight.
+constexpr float kDeepest = 40.f;
+constexpr uint32_t kTermMul = 0x48004800u;  // 2^3 in f16, twice
+constexpr float kTermInv = 0.125f;
 
 struct alignas(16) Ctl {
   uint64_t full[kStages];      // tile landed (each producer warp's copies)
@@ -135,7 +148,8 @@ struct alignas(16) Ctl {
   uint64_t piece_full[kPieces];   // piece written (scheduler warp)
   uint64_t piece_empty[kPieces];  // read by every warp that follows the pieces
   Piece piece[kPieces];
-  alignas(16) int vote[2][2][4];         // parity of the exchange, half, token quadrant
+  alignas(16) uint32_t vote[2][2][4];    // parity of the exchange, half, token quadrant
+  alignas(16) uint32_t k_range[kStages][kProducerWarps];  // of 32 tokens: largest k, and 15 - the least above it
   float part_max[2][2][4][kHalfRows];    // the same, and row
   float part_sum[2][4][kHalfRows];
   alignas(16) float unit[kRG]; // c_r: score factor of a row
@@ -189,6 +203,9 @@ __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t push_sign(uint32_t bits, float x) {  // into the lowest bit
+  return __funnelshift_l(__float_as_uint(x), bits, 1);
+}
 
 // ---------------------------------------------------------------------------
 // producers
@@ -238,7 +255,11 @@ __device__ void producer(const Params& p, const CUtensorMap& map, uint8_t* smem,
       const bool boxes = p.box > 0 && __all_sync(0xffffffffu, seen(v, pos_of(v)));
       if (!wait_warp(&c->empty[st], par, c)) return false;
       uint64_t* full = &c->full[st];
-      c->tok_k[st][32 * pw + lane] = scale_of(word);
+      const int k = scale_of(word);
+      const uint32_t range = __reduce_max_sync(0xffffffffu, slot >= 0 ? k : 0) |
+                             __reduce_max_sync(0xffffffffu, slot >= 0 ? kMaxK - k : 0) << 16;
+      c->tok_k[st][32 * pw + lane] = k;
+      if (lane == 0) c->k_range[st][pw] = range;
       __syncwarp();
       if (boxes) {
         if (lane == 0) mbar_arrive_expect_tx(full, kChunks * 32 * 128);
@@ -436,11 +457,11 @@ __device__ __forceinline__ void rescale_row(uint32_t tO, float a) {
 }
 
 // One piece's state of a row warp: per row, two by two, 2^(score + k) is weighted
-// by 2^shift, shift = kWeightShift - the running maximum; sum of the weights.
+// by 2^shift, shift = kWeightShift - m; sum of the weights.
 struct Rows {
   uint64_t shift[kHalfRows / 2], sum[kHalfRows / 2];
 };
-constexpr float kNone = 3.402823466e38f;  // shift before the first score: any score beats that maximum
+constexpr float kNone = 3.402823466e38f;  // shift before the first score: any score beats that m
 
 __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
   const int lane = threadIdx.x & 31;
@@ -481,6 +502,7 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
       R.sum[r] = 0;
     }
     if (lane < kHalfRows) c->shift[warp][lane] = kNone;
+    float best = -INFINITY;  // a row to a lane, twice: its largest score + k when m last moved
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1; ++t, ++j) {
       const uint32_t st = j % kStages, par = (j >> 1) & 1u;
@@ -525,40 +547,49 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
           y[r] = pair(see[0] ? lo_f32(y[r]) : -INFINITY, see[1] ? hi_f32(y[r]) : -INFINITY);
         }
       }
-      // A maximum moves only when the tile beats it by 2^kLazy, for the four warps of
-      // the half together; until they have all voted the weights are taken with the
-      // maximum as it is.
+      // m moves only when the tile's weights are too large or too small, for the four
+      // warps of the half together; until they have all voted the weights are taken with
+      // m as it is.  A vote: bit 16, no weight is too large; bits 0-15, a row whose weights
+      // are all too small (or that sees none of the tile).
       uint32_t hi[4] = {}, lo[4] = {}, third[4] = {};
       uint64_t x[kHalfRows / 2] = {}, sum[kHalfRows / 2];
       auto weigh = [&](int q) {  // two rows' weights, and their three terms
         const float e0 = ex2_approx(lo_f32(x[q])), e1 = ex2_approx(hi_f32(x[q]));
         sum[q] = fma_f32x2(pair(e0, e1), inv2, R.sum[q]);
         const uint32_t w = pack_f16(e0, e1);
-        const uint32_t r1 = sub_f16(w, w & 0xff00ff00u);                    // exact
-        const uint32_t r2 = sub_f16(r1, r1 & 0xff00ff00u) + 0x00800080u;    // exact, then rounded at the upper byte
+        const uint32_t r1 = kvq::hmul2_f16(sub_f16(w, w & 0xff00ff00u), kTermMul);  // exact
+        const uint32_t r2 = kvq::hmul2_f16(sub_f16(r1, r1 & 0xff00ff00u), kTermMul) + 0x00800080u;  // exact, then rounded at the upper byte
         const uint32_t place = q & 1 ? 0x7510u : 0x3275u;  // upper bytes into the pair's half of the word
         hi[q >> 1] = __byte_perm(hi[q >> 1], w, place);
         lo[q >> 1] = __byte_perm(lo[q >> 1], r1, place);
         third[q >> 1] = __byte_perm(third[q >> 1], r2, place);
       };
-      uint32_t moved = 0xffffffffu;  // rows; in a piece's first tile all, from no maximum at all
+      const uint4 ranges = *reinterpret_cast<const uint4*>(c->k_range[st]);
+      const uint32_t range = __vmaxu2(__vmaxu2(ranges.x, ranges.y), __vmaxu2(ranges.z, ranges.w));
+      const int d = max((int)(range & 0xffffu) + (int)(range >> 16) - kMaxK, 0);
+      const float least = (float)(32 - __clz(min(pc.N - pos0, kTK) - 1) + d - kLossLog2);  // F
+      uint32_t moved = 0xffffffffu;  // rows; in a piece's first tile all, from no m at all
       bool move = t == pc.t0;
       if (!move) {
+        const uint64_t least2 = pair(-least, -least);
         float top = -INFINITY;
+        uint32_t small = 0;
 #pragma unroll
         for (int r = 0; r < kHalfRows / 2; ++r) {
           x[r] = add_f32x2(y[r], R.shift[r]);
           top = fmaxf(top, fmaxf(lo_f32(x[r]), hi_f32(x[r])));
+          const uint64_t above = add_f32x2(x[r], least2);
+          small = push_sign(push_sign(small, lo_f32(above)), hi_f32(above));
         }
-        move = __any_sync(0xffffffffu, top > kWeightShift + kLazy);
-        if (lane == 0) c->vote[i & 1u][half][quad] = move;
+        const uint32_t mine = __reduce_and_sync(0xffffffffu, small | (top > kTop ? 0u : 1u << kHalfRows));
+        if (lane == 0) c->vote[i & 1u][half][quad] = mine;
         exchange();
 #pragma unroll
         for (int q = 0; q < kHalfRows / 2; ++q) weigh(q);
         if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
-        const int4 vote = *reinterpret_cast<const int4*>(c->vote[i & 1u][half]);
+        const uint4 vote = *reinterpret_cast<const uint4*>(c->vote[i & 1u][half]);
         ++i;
-        move = vote.x | vote.y | vote.z | vote.w;
+        move = (vote.x & vote.y & vote.z & vote.w) != 1u << kHalfRows;
       }
       if (move) {
         // the tile's maxima: of the warp's tokens, then of the half's four warps; a row to a lane
@@ -572,10 +603,14 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
         if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
         const int r = lane % kHalfRows;
         const float (&m4)[4][kHalfRows] = c->part_max[i & 1u][half];
-        const float m = fmaxf(fmaxf(m4[0][r], m4[1][r]), fmaxf(m4[2][r], m4[3][r])), was = c->shift[warp][r];
+        const float m = ceilf(fmaxf(fmaxf(m4[0][r], m4[1][r]), fmaxf(m4[2][r], m4[3][r]))), was = c->shift[warp][r];
         ++i;
-        const bool moves = m + was > kWeightShift + kLazy;
-        const float now = moves ? kWeightShift - m : was;
+        best = fmaxf(best, m);
+        const bool rises = m + was > kTop;
+        const float at = rises ? (was == kNone ? kWeightShift : kRisen) : fminf(least + kFallen, kTop);
+        const float to = fminf(at - m, kWeightShift + kDeepest - best);
+        const bool moves = rises || (m > -INFINITY && m + was <= least && to > was);
+        const float now = moves ? to : was;
         const float a = moves ? (was == kNone ? 0.f : exp2f(now - was)) : 1.f;
         __syncwarp();
         c->shift[warp][r] = now;
@@ -654,7 +689,8 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
       tmem_ld16_sync(tO + mb * kBlockO + 2 * kHalfRows, w);
 #pragma unroll
       for (int r = 0; r < kHalfRows; ++r) {
-        const float o = (__uint_as_float(u[r]) + (__uint_as_float(v[r]) + __uint_as_float(w[r]))) * inv[r];
+        const float lo = fmaf(__uint_as_float(w[r]), kTermInv, __uint_as_float(v[r]));
+        const float o = fmaf(lo, kTermInv, __uint_as_float(u[r])) * inv[r];
         if (r < live) {
           if (pc.slot < 0)
             static_cast<__nv_bfloat16*>(p.out)[(orow + r) * kDl + 128 * mb + latent] = __float2bfloat16_rn(o);

@@ -16,12 +16,16 @@
 //   weights  three e5m2 terms.  An e5m2 number is the upper byte of an f16 one, so the
 //            terms are cut off an f16 weight byte by byte: w = t1 + t2 + t3, t1 and t2
 //            the upper bytes of w and of what is left, t3 what is left then, rounded:
-//            3 + 3 + 3 significant bits, off by at most 2^-9, as bf16.
+//            3 + 3 + 3 significant bits, off by at most 2^-9, as bf16, or by 2^-17
+//            where that is more.
 // The rope product (bf16) accumulates in the same columns too.
 //
-// Blocks' scales: see kv8_attn.cu.  A row's score is s_j = c_r 2^k_j S_rj, the running
-// maximum that of s_j + k_j.  Where a tile's tokens share one k, c_r 2^k is one factor;
-// else the scores are replaced by s_j + k_j in Tensor Memory first, as masked ones
+// Blocks' scales: see kv8_attn.cu.  A row's score is s_j = c_r 2^k_j S_rj, and m follows
+// the largest s_j + k_j, up and down: it falls where a tile's largest weight T of a row is
+// not above 2^F, F = log2 n + d - 8 for n tokens whose k_j differ by d at most.  Beside
+// their 9 bits, they are then off by 2^-17 each, as softmax weights by n 2^-17 2^d / T <=
+// 2^-9 of the tile's largest together.  Where a tile's tokens share one k, c_r 2^k is one
+// factor; else the scores are replaced by s_j + k_j in Tensor Memory first, as masked ones
 // are by -infinity, so that the softmax's loops know of neither.
 //
 // What bounds it: the value CTA's products.  Per tile they are 12 MMAs of 128 cycles,
@@ -121,11 +125,15 @@ constexpr uint32_t kIdescPV = idesc_e5m2_e4m3_f32(kRG, 256, 0, 1);
 
 constexpr uint64_t kDrainLimitNs = 20000000ull;
 
-// Weights are 2^(s + k - max + kWeightShift): a lazy maximum lets them reach 2^kLazy
-// above 2^kWeightShift, 2^15 in all, below e5m2's 57,344, so that weights down to
-// 2^-15 of the maximum keep 9 bits and down to 2^-23 some.
-constexpr float kLazy = 8.f;
-constexpr float kWeightShift = 7.f;
+// Weights are 2^(s + k - m + kWeightShift), at most 2^kTop, below e5m2's 57,344.  m moves
+// rarely, since O's products wait meanwhile: the largest weight of a piece's first tile is
+// put at 2^kWeightShift, one that is too large, and thus rare, at 2^kRisen, a tile whose
+// weights are too small 2^kFallen above the least.
+constexpr float kTop = 15.f, kWeightShift = 7.f, kRisen = 14.f, kFallen = 3.f;
+constexpr int kLossLog2 = 8;
+// m stays within 2^kDeepest of the largest so far: O and the sums stay far from fp32's
+// limits, and what is lost is below 2^-64 of the largest weight.
+constexpr float kDeepest = 40.f;
 
 // Barriers that two groups of warps pass at different tiles have one instance
 // per buffer they guard: a wait must never be able to pass on the parity of an
@@ -138,7 +146,7 @@ struct alignas(16) Ctl {
   uint64_t q_ready[kPieces];   // score: a piece's queries in TMEM, stages free again (8 row warps)
   uint64_t q_in[3];            // score: three chunks of the queries copied (copy bytes)
   uint64_t q_max;              // score: halves' largest queries written (8 row warps)
-  uint64_t m_ready[2][4];      // score: running maxima after a tile written (per lane quadrant, 1 warp)
+  uint64_t m_ready[2][4];      // score: m_run, best after a tile written (per lane quadrant, 1 warp)
   uint64_t p_free[kPBufs];     // score: the PV MMAs that read rank 1's buffer are complete (its commit)
   uint64_t ps_free[kPStages];  // score: the staged weights have landed in rank 1 (its first row warp)
   uint64_t fin_free;           // score: rank 1 consumed lfin / mfin (256 arrivals)
@@ -154,9 +162,10 @@ struct alignas(16) Ctl {
   alignas(16) float alpha[kPBufs][kRG];  // rescale factors: staged in rank 0 ([kPStages]), landed in rank 1
   alignas(16) float inv[kInv][kTK];      // score: 2^-k of the tokens' blocks
   uint32_t q_big[2][kRG];      // score: largest magnitude of half a query, as bits
-  float m_run[2][kRG];         // score: running maxima after the last tile of each parity
+  float m_run[2][kRG];         // score: m after the last tile of each parity,
+  float best[2][kRG];          // and the largest score + k so far, rounded up
   float lfin[2][kRG];          // value: each group's row sums of the weights
-  float mfin[kRG];             // value: row maxima, base-2 units
+  float mfin[kRG];             // value: rows' m, base-2 units
   int64_t scan[kThreads / 32];
   int64_t left;                // units of this cluster's interval
   int64_t start_x;             // this cluster's first unit within sequence start_b
@@ -432,9 +441,9 @@ __device__ bool stage_queries(const Params& p, const QueryMaps& maps, uint8_t* s
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : ~0ull >> (64 - n); }
 
 // Online softmax: a thread per row and group of row warps; group `wg` takes
-// the tiles of its parity, all 64 columns of a row in one thread.  The running
-// maximum passes from group to group, warp to warp of the same rows, before
-// the exponentials; each group sums its own weights.
+// the tiles of its parity, all 64 columns of a row in one thread.  m passes
+// from group to group, warp to warp of the same rows, before the
+// exponentials; each group sums its own weights.
 __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* smem, Ctl* c, int warp) {
   const int lane = threadIdx.x & 31;
   const int wq = warp & 3, wg = warp >> 2;
@@ -463,7 +472,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
     const int past = p.window > 0 ? max(P - p.window + nv.depth, -1) : -1;
     const int past_any = p.window > 0 ? max(P - p.window + nq - 1, -1) : -1;
 
-    // m: running maximum of score + k (base-2 units) as of this group's last tile;
+    // m: as of this group's last tile, base-2 units;
     // l: its sum of the shifted weights before rounding, times 2^-k
     float m = -INFINITY, l = 0.f;
     const uint32_t jl = j + (uint32_t)(t1 - t0) - 1;  // the piece's last tile
@@ -492,6 +501,8 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
       const float factor = one ? unit * pow2(k0) : 1.f, kf = (float)k0;
       // which of the tile's 64 tokens the row sees, where not all of them
       const int pos0 = pc.tile(t) * kTK;
+      const int d = (int)(large >> 23) - (int)(small >> 23);
+      const float least = (float)(32 - __clz(min(pc.N - pos0, kTK) - 1) + d - kLossLog2);  // F
       const uint32_t tS = lane_off + kColS + sb * kTK;
       const bool masked = pos0 > P - kTK || pos0 <= past_any;
       if (masked || !one) {
@@ -530,22 +541,32 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
 #pragma unroll 1
       for (int hc = 0; hc < 2; ++hc) tmax = fmaxf(tmax, tmem_max32(tS + 32 * hc));
       // the factor is positive: the scaled maximum is the maximum of the scaled scores
-      tmax = fmaf(tmax, factor, kf);
-      // the maximum after the tile before, from the other group (in the first
-      // tile of a piece the wait only keeps the groups in step)
-      float mp = -INFINITY;
+      // rounded up: m is a whole number, so that O and the sums move exactly
+      tmax = ceilf(fmaf(tmax, factor, kf));
+      // m after the tile before, from the other group (in the first tile of a
+      // piece the wait only keeps the groups in step)
+      float mp = -INFINITY, best = -INFINITY;
       if (i > 0) {
         if (!wait_warp(&c->m_ready[wg ^ 1][wq], ((i - 1) >> 1) & 1u, c)) return false;
-        if (t > t0) mp = c->m_run[wg ^ 1][r];
+        if (t > t0) {
+          mp = c->m_run[wg ^ 1][r];
+          best = c->best[wg ^ 1][r];
+        }
       }
-      // It moves only when this tile beats it by 2^kLazy in some row of the warp, and then
-      // in all of them: O's rows are rescaled together, which holds up its products for
-      // 1,300 cycles, and so less often.
-      const float mn = __any_sync(0xffffffffu, tmax > mp + kLazy) ? fmaxf(tmax, mp) : mp;
+      // It rises only when this tile's weights are too large in some row of the warp, and
+      // then in all rows where they are large: O's rows are rescaled together, which holds
+      // up its products for 1,300 cycles, and so less often.  It falls row by row.
+      best = fmaxf(best, tmax);
+      float mn = mp;
+      if (__any_sync(0xffffffffu, tmax > mp + (kTop - kWeightShift)))
+        mn = mp == -INFINITY ? tmax : fmaxf(mp, tmax - (kRisen - kWeightShift));
+      if (tmax > -INFINITY && tmax - mn <= least - kWeightShift)
+        mn = fminf(mn, fmaxf(tmax + kWeightShift - fminf(least + kFallen, kTop), best - kDeepest));
       c->m_run[wg][r] = mn;
+      c->best[wg][r] = best;
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->m_ready[wg][wq]);
-      const float alpha = mn == mp ? 1.f : exp2f(mp - mn);  // 0 when mp is -inf
+      const float alpha = mn == mp ? 1.f : exp2f(mp - mn);  // 0 when mp is -infinity
       if (mn != m) {
         l *= exp2f(m - mn);
         m = mn;
@@ -599,8 +620,8 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
       if (lane == 0) mbar_arrive(&c->p_staged[ps]);
     }
 
-    // both groups' sums go to the value CTA relative to the final maximum,
-    // which the group of the last tile has
+    // both groups' sums go to the value CTA relative to the last m, which the
+    // group of the last tile has
     if ((jl & 1u) != (uint32_t)wg && !idle) {
       if (!wait_warp(&c->m_ready[wg ^ 1][wq], (jl >> 1) & 1u, c)) return false;
       const float mn = c->m_run[wg ^ 1][r];

@@ -300,6 +300,27 @@ def test_three_bytes_hold_a_weight():
     assert (err <= np.maximum(2.0 ** -9 * f(w), 2.0 ** -17)).all()
 
 
+def test_three_scaled_bytes_hold_a_weight():
+    # the kernel for few rows: what a byte leaves is taken times 2^3, exactly
+    w = np.arange(0x0001, 0x7801, dtype=np.uint16)  # every positive f16 number up to 2^15
+
+    def f(u):
+        return u.astype(np.uint16).view(np.float16).astype(np.float64)
+
+    def rest(u):
+        r = 8 * (f(u) - f(u & 0xff00))
+        h = r.astype(np.float16)
+        assert np.array_equal(h.astype(np.float64), r)
+        return h.view(np.uint16)
+    r1 = rest(w)
+    r2 = rest(r1)
+    t3 = (r2 + 0x80) & 0xff00
+    assert (f(t3) <= 2.0 ** 15).all()
+    err = np.abs(f(w) - f(w & 0xff00) - f(r1 & 0xff00) / 8 - f(t3) / 64)
+    assert (err <= np.maximum(2.0 ** -9 * f(w), 2.0 ** -23)).all()
+    assert (err <= f(w)).all()
+
+
 def test_two_codes_hold_a_query():
     # every bf16 significand at every exponent, in a row whose largest element is scaled to 448 or 255: hi keeps
     # sign, exponent and 3 bits, lo the other 4
