@@ -15,8 +15,9 @@
  * with k in 0..MLA_KV8_MAX_SCALE, once it does.  MLA has one key head, so one
  * scale per block is one per block and head.  `block` is any number of slots,
  * the page size of the tables in most servers; a zeroed array of words is an
- * empty cache, and mla_kv_tables (mla_kv_tables.h) empties the blocks of the
- * pages it hands out.
+ * empty cache, and mla_kv_tables (mla_kv_tables.h) empties the blocks inside the
+ * pages it hands out.  A block that is larger than a page is never emptied, so its
+ * scale never falls; at page_size 1 that leaves blocks of one slot.
  *
  * `exponent` is one number per cache: e4m3 codes lose precision below 2^-6 and
  * stop at 448, and k only makes units larger, so it should put the largest

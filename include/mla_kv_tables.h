@@ -49,8 +49,10 @@ typedef struct {
     int32_t *kv_indices;        /* out, may be NULL: the slots of all positions, request after request; entries
                                    behind the last are left as they were */
     int64_t indices_len;        /* entries of kv_indices */
-    int32_t *scales;            /* in/out, may be NULL: an 8-bit cache's scale words; those of blocks that lie wholly
-                                   in pages that the call hands out become 0 */
+    int32_t *scales;            /* in/out, may be NULL: an 8-bit cache's scale words; those of blocks all of whose
+                                   slots lie in one page that the call hands out become 0 (a block over several
+                                   pages, or over the last page's end, keeps its scale: let `block` divide
+                                   page_size) */
     int block;                  /* slots per block of that cache, >= 1; not used without scales */
 } mla_kv_tables_args;
 
@@ -63,7 +65,9 @@ typedef struct {
  *   or its entries need .. held - 1 go behind the ring's tail, requests in order,
  *     and become -1 in its row.  They can be handed out by the next call.
  * Other entries of block_table are left as they were.  The slot of position p is
- * block_table[b][p / page_size] * page_size + p % page_size.
+ * block_table[b][p / page_size] * page_size + p % page_size.  Every entry below
+ * need names a page: those that a window has passed stay held until the request
+ * ends, and must not be cleared in between.
  *
  * Nothing is written when the tables cannot be built: a prefix length below -1
  * or a negative new length (MLA_DEVERR_PREFIX), a request of more than max_pages
@@ -71,7 +75,8 @@ typedef struct {
  * (MLA_DEVERR_PAGES), too few free pages, a ring too small for the pages that
  * come back, or more positions or new tokens than kv_indices, slots or 32 bits
  * hold (MLA_DEVERR_CAPACITY).  A page id outside [0, num_pages) in a held entry
- * or in the ring records MLA_DEVERR_SLOT; its slots are written as -1. */
+ * or in the ring records MLA_DEVERR_SLOT; its slots are written as -1, and where
+ * its entry comes back it goes into the ring as it is. */
 mla_status mla_kv_tables(const mla_kv_tables_args *args, void *workspace, size_t ws_bytes, mla_stream_t stream);
 
 #ifdef __cplusplus

@@ -995,7 +995,8 @@ class BlockCache:
 
 
 def kv8_alloc(slots: int, block: int = 64, exponent: int = 0, device="cuda") -> BlockCache:
-    """An empty cache of ``slots`` rows."""
+    """An empty cache of ``slots`` rows.  Where kv_tables hands out its pages, ``block`` should divide
+    their size: blocks that are not inside a page are never emptied, and their scales never fall."""
     import torch
     return BlockCache(torch.zeros((slots, KV8_ROW_BYTES), dtype=torch.uint8, device=device),
                       torch.zeros((-(-slots // block),), dtype=torch.int32, device=device), block, exponent)
@@ -1118,7 +1119,7 @@ def kv_tables(ti: TableInputs, slots=None, kv_indptr=None, kv_indices=None, cach
     this step's lengths, in place, and fill the given outputs: ``slots`` of the new
     tokens ([B][Q] or flat; with new_lens any flat length, -1 behind the last),
     ``kv_indptr`` [B+1] and ``kv_indices``, the page-size-1 tables.  With ``cache`` the
-    blocks of pages that are handed out become empty.  Returns the workspace
+    blocks that lie inside a page that is handed out become empty.  Returns the workspace
     (kv8_check reads its error bits)."""
     if check:
         import torch

@@ -99,6 +99,21 @@ def test_random_steps_match_the_oracle(page, block, seed):
             s.step(prefix, Q=int(r.integers(0, 65)) if page > 4 else int(r.integers(0, 4)))
 
 
+def test_only_blocks_inside_a_page_are_emptied():
+    # every page is handed out at once: a block over two pages keeps its scale, and so does one over the last page's end
+    s = State(1, 7, 7, 100, block=64)
+    s.cache.scales.fill_(5)
+    s.host()
+    s.step([699], Q=1)
+    inside = [k * 64 // 100 == (k * 64 + 63) // 100 and k * 64 + 64 <= 700 for k in range(11)]
+    assert inside[10] is False and s.h["words"] == [0 if i else 5 for i in inside]
+    s = State(1, 40, 40, 1, block=8)
+    s.cache.scales.fill_(3)
+    s.host()
+    s.step([39], Q=1)
+    assert s.h["words"] == [3] * 5
+
+
 def test_lengths_of_zero_and_one_and_borders():
     s = State(8, 10, 40, 4, block=4)
     s.step([0, 1, 3, 4, 5, 0, -1, 8], [0, 0, 1, 0, 3, 1, 5, 32])   # the last fills its row of the table
