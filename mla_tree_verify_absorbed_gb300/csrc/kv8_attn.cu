@@ -28,8 +28,10 @@
 // them: O, in fp32, has room for both.  So m falls where a tile's largest weight T of a
 // row is below 2^F, F = log2 n + d - 14 for n tokens whose k_j differ by d at most.  Beside
 // their 9 bits, they are then off by 2^-23 each (and 2^-25 from f16), as softmax weights by
-// n 2^-22.6 2^d / T <= 2^-8.6 of the tile's largest together.  m is a whole number, so that
-// O and the sums move exactly.
+// n 2^-22.6 2^d / T <= 2^-8.6 of the tile's largest together.  It falls by whole numbers, so
+// that O and the sums move exactly, and rises to the largest itself, whose weight is then a
+// power of two and exact: with whole numbers there too, rows of which one token has the
+// most were off twice as much.
 //
 // What bounds it.  HBM where at most 32 rows share a token: 128 ragged sequences of up
 // to 16,384 tokens x 16 heads read their 280 MB in 67.5 us, 4.1 TB/s; the CTAs' loops run at
@@ -603,14 +605,16 @@ __device__ void softmax(const Params& p, uint8_t* smem, Ctl* c, int warp) {
         if (!wait_warp(&c->m_ready[half], i & 1u, c)) return false;
         const int r = lane % kHalfRows;
         const float (&m4)[4][kHalfRows] = c->part_max[i & 1u][half];
-        const float m = ceilf(fmaxf(fmaxf(m4[0][r], m4[1][r]), fmaxf(m4[2][r], m4[3][r]))), was = c->shift[warp][r];
+        const float m = fmaxf(fmaxf(m4[0][r], m4[1][r]), fmaxf(m4[2][r], m4[3][r])), was = c->shift[warp][r];
         ++i;
         best = fmaxf(best, m);
-        const bool rises = m + was > kTop;
-        const float at = rises ? (was == kNone ? kWeightShift : kRisen) : fminf(least + kFallen, kTop);
-        const float to = fminf(at - m, kWeightShift + kDeepest - best);
-        const bool moves = rises || (m > -INFINITY && m + was <= least && to > was);
-        const float now = moves ? to : was;
+        const float largest = m + was;
+        float now = was;
+        if (largest > kTop)
+          now = (was == kNone ? kWeightShift : kRisen) - m;
+        else if (m > -INFINITY && largest <= least)
+          now += floorf(fminf(fminf(least + kFallen, kTop) - largest, kWeightShift + kDeepest - best - was));
+        const bool moves = now != was;
         const float a = moves ? (was == kNone ? 0.f : exp2f(now - was)) : 1.f;
         __syncwarp();
         c->shift[warp][r] = now;

@@ -163,7 +163,7 @@ struct alignas(16) Ctl {
   alignas(16) float inv[kInv][kTK];      // score: 2^-k of the tokens' blocks
   uint32_t q_big[2][kRG];      // score: largest magnitude of half a query, as bits
   float m_run[2][kRG];         // score: m after the last tile of each parity,
-  float best[2][kRG];          // and the largest score + k so far, rounded up
+  float best[2][kRG];          // and the largest score + k so far
   float lfin[2][kRG];          // value: each group's row sums of the weights
   float mfin[kRG];             // value: rows' m, base-2 units
   int64_t scan[kThreads / 32];
@@ -541,8 +541,7 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
 #pragma unroll 1
       for (int hc = 0; hc < 2; ++hc) tmax = fmaxf(tmax, tmem_max32(tS + 32 * hc));
       // the factor is positive: the scaled maximum is the maximum of the scaled scores
-      // rounded up: m is a whole number, so that O and the sums move exactly
-      tmax = ceilf(fmaf(tmax, factor, kf));
+      tmax = fmaf(tmax, factor, kf);
       // m after the tile before, from the other group (in the first tile of a
       // piece the wait only keeps the groups in step)
       float mp = -INFINITY, best = -INFINITY;
@@ -555,13 +554,15 @@ __device__ void score_softmax(const Params& p, const QueryMaps& maps, uint8_t* s
       }
       // It rises only when this tile's weights are too large in some row of the warp, and
       // then in all rows where they are large: O's rows are rescaled together, which holds
-      // up its products for 1,300 cycles, and so less often.  It falls row by row.
+      // up its products for 1,300 cycles, and so less often.  It falls row by row, by whole
+      // numbers, which move O and the sums exactly.
       best = fmaxf(best, tmax);
       float mn = mp;
       if (__any_sync(0xffffffffu, tmax > mp + (kTop - kWeightShift)))
         mn = mp == -INFINITY ? tmax : fmaxf(mp, tmax - (kRisen - kWeightShift));
-      if (tmax > -INFINITY && tmax - mn <= least - kWeightShift)
-        mn = fminf(mn, fmaxf(tmax + kWeightShift - fminf(least + kFallen, kTop), best - kDeepest));
+      const float largest = tmax - mn + kWeightShift;
+      if (tmax > -INFINITY && largest <= least)
+        mn -= floorf(fminf(fminf(least + kFallen, kTop) - largest, mn - best + kDeepest));
       c->m_run[wg][r] = mn;
       c->best[wg][r] = best;
       __syncwarp();
