@@ -64,7 +64,8 @@ typedef struct {
  * its k grew by d, codes become the e4m3 numbers nearest code / 2^d, which is
  * exact for codes of at least 2^(d-6), and rope values are divided by 2^d.  (The
  * bytes of rows that were never written may change with them; those of a block
- * that was empty stay as they were.)
+ * that was empty stay as they were.)  One thread block moves a grown block: blocks of
+ * many thousand slots make such a write slow.
  *
  * An infinite latent is stored as the largest magnitude with its sign and does
  * not count for k, NaN is stored as 0, and MLA_DEVERR_NONFINITE is recorded.  A

@@ -34,10 +34,10 @@
 // most were off twice as much.
 //
 // What bounds it.  HBM where at most 32 rows share a token: 128 ragged sequences of up
-// to 16,384 tokens x 16 heads read their 280 MB in 67.5 us, 4.1 TB/s; the CTAs' loops run at
-// 90% of the measured copy rate, the rest is their start (7 us: the split, the queries,
+// to 16,384 tokens x 16 heads read their 280 MB in 69.0 us, 4.1 TB/s; the CTAs' loops run at
+// about 90% of the measured copy rate, the rest is their start (7 us: the split, the queries,
 // the first tiles), the output (2 us) and the merge (5 us).  With two row groups to a
-// sequence (16 sequences of 100,000 in windows of 4,096 x 64 heads: 33.4 us) that fixed
+// sequence (16 sequences of 100,000 in windows of 4,096 x 64 heads: 34.6 us) that fixed
 // part, and shared memory: a tile's S takes 1,260 cycles and its O 1,200, not the 640 and
 // 768 of the tensor pipe, since both read their A operand, the 64 or 80 KB of the tile.
 //
@@ -217,11 +217,11 @@ __device__ __forceinline__ uint32_t push_sign(uint32_t bits, float x) {  // into
 // of 16 or 32 tokens come by one tensor copy per chunk (128 bytes of a row), else row by
 // row by cp.async, eight lanes to 128 bytes, zeros for positions that no node sees.
 // Small copies cost the copy engine more than their bytes: 8 ragged sequences x 32 nodes
-// x 64 heads in the kernel for many rows take 170 us in pages of 64, 180 of 16, and of 8
-// 201 by cp.async and 221 by copies of 8 rows; here, where HBM bounds both, 128 ragged
-// sequences x 16 heads in pages of 8 take 67.5 us either way.  (Gathers of four rows take
+// x 64 heads in the kernel for many rows take 173 us in pages of 64, 181 of 16, and of 8
+// 206 by cp.async and 222 by copies of 8 rows; here, where HBM bounds both, 128 ragged
+// sequences x 16 heads in pages of 8 take 69 us either way.  (Gathers of four rows take
 // the engine 30 cycles each, 17 bytes per cycle: with them for two of the five chunks
-// those 201 us were 250.)
+// the same took a quarter longer.)
 __device__ void producer(const Params& p, const CUtensorMap& map, uint8_t* smem, Ctl* c, int pw) {
   const int lane = threadIdx.x & 31;
   uint32_t err = 0, j = 0;
@@ -967,9 +967,9 @@ bool cache_map(CUtensorMap* m, const mla_kv8_cache& cache, int rows) {
 // Which kernel a call takes, by the query rows of a sequence, its workers (CTAs, or
 // clusters of two), and the rows that a worker takes at once.  Two groups of 32 rows cost
 // less than one of 128 that is half empty, three do not; us, few rows' kernel and many
-// rows', 30 sequences of 4,096 to 8,192 tokens: 40 rows 57.0 and 63.1, 64 59.6 and 66.0,
-// 96 76.9 and 70.0, 128 93.1 and 74.2; 16 windows of 4,096: 64 rows 33.6 and 40.1, 128
-// 49.0 and 45.5.
+// rows', 30 sequences of 4,096 to 8,192 tokens: 40 rows 58.0 and 59.5, 64 61.4 and 61.1,
+// 96 78.9 and 64.8, 128 95.7 and 69.1; 16 windows of 4,096: 64 rows 33.9 and 37.2, 128
+// 51.6 and 41.2.
 constexpr int kFewRows = 64;
 struct Plan {
   bool many;

@@ -9,7 +9,8 @@
 // entry that this call writes: the ring gives from its head and takes at its tail.
 //
 // Bound: for short lists the chain launch, lengths, sums, entry (8 requests of one new
-// token: 5.5 us; 256 with ragged prefixes and a listing of 1.3 million slots: 9.7 us);
+// token: 5.4 us; 256 with ragged prefixes and a listing of 1.3 million slots: 9.8 us, and
+// 10.4 where 15,937 pages change hands);
 // for long ones the stores, 4 bytes per position.
 #include "kv8.cuh"
 
