@@ -30,13 +30,13 @@
 //
 // What bounds it: the value CTA's products.  Per tile they are 12 MMAs of 128 cycles,
 // 1,536, and their operands, the weights' arrival and the latents' loads pass 200 KB
-// through shared memory, 1,590 cycles; measured 1,690 where no m moves.  The score CTA has 36 MMAs of 32
-// cycles (the bf16 rate: two terms at twice the rate) and a softmax of 1,700 for two tiles
-// in turn.  A tree of 64 nodes x 64 heads over 200,000 tokens, 1.78e12 operations:
-// 1,340 us (1,260 at the best clocks), 1.33 PFLOP/s of the 1.93 measured for bf16; 1,490
-// with queries four times as large, where some m moves at most tiles.  Short work
-// adds a cluster's start, 6 us per piece for the queries' way into Tensor Memory, 4 us for
-// its output, and the merge: 30 sequences of 4,096 to 8,192 tokens x 128 heads 69 us.
+// through shared memory, 1,590 cycles; measured 1,690 where no m moves.  The score CTA has
+// 36 MMAs of 32 cycles (the bf16 rate: two terms at twice the rate) and a softmax of 1,700
+// for two tiles in turn.  A tree of 64 nodes x 64 heads over 200,000 tokens, 1.78e12
+// operations: 1,340 us (1,260 at the best clocks), 1.33 PFLOP/s of the 1.93 measured for
+// bf16; 1,490 with queries four times as large, where some m moves at most tiles.  Short
+// work adds a cluster's start, 6 us per piece for the queries' way into Tensor Memory, 4 us
+// for its output, and the merge: 30 sequences of 4,096 to 8,192 tokens x 128 heads 69 us.
 //
 // Work split as in split.cuh; pieces of a row group are merged by a second kernel.  Every
 // wait is bounded (2 s, less in the self-test); on timeout both CTAs stop issuing, drain
